@@ -282,35 +282,37 @@ def _plain_append(s):
 
 def _plain_attend(s):
     c = s["case"]
-    hkv, d, G, P = c["hkv"], c["d"], c["hq"] // c["hkv"], c["prefix"]
-    R = s["q"].shape[0]
-    out = torch.empty(R, c["hq"], d, dtype=s["q"].dtype, device=DEV)
-    lse = torch.empty(R, c["hq"], dtype=torch.float32, device=DEV)
-
-    def keys(cache, pages, n):     # [hkv, n, d] in 32 bits
-        return cache[pages.long()].flatten(0, 1)[:n].float().transpose(0, 1)
-
-    pk, pv = (keys(x, s["pre"], P) for x in (s["k_cache"], s["v_cache"]))
-    for i, (t, n) in enumerate(zip(s["rows"], s["kv"])):
-        if t == 0:
-            continue
-        r0 = s["starts"][i]
-        pages = s["table"][i, :-(-n // c["page"])]
-        k = torch.cat([pk, keys(s["k_cache"], pages, n)], dim=1)
-        v = torch.cat([pv, keys(s["v_cache"], pages, n)], dim=1)
-        q = s["q"][r0:r0 + t].float().unflatten(1, (hkv, G)).permute(1, 0, 2, 3).reshape(hkv, t * G, d)
-        sc = torch.matmul(q, k.transpose(1, 2)) * d ** -0.5
-        if c["causal"]:
-            last = P + n - t + torch.arange(t, device=DEV).repeat_interleave(G)
-            sc = torch.where(torch.arange(P + n, device=DEV)[None] <= last[:, None], sc, float("-inf"))
-        m = sc.amax(dim=-1, keepdim=True) if P + n else torch.full_like(q[..., :1], float("-inf"))
-        safe = torch.where(m == float("-inf"), 0.0, m)
-        p = torch.exp(sc - safe)
-        l = p.sum(dim=-1, keepdim=True)
-        o = torch.matmul(p, v) / torch.where(l == 0, 1.0, l)
-        out[r0:r0 + t] = o.unflatten(1, (t, G)).permute(1, 0, 2, 3).flatten(1, 2).to(out.dtype)
-        lse[r0:r0 + t] = (m + torch.log(l)).squeeze(-1).unflatten(1, (t, G)).permute(1, 0, 2).flatten(1, 2)
-    return out, lse
+    hkv, hq, d, P, page = c["hkv"], c["hq"], c["d"], c["prefix"], c["page"]
+    n, R, G = len(s["kv"]), s["q"].shape[0], c["hq"] // c["hkv"]
+    T, N = max(s["rows"]), max(s["kv"])
+    # the pages of [prefix ; own keys] of every sequence, padded to the longest
+    j = torch.arange(P + N, device=DEV)
+    own_j = (j - P).clamp(min=0)
+    pages, at = s["table"][:, own_j // page], torch.where(j < P, j, own_j) % page
+    if P:
+        pages = torch.where(j < P, s["pre"][j.clamp(max=P - 1) // page], pages)
+    kv_len, t_len = s["kv_len"][:, None], (s["row_start"][1:] - s["row_start"][:-1])[:, None]
+    there = j[None] < P + kv_len                                              # [n, keys]
+    pages = torch.where(there, pages, 0).long()
+    k = s["k_cache"][pages, at].float().permute(0, 2, 3, 1)                   # [n, hkv, d, keys]
+    v = torch.where(there[..., None, None], s["v_cache"][pages, at], 0).float().transpose(1, 2)
+    # the rows of every sequence, padded to the most
+    t = torch.arange(T, device=DEV)
+    at_row = (s["row_start"][:-1, None] + t).clamp(max=R - 1).long()          # [n, T]
+    q = s["q"][at_row].float().unflatten(2, (hkv, G)).permute(0, 2, 1, 3, 4).flatten(2, 3)
+    sc = torch.matmul(q, k) * d ** -0.5                                       # [n, hkv, T * G, keys]
+    seen = there[:, None]
+    if c["causal"]:
+        seen = seen & (j <= (P + kv_len - t_len + t)[..., None])              # [n, T, keys]
+    sc = torch.where(seen.expand(n, T, P + N).repeat_interleave(G, dim=1)[:, None], sc, float("-inf"))
+    m = sc.amax(dim=-1, keepdim=True)
+    p = torch.exp(sc - torch.where(m == float("-inf"), 0.0, m))
+    l = p.sum(dim=-1, keepdim=True)
+    o = torch.matmul(p, v) / torch.where(l == 0, 1.0, l)
+    real = t[None] < t_len
+    o = o.unflatten(2, (T, G)).permute(0, 2, 1, 3, 4).flatten(2, 3)           # [n, T, hq, d]
+    lse = (m + torch.log(l)).squeeze(-1).unflatten(2, (T, G)).transpose(1, 2).flatten(2, 3)
+    return o[real].to(s["q"].dtype), lse[real]
 
 
 def _plain_verify(s):
