@@ -61,7 +61,8 @@ enum dflash_status {
   DFLASH_ERR_UNSUPPORTED = -5   /* a shape or format this build does not run  */
 };
 
-enum dflash_dtype { DFLASH_F32 = 0, DFLASH_BF16 = 1, DFLASH_FP8_E4M3 = 2 };
+/* DFLASH_F16 is a type of the target-side calls only. */
+enum dflash_dtype { DFLASH_F32 = 0, DFLASH_BF16 = 1, DFLASH_FP8_E4M3 = 2, DFLASH_F16 = 3 };
 enum dflash_rope { DFLASH_ROPE_PLAIN = 0, DFLASH_ROPE_YARN = 1 };
 
 /* e4m3 KV cache (the FP8 block attention named on the dflash_head page;
@@ -378,6 +379,184 @@ int dflash_trace_launches(dflash_t *h, int32_t max_launches, int32_t *kinds, int
 
 /* Kernel launches issued by the handle since it was created. */
 int dflash_launch_count(dflash_t *h, int64_t *launches);
+
+/* ------------------------------------------------------------------------
+ * The target model's side of a speculative step.
+ *
+ * A step hands the target a few new rows of each of n_seq sequences (the
+ * anchor token and the drafted block, or one token, or a prompt).  In every
+ * target layer dflash_step_append puts the rows' keys and values into the
+ * target's paged cache and dflash_step_attention attends over it; after the
+ * target's lm_head dflash_verify_tokens decides which drafts stand.  These
+ * calls take no handle: every buffer is the caller's, and all of a step's
+ * lengths are read on the device, so a captured step replays with the
+ * lengths its arrays hold then.  Pointers are on the current device.
+ *
+ * Sequence i owns rows row_start[i] .. row_start[i+1]-1 of the step (T_i of
+ * them, 0 allowed).  Its keys are the prefix_len rows that every sequence of
+ * the batch shares (a common prompt, at prefix_pages) followed by kv_len[i]
+ * rows of its own (at its row of the block table), the step's rows last: row
+ * t of the step is own key kv_len[i] - T_i + t, and its position is
+ * prefix_len plus that.
+ *
+ * Out-of-range contents of the device arrays cannot be refused by the host;
+ * the kernels bound them instead: a row index, length or page outside its
+ * range writes nothing, and a page outside [0, n_pages) reads as zeros.
+ * ------------------------------------------------------------------------ */
+
+/* A paged cache of one target layer.  Key row r of a page, kv head h starts
+ * at k + page * page_stride + r * row_stride + h * head_stride (elements;
+ * its head_dim elements are contiguous), values alike; the same pages and
+ * strides serve both.  Both bases start on a 16-byte boundary and strides
+ * are multiples of 8 elements. */
+typedef struct dflash_paged_cache {
+  void *k, *v;
+  int32_t dtype;       /* DFLASH_BF16 or DFLASH_F16                        */
+  int32_t n_pages;
+  int32_t page_size;   /* rows of a page: 16, 32, 64, 128 or 256           */
+  int32_t n_kv_heads;
+  int32_t head_dim;    /* 64 or 128                                        */
+  int64_t page_stride, row_stride, head_stride;
+} dflash_paged_cache;
+
+/* The rows of a step and where their sequences' keys are. */
+typedef struct dflash_step {
+  int32_t n_seq;                /* 1 .. 4096                               */
+  int32_t n_rows;               /* rows of the step's buffers; those from
+                                   row_start[n_seq] on are left as they are */
+  const int32_t *row_start;     /* device [n_seq + 1], non-decreasing from 0 */
+  const int32_t *kv_len;        /* device [n_seq]                          */
+  const int32_t *block_table;   /* device [n_seq, table_cols] page ids     */
+  int32_t table_cols;
+  int64_t table_stride;         /* elements between its rows               */
+  int32_t prefix_len;           /* 0: no shared prefix                     */
+  const int32_t *prefix_pages;  /* device, ceil(prefix_len / page_size)    */
+} dflash_step;
+
+/* RoPE inverse frequencies, the drafter's formulas: plain theta^(-2j/rot_dim),
+ * or the YaRN remap when yarn_factor > 1 (else 1 or 0), for j < rot_dim / 2
+ * into inv_freq (host), and the factor on cos and sin into *mscale (1, or
+ * YaRN's).  rot_dim even, theta > 1.  Host only. */
+int dflash_rope_frequencies(int32_t rot_dim, double theta, double yarn_factor, int32_t yarn_original_max_pos,
+                            double yarn_beta_fast, double yarn_beta_slow, double *inv_freq, double *mscale);
+
+typedef struct dflash_append_args {
+  int32_t dtype;             /* of q, k and v: DFLASH_F32, or the cache's  */
+  int32_t n_heads;           /* query heads (0: no queries)                */
+  const void *q, *k, *v;     /* device [n_rows, heads, head_dim]           */
+  int64_t q_stride, k_stride, v_stride;   /* elements between rows         */
+  const float *q_gain, *k_gain;  /* device [head_dim] head RMSNorm gains, or
+                                    NULL: that side has no norm            */
+  double eps;                /* of the head norms, > 0                     */
+  int32_t rot_dim;           /* rotated leading elements of a head, a
+                                multiple of 16 up to head_dim (0: none)    */
+  const double *inv_freq;    /* host [rot_dim / 2], read during the call   */
+  double mscale;             /* factor on cos and sin                      */
+  const int32_t *positions;  /* device [n_rows], or NULL: as above         */
+  void *q_out;               /* device [n_rows, n_heads, head_dim], cache
+                                dtype; may be q itself when the types and
+                                strides are the same                       */
+  int64_t q_out_stride;
+} dflash_append_args;
+
+/* Queries and keys of the step's rows: per head x / sqrt(mean x^2 + eps) *
+ * gain, then RoPE (pairs j, j + rot_dim / 2; the rest of a head passes
+ * through); keys and values go to their rows of the cache, queries to q_out,
+ * each rounded once.  Row pointers start on 16-byte boundaries (bases and
+ * strides).  Rows of the caches that no row of the step names stay as they
+ * are; a row whose own index would be negative, or past the block table,
+ * writes no key or value (its query is written).  One launch. */
+int dflash_step_append(const dflash_paged_cache *cache, const dflash_step *step, const dflash_append_args *args,
+                       void *stream);
+
+/* Bytes of workspace for dflash_step_attention of up to n_rows rows (the
+ * current device's SM count sizes it).  Start: 256-byte aligned.  Calls that
+ * share a workspace, replays of captured ones too, must not overlap. */
+int dflash_step_attention_workspace(const dflash_paged_cache *cache, int32_t n_rows, int32_t n_heads, size_t *bytes);
+
+typedef struct dflash_attention_args {
+  int32_t n_heads;       /* a multiple of n_kv_heads, at most 64 times it  */
+  int32_t causal;        /* 1: row t sees own keys up to its own;
+                            0: every own key                               */
+  float scale;           /* on q.k; 0: 1 / sqrt(head_dim)                  */
+  const void *q;         /* device [n_rows, n_heads, head_dim], cache dtype */
+  int64_t q_stride;      /* elements between rows (a multiple of 8)        */
+  void *out;             /* device [n_rows, n_heads, head_dim], cache dtype */
+  int64_t out_stride;
+  float *lse;            /* device [n_rows, n_heads], or NULL              */
+} dflash_attention_args;
+
+/* out = softmax(scale q K^T) V over each row's keys, lse = log of the sum of
+ * exp(scale q.k) over them (natural).  The shared prefix is read once for the
+ * whole batch.  A row without keys gives zeros and lse -inf.  What the cache
+ * holds past a sequence's or the prefix's last key has no effect, whatever
+ * it is.  A value element of the step's own rows that is not finite makes
+ * that element NaN in every row that sees it, and only there; keys and
+ * values before the step's rows are finite or spread to the whole sequence
+ * (the prefix's to the batch).  Scores and sums are f32; softmax weights are
+ * rounded to the cache's type for the product with V.  Two launches. */
+int dflash_step_attention(const dflash_paged_cache *cache, const dflash_step *step,
+                          const dflash_attention_args *args, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The pieces the attention of a step is cut into (inspection; host only, no
+ * device).  cache and step as above, but row_start and kv_len are host arrays
+ * and nothing else of them is followed.  Query rows go in items of up to
+ * 2 floor(128 / G) tokens of one kv head (G query heads each), keys in blocks
+ * of 128; an item counts one unit and one per block, the prefix's items
+ * first, then each sequence's, and n_cta CTAs take equal runs of units. */
+typedef struct dflash_step_piece {
+  int32_t cta;
+  int32_t segment;             /* 0: shared prefix, 1: own keys            */
+  int32_t seq;                 /* -1 for the prefix                        */
+  int32_t kv_head;
+  int32_t row0, n_tokens;      /* the item's rows of the step              */
+  int32_t block0, block1;      /* key blocks [block0, block1) of the segment */
+  int32_t first;               /* 1: the item's first piece                */
+  int32_t last_cta;            /* then the CTA of its last one, else -1    */
+} dflash_step_piece;
+int dflash_step_attention_plan(const dflash_paged_cache *cache, const dflash_step *step, int32_t n_heads,
+                               int32_t causal, int32_t n_cta, int32_t *n_pieces, dflash_step_piece *pieces,
+                               int32_t max_pieces);
+
+/* Synchronise the stream and report whether the last dflash_step_attention
+ * on this workspace completed: DFLASH_ERR_TIMEOUT when a bounded device-side
+ * wait gave up (its rows then hold NaN). */
+int dflash_step_attention_status(const void *workspace, void *stream);
+
+typedef struct dflash_verify_args {
+  int32_t n_seq;
+  int32_t k;                    /* drafted tokens of a sequence, at most    */
+  int32_t vocab;
+  int32_t dtype;                /* of both probabilities: F32, BF16 or F16  */
+  const int32_t *draft;         /* device [n_seq, k]                        */
+  int64_t draft_stride;
+  const int32_t *n_draft;       /* device [n_seq]: how many, 0 .. k; NULL: k */
+  const void *target_probs;     /* device [n_seq, k + 1, vocab]: row j after
+                                   j accepted drafts                        */
+  int64_t target_seq_stride, target_row_stride;
+  const void *draft_probs;      /* device [n_seq, k, vocab] that draft j was
+                                   drawn from; NULL: greedy drafts (all of
+                                   the probability on draft j)              */
+  int64_t draft_seq_stride, draft_row_stride;
+  const float *u_accept;        /* device [n_seq, k], uniform in [0, 1)     */
+  int64_t u_accept_stride;
+  const float *u_token;         /* device [n_seq], uniform in [0, 1)        */
+  int32_t *tokens;              /* device out [n_seq, k + 1]: accepted
+                                   drafts, the sampled token, then -1       */
+  int32_t *n_accepted;          /* device out [n_seq]                       */
+} dflash_verify_args;
+
+/* Verification of drafted tokens.  Draft x_j is accepted while
+ * u_accept[j] q_j(x_j) < p_j(x_j).  At the first rejection j the next token
+ * is drawn from the positive part of p_j - q_j, after n_draft acceptances
+ * from p_{n_draft}: the lowest index whose cumulative sum exceeds
+ * u_token * total.  The tokens are then distributed as the target's own.
+ * Probabilities need not sum to one; NaN, infinite and negative ones count
+ * as zero, and a draft outside [0, vocab) is rejected.  Where nothing is left
+ * of p_j - q_j the token is drawn from p_j, and without any positive p_j it
+ * is 0.  Sums carry 46 bits or more and are taken in a fixed order.  One
+ * launch, no workspace; the rows need no alignment beyond their type's. */
+int dflash_verify_tokens(const dflash_verify_args *args, void *stream);
 
 /* Release the handle (the workspace stays the caller's). */
 void dflash_destroy(dflash_t *h);

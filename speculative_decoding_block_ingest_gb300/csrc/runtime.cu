@@ -308,6 +308,29 @@ CUtensorMap make_map_u8(const void* base, uint64_t rows, uint64_t cols, uint32_t
 
 }  // namespace
 
+namespace dfl {
+
+int report_error(int code, const char* message) {
+  g_last_error = message;
+  return code;
+}
+
+bool encode_tiled_map(CUtensorMap* m, int dtype, uint32_t rank, const void* base, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box) {
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  try {
+    return tensor_map_encoder()(m,
+                                dtype == DFLASH_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                                rank, const_cast<void*>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  } catch (const CudaError&) {
+    return false;
+  }
+}
+
+}  // namespace dfl
+
 struct dflash_handle {
   dflash_config cfg;
   Layout lo;
@@ -1982,6 +2005,33 @@ int dflash_trace_launches(dflash_t* h, int32_t max_launches, int32_t* kinds, int
     if (offsets) offsets[i] = h->trace_recs[i].offset;
   }
   return DFLASH_OK;
+}
+
+int dflash_rope_frequencies(int32_t rot_dim, double theta, double yarn_factor, int32_t yarn_original_max_pos,
+                            double yarn_beta_fast, double yarn_beta_slow, double* inv_freq, double* mscale) {
+  g_last_error.clear();
+  if (!inv_freq || !mscale) return fail(DFLASH_ERR_INVALID_ARG, "null argument");
+  if (rot_dim < 2 || rot_dim % 2) return fail(DFLASH_ERR_INVALID_ARG, "rot_dim must be even and positive");
+  if (!(theta > 1.0)) return fail(DFLASH_ERR_INVALID_ARG, "theta must be > 1");
+  dflash_config c{};
+  c.head_dim = rot_dim;
+  c.rope_theta = theta;
+  c.rope_type = yarn_factor > 1.0 ? DFLASH_ROPE_YARN : DFLASH_ROPE_PLAIN;
+  c.yarn_factor = yarn_factor;
+  c.yarn_original_max_pos = yarn_original_max_pos;
+  c.yarn_beta_fast = yarn_beta_fast;
+  c.yarn_beta_slow = yarn_beta_slow;
+  if (!(yarn_factor == 0.0 || (yarn_factor >= 1.0 && std::isfinite(yarn_factor))) ||
+      (yarn_factor > 1.0 && (yarn_original_max_pos < 1 || !(yarn_beta_fast > 0) || !(yarn_beta_slow > 0))))
+    return fail(DFLASH_ERR_INVALID_ARG, "bad YaRN parameters");
+  return guarded([&]() -> int {
+    std::vector<double> inv;
+    float ms;
+    rope_table(c, inv, ms);
+    std::copy(inv.begin(), inv.end(), inv_freq);
+    *mscale = ms;
+    return DFLASH_OK;
+  });
 }
 
 int dflash_launch_count(dflash_t* h, int64_t* launches) {

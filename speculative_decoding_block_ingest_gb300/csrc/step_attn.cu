@@ -1,0 +1,728 @@
+// step_attn.cu -- attention of a step's rows over [shared prefix ; own keys]
+// of a paged cache, on the 5th-generation tensor cores.
+//
+// For row t, head h of kv head g = h / G, with M its largest scaled score:
+//   l = sum_j exp(s_j - M),  o = sum_j exp(s_j - M) v_j / l,  s_j = scale q.k_j
+// over its keys, computed block by block (128 keys) with a running M and l.
+//
+// Items.  The G query heads of a kv head and consecutive tokens fill query
+// tiles of 128 rows (floor(128 / G) tokens).  The prefix is attended by tiles
+// that run over the rows of the whole batch, so its keys are read once per
+// kv head and 256 rows instead of once per sequence; own keys by tiles of one
+// sequence.  Item = (segment, sequence, kv head, two tiles).  Partial results
+// (o, max, sum) of the segments are merged by a second kernel.
+//
+// Balance.  One CTA per SM; the items' key blocks form one line of units that
+// is cut into equal pieces (StepAttnArgs), so a single long sequence, many
+// short ones and any mixture load the SMs alike, with lengths known only on
+// the device.  A CTA continues at most one item begun by another (its first),
+// which bounds the partials: one per row and segment plus one tile per CTA.
+//
+// A CTA runs two streams of 128 query rows each:
+//   pair   (an item with rows for both tiles)  both streams take every key
+//          block, so a K/V tile feeds 256 rows;
+//   single (at most one tile of rows: decoding)  stream 0 takes the even
+//          blocks and stream 1 the odd ones of the same rows, and their
+//          results are merged in tensor memory.
+// Either way one stream's products run under the other's softmax.
+//   warps 0..3, 4..7  softmax of stream 0 / 1, one thread per query row
+//   warp 8            TMA: query tiles (ring of 2), K and V tiles (ring)
+//   warp 10, one lane the pieces of items this CTA runs, described in a ring
+//   warp 9, one lane  tcgen05.mma: S = Q K^T into TMEM, O += P V with P (in
+//                     the cache's type, over S) read from TMEM
+// V tiles are used as they lie in the cache (rows are keys), as the MN-major
+// operand of the second product.
+#include "../../include/dflash.h"
+#include "kernels.cuh"
+#include "ptx.cuh"
+#include "step_plan.cuh"
+
+namespace dfl {
+namespace {
+
+constexpr int kStepThreads = 384;
+// registers of a softmax / other thread: 2 x 208 + 88 = 3 x 168, the launch's own
+constexpr int kSoftRegs = 208, kOtherRegs = 88;
+constexpr int kSoftThreads = 256;        // warps 0..7
+constexpr int kAtomBytes = kKeys * 128;  // 128 rows x 128 bytes
+constexpr int kMaxStages = 11;
+constexpr size_t kSmemLimit = 227 * 1024;
+constexpr float kGrow = 8.f;             // O is rescaled when a row's max grows by more than 2^8
+constexpr int kFrags = 2;                // fragments described ahead
+constexpr int kBarPair = 3;              // named barrier of the 256 softmax threads
+
+// ---------------------------------------------------------------- TMEM access
+// 128 columns of a row are loaded at once and waited for once; the wait takes
+// the registers as operands so that no use of them can move above it.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait32(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                 "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                 "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ float pack2(float2 p) {   // two weights in the cache's type (the lower key in the low half)
+  if constexpr (BF16) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
+    return __uint_as_float(reinterpret_cast<const uint32_t&>(b));
+  } else {
+    const __half2 b = __floats2half2_rn(p.x, p.y);
+    return __uint_as_float(reinterpret_cast<const uint32_t&>(b));
+  }
+}
+
+// Descriptor of an MN-major tile in the 128-byte swizzle: rows are K (keys)
+// of 128 B (64 MN elements), 8-key atoms 1024 B apart along K, the next 64
+// MN elements one tile of 128 keys further.
+__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kAtomBytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* map, uint64_t* bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+struct Shared {
+  uint64_t kvfull[kMaxStages], kvempty[kMaxStages];
+  uint64_t qfull[2], qempty[2], sfull[2], pfull[2], pvdone[2];
+  uint64_t drained;
+  uint32_t tmem;
+  int abort;
+  // scheduling: this CTA's fragments, in a ring
+  uint64_t ffull[kFrags], fempty[kFrags];
+  Frag frag[kFrags];
+  long base;
+  int seq0;
+  union {
+    long warp_units[kStepThreads / 32];   // scheduling
+    float2 ml[2][128];                    // merge of the two streams of a single item
+  };
+  // first own key whose value element is not finite, per element
+  int bad[128];
+  int any_bad;
+};
+constexpr int kSharedBytes = 3072;
+static_assert(sizeof(Shared) <= kSharedBytes, "control block of the attention kernel");
+
+// Waits on the fragment ring outlast any one fragment; a failed wait
+// elsewhere ends the others within kWaitNs, so this limit is not met.
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer() - t0 > 10 * kWaitNs) return false;
+  return true;
+}
+
+// ---------------------------------------------------------------- the kernel
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kStepThreads, 1)
+    step_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ StepAttnArgs a) {
+  constexpr int kDAtoms = D / 64;
+  constexpr int kTile = kDAtoms * kAtomBytes;          // a Q, K or V tile
+  constexpr uint32_t kFmt = BF16 ? (1u << 7) | (1u << 10) : 0u;
+  constexpr uint32_t kIdescS = (1u << 4) | kFmt | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+  constexpr uint32_t kIdescO = (1u << 4) | kFmt | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
+  constexpr uint32_t kColO = 256;                      // TMEM: S / P of the streams at 0 and 128, O at 256 and 384
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + 2 * kTile;
+  Shared& sh = *reinterpret_cast<Shared*>(sKV + a.stages * kTile);
+  volatile int* abort = &sh.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(&sh.kvfull[i], 1);
+      mbar_init(&sh.kvempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.qfull[i], 1);
+      mbar_init(&sh.qempty[i], 1);
+      mbar_init(&sh.sfull[i], 1);
+      mbar_init(&sh.pfull[i], 128);
+      mbar_init(&sh.pvdone[i], 1);
+    }
+    mbar_init(&sh.drained, 1);
+    for (int i = 0; i < kFrags; ++i) {
+      mbar_init(&sh.ffull[i], 1);
+      mbar_init(&sh.fempty[i], 10);   // the TMA and MMA warps and the eight softmax warps
+    }
+    sh.abort = 0;
+    sh.any_bad = 0;
+    sh.seq0 = -1;
+    sh.base = 0;
+    fence_barrier_init();
+    tma_prefetch_map(&tmQ);
+    tma_prefetch_map(&tmK);
+    tma_prefetch_map(&tmV);
+  }
+  if (tid < 128) sh.bad[tid] = INT_MAX;
+  if (warp == 9) tmem_alloc(&sh.tmem, 512);
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- this CTA's units: every thread counts a run of sequences
+  Walk w(a);
+  {
+    const int per = (a.s.n_seq + kStepThreads - 1) / kStepThreads;
+    const int i0 = min(tid * per, a.s.n_seq), i1 = min(i0 + per, a.s.n_seq);
+    long mine = 0;
+    for (int i = i0; i < i1; ++i) mine += (long)a.Hkv * w.head_units(i);
+    long inc = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) sh.warp_units[warp] = inc;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    long at = w.prefix_units(), total = at;
+    for (int v = 0; v < kStepThreads / 32; ++v) {
+      if (v < warp) at += sh.warp_units[v];
+      total += sh.warp_units[v];
+    }
+    at += inc - mine;                    // this thread's first unit
+    share_units(w, total, a.n_cta, blockIdx.x);
+    if (w.ua < w.ub && w.ua >= at && w.ua < at + mine)  // the sequence that holds unit ua
+      for (int i = i0; i < i1; ++i) {
+        const long n = (long)a.Hkv * w.head_units(i);
+        if (w.ua < at + n) {
+          sh.seq0 = i;
+          sh.base = at;
+          break;
+        }
+        at += n;
+      }
+    __syncthreads();
+  }
+  const uint32_t tmem = sh.tmem;
+  // Every role takes every fragment, also after a failed wait (it then skips
+  // the work), so the ring and the named barriers never starve.
+  uint32_t nf = 0;
+  auto take = [&](Frag& f, bool alone = false) -> bool {   // alone: one lane takes for its warp
+    const int i = nf % kFrags;
+    ring_wait(&sh.ffull[i], (nf / kFrags) & 1);
+    f = sh.frag[i];
+    ++nf;
+    if (!alone) __syncwarp();
+    if (alone || lane == 0) mbar_arrive(&sh.fempty[i]);
+    return f.seg >= 0;
+  };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8) {
+      // ------------------------------------------------------------------ TMA
+      bool ok = true;
+      uint32_t nq = 0, nkv = 0;                       // query tiles and K/V tiles so far
+      const uint32_t q_bytes = (uint32_t)(kDAtoms * a.tpt * a.G * 128);
+      const uint32_t box_bytes = (uint32_t)a.box_rows * 128;
+      const int box_shift = __ffs(a.box_rows) - 1;
+      Frag f;
+      while (take(f)) {
+        if (!ok || f.b0 >= f.b1) continue;
+        const int tiles = f.ntok > a.tpt ? 2 : 1;
+        for (int i = 0; i < tiles && ok; ++i, ++nq) {
+          const int slot = nq & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(&sh.qempty[slot], ((nq >> 1) & 1) ^ 1, abort));
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sh.qfull[slot], q_bytes);
+            for (int at = 0; at < kDAtoms; ++at)
+              tma_load_3d(sQ + slot * kTile + at * kAtomBytes, &tmQ, &sh.qfull[slot], at * 64, f.h * a.G,
+                          f.tok0 + i * a.tpt);
+          }
+          __syncwarp();
+        }
+        // page ids: one lane per box of the next 32, the following 32 in flight
+        const int* table = f.seg ? a.s.block_table + f.seq * a.s.table_stride : a.s.prefix_pages;
+        const int n_box = (f.keys + a.box_rows - 1) >> box_shift;
+        auto page_of = [&](int box) -> int {
+          return box < n_box ? table[(int)(((long)box << box_shift) >> a.s.page_shift)] : 0;
+        };
+        const int first_box = f.b0 * a.boxes;
+        int cur = page_of(first_box + lane), nxt = page_of(first_box + 32 + lane), win = first_box;
+        for (int b = f.b0; b < f.b1 && ok; ++b) {
+          const int box0 = b * a.boxes, n = min(a.boxes, n_box - box0);
+          if (box0 >= win + 32) {                      // boxes of a block never straddle a window
+            cur = nxt;
+            win += 32;
+            nxt = page_of(win + 32 + lane);
+          }
+          for (int kv = 0; kv < 2 && ok; ++kv, ++nkv) {
+            const int st = (int)(nkv % a.stages);
+            ok = __all_sync(0xffffffffu, mbar_wait(&sh.kvempty[st], ((nkv / a.stages) & 1) ^ 1, abort));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&sh.kvfull[st], (uint32_t)n * kDAtoms * box_bytes);
+            __syncwarp();
+            const int bi = lane / kDAtoms, at = lane % kDAtoms;
+            const int page = __shfl_sync(0xffffffffu, cur, min(box0 - win + bi, 31));
+            if (bi < n)
+              tma_load_4d(sKV + st * kTile + at * kAtomBytes + bi * box_bytes, kv ? &tmV : &tmK, &sh.kvfull[st], at * 64,
+                          f.h, (int)(((long)(box0 + bi) << box_shift) & (a.s.page_size - 1)), page);
+            __syncwarp();
+          }
+        }
+      }
+      if (!ok) {   // leave no copy in flight behind
+        sh.abort = 1;
+        int none = 0;
+        for (uint32_t i = nkv > (uint32_t)a.stages ? nkv - a.stages : 0; i < nkv; ++i)
+          mbar_wait(&sh.kvfull[i % a.stages], (i / a.stages) & 1, &none);
+        for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) mbar_wait(&sh.qfull[i & 1], (i >> 1) & 1, &none);
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------------ MMA
+      if (lane == 0) {
+        bool ok = true;
+        uint32_t nq = 0, nb = 0;                       // query tiles and key blocks before this fragment
+        uint32_t np[2] = {0, 0};                       // P tiles used by each stream
+        const uint32_t q_addr = smem_u32(sQ), kv_addr = smem_u32(sKV);
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          if (ok && !mbar_wait(bar, parity, abort)) ok = false;
+          tc_fence_after();
+          return ok;
+        };
+        auto stage = [&](uint32_t tile) { return (int)(tile % a.stages); };
+        auto landed = [&](uint32_t tile) { return wait(&sh.kvfull[stage(tile)], (tile / a.stages) & 1); };
+        Frag f;
+        while (take(f, true)) {
+          const int n = f.b1 - f.b0;
+          if (!ok || n <= 0) continue;
+          const bool pair = f.ntok > a.tpt;
+          const int cnt[2] = {pair ? n : (n + 1) / 2, pair ? n : n / 2};
+          // the K tile of a stream's j-th block (its V tile follows)
+          auto k_tile = [&](int s, int j) { return 2 * (nb + (uint32_t)(pair ? j : 2 * j + s)); };
+          const int slot0 = nq & 1;
+          if (!wait(&sh.qfull[slot0], (nq >> 1) & 1)) continue;
+          if (pair && !wait(&sh.qfull[slot0 ^ 1], ((nq + 1) >> 1) & 1)) continue;
+          auto issue_s = [&](int s, int j) {
+            const uint32_t t = k_tile(s, j);
+            if (!landed(t)) return;
+            const uint32_t qa = q_addr + (uint32_t)((pair ? slot0 ^ s : slot0) * kTile);
+            const uint32_t ka = kv_addr + (uint32_t)(stage(t) * kTile);
+  #pragma unroll
+            for (int kk = 0; kk < 4 * kDAtoms; ++kk) {
+              const uint32_t at = (uint32_t)(kk >> 2) * kAtomBytes;
+              const uint64_t adv = (uint64_t)((kk & 3) * 2);
+              mma_bf16(tmem + 128u * s, desc_sw128(qa + at) + adv, desc_sw128(ka + at) + adv, kIdescS, kk > 0);
+            }
+            mma_commit(&sh.sfull[s]);
+            if (!pair || s == 1) mma_commit(&sh.kvempty[stage(t)]);
+            // the last product on a query tile frees its slot
+            if (j + 1 == cnt[s]) {
+              if (pair) mma_commit(&sh.qempty[slot0 ^ s]);
+              else if (n == 1 || s == ((n - 1) & 1)) mma_commit(&sh.qempty[slot0]);
+            }
+          };
+          auto issue_pv = [&](int s, int j) {
+            const uint32_t t = k_tile(s, j) + 1;
+            if (!wait(&sh.pfull[s], np[s] & 1) || !landed(t)) return;
+            ++np[s];
+            const uint32_t va = kv_addr + (uint32_t)(stage(t) * kTile);
+  #pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma_f16_ts(tmem + kColO + 128u * s, tmem + 128u * s + (uint32_t)(kk * 8),
+                         desc_sw128_mn(va) + (uint64_t)(kk * (2048 >> 4)), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(&sh.pvdone[s]);
+            if (!pair || s == 1) mma_commit(&sh.kvempty[stage(t)]);
+          };
+          for (int s = 0; s < 2 && ok; ++s)
+            if (cnt[s]) issue_s(s, 0);
+          for (int j = 0; j < cnt[0] && ok; ++j)
+            for (int s = 0; s < 2 && ok; ++s) {
+              if (j >= cnt[s]) continue;
+              issue_pv(s, j);
+              if (ok && j + 1 < cnt[s]) issue_s(s, j + 1);
+            }
+          nq += pair ? 2 : 1;
+          nb += (uint32_t)n;
+        }
+        if (!ok) sh.abort = 1;
+        // every product is done before tensor memory is freed
+        int none = 0;
+        mma_commit(&sh.drained);
+        mbar_wait(&sh.drained, 0, &none);
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      // ------------------------------------------------------------------ fragments
+      if (lane == 0) {
+        if (w.ua < w.ub) w.begin(sh.seq0, sh.base);
+        else w.pos = w.ub;
+        for (uint32_t i = 0, more = 1; more; ++i) {
+          Frag f;
+          more = w.next(f);
+          if (!more) f.seg = -1;
+          if (!ring_wait(&sh.fempty[i % kFrags], ((i / kFrags) & 1) ^ 1)) break;
+          sh.frag[i % kFrags] = f;
+          mbar_arrive(&sh.ffull[i % kFrags]);
+        }
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ------------------------------------------------------------------ softmax
+    const int st = warp >> 2;                        // stream
+    const int r = tid & 127;                         // row of its tile
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t s_addr = tmem + lanes + 128u * st;
+    const int tok = r / a.G, head = r - tok * a.G;
+    bool ok = true;
+    uint32_t np = 0, nb = 0;
+    auto both = [&]() { asm volatile("barrier.sync %0, %1;" ::"r"(kBarPair), "r"(kSoftThreads) : "memory"); };
+    Frag f;
+    while (take(f)) {
+      const int n = f.b1 - f.b0;
+      const bool pair = f.ntok > a.tpt;
+      const int cnt = pair ? n : (n + 1 - st) / 2;
+      const int t = (pair ? st * a.tpt : 0) + tok;   // token within the item
+      const bool live = tok < a.tpt && t < f.ntok;
+      const bool causal = f.seg == 1 && a.causal;
+      // keys this row sees; rows without a token skip the mask
+      const int lim = !live ? INT_MAX : min(causal ? max(f.lim0 + t, 0) : f.keys, f.keys);
+      const bool any_live = __any_sync(0xffffffffu, live);
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < cnt; ++j, ++np) {
+        const int bi = pair ? j : 2 * j + st;        // block of the fragment
+        const int key0 = (f.b0 + bi) * kKeys;
+        if (ok && !__all_sync(0xffffffffu, mbar_wait(&sh.sfull[st], np & 1, abort))) ok = false;
+        tc_fence_after();
+        if (ok && any_live) {
+          float x[kKeys];
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 32) tmem_ld32_async(s_addr + i, x + i);
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 32) tmem_ld_wait32(x + i);
+          if (!__all_sync(0xffffffffu, lim - key0 >= kKeys)) {
+            const int seen = lim - key0;
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) x[i] = i < seen ? x[i] : -INFINITY;
+          }
+          float mx[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(x[i], x[i + 4]);
+#pragma unroll
+          for (int i = 8; i < kKeys; i += 8)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) mx[v] = max3(mx[v], x[i + v], x[i + v + 4]);
+          const float mj = a.scale_log2 * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // the running maximum moves only when it grows by more than 2^8:
+          // weights stay below 2^8 and the final division uses the same one
+          const bool grow = mj > m + kGrow;
+          if (j > 0 && __any_sync(0xffffffffu, grow)) {
+            // O holds the products through this stream's block j - 1
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh.pvdone[st], (np - 1) & 1, abort))) ok = false;
+            tc_fence_after();
+            const float f0 = grow ? ex2_fast(m - mj) : 1.f;
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              const uint32_t oa = tmem + lanes + kColO + 128u * st + c;
+              tmem_ld32_async(oa, o);
+              tmem_ld_wait32(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= f0;
+              tmem_st32(oa, o);
+            }
+            l *= f0;
+          }
+          if (grow) m = mj;
+          const float2 neg = make_float2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m);
+          const float2 sc = make_float2(a.scale_log2, a.scale_log2);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 64) {
+            float pw[32];
+#pragma unroll
+            for (int v = 0; v < 32; ++v) {
+              float2 p = fma2(make_float2(x[i + 2 * v], x[i + 2 * v + 1]), sc, neg);
+              p.x = ex2_fast(p.x);
+              p.y = ex2_fast(p.y);
+              sum[v & 1] = add2(sum[v & 1], p);
+              pw[v] = pack2<BF16>(p);
+            }
+            tmem_st32(s_addr + i / 2, pw);
+          }
+          const float2 tot = add2(sum[0], sum[1]);
+          l += tot.x + tot.y;
+        }
+        // V rows behind the last key hold anything: zero them.  Own keys that
+        // some row of the step must not see may hold anything too: their
+        // elements that are not finite are taken out and remembered.
+        const int own0 = causal && f.lim0 < f.keys ? max(f.lim0, 0) : INT_MAX;   // first key not seen by all rows
+        if (ok && (st == 0 || !pair) && (key0 + kKeys > f.keys || key0 + kKeys > own0)) {
+          const uint32_t tile = 2 * (nb + (uint32_t)bi) + 1;
+          if (!__all_sync(0xffffffffu, mbar_wait(&sh.kvfull[tile % a.stages], (tile / a.stages) & 1, abort))) ok = false;
+          uint8_t* v = sKV + (tile % a.stages) * kTile + r * 128;
+          const int key = key0 + r;
+          if (key >= f.keys) {
+#pragma unroll
+            for (int c = 0; c < 8 * kDAtoms; ++c)
+              *reinterpret_cast<uint4*>(v + (c >> 3) * kAtomBytes + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          } else if (key >= own0) {
+            for (int c = 0; c < 8 * kDAtoms; ++c) {
+              uint16_t* e = reinterpret_cast<uint16_t*>(v + (c >> 3) * kAtomBytes + (((c & 7) ^ (r & 7)) * 16));
+              for (int i = 0; i < 8; ++i) {
+                constexpr uint16_t kExp = BF16 ? 0x7F80 : 0x7C00;
+                if ((e[i] & kExp) == kExp) {
+                  e[i] = 0;
+                  atomicMin(&sh.bad[c * 8 + i], key);
+                  sh.any_bad = 1;
+                }
+              }
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        mbar_arrive(&sh.pfull[st]);
+      }
+      nb += (uint32_t)n;
+      // ---- the fragment's result
+      if (ok && cnt > 0 && !__all_sync(0xffffffffu, mbar_wait(&sh.pvdone[st], (np - 1) & 1, abort))) ok = false;
+      tc_fence_after();
+      const long row = f.tok0 + t;                   // row of the step
+      float* po;
+      float2* pml;
+      if (f.first) {
+        const long at = row * a.Hq + f.h * a.G + head;
+        po = a.seg_o[f.seg] + at * D;
+        pml = a.seg_ml[f.seg] + at;
+      } else {
+        const long at = (long)blockIdx.x * 256 + (pair ? st * 128 : 0) + r;
+        po = a.cta_o + at * D;
+        pml = a.cta_ml + at;
+      }
+      float m0 = m, l0 = l, w0 = 1.f, w1 = 0.f;      // this stream's part, or the merge of both
+      if (!pair) sh.ml[st][r] = make_float2(m, l);
+      both();
+      if (!pair) {
+        const float2 e0 = sh.ml[0][r], e1 = sh.ml[1][r];
+        m0 = fmaxf(e0.x, e1.x);
+        w0 = e0.x == -INFINITY ? 0.f : ex2_fast(e0.x - m0);
+        w1 = e1.x == -INFINITY ? 0.f : ex2_fast(e1.x - m0);
+        l0 = e0.y * w0 + e1.y * w1;
+        // a row whose every score is NaN has no maximum but a NaN sum
+        if (e0.x == -INFINITY && e0.y != 0.f) l0 = e0.y, w0 = 1.f;
+        if (e1.x == -INFINITY && e1.y != 0.f) l0 = e1.y, w1 = 1.f;
+      }
+      const bool empty = pair ? cnt == 0 : n == 0;
+      const bool poisoned = sh.any_bad;
+      // a pair's streams write their own rows; of a single item each writes
+      // half of the elements
+      const int c_lo = pair ? 0 : st * (D / 2), c_hi = pair ? D : c_lo + D / 2;
+      if (any_live) {
+        for (int c = c_lo; c < c_hi; c += 32) {
+          float o[32];
+          if (empty || !ok) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          } else {
+            const uint32_t oa = tmem + lanes + kColO + c;
+            tmem_ld32_async(oa + (pair ? 128u * st : 0u), o);
+            tmem_ld_wait32(o);
+            if (!pair) {
+              float o1[32];
+              tmem_ld32_async(oa + 128u, o1);
+              tmem_ld_wait32(o1);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                o[i] = w0 != 0.f ? o[i] * w0 : 0.f;
+                o[i] = w1 != 0.f ? fmaf(o1[i], w1, o[i]) : o[i];
+              }
+            }
+          }
+          if (poisoned) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (sh.bad[c + i] < lim) o[i] = __int_as_float(0x7fc00000);
+          }
+          if (live) {
+            float4* dst = reinterpret_cast<float4*>(po + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+      }
+      if (live && (pair || st == 0)) {
+        *pml = make_float2(m0, l0);
+        if (f.first && head == 0) {
+          a.meta[((long)f.seg * a.s.n_rows + row) * a.Hkv + f.h] = make_int4(blockIdx.x, f.last_cta, t, 0);
+        }
+      }
+      tc_fence_before();
+      both();                                        // both streams have read O, and the notes on bad values
+      if (poisoned) {
+        if (tid < 128) sh.bad[tid] = INT_MAX;
+        if (tid == 0) sh.any_bad = 0;
+        both();
+      }
+      tc_fence_after();
+    }
+    if (!ok) sh.abort = 1;
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0) a.status[blockIdx.x] = sh.abort ? DERR_TIMEOUT : 0;
+  if (warp == 9) {
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- merge
+// One warp per (row, head): o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i
+// over the row's fragments, at most one per segment and CTA.
+constexpr int kMergeThreads = 256;
+
+template <int D, typename Out>
+__global__ void __launch_bounds__(kMergeThreads) step_merge_kernel(const __grid_constant__ StepAttnArgs a) {
+  constexpr int kPer = D / 32;   // elements of a lane
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long item = (long)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  const long row = item / a.Hq;
+  const int head = (int)(item % a.Hq), h = head / a.G;
+  if (row >= a.s.start(a.s.n_seq)) return;   // behind the last sequence: left as it is
+  float m = -INFINITY, l = 0.f, o[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[i] = 0.f;
+  bool bad = false;
+  for (int seg = a.s.prefix_len > 0 ? 0 : 1; seg < 2; ++seg) {
+    const int4 meta = a.meta[((long)seg * a.s.n_rows + row) * a.Hkv + h];
+    const int c0 = min(max(meta.x, 0), a.n_cta - 1), c1 = min(max(meta.y, c0), a.n_cta - 1);
+    const int in_tile = min(max(meta.z, 0), 2 * a.tpt - 1);
+    // rows of a pair's second tile lie behind the first's 128
+    const int trow = in_tile < a.tpt ? in_tile * a.G : 128 + (in_tile - a.tpt) * a.G;
+    const int n = c1 - c0 + 1;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      // lane i: fragment i's max and sum
+      const int i = i0 + lane;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (i < n) {
+        ml = i == 0 ? a.seg_ml[seg][row * a.Hq + head] : a.cta_ml[(long)(c0 + i) * 256 + trow + head - h * a.G];
+        bad |= a.status[c0 + i] != 0;
+      }
+      float mx = ml.x;
+#pragma unroll
+      for (int s = 16; s; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+      const float mn = fmaxf(m, mx);
+      const float keep = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2_fast(m - mn);
+      const float wt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_fast(ml.x - mn);
+      m = mn;
+      float add = wt == 0.f ? 0.f : wt * ml.y;
+#pragma unroll
+      for (int s = 16; s; s >>= 1) add += __shfl_xor_sync(0xffffffffu, add, s);
+      l = (keep == 0.f ? 0.f : l * keep) + add;
+#pragma unroll
+      for (int v = 0; v < kPer; ++v) o[v] = keep == 0.f ? 0.f : o[v] * keep;
+      const int cnt = min(32, n - i0);
+#pragma unroll 4
+      for (int f = 0; f < cnt; ++f) {
+        const float g = __shfl_sync(0xffffffffu, wt, f);
+        const float* src = i0 + f == 0 ? a.seg_o[seg] + (row * a.Hq + head) * D
+                                       : a.cta_o + ((long)(c0 + i0 + f) * 256 + trow + head - h * a.G) * D;
+        float x[kPer];
+        if constexpr (kPer == 4) {
+          const float4 q = reinterpret_cast<const float4*>(src)[lane];
+          x[0] = q.x, x[1] = q.y, x[2] = q.z, x[3] = q.w;
+        } else {
+          const float2 q = reinterpret_cast<const float2*>(src)[lane];
+          x[0] = q.x, x[1] = q.y;
+        }
+#pragma unroll
+        for (int v = 0; v < kPer; ++v) o[v] = g == 0.f ? o[v] : fmaf(x[v], g, o[v]);
+      }
+    }
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  const float inv = bad ? __int_as_float(0x7fc00000) : (l == 0.f ? 0.f : 1.f / l);
+  Out* dst = static_cast<Out*>(a.out) + row * a.out_stride + (long)head * D + lane * kPer;
+#pragma unroll
+  for (int v = 0; v < kPer; ++v) o[v] *= inv;
+  Out y[kPer];
+#pragma unroll
+  for (int v = 0; v < kPer; ++v) y[v] = Out(o[v]);
+  if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(y);
+  else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(y);
+  if (a.lse && lane == 0)
+    a.lse[row * a.Hq + head] = bad ? inv : (l == 0.f ? -INFINITY : 0.69314718055994531f * (m + log2f(l)));
+}
+
+size_t step_attention_smem(int d, int stages) { return (size_t)(2 + stages) * (d / 64) * kAtomBytes + kSharedBytes; }
+
+template <int D, bool BF16>
+cudaError_t launch(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                   cudaStream_t s) {
+  auto* attn = step_attn_kernel<D, BF16>;
+  const size_t smem = step_attention_smem(D, a.stages);
+  cudaError_t e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn, dim3(a.n_cta), dim3(kStepThreads), smem, s, q, k, v, a);
+  if (e != cudaSuccess) return e;
+  const long warps = (long)a.s.n_rows * a.Hq;
+  const long ctas = (warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
+  auto* merge = step_merge_kernel<D, std::conditional_t<BF16, __nv_bfloat16, __half>>;
+  return launch_pdl(merge, dim3((unsigned)ctas), dim3(kMergeThreads), 0, s, a);
+}
+
+}  // namespace
+
+// K and V tiles in flight: as many as shared memory holds (5 at d = 128, 11 at 64)
+int step_attention_stages(int d) {
+  int n = kMaxStages;
+  while (step_attention_smem(d, n) > kSmemLimit) --n;
+  return n;
+}
+
+cudaError_t launch_step_attention(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMap& k,
+                                  const CUtensorMap& v, cudaStream_t s) {
+  if (a.d == 128) return a.bf16 ? launch<128, true>(a, q, k, v, s) : launch<128, false>(a, q, k, v, s);
+  return a.bf16 ? launch<64, true>(a, q, k, v, s) : launch<64, false>(a, q, k, v, s);
+}
+
+}  // namespace dfl

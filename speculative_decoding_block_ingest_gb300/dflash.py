@@ -19,7 +19,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libdflash.so")
 
 OK, ERR_INVALID_ARG, ERR_CAPACITY, ERR_CUDA, ERR_TIMEOUT, ERR_UNSUPPORTED = 0, -1, -2, -3, -4, -5
-F32, BF16, FP8 = 0, 1, 2
+F32, BF16, FP8, F16 = 0, 1, 2, 3
 ROPE_PLAIN, ROPE_YARN = 0, 1
 _DT = {"f32": F32, "bf16": BF16, "fp8": FP8}
 
@@ -28,7 +28,9 @@ EXPORTS = ("dflash_workspace_bytes", "dflash_create", "dflash_ingest_ctx", "dfla
            "dflash_draft_tokens", "dflash_set_ctx_cap", "dflash_seq_reset", "dflash_seq_len", "dflash_kv_read",
            "dflash_device_status", "dflash_destroy", "dflash_last_error", "dflash_profile_enable",
            "dflash_profile_read", "dflash_launch_count", "dflash_trace_begin", "dflash_trace_launches",
-           "dflash_selftest_wait_timeout", "dflash_attention_plan")
+           "dflash_selftest_wait_timeout", "dflash_attention_plan", "dflash_rope_frequencies", "dflash_step_append",
+           "dflash_step_attention_workspace", "dflash_step_attention", "dflash_step_attention_status",
+           "dflash_step_attention_plan", "dflash_verify_tokens")
 TRACE_WORDS = 16   # u64 words per traced CTA (see dflash_trace_begin)
 KERNEL_KINDS = ("gemm", "attention", "combine", "init", "norm", "finish")
 
@@ -59,6 +61,53 @@ class LayerWeights(ctypes.Structure):
 class Weights(ctypes.Structure):
     _fields_ = [("fc", ctypes.c_void_p), ("fc_scale", ctypes.c_void_p), ("hidden_norm", ctypes.c_void_p),
                 ("norm", ctypes.c_void_p), ("layers", ctypes.POINTER(LayerWeights))]
+
+
+PDOUBLE = ctypes.POINTER(ctypes.c_double)
+
+
+class PagedCacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class StepDesc(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("row_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("table_cols", ctypes.c_int32),
+                ("table_stride", ctypes.c_int64), ("prefix_len", ctypes.c_int32), ("prefix_pages", ctypes.c_void_p)]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("q", ctypes.c_void_p),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("q_gain", ctypes.c_void_p),
+                ("k_gain", ctypes.c_void_p), ("eps", ctypes.c_double), ("rot_dim", ctypes.c_int32),
+                ("inv_freq", PDOUBLE), ("mscale", ctypes.c_double), ("positions", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_int64)]
+
+
+class AttentionArgs(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_int64), ("lse", ctypes.c_void_p)]
+
+
+class StepPiece(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("cta", "segment", "seq", "kv_head", "row0", "n_tokens", "block0",
+                                               "block1", "first", "last_cta")]
+
+
+class VerifyArgs(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("k", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("draft", ctypes.c_void_p), ("draft_stride", ctypes.c_int64),
+                ("n_draft", ctypes.c_void_p), ("target_probs", ctypes.c_void_p),
+                ("target_seq_stride", ctypes.c_int64), ("target_row_stride", ctypes.c_int64),
+                ("draft_probs", ctypes.c_void_p), ("draft_seq_stride", ctypes.c_int64),
+                ("draft_row_stride", ctypes.c_int64), ("u_accept", ctypes.c_void_p),
+                ("u_accept_stride", ctypes.c_int64), ("u_token", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+                ("n_accepted", ctypes.c_void_p)]
 
 
 _lib = None
@@ -97,6 +146,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dflash_trace_launches.argtypes = [vp, i32, p32, p32, ctypes.POINTER(ctypes.c_int64), p32]
     p64 = ctypes.POINTER(ctypes.c_int64)
     lib.dflash_attention_plan.argtypes = [ctypes.POINTER(Config), i32, i32, p64, p64, p32, p32, p32, p32, i32]
+    dbl = ctypes.c_double
+    lib.dflash_rope_frequencies.argtypes = [i32, dbl, dbl, i32, dbl, dbl, PDOUBLE, PDOUBLE]
+    cache_p, step_p = ctypes.POINTER(PagedCacheDesc), ctypes.POINTER(StepDesc)
+    lib.dflash_step_append.argtypes = [cache_p, step_p, ctypes.POINTER(AppendArgs), vp]
+    lib.dflash_step_attention_workspace.argtypes = [cache_p, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
+    lib.dflash_step_attention.argtypes = [cache_p, step_p, ctypes.POINTER(AttentionArgs), vp, ctypes.c_size_t, vp]
+    lib.dflash_step_attention_status.argtypes = [vp, vp]
+    lib.dflash_step_attention_plan.argtypes = [cache_p, step_p, i32, i32, i32, p32, ctypes.POINTER(StepPiece), i32]
+    lib.dflash_verify_tokens.argtypes = [ctypes.POINTER(VerifyArgs), vp]
     lib.dflash_destroy.argtypes = [vp]
     lib.dflash_destroy.restype = None
     lib.dflash_last_error.restype = ctypes.c_char_p
