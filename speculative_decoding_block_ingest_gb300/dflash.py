@@ -84,7 +84,7 @@ class AppendArgs(ctypes.Structure):
                 ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
                 ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("q_gain", ctypes.c_void_p),
                 ("k_gain", ctypes.c_void_p), ("eps", ctypes.c_double), ("rot_dim", ctypes.c_int32),
-                ("inv_freq", PDOUBLE), ("mscale", ctypes.c_double), ("positions", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("mscale", ctypes.c_double), ("positions", ctypes.c_void_p),
                 ("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_int64)]
 
 

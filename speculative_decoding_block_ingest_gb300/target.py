@@ -15,6 +15,7 @@ captured step replays with whatever they hold then.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional, Tuple
 
@@ -37,53 +38,53 @@ def _dtype(t: torch.Tensor, what: str) -> int:
     return d
 
 
-def _on(device: torch.device, what: str, t: torch.Tensor, dtype=None, dim: Optional[int] = None):
-    if t.device != device or device.type != "cuda":
-        _refuse(f"{what} is on {t.device}, expected the cache's CUDA device ({device})")
-    if dtype is not None and t.dtype != dtype:
-        _refuse(f"{what} has dtype {t.dtype}, expected {dtype}")
-    if dim is not None and t.dim() != dim:
-        _refuse(f"{what} has {t.dim()} dimensions, expected {dim}")
+def _cuda(device: torch.device, what: str) -> torch.device:
+    if device.type != "cuda":
+        _refuse(f"{what} is on {device}, expected a CUDA device")
+    return device
 
 
-def _index(device: torch.device, what: str, t: torch.Tensor, dim: int) -> int:
-    """Device pointer of an int32 tensor whose last dimension is contiguous."""
-    _on(device, what, t, torch.int32, dim)
-    if t.numel() and t.stride(-1) != 1 and t.shape[-1] > 1:
+def _vector(device: torch.device, what: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype = torch.int32) -> int:
+    """Device pointer of a tensor of this shape whose rows are contiguous."""
+    if t.device != device:
+        _refuse(f"{what} is on {t.device}, expected {device}")
+    if t.dtype != dtype or t.shape != shape:
+        _refuse(f"{what} is {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape)}")
+    if shape[-1] > 1 and t.stride(-1) != 1:
         _refuse(f"{what} must be contiguous in its last dimension")
     return t.data_ptr()
 
 
-class _Launch:
-    """The device and stream of one call: makes the device current, allocates
-    outputs on the call's stream, and tells the allocator of tensors that
-    belong to another one."""
+@contextlib.contextmanager
+def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
+    """The device (and the caller's stream, if any) made current."""
+    if stream is None:
+        with torch.cuda.device(device):
+            yield
+        return
+    if stream.device != device:
+        _refuse(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):     # makes its device current too; outputs are allocated on it
+        yield
 
-    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
-        self.device, self.stream = device, stream
-        self.ctx = None
 
-    def __enter__(self):
-        if self.stream is not None:
-            if self.stream.device != self.device:
-                _refuse(f"stream is on {self.stream.device}, the tensors on {self.device}")
-            self.ctx = torch.cuda.stream(self.stream)     # makes its device current too
-        elif torch.cuda.current_device() != self.device.index:
-            self.ctx = torch.cuda.device(self.device)
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        self.ptr = ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
-        return self
+def _stream(device: torch.device) -> int:
+    """Handle of the device's current stream (the public call makes a Stream
+    object, 2 us of a 10 us call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
-    def uses(self, *tensors):
-        if self.stream is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _used(stream: Optional[torch.cuda.Stream], *tensors):
+    """The caller named a stream: its tensors, which may belong to another
+    one, are not to be reused before the call has run."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _elsewhere(device: torch.device, stream: Optional[torch.cuda.Stream]) -> bool:
+    return stream is not None or torch.cuda.current_device() != device.index
 
 
 class Rope:
@@ -94,6 +95,7 @@ class Rope:
                  yarn_beta_fast: float = 32.0, yarn_beta_slow: float = 1.0):
         self.rot_dim = int(rot_dim)
         self.inv_freq = (ctypes.c_double * max(1, self.rot_dim // 2))()
+        self.ptr = ctypes.addressof(self.inv_freq)
         ms = ctypes.c_double(0)
         _check(dflash.load_library().dflash_rope_frequencies(
             self.rot_dim, float(theta), float(yarn_factor), int(yarn_original_max_pos), float(yarn_beta_fast),
@@ -107,20 +109,19 @@ class PagedCache:
     ``[n_pages, n_kv_heads, page_size, head_dim]`` pool passes its transpose)."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
-        _on(k.device, "k cache", k, dim=4)
-        _on(k.device, "v cache", v, k.dtype, 4)
-        if k.shape != v.shape or k.stride() != v.stride():
-            _refuse("k and v caches must have one shape and strides")
-        self.k, self.v = k, v
-        self.device = k.device
-        self.n_kv_heads, self.head_dim = k.shape[2], k.shape[3]
+        self.device = _cuda(k.device, "k cache")
+        if k.dim() != 4 or v.device != k.device or v.dtype != k.dtype or k.shape != v.shape or k.stride() != v.stride():
+            _refuse("k and v caches must be alike: [n_pages, page_size, n_kv_heads, head_dim], device, dtype, strides")
         if k.stride(3) != 1:
             _refuse("head elements of the caches must be contiguous")
+        self.k, self.v, self.dtype = k, v, k.dtype
+        self.n_kv_heads, self.head_dim = k.shape[2], k.shape[3]
         # the stride of a dimension of one element is never used
         st = [s if n > 1 else max(self.head_dim, 8) for s, n in zip(k.stride(), k.shape)]
         self.c = dflash.PagedCacheDesc(k=k.data_ptr(), v=v.data_ptr(), dtype=_dtype(k, "cache"), n_pages=k.shape[0],
                                        page_size=k.shape[1], n_kv_heads=k.shape[2], head_dim=k.shape[3],
                                        page_stride=st[0], row_stride=st[1], head_stride=st[2])
+        self.ref = ctypes.byref(self.c)
         self._ws = {}
 
     def workspace_bytes(self, n_rows: int, n_heads: int) -> int:
@@ -129,8 +130,7 @@ class PagedCache:
         if key not in self._ws:
             n = ctypes.c_size_t(0)
             with torch.cuda.device(self.device):
-                _check(dflash.load_library().dflash_step_attention_workspace(ctypes.byref(self.c), n_rows, n_heads,
-                                                                             ctypes.byref(n)))
+                _check(dflash.load_library().dflash_step_attention_workspace(self.ref, n_rows, n_heads, ctypes.byref(n)))
             if len(self._ws) > 64:
                 self._ws.clear()
             self._ws[key] = n.value
@@ -145,41 +145,47 @@ class Step:
 
     def __init__(self, row_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor,
                  prefix_pages: Optional[torch.Tensor] = None, prefix_len: int = 0):
-        dev = row_start.device
-        rs, kl = _index(dev, "row_start", row_start, 1), _index(dev, "kv_len", kv_len, 1)
-        bt = _index(dev, "block_table", block_table, 2)
-        n = kv_len.shape[0]
-        if row_start.shape[0] != n + 1 or block_table.shape[0] != n:
-            _refuse("row_start, kv_len and block_table disagree about the number of sequences")
-        pp = _index(dev, "prefix_pages", prefix_pages, 1) if prefix_pages is not None else None
-        self.tensors = (row_start, kv_len, block_table, prefix_pages)
-        self.device = dev
+        self.device = dev = _cuda(row_start.device, "row_start")
+        if row_start.dim() != 1 or row_start.shape[0] < 2 or block_table.dim() != 2:
+            _refuse("row_start must be [n_seq + 1] and block_table [n_seq, pages]")
+        n, cols = row_start.shape[0] - 1, block_table.shape[1]
+        rs = _vector(dev, "row_start", row_start, (n + 1,))
+        kl = _vector(dev, "kv_len", kv_len, (n,))
+        bt = _vector(dev, "block_table", block_table, (n, cols)) if cols else 0
         self.prefix_pages = 0 if prefix_pages is None else prefix_pages.shape[0]
-        cols = block_table.shape[1]
-        self.c = dflash.StepDesc(n_seq=n, n_rows=0, row_start=rs, kv_len=kl, block_table=bt, table_cols=cols,
-                                 table_stride=max(block_table.stride(0), cols) if n > 1 else cols,
-                                 prefix_len=int(prefix_len), prefix_pages=pp)
+        pp = _vector(dev, "prefix_pages", prefix_pages, (self.prefix_pages,)) if self.prefix_pages else 0
+        self.tensors = (row_start, kv_len, block_table, prefix_pages)
+        self.prefix_len = int(prefix_len)
+        self.fields = (rs, kl, bt, cols, max(block_table.stride(0), cols) if n > 1 else cols, self.prefix_len, pp)
+        self.n_seq = n
+        self._refs = {}
 
     def rows(self, cache: PagedCache, n_rows: int):
         """This step's descriptor for buffers of n_rows rows."""
         if self.device != cache.device:
             _refuse(f"the step is on {self.device}, the cache on {cache.device}")
-        if self.c.prefix_len > self.prefix_pages * cache.c.page_size:
+        if self.prefix_len > self.prefix_pages * cache.c.page_size:
             _refuse("prefix_pages does not hold prefix_len keys")
-        d = dflash.StepDesc.from_buffer_copy(self.c)
-        d.n_rows = n_rows
-        return d
+        ref = self._refs.get(n_rows)
+        if ref is None:
+            if len(self._refs) > 64:
+                self._refs = {}
+            ref = self._refs[n_rows] = ctypes.byref(dflash.StepDesc(self.n_seq, n_rows, *self.fields))
+        return ref
 
 
-def _rows(cache: PagedCache, what: str, t: torch.Tensor, heads: Optional[int] = None, n_rows: Optional[int] = None):
-    """Row stride of a [n_rows, heads, head_dim] tensor with contiguous heads."""
-    _on(cache.device, what, t, dim=3)
-    n, h, d = t.shape
-    if d != cache.head_dim or (heads is not None and h != heads) or (n_rows is not None and n != n_rows):
-        _refuse(f"{what} has shape {tuple(t.shape)}")
-    if t.numel() and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+def _rows(cache: PagedCache, what: str, t: torch.Tensor, n_rows: Optional[int] = None, heads: Optional[int] = None):
+    """(rows, heads, row stride) of a [n_rows, heads, head_dim] tensor with contiguous heads."""
+    shape, st, d = t.shape, t.stride(), cache.head_dim
+    if t.device != cache.device:
+        _refuse(f"{what} is on {t.device}, the cache on {cache.device}")
+    if len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads) or (
+            n_rows is not None and shape[0] != n_rows):
+        _refuse(f"{what} has shape {tuple(shape)}")
+    n, h = shape[0], shape[1]
+    if n and (st[2] != 1 or (h > 1 and st[1] != d)):
         _refuse(f"{what}: the heads of a row must be contiguous")
-    return t.stride(0) if n > 1 else h * d
+    return n, h, (st[0] if n > 1 else h * d)
 
 
 def append(cache: PagedCache, step: Step, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, *,
@@ -194,39 +200,41 @@ def append(cache: PagedCache, step: Step, q: Optional[torch.Tensor], k: torch.Te
     any row stride (views of one fused projection will do); gains f32
     ``[head_dim]``; positions int32 ``[n_rows]`` (default: prefix_len plus the
     row's own key index); q may be None.  ``q_out`` may be q itself."""
-    kv = cache.n_kv_heads
-    ks = _rows(cache, "k", k, kv)
-    n_rows = k.shape[0]
-    vs = _rows(cache, "v", v, kv, n_rows)
+    dev = cache.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            q_out = append(cache, step, q, k, v, rope=rope, q_gain=q_gain, k_gain=k_gain, eps=eps,
+                           positions=positions, q_out=q_out)
+        _used(stream, cache.k, cache.v, *step.tensors, q, k, v, q_gain, k_gain, positions, q_out)
+        return q_out
+    n, _, ks = _rows(cache, "k", k, None, cache.n_kv_heads)
+    _, _, vs = _rows(cache, "v", v, n, cache.n_kv_heads)
     if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
         _refuse("q, k and v must have one dtype")
-    a = dflash.AppendArgs(dtype=_dtype(k, "rows"), k=k.data_ptr(), v=v.data_ptr(), k_stride=ks, v_stride=vs, eps=eps)
-    for name, g in (("q_gain", q_gain), ("k_gain", k_gain)):
-        if g is not None:
-            _on(cache.device, name, g, torch.float32, 1)
-            if g.shape[0] != cache.head_dim or not g.is_contiguous():
-                _refuse(f"{name} must be a contiguous [head_dim] tensor")
-            setattr(a, name, g.data_ptr())
-    if rope is not None:
-        a.rot_dim, a.inv_freq, a.mscale = rope.rot_dim, ctypes.cast(rope.inv_freq, dflash.PDOUBLE), rope.mscale
-    if positions is not None:
-        a.positions = _index(cache.device, "positions", positions, 1)
-        if positions.shape[0] != n_rows:
-            _refuse("positions must have one entry per row")
-    with _Launch(cache.device, stream) as call:
-        if q is not None:
-            a.n_heads, a.q, a.q_stride = q.shape[1], q.data_ptr(), _rows(cache, "q", q, n_rows=n_rows)
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=cache.k.dtype, device=cache.device)
-            elif q_out.dtype != cache.k.dtype:
+    hq = qp = qs = qop = qos = 0
+    if q is not None:
+        _, hq, qs = _rows(cache, "q", q, n)
+        qp = q.data_ptr()
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=cache.dtype, device=dev)
+            qos = hq * cache.head_dim
+        else:
+            if q_out.dtype != cache.dtype:
                 _refuse("q_out must have the cache's dtype")
-            a.q_out, a.q_out_stride = q_out.data_ptr(), _rows(cache, "q_out", q_out, q.shape[1], n_rows)
-        elif q_out is not None:
-            _refuse("q_out without q")
-        s = step.rows(cache, n_rows)
-        _check(dflash.load_library().dflash_step_append(ctypes.byref(cache.c), ctypes.byref(s), ctypes.byref(a),
-                                                        call.ptr))
-        call.uses(cache.k, cache.v, *step.tensors, q, k, v, q_gain, k_gain, positions, q_out)
+            _, _, qos = _rows(cache, "q_out", q_out, n, hq)
+        qop = q_out.data_ptr()
+    elif q_out is not None:
+        _refuse("q_out without q")
+    head = (cache.head_dim,)
+    a = dflash.AppendArgs(
+        _dtype(k, "rows"), hq, qp, k.data_ptr(), v.data_ptr(), qs, ks, vs,
+        0 if q_gain is None else _vector(dev, "q_gain", q_gain, head, torch.float32),
+        0 if k_gain is None else _vector(dev, "k_gain", k_gain, head, torch.float32), eps,
+        0 if rope is None else rope.rot_dim, 0 if rope is None else rope.ptr, 1.0 if rope is None else rope.mscale,
+        0 if positions is None else _vector(dev, "positions", positions, (n,)), qop, qos)
+    rc = dflash.load_library().dflash_step_append(cache.ref, step.rows(cache, n), ctypes.byref(a), _stream(dev))
+    if rc:
+        _check(rc)
     return q_out
 
 
@@ -242,42 +250,50 @@ def attention(cache: PagedCache, step: Step, q: torch.Tensor, *, scale: Optional
     them.  Rows without keys give zeros and -inf.  ``workspace``: uint8, at
     least ``cache.workspace_bytes(n_rows, n_heads)``; calls that share one
     must not overlap (default: a fresh one)."""
-    qs = _rows(cache, "q", q)
-    n_rows, n_heads = q.shape[:2]
-    if q.dtype != cache.k.dtype:
+    dev = cache.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            out, lse = attention(cache, step, q, scale=scale, causal=causal, out=out, lse=lse, workspace=workspace)
+        _used(stream, cache.k, cache.v, *step.tensors, q, out, lse, workspace)
+        return out, lse
+    n, hq, qs = _rows(cache, "q", q)
+    if q.dtype != cache.dtype:
         _refuse("q must have the cache's dtype")
-    s = step.rows(cache, n_rows)
-    need = cache.workspace_bytes(n_rows, n_heads)
-    with _Launch(cache.device, stream) as call:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=cache.device)
-        elif out.dtype != q.dtype:
+    if scale is not None and not scale > 0:
+        _refuse("scale must be positive")
+    ref, need = step.rows(cache, n), cache.workspace_bytes(n, hq)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        os = hq * cache.head_dim
+    else:
+        if out.dtype != q.dtype:
             _refuse("out must have the cache's dtype")
-        if lse is None:
-            lse = torch.empty(n_rows, n_heads, dtype=torch.float32, device=cache.device)
-        _on(cache.device, "lse", lse, torch.float32, 2)
-        if tuple(lse.shape) != (n_rows, n_heads) or not lse.is_contiguous():
-            _refuse("lse must be a contiguous [n_rows, n_heads] tensor")
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
-        _on(cache.device, "workspace", workspace, torch.uint8, 1)
-        a = dflash.AttentionArgs(n_heads=n_heads, causal=1 if causal else 0, scale=0.0 if scale is None else scale,
-                                 q=q.data_ptr(), q_stride=qs, out=out.data_ptr(),
-                                 out_stride=_rows(cache, "out", out, n_heads, n_rows), lse=lse.data_ptr())
-        if scale is not None and not scale > 0:
-            _refuse("scale must be positive")
-        _check(dflash.load_library().dflash_step_attention(
-            ctypes.byref(cache.c), ctypes.byref(s), ctypes.byref(a), ctypes.c_void_p(workspace.data_ptr()),
-            workspace.numel(), call.ptr))
-        call.uses(cache.k, cache.v, *step.tensors, q, out, lse, workspace)
+        _, _, os = _rows(cache, "out", out, n, hq)
+    if lse is None:
+        lse = torch.empty((n, hq), dtype=torch.float32, device=dev)
+    else:
+        _vector(dev, "lse", lse, (n, hq), torch.float32)
+        if not lse.is_contiguous():
+            _refuse("lse must be contiguous")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _vector(dev, "workspace", workspace, (workspace.numel(),), torch.uint8)
+    a = dflash.AttentionArgs(hq, 1 if causal else 0, 0.0 if scale is None else scale, q.data_ptr(), qs, out.data_ptr(),
+                             os, lse.data_ptr())
+    rc = dflash.load_library().dflash_step_attention(cache.ref, ref, ctypes.byref(a), workspace.data_ptr(),
+                                                     workspace.numel(), _stream(dev))
+    if rc:
+        _check(rc)
     return out, lse
 
 
 def attention_status(workspace: torch.Tensor, stream: Optional[torch.cuda.Stream] = None):
     """Wait for the stream; raise if a bounded device-side wait of the last
     attention on this workspace gave up."""
-    with _Launch(workspace.device, stream) as call:
-        _check(dflash.load_library().dflash_step_attention_status(ctypes.c_void_p(workspace.data_ptr()), call.ptr))
+    dev = _cuda(workspace.device, "workspace")
+    with _on(dev, stream):
+        _check(dflash.load_library().dflash_step_attention_status(workspace.data_ptr(), _stream(dev)))
 
 
 def verify_tokens(draft: torch.Tensor, target_probs: torch.Tensor, u_accept: torch.Tensor, u_token: torch.Tensor, *,
@@ -291,37 +307,31 @@ def verify_tokens(draft: torch.Tensor, target_probs: torch.Tensor, u_accept: tor
     u_token ``[n_seq]`` uniform in [0, 1); n_draft int32 ``[n_seq]`` where
     sequences drafted fewer than k.  Returns int32 tokens ``[n_seq, k + 1]``
     (accepted drafts, the next token, then -1) and the accepted counts."""
-    dev = target_probs.device
-    _on(dev, "target_probs", target_probs, dim=3)
+    dev = _cuda(target_probs.device, "target_probs")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            got = verify_tokens(draft, target_probs, u_accept, u_token, draft_probs=draft_probs, n_draft=n_draft)
+        _used(stream, draft, target_probs, u_accept, u_token, draft_probs, n_draft)
+        return got
+    if target_probs.dim() != 3 or target_probs.shape[1] < 1:
+        _refuse("target_probs must be [n_seq, k + 1, vocab]")
     n, k1, vocab = target_probs.shape
-    _on(dev, "draft", draft, torch.int32, 2)
-    _on(dev, "u_accept", u_accept, torch.float32, 2)
-    _on(dev, "u_token", u_token, torch.float32, 1)
-    if tuple(draft.shape) != (n, k1 - 1) or tuple(u_accept.shape) != (n, k1 - 1) or u_token.shape[0] != n:
-        _refuse("draft, u_accept, u_token and target_probs disagree about n_seq or k")
-    for name, t in (("draft", draft), ("u_accept", u_accept), ("u_token", u_token), ("target_probs", target_probs)):
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
-            _refuse(f"{name} must be contiguous in its last dimension")
-    a = dflash.VerifyArgs(n_seq=n, k=k1 - 1, vocab=vocab, dtype=_dtype(target_probs, "target_probs"),
-                          draft=draft.data_ptr(), draft_stride=draft.stride(0), target_probs=target_probs.data_ptr(),
-                          target_seq_stride=target_probs.stride(0),
-                          target_row_stride=target_probs.stride(1) if k1 > 1 else vocab,
-                          u_accept=u_accept.data_ptr(), u_accept_stride=u_accept.stride(0),
-                          u_token=u_token.data_ptr())
-    if draft_probs is not None:
-        _on(dev, "draft_probs", draft_probs, target_probs.dtype, 3)
-        if tuple(draft_probs.shape) != (n, k1 - 1, vocab) or (vocab > 1 and draft_probs.stride(2) != 1):
-            _refuse("draft_probs must be [n_seq, k, vocab] with contiguous rows")
-        a.draft_probs, a.draft_seq_stride = draft_probs.data_ptr(), draft_probs.stride(0)
-        a.draft_row_stride = draft_probs.stride(1) if k1 > 2 else vocab
-    if n_draft is not None:
-        a.n_draft = _index(dev, "n_draft", n_draft, 1)
-        if n_draft.shape[0] != n:
-            _refuse("n_draft must have one entry per sequence")
-    with _Launch(dev, stream) as call:
-        tokens = torch.empty(n, k1, dtype=torch.int32, device=dev)
-        accepted = torch.empty(n, dtype=torch.int32, device=dev)
-        a.tokens, a.n_accepted = tokens.data_ptr(), accepted.data_ptr()
-        _check(dflash.load_library().dflash_verify_tokens(ctypes.byref(a), call.ptr))
-        call.uses(draft, target_probs, u_accept, u_token, draft_probs, n_draft)
+    k, dt, ts = k1 - 1, target_probs.dtype, target_probs.stride()
+    dp = dss = drs = 0
+    if draft_probs is not None and k:
+        dp = _vector(dev, "draft_probs", draft_probs, (n, k, vocab), dt)
+        dss, drs = draft_probs.stride(0), draft_probs.stride(1) if k > 1 else vocab
+    d = _vector(dev, "draft", draft, (n, k)) if k else 0
+    ua = _vector(dev, "u_accept", u_accept, (n, k), torch.float32) if k else 0
+    tokens = torch.empty((n, k1), dtype=torch.int32, device=dev)
+    accepted = torch.empty(n, dtype=torch.int32, device=dev)
+    a = dflash.VerifyArgs(
+        n, k, vocab, _dtype(target_probs, "target_probs"), d, draft.stride(0),
+        0 if n_draft is None else _vector(dev, "n_draft", n_draft, (n,)),
+        _vector(dev, "target_probs", target_probs, (n, k1, vocab), dt), ts[0], ts[1] if k else vocab, dp, dss, drs,
+        ua, u_accept.stride(0), _vector(dev, "u_token", u_token, (n,), torch.float32), tokens.data_ptr(),
+        accepted.data_ptr())
+    rc = dflash.load_library().dflash_verify_tokens(ctypes.byref(a), _stream(dev))
+    if rc:
+        _check(rc)
     return tokens, accepted

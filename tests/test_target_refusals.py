@@ -38,7 +38,7 @@ INV_FREQ = (ctypes.c_double * 64)(*[1.0] * 64)
 
 def append_args(**kw):
     a = dict(dtype=dflash.BF16, n_heads=4, q=P, k=P, v=P, q_stride=512, k_stride=256, v_stride=256, eps=1e-6,
-             rot_dim=128, inv_freq=ctypes.cast(INV_FREQ, dflash.PDOUBLE), mscale=1.0, q_out=P, q_out_stride=512)
+             rot_dim=128, inv_freq=ctypes.addressof(INV_FREQ), mscale=1.0, q_out=P, q_out_stride=512)
     a.update(kw)
     return dflash.AppendArgs(**a)
 
