@@ -8,17 +8,17 @@
 // the accepted drafts is read: 4 (V + V) bytes a sequence bound it, and for
 // one sequence the latency of two gathers, one sweep and a search.
 //
-// One cluster of 8 CTAs per sequence.  The row is cut into 128 runs, one per
-// warp of the cluster; each warp sums its run, the sums are exchanged through
-// distributed shared memory, every CTA scans all 128, and the CTA that holds
-// the run where u * total falls searches it (its entries are in L1 / L2).
+// One cluster of CTAs per sequence.  The row is cut into runs, one per warp of
+// the cluster; each warp sums its run, the sums are exchanged through
+// distributed shared memory, every CTA finds the run where u * total falls,
+// and the CTA that holds it searches it (its entries are in L1 / L2).
 //
 // A cumulative sum is compared with a number, and a vocabulary has 10^5
 // boundaries, so f32 sums (2^-24) would move one draw in a few hundred to a
-// neighbouring token.  f64 adds run at 1/64 of the f32 rate here, so the
-// sweep keeps each sum in two floats: p - q and every addition are split into
-// result and rounding error without loss, the errors are summed beside, and
-// only the lanes' totals and the search work in f64.
+// neighbouring token.  The f64 unit issues one warp instruction in 64 cycles
+// here (a search in f64 took 9 us of a 16 us call), so every sum is kept in
+// two floats: p - q and every addition are split into result and rounding
+// error without loss, and the errors are summed beside: 2^-44 or better.
 #include <cooperative_groups.h>
 
 #include "../../include/dflash.h"
@@ -31,17 +31,20 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kVerifyCtas = 8;      // CTAs of a cluster (the portable limit)
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kRuns = kVerifyCtas * kVerifyWarps;
+constexpr int kMaxCluster = 8;      // the portable limit
+constexpr int kMaxRuns = kMaxCluster * kVerifyWarps;
 
 __device__ __forceinline__ float as_f32(float x) { return x; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float as_f32(__half x) { return __half2float(x); }
 
-// NaN, infinite and negative probabilities count as zero.
-__device__ __forceinline__ float weight(float x) { return x > 0.f && x < INFINITY ? x : 0.f; }
+// NaN, infinite and negative probabilities count as zero: the positive finite
+// floats are the bit patterns 1 .. 0x7f7fffff.
+__device__ __forceinline__ float weight(float x) {
+  return __float_as_uint(x) - 1u < 0x7f7fffffu ? x : 0.f;
+}
 
 // a + b = s + e exactly
 __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
@@ -50,49 +53,88 @@ __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
   e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
 }
 
+// A sum in two floats, |lo| at most half a step of hi once normal.
 struct Sum {
   float hi = 0.f, lo = 0.f;
+  // + x + err, errors gathered in lo
   __device__ __forceinline__ void add(float x, float err) {
     float s, e;
     two_sum(hi, x, s, e);
     hi = s;
     lo += e + err;
   }
-  // max(p - q, 0)
-  __device__ __forceinline__ void add_diff(float p, float q) {
-    p = weight(p);
-    q = weight(q);
-    if (p > q) {
-      float d, e;
-      two_sum(p, -q, d, e);
-      add(d, e);
-    }
+  __device__ __forceinline__ Sum normal() const {
+    Sum r;
+    r.hi = __fadd_rn(hi, lo);
+    r.lo = __fsub_rn(lo, __fsub_rn(r.hi, hi));
+    return r;
+  }
+  __device__ __forceinline__ Sum operator+(const Sum& b) const {
+    Sum r = *this;
+    r.add(b.hi, b.lo);
+    return r.normal();
+  }
+  __device__ __forceinline__ bool operator>(const Sum& b) const { return hi > b.hi || (hi == b.hi && lo > b.lo); }
+  __device__ __forceinline__ Sum operator*(float u) const {
+    Sum r;
+    r.hi = __fmul_rn(hi, u);
+    r.lo = fmaf(lo, u, fmaf(hi, u, -r.hi));
+    return r.normal();
   }
 };
+__device__ __forceinline__ Sum shfl_xor(const Sum& s, int o) {
+  Sum r;
+  r.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
+  r.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+  return r;
+}
+__device__ __forceinline__ Sum shfl(const Sum& s, int lane) {
+  Sum r;
+  r.hi = __shfl_sync(0xffffffffu, s.hi, lane);
+  r.lo = __shfl_sync(0xffffffffu, s.lo, lane);
+  return r;
+}
+// Sum over this and the lower lanes (inclusive); `before`: over the lower ones.
+__device__ __forceinline__ Sum scan(Sum s, int lane, Sum& before) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    Sum x;
+    x.hi = __shfl_up_sync(0xffffffffu, s.hi, o);
+    x.lo = __shfl_up_sync(0xffffffffu, s.lo, o);
+    if (lane >= o) s = x + s;
+  }
+  before.hi = __shfl_up_sync(0xffffffffu, s.hi, 1);
+  before.lo = __shfl_up_sync(0xffffffffu, s.lo, 1);
+  if (lane == 0) before = Sum{};
+  return s;
+}
 
-// The weights of the row that the token is drawn from.
+// The weights of the row that the token is drawn from: p, or max(p - q, 0).
 template <typename T>
 struct Row {
   const T* p;
   const T* q;     // subtracted, or null
   int skip;       // index without weight (a rejected greedy draft), or -1
-  __device__ __forceinline__ double at(int i) const {
-    if (i == skip) return 0.0;
-    const double x = weight(as_f32(p[i]));
-    return q ? fmax(x - (double)weight(as_f32(q[i])), 0.0) : x;
-  }
 };
+__device__ __forceinline__ void add_weight(Sum& s, bool diff, float p, float q) {
+  p = weight(p);
+  if (!diff) {
+    s.add(p, 0.f);
+    return;
+  }
+  float d, e;
+  two_sum(p, -weight(q), d, e);
+  s.add(fmaxf(d, 0.f), d > 0.f ? e : 0.f);
+}
 
 // Sum of entries [a, b) over the warp's lanes (every lane gets it).
-template <typename T>
-__device__ double warp_sum(const Row<T>& r, int a, int b, int lane) {
-  constexpr int kVec = 16 / sizeof(T), kDepth = 4;
+template <typename T, bool DIFF>
+__device__ __forceinline__ Sum run_total(const Row<T>& r, int a, int b, int lane) {
+  constexpr int kVec = 16 / sizeof(T), kDepth = 2;
   Sum s[2];
-  auto take = [&](Sum& t, int i, T p, T q) { t.add_diff(i == r.skip ? 0.f : as_f32(p), r.q ? as_f32(q) : 0.f); };
   const T zero = T(0.f);
-  const bool vec = ((reinterpret_cast<uintptr_t>(r.p + a) | (r.q ? reinterpret_cast<uintptr_t>(r.q + a) : 0)) & 15) == 0;
   int i = a;
-  if (vec) {
+  if (((reinterpret_cast<uintptr_t>(r.p + a) | (DIFF ? reinterpret_cast<uintptr_t>(r.q + a) : 0)) & 15) == 0) {
     struct alignas(16) Pack {
       T v[kVec];
     };
@@ -102,13 +144,15 @@ __device__ double warp_sum(const Row<T>& r, int a, int b, int lane) {
       for (int u = 0; u < kDepth; ++u) {
         const int at = i + (u * 32 + lane) * kVec;
         p[u] = *reinterpret_cast<const Pack*>(r.p + at);
-        if (r.q) q[u] = *reinterpret_cast<const Pack*>(r.q + at);
+        if (DIFF) q[u] = *reinterpret_cast<const Pack*>(r.q + at);
       }
 #pragma unroll
       for (int u = 0; u < kDepth; ++u)
 #pragma unroll
-        for (int v = 0; v < kVec; ++v)
-          take(s[v & 1], i + (u * 32 + lane) * kVec + v, p[u].v[v], r.q ? q[u].v[v] : zero);
+        for (int v = 0; v < kVec; ++v) {
+          const float x = i + (u * 32 + lane) * kVec + v == r.skip ? 0.f : as_f32(p[u].v[v]);
+          add_weight(s[v & 1], DIFF, x, DIFF ? as_f32(q[u].v[v]) : 0.f);
+        }
     }
   }
   constexpr int kScalar = 8;
@@ -117,26 +161,27 @@ __device__ double warp_sum(const Row<T>& r, int a, int b, int lane) {
 #pragma unroll
     for (int u = 0; u < kScalar; ++u) {
       const int at = i + u * 32 + lane;
-      p[u] = at < b ? r.p[at] : zero;
-      q[u] = r.q && at < b ? r.q[at] : zero;
+      p[u] = at < b && at != r.skip ? r.p[at] : zero;
+      q[u] = DIFF && at < b ? r.q[at] : zero;
     }
 #pragma unroll
-    for (int u = 0; u < kScalar; ++u) take(s[u & 1], i + u * 32 + lane, p[u], q[u]);
+    for (int u = 0; u < kScalar; ++u) add_weight(s[u & 1], DIFF, as_f32(p[u]), as_f32(q[u]));
   }
-  double t = ((double)s[0].hi + (double)s[0].lo) + ((double)s[1].hi + (double)s[1].lo);
+  Sum t = s[0].normal() + s[1].normal();
 #pragma unroll
-  for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  for (int o = 16; o; o >>= 1) t = t + shfl_xor(t, o);
   return t;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
-  __shared__ double run_sum[kRuns];       // every run's sum, written by the whole cluster
-  __shared__ double warp_tot[kVerifyWarps];
-  __shared__ double sh_base, sh_th;
-  __shared__ int sh_acc, sh_run, sh_first, sh_last;
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
+  __shared__ Sum run_sum[kMaxRuns];       // every run's sum, written by the whole cluster
+  __shared__ Sum warp_sum[kVerifyWarps];
+  __shared__ Sum sh_base, sh_th;
+  __shared__ int sh_acc, sh_run, sh_token;
   cg::cluster_group cl = cg::this_cluster();
-  const int rank = (int)cl.block_rank(), seq = blockIdx.x / kVerifyCtas;
+  const int rank = (int)cl.block_rank(), ctas = (int)cl.num_blocks(), seq = blockIdx.x / ctas;
+  const int runs = ctas * kVerifyWarps;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_launch_dependents();
@@ -144,6 +189,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
   const int* draft = a.draft + seq * a.draft_stride;
   const T* P = static_cast<const T*>(a.p) + seq * a.p_seq;
   const T* Q = a.q ? static_cast<const T*>(a.q) + seq * a.q_seq : nullptr;
+  const float u0 = a.u_token[seq];
 
   if (warp == 0) {   // accepted drafts, the same in every CTA of the cluster
     int acc = 0;
@@ -152,25 +198,27 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
       bool take = false;
       if (j < nd) {
         const int x = draft[j];
+        const float u = a.u_accept[seq * a.u_stride + j];
         if (x >= 0 && x < a.vocab) {
           const float p = weight(as_f32(P[j * a.p_row + x]));
           const float q = Q ? weight(as_f32(Q[j * a.q_row + x])) : 1.f;
-          take = (double)a.u_accept[seq * a.u_stride + j] * (double)q < (double)p;
+          // u q < p, the product with its rounding error
+          const float h = __fmul_rn(u, q);
+          take = h < p || (h == p && fmaf(u, q, -h) < 0.f);
         }
       }
       const unsigned refused = ~__ballot_sync(0xffffffffu, take);
       acc += refused ? __ffs(refused) - 1 : 32;
       if (refused) break;
     }
-    if (lane == 0) sh_acc = acc;
+    if (lane == 0) sh_acc = min(acc, nd);
   }
   __syncthreads();
   const int acc = sh_acc;
-  const float u0 = a.u_token[seq];
-  const double u = u0 > 0.f ? (double)fminf(u0, 1.f) : 0.0;
+  const float u = u0 > 0.f ? fminf(u0, 1.f) : 0.f;
   const int V = a.vocab;
   // runs start on multiples of 16 entries
-  const int len = ((V + kRuns - 1) / kRuns + 15) & ~15;
+  const int len = ((V + runs - 1) / runs + 15) & ~15;
   Row<T> r{P + acc * a.p_row, nullptr, -1};
   if (acc < nd) {
     if (Q) r.q = Q + acc * a.q_row;
@@ -178,43 +226,47 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
   }
   for (bool retry = true;; retry = false) {
     const int my = rank * kVerifyWarps + warp;
-    const double t = warp_sum(r, min(my * len, V), min((my + 1) * len, V), lane);
+    const int lo = min(my * len, V), hi = min((my + 1) * len, V);
+    const Sum t = r.q ? run_total<T, true>(r, lo, hi, lane) : run_total<T, false>(r, lo, hi, lane);
     cl.sync();   // every CTA runs, and has read the sums of a first try
-    if (lane < kVerifyCtas) *cl.map_shared_rank(&run_sum[my], lane) = t;
+    if (lane < ctas) *cl.map_shared_rank(&run_sum[my], lane) = t;
     cl.sync();
-    if (warp == 0) {   // where u * total falls among the runs
-      double v[kRuns / 32], c = 0.0;
+    if (warp == 0) {   // where u * total falls among the runs: a few neighbours per lane
+      constexpr int kPer = kMaxRuns / 32;
+      Sum v[kPer], c;
+      int last = -1;   // last run with weight
 #pragma unroll
-      for (int i = 0; i < kRuns / 32; ++i) v[i] = c += run_sum[lane * (kRuns / 32) + i];
-      double inc = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
+      for (int i = 0; i < kPer; ++i) {
+        const int k = lane * kPer + i;
+        if (k < runs) {
+          c = c + run_sum[k];
+          if (run_sum[k].hi > 0.f) last = k;
+        }
+        v[i] = c;
       }
-      double base = __shfl_up_sync(0xffffffffu, inc, 1);
-      if (lane == 0) base = 0.0;
-      const double th = u * __shfl_sync(0xffffffffu, inc, 31);
-      int run = kRuns, last = -1;   // first run past th; last run with weight
-      double before = 0.0;
+      Sum before;
+      const Sum inc = scan(c, lane, before);
+      const Sum th = shfl(inc, 31) * u;
+      int run = kMaxRuns;   // first run past th
+      Sum base;
 #pragma unroll
-      for (int i = kRuns / 32 - 1; i >= 0; --i) {
-        const double prev = base + (i ? v[i - 1] : 0.0);
-        if (base + v[i] > th) run = lane * (kRuns / 32) + i, before = prev;
-        if (last < 0 && run_sum[lane * (kRuns / 32) + i] > 0.0) last = lane * (kRuns / 32) + i;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, run < kRuns);
+      for (int i = kPer - 1; i >= 0; --i)
+        if (before + v[i] > th) {
+          run = lane * kPer + i;
+          base = i ? before + v[i - 1] : before;
+        }
+      const unsigned hit = __ballot_sync(0xffffffffu, run < kMaxRuns);
       const int src = hit ? __ffs(hit) - 1 : 0;
       run = __shfl_sync(0xffffffffu, run, src);
-      before = __shfl_sync(0xffffffffu, before, src);
-      // u * total at or past the total: the last run that has weight
+      base = shfl(base, src);
+      // u * total at or past the total: the last entry that has weight
       last = __reduce_max_sync(0xffffffffu, last);
       if (lane == 0) {
         sh_run = hit ? run : last;
-        sh_base = before;
-        sh_th = hit ? th : INFINITY;
-        sh_first = INT_MAX;
-        sh_last = -1;
+        sh_base = base;
+        sh_th = th;
+        if (!hit) sh_th.hi = INFINITY;
+        sh_token = -1;
       }
     }
     __syncthreads();
@@ -234,60 +286,80 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const __grid_con
     }
   }
   if (run < 0 || run / kVerifyWarps != rank) return;
-  // the entry of the run: each thread takes a few neighbours, the CTA scans
-  const double th = sh_th;
-  double base = sh_base;
+  // The entry of the run: each thread takes a few neighbours; the warp, the
+  // lane and the entry where the sum passes th follow from the warps' and the
+  // lanes' sums.  `fallback` is the last entry with weight so far: the answer
+  // at u = 1, or if the sums here round below the run's own.
+  constexpr int kPer = 4;
+  const Sum th = sh_th;
+  Sum base = sh_base;
   const int end = min((run + 1) * len, V);
-  for (int i0 = run * len; i0 < end; i0 += kVerifyThreads * 4) {
-    const int i = i0 + tid * 4;
-    double w[4], c = 0.0;
+  int fallback = 0;
+  for (int i0 = run * len; i0 < end; i0 += kVerifyThreads * kPer) {
+    const int i = i0 + tid * kPer;
+    Sum w[kPer], c;
     int last = -1;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const double x = i + j < end ? r.at(i + j) : 0.0;
-      if (x > 0.0) last = i + j;
-      w[j] = c += x;
+    for (int j = 0; j < kPer; ++j) {
+      if (i + j < end && i + j != r.skip) {
+        Sum x;
+        add_weight(x, r.q != nullptr, as_f32(r.p[i + j]), r.q ? as_f32(r.q[i + j]) : 0.f);
+        if (x.hi > 0.f) {
+          last = i + j;
+          c = c + x;
+        }
+      }
+      w[j] = c;
     }
-    double inc = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-    if (lane == 31) warp_tot[warp] = inc;
-    __syncthreads();
-    double before = base;
-    for (int v = 0; v < kVerifyWarps; ++v) {
-      if (v < warp) before += warp_tot[v];
-      base += warp_tot[v];
-    }
-    before += inc - c;
-    int first = INT_MAX;
-#pragma unroll
-    for (int j = 3; j >= 0; --j)
-      if (before + w[j] > th && w[j] > (j ? w[j - 1] : 0.0)) first = i + j;
-    first = __reduce_min_sync(0xffffffffu, first);
+    Sum before;
+    const Sum inc = scan(c, lane, before);
     last = __reduce_max_sync(0xffffffffu, last);
-    if (lane == 0) {
-      if (first != INT_MAX) atomicMin(&sh_first, first);
-      if (last >= 0) atomicMax(&sh_last, last);
-    }
+    if (lane == 31) warp_sum[warp] = inc;
+    if (lane == 0 && last >= 0) atomicMax(&sh_token, last);
     __syncthreads();
-    if (sh_first != INT_MAX) break;
+    fallback = max(fallback, sh_token);
+    Sum wb;
+    const Sum winc = scan(lane < kVerifyWarps ? warp_sum[lane] : Sum{}, lane, wb);
+    const unsigned past = __ballot_sync(0xffffffffu, base + winc > th);
+    if (past) {   // the same in every warp
+      if (warp != __ffs(past) - 1) return;
+      const Sum mine = base + shfl(wb, warp);
+      int first = INT_MAX;
+#pragma unroll
+      for (int j = kPer - 1; j >= 0; --j)
+        if (mine + (before + w[j]) > th && w[j] > (j ? w[j - 1] : Sum{})) first = i + j;
+      first = __reduce_min_sync(0xffffffffu, first);
+      if (lane == 0) out[acc] = first != INT_MAX ? first : (last >= 0 ? last : fallback);
+      return;
+    }
+    base = base + shfl(winc, 31);
+    __syncthreads();
   }
-  // the scan may round below the run's own sum: then its last entry with weight
-  if (tid == 0) out[acc] = sh_first != INT_MAX ? sh_first : max(sh_last, 0);
+  if (tid == 0) out[acc] = fallback;
+}
+
+// CTAs of a sequence's cluster: 8 while they all fit the SMs at once (two to
+// an SM), fewer for larger batches, whose sequences fill the SMs by themselves.
+int cluster_size(int n_seq, int n_sm) {
+  int c = kMaxCluster;
+  while (c > 1 && (long)n_seq * c > 4L * n_sm) c /= 2;
+  return c;
 }
 
 template <typename T>
 cudaError_t launch(const VerifyArgs& a, cudaStream_t s) {
+  int dev = 0, n_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const unsigned ctas = cluster_size(a.n_seq, n_sm);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.n_seq * kVerifyCtas);
+  cfg.gridDim = dim3(a.n_seq * ctas);
   cfg.blockDim = dim3(kVerifyThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {kVerifyCtas, 1, 1};
+  attr[0].val.clusterDim = {ctas, 1, 1};
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
