@@ -89,7 +89,6 @@ struct StepAttnArgs {
   float scale_log2;    // scale * log2(e)
   int bf16;            // else f16
   int box_rows, boxes; // rows of one cache box (a page, at most 128) and boxes of a 128-key tile
-  int stages;
   void* out;
   long out_stride;
   float* lse;
@@ -102,7 +101,6 @@ struct StepAttnArgs {
   float2* cta_ml;      // [n_cta][256]
   int n_cta;
 };
-int step_attention_stages(int d);
 cudaError_t launch_step_attention(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMap& k,
                                   const CUtensorMap& v, cudaStream_t s);
 

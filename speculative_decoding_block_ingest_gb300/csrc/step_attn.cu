@@ -46,7 +46,14 @@ constexpr int kSoftRegs = 208, kOtherRegs = 88;
 constexpr int kSoftThreads = 256;        // warps 0..7
 constexpr int kAtomBytes = kKeys * 128;  // 128 rows x 128 bytes
 constexpr int kMaxStages = 11;
-constexpr size_t kSmemLimit = 227 * 1024;
+constexpr int kSharedBytes = 3072;       // control block
+constexpr size_t step_smem(int d, int stages) { return (size_t)(2 + stages) * (d / 64) * kAtomBytes + kSharedBytes; }
+// as many K and V tiles as shared memory holds beside two query tiles: 5 at d = 128, 11 at 64
+constexpr int step_stages(int d) {
+  int n = kMaxStages;
+  while (step_smem(d, n) > 227 * 1024) --n;
+  return n;
+}
 constexpr float kGrow = 8.f;             // O is rescaled when a row's max grows by more than 2^8
 constexpr int kFrags = 2;                // fragments described ahead
 constexpr int kBarPair = 3;              // named barrier of the 256 softmax threads
@@ -72,6 +79,22 @@ __device__ __forceinline__ void tmem_ld_wait32(float* v) {
                  "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
                  "+f"(v[30]), "+f"(v[31])
                :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 32 aligned bytes at once: rows of a tile lie far apart, so a lane's store
+// fills whole sectors by itself.
+__device__ __forceinline__ void store_sector(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -122,7 +145,7 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, uint64_t
 
 struct Shared {
   uint64_t kvfull[kMaxStages], kvempty[kMaxStages];
-  uint64_t qfull[2], qempty[2], sfull[2], pfull[2], pvdone[2];
+  uint64_t qfull[2], qempty[2], sfull[2], pfull[2][2], pvdone[2];
   uint64_t drained;
   uint32_t tmem;
   int abort;
@@ -139,8 +162,40 @@ struct Shared {
   int bad[128];
   int any_bad;
 };
-constexpr int kSharedBytes = 3072;
 static_assert(sizeof(Shared) <= kSharedBytes, "control block of the attention kernel");
+
+// One lane of a converged warp, the same in every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
+// Wait for the phase of `parity` of a pipeline barrier; false once `abort` is
+// raised or kWaitNs have passed (the clock is read once in 64 tries).
+__device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 0) {
+      if (*abort) return false;
+      const uint64_t t = globaltimer();
+      if (t0 == 0) t0 = t;
+      else if (t - t0 > kWaitNs) return false;
+    }
+  }
+}
+
+// Place of a K (kv = 0) or V (1) tile of a fragment's block among its 2 n
+// tiles.  A single item's two streams each hold a V tile while its softmax
+// runs, so the K tiles of both blocks go first: the next pair's keys land
+// meanwhile.
+__device__ __forceinline__ uint32_t tile_of(bool pair, int block, int n, int kv) {
+  if (pair) return 2 * block + kv;
+  const int first = block & ~1;
+  return 2 * first + (block & 1) + kv * min(2, n - first);
+}
 
 // Waits on the fragment ring outlast any one fragment; a failed wait
 // elsewhere ends the others within kWaitNs, so this limit is not met.
@@ -158,6 +213,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ StepAttnArgs a) {
   constexpr int kDAtoms = D / 64;
   constexpr int kTile = kDAtoms * kAtomBytes;          // a Q, K or V tile
+  constexpr int kStages = step_stages(D);              // K and V tiles in flight
   constexpr uint32_t kFmt = BF16 ? (1u << 7) | (1u << 10) : 0u;
   constexpr uint32_t kIdescS = (1u << 4) | kFmt | ((128u >> 3) << 17) | ((128u >> 4) << 24);
   constexpr uint32_t kIdescO = (1u << 4) | kFmt | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
@@ -165,12 +221,12 @@ __global__ void __launch_bounds__(kStepThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + 2 * kTile;
-  Shared& sh = *reinterpret_cast<Shared*>(sKV + a.stages * kTile);
+  Shared& sh = *reinterpret_cast<Shared*>(sKV + kStages * kTile);
   volatile int* abort = &sh.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < a.stages; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh.kvfull[i], 1);
       mbar_init(&sh.kvempty[i], 1);
     }
@@ -178,7 +234,8 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       mbar_init(&sh.qfull[i], 1);
       mbar_init(&sh.qempty[i], 1);
       mbar_init(&sh.sfull[i], 1);
-      mbar_init(&sh.pfull[i], 128);
+      mbar_init(&sh.pfull[i][0], 128);
+      mbar_init(&sh.pfull[i][1], 128);
       mbar_init(&sh.pvdone[i], 1);
     }
     mbar_init(&sh.drained, 1);
@@ -239,13 +296,13 @@ __global__ void __launch_bounds__(kStepThreads, 1)
   // Every role takes every fragment, also after a failed wait (it then skips
   // the work), so the ring and the named barriers never starve.
   uint32_t nf = 0;
-  auto take = [&](Frag& f, bool alone = false) -> bool {   // alone: one lane takes for its warp
+  auto take = [&](Frag& f) -> bool {
     const int i = nf % kFrags;
     ring_wait(&sh.ffull[i], (nf / kFrags) & 1);
     f = sh.frag[i];
     ++nf;
-    if (!alone) __syncwarp();
-    if (alone || lane == 0) mbar_arrive(&sh.fempty[i]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.fempty[i]);
     return f.seg >= 0;
   };
 
@@ -264,7 +321,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
         const int tiles = f.ntok > a.tpt ? 2 : 1;
         for (int i = 0; i < tiles && ok; ++i, ++nq) {
           const int slot = nq & 1;
-          ok = __all_sync(0xffffffffu, mbar_wait(&sh.qempty[slot], ((nq >> 1) & 1) ^ 1, abort));
+          ok = __all_sync(0xffffffffu, pipe_wait(&sh.qempty[slot], ((nq >> 1) & 1) ^ 1, abort));
           if (!ok) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(&sh.qfull[slot], q_bytes);
@@ -282,24 +339,26 @@ __global__ void __launch_bounds__(kStepThreads, 1)
         };
         const int first_box = f.b0 * a.boxes;
         int cur = page_of(first_box + lane), nxt = page_of(first_box + 32 + lane), win = first_box;
-        for (int b = f.b0; b < f.b1 && ok; ++b) {
-          const int box0 = b * a.boxes, n = min(a.boxes, n_box - box0);
-          if (box0 >= win + 32) {                      // boxes of a block never straddle a window
+        const int step = tiles == 2 ? 1 : 2;           // blocks whose K tiles go before their V tiles
+        for (int b = f.b0; b < f.b1 && ok; b += step) {
+          if (b * a.boxes >= win + 32) {               // boxes of a step never straddle a window
             cur = nxt;
             win += 32;
             nxt = page_of(win + 32 + lane);
           }
-          for (int kv = 0; kv < 2 && ok; ++kv, ++nkv) {
-            const int st = (int)(nkv % a.stages);
-            ok = __all_sync(0xffffffffu, mbar_wait(&sh.kvempty[st], ((nkv / a.stages) & 1) ^ 1, abort));
+          const int blocks = min(step, f.b1 - b);
+          for (int i = 0; i < 2 * blocks && ok; ++i, ++nkv) {
+            const int kv = i >= blocks, box0 = (b + i - kv * blocks) * a.boxes, n = min(a.boxes, n_box - box0);
+            const int st = (int)(nkv % kStages);
+            ok = __all_sync(0xffffffffu, pipe_wait(&sh.kvempty[st], ((nkv / kStages) & 1) ^ 1, abort));
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&sh.kvfull[st], (uint32_t)n * kDAtoms * box_bytes);
             __syncwarp();
             const int bi = lane / kDAtoms, at = lane % kDAtoms;
             const int page = __shfl_sync(0xffffffffu, cur, min(box0 - win + bi, 31));
             if (bi < n)
-              tma_load_4d(sKV + st * kTile + at * kAtomBytes + bi * box_bytes, kv ? &tmV : &tmK, &sh.kvfull[st], at * 64,
-                          f.h, (int)(((long)(box0 + bi) << box_shift) & (a.s.page_size - 1)), page);
+              tma_load_4d(sKV + st * kTile + at * kAtomBytes + bi * box_bytes, kv ? &tmV : &tmK, &sh.kvfull[st],
+                          at * 64, f.h, (int)(((long)(box0 + bi) << box_shift) & (a.s.page_size - 1)), page);
             __syncwarp();
           }
         }
@@ -307,84 +366,96 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       if (!ok) {   // leave no copy in flight behind
         sh.abort = 1;
         int none = 0;
-        for (uint32_t i = nkv > (uint32_t)a.stages ? nkv - a.stages : 0; i < nkv; ++i)
-          mbar_wait(&sh.kvfull[i % a.stages], (i / a.stages) & 1, &none);
-        for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) mbar_wait(&sh.qfull[i & 1], (i >> 1) & 1, &none);
+        for (uint32_t i = nkv > (uint32_t)kStages ? nkv - kStages : 0; i < nkv; ++i)
+          pipe_wait(&sh.kvfull[i % kStages], (i / kStages) & 1, &none);
+        for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) pipe_wait(&sh.qfull[i & 1], (i >> 1) & 1, &none);
       }
     } else if (warp == 9) {
       // ------------------------------------------------------------------ MMA
-      if (lane == 0) {
-        bool ok = true;
-        uint32_t nq = 0, nb = 0;                       // query tiles and key blocks before this fragment
-        uint32_t np[2] = {0, 0};                       // P tiles used by each stream
-        const uint32_t q_addr = smem_u32(sQ), kv_addr = smem_u32(sKV);
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          if (ok && !mbar_wait(bar, parity, abort)) ok = false;
-          tc_fence_after();
-          return ok;
-        };
-        auto stage = [&](uint32_t tile) { return (int)(tile % a.stages); };
-        auto landed = [&](uint32_t tile) { return wait(&sh.kvfull[stage(tile)], (tile / a.stages) & 1); };
-        Frag f;
-        while (take(f, true)) {
-          const int n = f.b1 - f.b0;
-          if (!ok || n <= 0) continue;
-          const bool pair = f.ntok > a.tpt;
-          const int cnt[2] = {pair ? n : (n + 1) / 2, pair ? n : n / 2};
-          // the K tile of a stream's j-th block (its V tile follows)
-          auto k_tile = [&](int s, int j) { return 2 * (nb + (uint32_t)(pair ? j : 2 * j + s)); };
-          const int slot0 = nq & 1;
-          if (!wait(&sh.qfull[slot0], (nq >> 1) & 1)) continue;
-          if (pair && !wait(&sh.qfull[slot0 ^ 1], ((nq + 1) >> 1) & 1)) continue;
-          auto issue_s = [&](int s, int j) {
-            const uint32_t t = k_tile(s, j);
-            if (!landed(t)) return;
-            const uint32_t qa = q_addr + (uint32_t)((pair ? slot0 ^ s : slot0) * kTile);
-            const uint32_t ka = kv_addr + (uint32_t)(stage(t) * kTile);
-  #pragma unroll
+      // The warp runs converged and elects a lane only around the tensor
+      // instructions: their descriptors then stay in uniform registers (issued
+      // from one lane's branch, each cost about 110 cycles).
+      bool ok = true;
+      uint32_t nq = 0, nb = 0;                         // query tiles and key blocks before this fragment
+      uint32_t np[2] = {0, 0};                         // P tiles used by each stream
+      const uint64_t q_desc = desc_sw128(smem_u32(sQ)), k_desc = desc_sw128(smem_u32(sKV));
+      const uint64_t v_desc = desc_sw128_mn(smem_u32(sKV));
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !__all_sync(0xffffffffu, pipe_wait(bar, parity, abort))) ok = false;
+        tc_fence_after();
+        return ok;
+      };
+      auto landed = [&](uint32_t tile) { return wait(&sh.kvfull[tile % kStages], (tile / kStages) & 1); };
+      Frag f;
+      while (take(f)) {
+        const int n = f.b1 - f.b0;
+        if (!ok || n <= 0) continue;
+        const bool pair = f.ntok > a.tpt;
+        const int cnt[2] = {pair ? n : (n + 1) / 2, pair ? n : n / 2};
+        auto tile = [&](int s, int j, int kv) { return 2 * nb + tile_of(pair, pair ? j : 2 * j + s, n, kv); };
+        const int slot0 = nq & 1;
+        if (!wait(&sh.qfull[slot0], (nq >> 1) & 1)) continue;
+        if (pair && !wait(&sh.qfull[slot0 ^ 1], ((nq + 1) >> 1) & 1)) continue;
+        auto issue_s = [&](int s, int j) {
+          const uint32_t t = tile(s, j, 0);
+          if (!landed(t)) return;
+          const int st = t % kStages, slot = pair ? slot0 ^ s : slot0;
+          const uint64_t qd = q_desc + (uint64_t)(slot * (kTile >> 4)), kd = k_desc + (uint64_t)(st * (kTile >> 4));
+          // the last product on a query tile frees its slot
+          const bool last = j + 1 == cnt[s] && (pair || s == ((n - 1) & 1));
+          if (elect_one()) {
+#pragma unroll
             for (int kk = 0; kk < 4 * kDAtoms; ++kk) {
-              const uint32_t at = (uint32_t)(kk >> 2) * kAtomBytes;
-              const uint64_t adv = (uint64_t)((kk & 3) * 2);
-              mma_bf16(tmem + 128u * s, desc_sw128(qa + at) + adv, desc_sw128(ka + at) + adv, kIdescS, kk > 0);
+              const uint64_t at = (uint64_t)((kk >> 2) * (kAtomBytes >> 4) + (kk & 3) * 2);
+              mma_bf16(tmem + 128u * s, qd + at, kd + at, kIdescS, kk > 0);
             }
             mma_commit(&sh.sfull[s]);
-            if (!pair || s == 1) mma_commit(&sh.kvempty[stage(t)]);
-            // the last product on a query tile frees its slot
-            if (j + 1 == cnt[s]) {
-              if (pair) mma_commit(&sh.qempty[slot0 ^ s]);
-              else if (n == 1 || s == ((n - 1) & 1)) mma_commit(&sh.qempty[slot0]);
+            if (!pair || s == 1) mma_commit(&sh.kvempty[st]);
+            if (last) mma_commit(&sh.qempty[slot]);
+          }
+          __syncwarp();
+        };
+        auto issue_pv = [&](int s, int j) {
+          const uint32_t t = tile(s, j, 1), parity = np[s]++ & 1;
+          if (!landed(t)) return;
+          const int st = t % kStages;
+          const uint64_t vd = v_desc + (uint64_t)(st * (kTile >> 4));
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {   // P arrives in two halves of 64 keys
+            if (!wait(&sh.pfull[s][half], parity)) return;
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                mma_f16_ts(tmem + kColO + 128u * s, tmem + 128u * s + (uint32_t)(kk * 8),
+                           vd + (uint64_t)(kk * (2048 >> 4)), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+              if (half == 1) {
+                mma_commit(&sh.pvdone[s]);
+                if (!pair || s == 1) mma_commit(&sh.kvempty[st]);
+              }
             }
-          };
-          auto issue_pv = [&](int s, int j) {
-            const uint32_t t = k_tile(s, j) + 1;
-            if (!wait(&sh.pfull[s], np[s] & 1) || !landed(t)) return;
-            ++np[s];
-            const uint32_t va = kv_addr + (uint32_t)(stage(t) * kTile);
-  #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              mma_f16_ts(tmem + kColO + 128u * s, tmem + 128u * s + (uint32_t)(kk * 8),
-                         desc_sw128_mn(va) + (uint64_t)(kk * (2048 >> 4)), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(&sh.pvdone[s]);
-            if (!pair || s == 1) mma_commit(&sh.kvempty[stage(t)]);
-          };
-          for (int s = 0; s < 2 && ok; ++s)
-            if (cnt[s]) issue_s(s, 0);
-          for (int j = 0; j < cnt[0] && ok; ++j)
-            for (int s = 0; s < 2 && ok; ++s) {
-              if (j >= cnt[s]) continue;
-              issue_pv(s, j);
-              if (ok && j + 1 < cnt[s]) issue_s(s, j + 1);
-            }
-          nq += pair ? 2 : 1;
-          nb += (uint32_t)n;
+            __syncwarp();
+          }
+        };
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          if (ok && cnt[s]) issue_s(s, 0);
+        for (int j = 0; j < cnt[0] && ok; ++j) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (!ok || j >= cnt[s]) continue;
+            issue_pv(s, j);
+            if (ok && j + 1 < cnt[s]) issue_s(s, j + 1);
+          }
         }
-        if (!ok) sh.abort = 1;
-        // every product is done before tensor memory is freed
-        int none = 0;
-        mma_commit(&sh.drained);
-        mbar_wait(&sh.drained, 0, &none);
+        nq += pair ? 2 : 1;
+        nb += (uint32_t)n;
       }
+      if (!ok) sh.abort = 1;
+      // every product is done before tensor memory is freed
+      if (elect_one()) mma_commit(&sh.drained);
       __syncwarp();
+      int none = 0;
+      pipe_wait(&sh.drained, 0, &none);
     } else if (warp == 10) {
       // ------------------------------------------------------------------ fragments
       if (lane == 0) {
@@ -427,19 +498,57 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       for (int j = 0; j < cnt; ++j, ++np) {
         const int bi = pair ? j : 2 * j + st;        // block of the fragment
         const int key0 = (f.b0 + bi) * kKeys;
-        if (ok && !__all_sync(0xffffffffu, mbar_wait(&sh.sfull[st], np & 1, abort))) ok = false;
+        if (ok && !__all_sync(0xffffffffu, pipe_wait(&sh.sfull[st], np & 1, abort))) ok = false;
         tc_fence_after();
+        // V rows behind the last key hold anything: zero them.  Own keys that
+        // some row of the step must not see may hold anything too: their
+        // elements that are not finite are taken out and remembered.
+        const int own0 = causal && f.lim0 < f.keys ? max(f.lim0, 0) : INT_MAX;   // first key not seen by all rows
+        if (ok && (st == 0 || !pair) && (key0 + kKeys > f.keys || key0 + kKeys > own0)) {
+          const uint32_t tile = 2 * nb + tile_of(pair, bi, n, 1);
+          if (!__all_sync(0xffffffffu, pipe_wait(&sh.kvfull[tile % kStages], (tile / kStages) & 1, abort))) ok = false;
+          uint8_t* v = sKV + (tile % kStages) * kTile + r * 128;
+          const int key = key0 + r;
+          if (key >= f.keys) {
+#pragma unroll
+            for (int c = 0; c < 8 * kDAtoms; ++c)
+              *reinterpret_cast<uint4*>(v + (c >> 3) * kAtomBytes + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          } else if (key >= own0) {
+            // an exponent of ones carries into the sign's place
+            constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
+            auto odd = [&](uint32_t x) { return ((x & kExp) + kOne) & 0x80008000u; };
+#pragma unroll 4
+            for (int c = 0; c < 8 * kDAtoms; ++c) {
+              uint4* e = reinterpret_cast<uint4*>(v + (c >> 3) * kAtomBytes + (((c & 7) ^ (r & 7)) * 16));
+              const uint4 x = *e;
+              if (odd(x.x) | odd(x.y) | odd(x.z) | odd(x.w)) {
+                uint32_t y[4] = {x.x, x.y, x.z, x.w};
+                for (int i = 0; i < 8; ++i)
+                  if (odd(y[i >> 1]) & (i & 1 ? 0x80000000u : 0x8000u)) atomicMin(&sh.bad[c * 8 + i], key);
+                sh.any_bad = 1;
+                for (int i = 0; i < 4; ++i)
+                  y[i] &= (odd(y[i]) & 0x80000000u ? 0u : 0xFFFF0000u) | (odd(y[i]) & 0x8000u ? 0u : 0xFFFFu);
+                *e = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+            }
+          }
+          fence_proxy_async_smem();
+        }
         if (ok && any_live) {
           float x[kKeys];
+          const int seen = lim - key0;
+          const bool whole = __all_sync(0xffffffffu, seen >= kKeys);
+          auto scores = [&]() {
 #pragma unroll
-          for (int i = 0; i < kKeys; i += 32) tmem_ld32_async(s_addr + i, x + i);
+            for (int i = 0; i < kKeys; i += 32) tmem_ld32_async(s_addr + i, x + i);
 #pragma unroll
-          for (int i = 0; i < kKeys; i += 32) tmem_ld_wait32(x + i);
-          if (!__all_sync(0xffffffffu, lim - key0 >= kKeys)) {
-            const int seen = lim - key0;
+            for (int i = 0; i < kKeys; i += 32) tmem_ld_wait32(x + i);
+            if (!whole) {
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i) x[i] = i < seen ? x[i] : -INFINITY;
-          }
+              for (int i = 0; i < kKeys; ++i) x[i] = i < seen ? x[i] : -INFINITY;
+            }
+          };
+          scores();
           float mx[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) mx[i] = fmaxf(x[i], x[i + 4]);
@@ -453,7 +562,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
           const bool grow = mj > m + kGrow;
           if (j > 0 && __any_sync(0xffffffffu, grow)) {
             // O holds the products through this stream's block j - 1
-            if (!__all_sync(0xffffffffu, mbar_wait(&sh.pvdone[st], (np - 1) & 1, abort))) ok = false;
+            if (!__all_sync(0xffffffffu, pipe_wait(&sh.pvdone[st], (np - 1) & 1, abort))) ok = false;
             tc_fence_after();
             const float f0 = grow ? ex2_fast(m - mj) : 1.f;
             for (int c = 0; c < D; c += 32) {
@@ -466,61 +575,41 @@ __global__ void __launch_bounds__(kStepThreads, 1)
               tmem_st32(oa, o);
             }
             l *= f0;
+            scores();   // read again rather than kept beside O
           }
           if (grow) m = mj;
-          const float2 neg = make_float2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m);
-          const float2 sc = make_float2(a.scale_log2, a.scale_log2);
+          const float nm = m == -INFINITY ? 0.f : -m;
+          const float2 neg = make_float2(nm, nm), sc = make_float2(a.scale_log2, a.scale_log2);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int i = 0; i < kKeys; i += 64) {
-            float pw[32];
+          for (int i = 0; i < kKeys; i += 32) {
+            float pw[16];
 #pragma unroll
-            for (int v = 0; v < 32; ++v) {
+            for (int v = 0; v < 16; ++v) {
               float2 p = fma2(make_float2(x[i + 2 * v], x[i + 2 * v + 1]), sc, neg);
               p.x = ex2_fast(p.x);
               p.y = ex2_fast(p.y);
               sum[v & 1] = add2(sum[v & 1], p);
               pw[v] = pack2<BF16>(p);
             }
-            tmem_st32(s_addr + i / 2, pw);
+            tmem_st16(s_addr + i / 2, pw);
+            if (i % 64 == 32) {
+              tmem_st_wait();
+              tc_fence_before();
+              mbar_arrive(&sh.pfull[st][i / 64]);
+            }
           }
           const float2 tot = add2(sum[0], sum[1]);
           l += tot.x + tot.y;
+        } else {
+          tc_fence_before();
+          mbar_arrive(&sh.pfull[st][0]);
+          mbar_arrive(&sh.pfull[st][1]);
         }
-        // V rows behind the last key hold anything: zero them.  Own keys that
-        // some row of the step must not see may hold anything too: their
-        // elements that are not finite are taken out and remembered.
-        const int own0 = causal && f.lim0 < f.keys ? max(f.lim0, 0) : INT_MAX;   // first key not seen by all rows
-        if (ok && (st == 0 || !pair) && (key0 + kKeys > f.keys || key0 + kKeys > own0)) {
-          const uint32_t tile = 2 * (nb + (uint32_t)bi) + 1;
-          if (!__all_sync(0xffffffffu, mbar_wait(&sh.kvfull[tile % a.stages], (tile / a.stages) & 1, abort))) ok = false;
-          uint8_t* v = sKV + (tile % a.stages) * kTile + r * 128;
-          const int key = key0 + r;
-          if (key >= f.keys) {
-#pragma unroll
-            for (int c = 0; c < 8 * kDAtoms; ++c)
-              *reinterpret_cast<uint4*>(v + (c >> 3) * kAtomBytes + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-          } else if (key >= own0) {
-            for (int c = 0; c < 8 * kDAtoms; ++c) {
-              uint16_t* e = reinterpret_cast<uint16_t*>(v + (c >> 3) * kAtomBytes + (((c & 7) ^ (r & 7)) * 16));
-              for (int i = 0; i < 8; ++i) {
-                constexpr uint16_t kExp = BF16 ? 0x7F80 : 0x7C00;
-                if ((e[i] & kExp) == kExp) {
-                  e[i] = 0;
-                  atomicMin(&sh.bad[c * 8 + i], key);
-                  sh.any_bad = 1;
-                }
-              }
-            }
-          }
-          fence_proxy_async_smem();
-        }
-        tc_fence_before();
-        mbar_arrive(&sh.pfull[st]);
       }
       nb += (uint32_t)n;
       // ---- the fragment's result
-      if (ok && cnt > 0 && !__all_sync(0xffffffffu, mbar_wait(&sh.pvdone[st], (np - 1) & 1, abort))) ok = false;
+      if (ok && cnt > 0 && !__all_sync(0xffffffffu, pipe_wait(&sh.pvdone[st], (np - 1) & 1, abort))) ok = false;
       tc_fence_after();
       const long row = f.tok0 + t;                   // row of the step
       float* po;
@@ -579,9 +668,8 @@ __global__ void __launch_bounds__(kStepThreads, 1)
               if (sh.bad[c + i] < lim) o[i] = __int_as_float(0x7fc00000);
           }
           if (live) {
-            float4* dst = reinterpret_cast<float4*>(po + c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 32; i += 8) store_sector(po + c + i, o + i);
           }
         }
       }
@@ -693,13 +781,11 @@ __global__ void __launch_bounds__(kMergeThreads) step_merge_kernel(const __grid_
     a.lse[row * a.Hq + head] = bad ? inv : (l == 0.f ? -INFINITY : 0.69314718055994531f * (m + log2f(l)));
 }
 
-size_t step_attention_smem(int d, int stages) { return (size_t)(2 + stages) * (d / 64) * kAtomBytes + kSharedBytes; }
-
 template <int D, bool BF16>
 cudaError_t launch(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                    cudaStream_t s) {
   auto* attn = step_attn_kernel<D, BF16>;
-  const size_t smem = step_attention_smem(D, a.stages);
+  const size_t smem = step_smem(D, step_stages(D));
   cudaError_t e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(attn, dim3(a.n_cta), dim3(kStepThreads), smem, s, q, k, v, a);
@@ -711,13 +797,6 @@ cudaError_t launch(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMa
 }
 
 }  // namespace
-
-// K and V tiles in flight: as many as shared memory holds (5 at d = 128, 11 at 64)
-int step_attention_stages(int d) {
-  int n = kMaxStages;
-  while (step_attention_smem(d, n) > kSmemLimit) --n;
-  return n;
-}
 
 cudaError_t launch_step_attention(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMap& k,
                                   const CUtensorMap& v, cudaStream_t s) {

@@ -230,7 +230,6 @@ int dflash_step_attention(const dflash_paged_cache* cache, const dflash_step* st
   a.bf16 = cache->dtype == DFLASH_BF16;
   a.box_rows = cache->page_size < kKeys ? cache->page_size : kKeys;
   a.boxes = kKeys / a.box_rows;
-  a.stages = step_attention_stages(d);
   a.out = p->out;
   a.out_stride = p->out_stride;
   a.lse = p->lse;
