@@ -502,8 +502,11 @@ int dflash_step_attention(const dflash_paged_cache *cache, const dflash_step *st
  * device).  cache and step as above, but row_start and kv_len are host arrays
  * and nothing else of them is followed.  Query rows go in items of up to
  * 2 floor(128 / G) tokens of one kv head (G query heads each), keys in blocks
- * of 128; an item counts one unit and one per block, the prefix's items
- * first, then each sequence's, and n_cta CTAs take equal runs of units. */
+ * of 128.  The prefix's items come first, then each sequence's (by head, then
+ * rows).  An item costs 3 + rows G / 32 units for its ends and 4 (more than
+ * floor(128 / G) tokens) or 3 for each block; CTA c of C = min(n_cta,
+ * ceil(total / 3)) takes the units [c total / C, (c + 1) total / C) and with
+ * them the blocks that start there. */
 typedef struct dflash_step_piece {
   int32_t cta;
   int32_t segment;             /* 0: shared prefix, 1: own keys            */

@@ -7,6 +7,13 @@ namespace dfl {
 
 constexpr int kKeys = 128;   // keys of a block
 
+// What a CTA's work costs, in units of about 900 cycles: a block of keys for
+// two tiles (bound by shared-memory and L2 reads, 3500 cycles measured) or
+// for one (by HBM, 2650), and an item's start and end, which writes up to 128
+// KB of partial rows (2500 cycles for 8 rows, 10600 for 256).
+constexpr int kPairUnits = 4, kSingleUnits = 3;
+__host__ __device__ inline int end_units(int rows) { return 3 + rows / 32; }
+
 // One piece of an item that a CTA runs: key blocks [b0, b1) of the segment.
 struct Frag {
   int seg;             // 0 prefix, 1 own keys, -1: no further piece
@@ -15,11 +22,13 @@ struct Frag {
   int keys;            // keys of the segment that may be read
   int lim0;            // own, causal: keys that token tok0 sees (may be <= 0)
   int b0, b1;
-  int first;           // holds the item's own unit
+  int first;           // holds the item's first unit
   int last_cta;        // and then: the CTA of the item's last unit
 };
 
-// Units of one sequence's tile pair j, and the walk over a CTA's fragments.
+// The items in order: the prefix's by kv head and tile pair, then every
+// sequence's.  An item takes end_units, then its blocks' units one block after
+// the other; a CTA runs the blocks that start in its share.
 struct Walk {
   const StepAttnArgs& a;
   int pair_tok;        // tokens of two tiles
@@ -36,18 +45,29 @@ struct Walk {
     pre_blocks = (a.s.prefix_len + kKeys - 1) / kKeys;
     pre_tiles = pre_blocks ? (rows + pair_tok - 1) / pair_tok : 0;
   }
-  __host__ __device__ long prefix_units() const { return (long)a.Hkv * pre_tiles * (pre_blocks + 1); }
   __host__ __device__ int tokens(int i) const { return max(a.s.start(i + 1) - a.s.start(i), 0); }
+  __host__ __device__ int weight(int ntok) const { return ntok > a.tpt ? kPairUnits : kSingleUnits; }
+  __host__ __device__ long units(int ntok, int blocks) const {
+    return end_units(ntok * a.G) + (long)blocks * weight(ntok);
+  }
+  // tokens of tile pair j out of T
+  __host__ __device__ int pair_tokens(int j, int T) const { return min(pair_tok, T - j * pair_tok); }
   // key blocks that tile pair j of sequence i needs
   __host__ __device__ int blocks(int i, int j, int T) const {
     const int len = a.s.len(i);
     const int seen = a.causal ? len - T + min((j + 1) * pair_tok, T) : len;
     return (min(max(seen, 0), a.s.room()) + kKeys - 1) / kKeys;
   }
-  __host__ __device__ long head_units(int i) const {   // units of one kv head of sequence i
+  // units of one kv head: of the prefix, and of sequence i
+  __host__ __device__ long prefix_head() const {
+    if (!pre_tiles) return 0;
+    return (pre_tiles - 1) * units(pair_tok, pre_blocks) + units(pair_tokens(pre_tiles - 1, rows), pre_blocks);
+  }
+  __host__ __device__ long prefix_units() const { return a.Hkv * prefix_head(); }
+  __host__ __device__ long head_units(int i) const {
     const int T = tokens(i);
     long u = 0;
-    for (int j = 0; j * pair_tok < T; ++j) u += 1 + blocks(i, j, T);
+    for (int j = 0; j * pair_tok < T; ++j) u += units(pair_tokens(j, T), blocks(i, j, T));
     return u;
   }
   // Go to the item that holds unit ua; `seq0` is its sequence (-1: the
@@ -55,25 +75,28 @@ struct Walk {
   __host__ __device__ void begin(int seq0, long base) {
     seg = seq0 < 0 ? 0 : 1;
     seq = seq0;
-    const long per_head = seg ? head_units(seq) : (long)pre_tiles * (pre_blocks + 1);
+    const long per_head = seg ? head_units(seq) : prefix_head();
     h = per_head ? (int)((ua - base) / per_head) : 0;
     pos = base + h * per_head;
     tile = 0;
-    if (!seg) {
-      tile = (int)((ua - pos) / (pre_blocks + 1));
-      pos += (long)tile * (pre_blocks + 1);
+    if (!seg) {   // every pair but the last is full
+      const long full = units(pair_tok, pre_blocks);
+      tile = (int)min((ua - pos) / full, (long)pre_tiles - 1);
+      pos += tile * full;
     } else {
       const int T = tokens(seq);
-      for (long n; tile * pair_tok < T && pos + (n = 1 + blocks(seq, tile, T)) <= ua; ++tile) pos += n;
+      for (; tile * pair_tok < T; ++tile) {
+        const long n = units(pair_tokens(tile, T), blocks(seq, tile, T));
+        if (pos + n > ua) break;
+        pos += n;
+      }
     }
   }
   // The next fragment, or false behind the last.
   __host__ __device__ bool next(Frag& f) {
     while (pos < ub) {
-      int n, T = rows;
-      if (seg == 0) {
-        n = 1 + pre_blocks;
-      } else {
+      int n = pre_blocks, T = rows;
+      if (seg) {
         T = tokens(seq);
         if (tile * pair_tok >= T) {   // the next head, or sequence
           tile = 0;
@@ -83,20 +106,22 @@ struct Walk {
           }
           continue;
         }
-        n = 1 + blocks(seq, tile, T);
+        n = blocks(seq, tile, T);
       }
       f.seg = seg;
       f.seq = seq;
       f.h = h;
       f.tok0 = tile * pair_tok + (seg ? a.s.start(seq) : 0);
-      f.ntok = min(pair_tok, T - tile * pair_tok);
+      f.ntok = pair_tokens(tile, T);
       f.keys = seg ? min(a.s.len(seq), a.s.room()) : a.s.prefix_len;
       f.lim0 = seg && a.causal ? a.s.len(seq) - T + tile * pair_tok + 1 : f.keys;
-      f.b0 = (int)max(ua - pos - 1, 0L);
-      f.b1 = (int)min((long)n, ub - pos) - 1;
+      const int w = weight(f.ntok);
+      const long first_block = pos + end_units(f.ntok * a.G), end = first_block + (long)n * w;
+      f.b0 = (int)min(max(ua - first_block + w - 1, 0L) / w, (long)n);
+      f.b1 = (int)min(max(ub - first_block + w - 1, 0L) / w, (long)n);
       f.first = ua <= pos;
-      f.last_cta = (int)min(((pos + n) * n_cta + total - 1) / total - 1, n_cta - 1);
-      pos += n;
+      f.last_cta = (int)min((end * n_cta + total - 1) / total - 1, n_cta - 1);
+      pos = end;
       ++tile;
       if (seg == 0 && tile == pre_tiles) {
         tile = 0;
@@ -108,12 +133,12 @@ struct Walk {
   }
 };
 
-
-// CTA c's share [ua, ub) of `total` units over at most `n_cta` CTAs.  No CTA
-// in use is without a unit, so the CTAs of an item are consecutive.
+// CTA c's share [ua, ub) of `total` units.  At most n_cta CTAs, none with less
+// than a block of one tile, so every CTA in use has units and the CTAs of an
+// item are consecutive (one may find no block starting in its share of it).
 __host__ __device__ inline void share_units(Walk& w, long total, int n_cta, int c) {
   w.total = total;
-  w.n_cta = min((long)n_cta, total);
+  w.n_cta = min((long)n_cta, (total + kSingleUnits - 1) / kSingleUnits);
   w.ua = w.ub = 0;
   if (c < w.n_cta) {
     w.ua = c * total / w.n_cta;

@@ -46,7 +46,7 @@ def items(rows, kv, *, hq, hkv, prefix=0, page=64, causal=True, cols=None):
     """{(segment, seq, kv head, first row): (tokens, blocks)} from the definition."""
     pair = 2 * (128 // (hq // hkv))
     room = 10 ** 9 if cols is None else cols * page
-    want, total = {}, sum(rows)
+    want, total = {}, sum(rows)       # in the pieces' order
     if prefix:
         for h in range(hkv):
             for r in range(0, total, pair):
@@ -63,32 +63,41 @@ def items(rows, kv, *, hq, hkv, prefix=0, page=64, causal=True, cols=None):
 
 def check(rows, kv, n_cta=152, **kw):
     pieces = plan(rows, kv, n_cta=n_cta, **kw)
-    kw.pop("n_rows", None)
     want = items(rows, kv, **kw)
-    units = sum(1 + b for _, b in want.values())
-    got, ctas, load = {}, {}, {}
+    G = kw["hq"] // kw["hkv"]
+    start, pos, weight = {}, 0, {}
+    for key, (tokens, blocks) in want.items():           # prefix first, then by sequence, head and rows
+        start[key] = pos
+        weight[key] = 4 if tokens > 128 // G else 3
+        pos += 3 + tokens * G // 32 + weight[key] * blocks
+    C = min(n_cta, -(-pos // 3))
+    share = [(c * pos // C, (c + 1) * pos // C) for c in range(C)]
+    assert max(b - a for a, b in share) - min(b - a for a, b in share) <= 1
+    got, ctas = {}, {}
     for p in pieces:
         key = (p["segment"], p["seq"], p["kv_head"], p["row0"])
         tokens, blocks = want[key]
         assert p["n_tokens"] == tokens and 0 <= p["block0"] <= p["block1"] <= blocks
+        a, b = share[p["cta"]]
+        assert p["first"] == (a <= start[key] < b)
+        at = start[key] + 3 + tokens * G // 32            # the blocks that start in the CTA's share
+        starts = [i for i in range(p["block0"], p["block1"])]
+        assert all(a <= at + weight[key] * i < b for i in starts)
         got.setdefault(key, []).append((p["block0"], p["block1"], p["first"]))
         ctas.setdefault(key, []).append((p["cta"], p["first"], p["last_cta"]))
-        load[p["cta"]] = load.get(p["cta"], 0) + p["block1"] - p["block0"] + p["first"]
     assert set(got) == set(want)
     for key, parts in got.items():
         at = 0
         for i, (b0, b1, first) in enumerate(parts):      # pieces come in CTA order
-            assert first == (i == 0) and b0 == at
-            at = b1
+            assert first == (i == 0) and (b0 == at or b0 == b1)
+            at = max(at, b1)
         assert at == want[key][1]
         c = [x for x, _, _ in ctas[key]]
         assert c == list(range(c[0], c[0] + len(c)))     # one CTA after the other
         assert ctas[key][0][2] == c[-1] and all(x[2] == -1 for x in ctas[key][1:])
-    # equal shares, and at most one continued item (its first) in a CTA
-    n = min(n_cta, units)
-    assert sorted(load) == list(range(n))
-    assert max(load.values()) - min(load.values()) <= 1
-    for c in range(n):
+    # every CTA in use has a piece, and continues at most one item (its first)
+    assert sorted({p["cta"] for p in pieces}) == list(range(C))
+    for c in range(C):
         mine = [p for p in pieces if p["cta"] == c]
         assert all(p["first"] for p in mine[1:])
 
