@@ -54,10 +54,10 @@ struct AppendArgs {
   const int* positions;
   void* q_out;
   long q_out_stride;
-  double turns[64];   // inverse frequencies in turns (over 2 pi)
+  uint64_t turns[64];   // turns per position modulo 1, times 2^64
 };
 // in_dtype / out_dtype: dflash_dtype values of q, k, v and of the cache
-cudaError_t launch_step_append(const AppendArgs& a, int in_dtype, int out_dtype, cudaStream_t s);
+cudaError_t launch_step_append(const AppendArgs& a, int in_dtype, int out_dtype, int n_sm, cudaStream_t s);
 
 struct VerifyArgs {
   int n_seq, k, vocab;
@@ -74,12 +74,9 @@ struct VerifyArgs {
   int* tokens;
   int* n_accepted;
 };
-cudaError_t launch_verify(const VerifyArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_verify(const VerifyArgs& a, int dtype, int n_sm, cudaStream_t s);
 
-// Attention of a step.  Work is counted in units: every item (a shared-prefix
-// or own-key segment of one kv head and one tile of query rows) has one unit
-// of its own plus one per block of 128 keys, and CTA c of n_cta takes units
-// [c W / n_cta, (c + 1) W / n_cta) of the W in all.
+// Attention of a step (step_attn.cu; how it is cut into pieces: step_plan.cuh).
 constexpr int kStepStatusWords = 1024;   // most CTAs (one status word each)
 struct StepAttnArgs {
   StepView s;

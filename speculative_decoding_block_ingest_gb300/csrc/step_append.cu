@@ -9,12 +9,16 @@
 // flops an element: bytes bound it, for one token the launch and a chain of
 // dependent loads (row -> sequence -> length -> page).
 //
-// One CTA per row of the step.  A group of d / 16 threads takes one head row,
-// each thread the two 8-element chunks that RoPE pairs, so the rotation needs
-// no exchange and the norm three shuffles.  The row's angles are shared by
-// all of its heads: they are formed once per CTA while the first head rows'
-// loads are in flight.  An angle is reduced in f64 (p * turns, minus its
-// nearest integer): in f32 a position of 10^5 would leave 2^-7 of a radian.
+// A warp takes a whole row, or (few rows) an eighth of its heads: d / 16 lanes
+// hold a head row, each the two 8-element chunks that RoPE pairs, so the
+// rotation needs no exchange, the norm three shuffles and no warp waits for
+// another.  Sequence, cache row and angles are found while the first head
+// rows' loads are in flight; the 8 (cos, sin) pairs a lane needs are the same
+// for all heads and stay in registers.
+//
+// Angles are counted in turns modulo 1 as 64-bit integers: position times
+// frequency wraps around by itself, exactly, where f32 would leave 2^-7 of a
+// radian at position 10^5 and f64 runs at 1/64 of the f32 rate.
 #include "../../include/dflash.h"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -24,7 +28,7 @@ namespace dfl {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendDepth = 2;   // head rows a thread group has in flight
+constexpr int kFewWarps = 8;      // warps of a row when there are few rows
 
 struct Chunk {
   float v[8];
@@ -77,131 +81,146 @@ __device__ __forceinline__ void store8(__half* p, const Chunk& c) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename In, typename Out, int D>
+template <typename In, typename Out, int D, int WARPS>
 __global__ void __launch_bounds__(kAppendThreads) step_append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int kLanes = D / 16;                     // threads of a head row
-  constexpr int kGroups = kAppendThreads / kLanes;   // head rows of one sweep
-  __shared__ float2 cs[D / 2];
+  constexpr int kLanes = D / 16;               // lanes of a head row
+  constexpr int kGroups = 32 / kLanes;         // head rows of a warp at once
+  constexpr int kDepth = sizeof(In) == 4 ? 2 : 4;   // of those, in flight
+  constexpr int kStep = WARPS * kGroups;       // heads between a lane's
+  __shared__ float2 cs_all[kAppendThreads / 32][D / 2];
   pdl_wait();
   pdl_launch_dependents();
   const StepView& s = a.s;
-  const int row = blockIdx.x, tid = threadIdx.x;
-  const int lane = tid % kLanes, group = tid / kLanes;
+  const int lane = threadIdx.x & 31, l = lane % kLanes;
+  const int id = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  const int first = id % WARPS * kGroups + lane / kLanes;   // this lane's first head
   const int Hq = a.n_heads, Hkv = a.c.n_kv_heads, heads = Hq + 2 * Hkv;
-  // the two chunks of a head row this thread holds: a RoPE pair, or two of
-  // the chunks behind the rotated ones
+  float2* cs = cs_all[threadIdx.x >> 5];
+  // the two chunks of a head row this lane holds: a RoPE pair, or two of the
+  // chunks behind the rotated ones
   const int pairs = a.rot / 16;
-  const bool rot = lane < pairs;
-  const int c0 = rot ? lane : 2 * pairs + (lane - pairs);
-  const int c1 = rot ? lane + pairs : c0 + (kLanes - pairs);
-
-  // rows behind the last sequence stay as they are
-  int before = 0;
-  for (int i = tid; i < s.n_seq; i += kAppendThreads) before += s.start(i + 1) <= row;
-  int seq = __syncthreads_count(before > 0);
-  if (s.n_seq > kAppendThreads) {   // more than one sequence a thread: sum the counts
-    __shared__ int total;
-    if (tid == 0) total = 0;
-    __syncthreads();
-    if (before) atomicAdd(&total, before);
-    __syncthreads();
-    seq = total;
-  }
-  if (seq >= s.n_seq) return;
-
-  auto source = [&](int h) -> const In* {
-    if (h < Hq) return static_cast<const In*>(a.q) + row * a.q_stride + (long)h * D;
-    if (h < Hq + Hkv) return static_cast<const In*>(a.k) + row * a.k_stride + (long)(h - Hq) * D;
-    return static_cast<const In*>(a.v) + row * a.v_stride + (long)(h - Hq - Hkv) * D;
-  };
-  Chunk x0[kAppendDepth], x1[kAppendDepth];
-  auto fetch = [&](int h0) {
+  const bool rot = l < pairs;
+  const int c0 = 8 * (rot ? l : 2 * pairs + (l - pairs));
+  const int c1 = rot ? c0 + 8 * pairs : c0 + 8 * (kLanes - pairs);
+  // turns per position of the angles this lane forms
+  uint64_t turn[D / 64];
 #pragma unroll
-    for (int i = 0; i < kAppendDepth; ++i) {
-      const int h = h0 + i * kGroups + group;
-      if (h < heads) {
-        const In* p = source(h);
-        x0[i] = load8(p + 8 * c0);
-        x1[i] = load8(p + 8 * c1);
+  for (int i = 0; i < D / 64; ++i) turn[i] = a.turns[lane + 32 * i];
+
+  const int stride = gridDim.x * (kAppendThreads / 32) / WARPS;
+  for (int row = id / WARPS; row < s.n_rows; row += stride) {
+    Chunk x0[kDepth], x1[kDepth];
+    auto fetch = [&](int h0) {
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i) {
+        const int h = h0 + i * kStep;
+        if (h < heads) {
+          const In* p = h < Hq ? static_cast<const In*>(a.q) + row * a.q_stride + (long)h * D
+                        : h < Hq + Hkv ? static_cast<const In*>(a.k) + row * a.k_stride + (long)(h - Hq) * D
+                                       : static_cast<const In*>(a.v) + row * a.v_stride + (long)(h - Hq - Hkv) * D;
+          x0[i] = load8(p + c0);
+          x1[i] = load8(p + c1);
+        }
       }
+    };
+    fetch(first);
+    // the row's sequence: those that end at or before it lie below
+    int seq = 0;
+#pragma unroll 4
+    for (int i = lane; i < s.n_seq; i += 32) seq += s.start(i + 1) <= row;
+    seq = __reduce_add_sync(0xffffffffu, seq);
+    if (seq >= s.n_seq) break;   // rows behind the last sequence stay as they are
+    const int own = s.len(seq) - s.start(seq + 1) + row;   // this row's own key index
+    long dst = -1;                                         // its row in the cache
+    if (own >= 0 && (own >> s.page_shift) < s.table_cols) {
+      const int page = s.block_table[seq * s.table_stride + (own >> s.page_shift)];
+      if (page >= 0 && page < s.n_pages)
+        dst = page * a.c.page_stride + (long)(own & (s.page_size - 1)) * a.c.row_stride;
     }
-  };
-  fetch(0);
-
-  const int own = s.len(seq) - s.start(seq + 1) + row;   // this row's own key index
-  long dst = -1;                                          // its row in the cache
-  if (own >= 0 && (own >> s.page_shift) < s.table_cols) {
-    const int page = s.block_table[seq * s.table_stride + (own >> s.page_shift)];
-    if (page >= 0 && page < s.n_pages)
-      dst = page * a.c.page_stride + (long)(own & (s.page_size - 1)) * a.c.row_stride;
-  }
-  if (tid < a.rot / 2) {
-    const long pos = a.positions ? (long)a.positions[row] : (long)s.prefix_len + own;
-    const double t = (double)pos * a.turns[tid];
-    float sn, cn;
-    sincospif(2.f * (float)(t - rint(t)), &sn, &cn);
-    cs[tid] = make_float2(cn * a.mscale, sn * a.mscale);
-  }
-  __syncthreads();
-
-  for (int h0 = 0; h0 < heads; h0 += kAppendDepth * kGroups) {
-    if (h0) fetch(h0);
+    float2 w[8];
+    if (a.rot) {
+      const long pos = a.positions ? (long)a.positions[row] : (long)s.prefix_len + own;
 #pragma unroll
-    for (int i = 0; i < kAppendDepth; ++i) {
-      const int h = h0 + i * kGroups + group;
-      const bool is_q = h < Hq, is_v = h >= Hq + Hkv;
-      const float* gain = is_q ? a.q_gain : (is_v ? nullptr : a.k_gain);
-      Chunk y0 = x0[i], y1 = x1[i];
-      float ss = 0.f;
+      for (int i = 0; i < D / 64; ++i) {
+        // a signed fraction of a turn, times 2: sin and cos of pi x
+        const float x = __ll2float_rn((long long)((uint64_t)pos * turn[i])) * 0x1p-63f;
+        float sn, cn;
+        sincospif(x, &sn, &cn);
+        cs[lane + 32 * i] = make_float2(cn * a.mscale, sn * a.mscale);
+      }
+      __syncwarp();
+      if (rot) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss += y0.v[j] * y0.v[j] + y1.v[j] * y1.v[j];
-#pragma unroll
-      for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (h >= heads) continue;
-      if (gain) {
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
-        const Chunk g0 = load8(gain + 8 * c0), g1 = load8(gain + 8 * c1);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          y0.v[j] *= r * g0.v[j];
-          y1.v[j] *= r * g1.v[j];
+        for (int j = 0; j < 8; j += 2) {
+          const float4 v = *reinterpret_cast<const float4*>(&cs[8 * l + j]);
+          w[j] = make_float2(v.x, v.y);
+          w[j + 1] = make_float2(v.z, v.w);
         }
       }
-      if (rot && !is_v) {
+      __syncwarp();
+    }
+    for (int h0 = first; __any_sync(0xffffffffu, h0 < heads); h0 += kDepth * kStep) {
+      if (h0 != first) fetch(h0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 w = cs[8 * lane + j];
-          const float u = y0.v[j], t = y1.v[j];
-          y0.v[j] = u * w.x - t * w.y;
-          y1.v[j] = t * w.x + u * w.y;
+      for (int i = 0; i < kDepth; ++i) {
+        const int h = h0 + i * kStep;
+        const bool is_q = h < Hq, is_v = h >= Hq + Hkv;
+        const float* gain = is_q ? a.q_gain : (is_v ? nullptr : a.k_gain);
+        Chunk y0 = x0[i], y1 = x1[i];
+        if (a.q_gain || a.k_gain) {
+          float ss = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ss += y0.v[j] * y0.v[j] + y1.v[j] * y1.v[j];
+#pragma unroll
+          for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          if (h < heads && gain) {
+            const float r = rsqrtf(ss * (1.f / D) + a.eps);
+            const Chunk g0 = load8(gain + c0), g1 = load8(gain + c1);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              y0.v[j] *= r * g0.v[j];
+              y1.v[j] *= r * g1.v[j];
+            }
+          }
         }
+        if (h >= heads || (!is_q && dst < 0)) continue;
+        if (rot && !is_v) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float u = y0.v[j], t = y1.v[j];
+            y0.v[j] = u * w[j].x - t * w[j].y;
+            y1.v[j] = t * w[j].x + u * w[j].y;
+          }
+        }
+        Out* o = is_q   ? static_cast<Out*>(a.q_out) + row * a.q_out_stride + (long)h * D
+                 : is_v ? static_cast<Out*>(a.c.v) + dst + (h - Hq - Hkv) * a.c.head_stride
+                        : static_cast<Out*>(a.c.k) + dst + (h - Hq) * a.c.head_stride;
+        store8(o + c0, y0);
+        store8(o + c1, y1);
       }
-      Out* o;
-      if (is_q) {
-        o = static_cast<Out*>(a.q_out) + row * a.q_out_stride + (long)h * D;
-      } else {
-        if (dst < 0) continue;
-        o = is_v ? static_cast<Out*>(a.c.v) + dst + (h - Hq - Hkv) * a.c.head_stride
-                 : static_cast<Out*>(a.c.k) + dst + (h - Hq) * a.c.head_stride;
-      }
-      store8(o + 8 * c0, y0);
-      store8(o + 8 * c1, y1);
     }
   }
 }
 
 template <typename In, typename Out>
-cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
-  auto* kernel = a.c.d == 128 ? step_append_kernel<In, Out, 128> : step_append_kernel<In, Out, 64>;
-  return launch_pdl(kernel, dim3(a.s.n_rows), dim3(kAppendThreads), 0, s, a);
+cudaError_t launch(const AppendArgs& a, int n_sm, cudaStream_t s) {
+  // Eight warps a row while they are resident together (32 warps an SM);
+  // beyond, the repeated look-ups cost more than the shorter rows save.
+  const bool few = (long)a.s.n_rows * kFewWarps <= 32L * n_sm;
+  const long warps = (long)a.s.n_rows * (few ? kFewWarps : 1);
+  const long ctas = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+  const dim3 grid((unsigned)(ctas < 4L * n_sm ? ctas : 4L * n_sm)), block(kAppendThreads);
+  auto* kernel = few ? (a.c.d == 128 ? step_append_kernel<In, Out, 128, kFewWarps> : step_append_kernel<In, Out, 64, kFewWarps>)
+                     : (a.c.d == 128 ? step_append_kernel<In, Out, 128, 1> : step_append_kernel<In, Out, 64, 1>);
+  return launch_pdl(kernel, grid, block, 0, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_step_append(const AppendArgs& a, int in_dtype, int out_dtype, cudaStream_t s) {
+cudaError_t launch_step_append(const AppendArgs& a, int in_dtype, int out_dtype, int n_sm, cudaStream_t s) {
   if (out_dtype == DFLASH_BF16)
-    return in_dtype == DFLASH_F32 ? launch<float, __nv_bfloat16>(a, s) : launch<__nv_bfloat16, __nv_bfloat16>(a, s);
-  return in_dtype == DFLASH_F32 ? launch<float, __half>(a, s) : launch<__half, __half>(a, s);
+    return in_dtype == DFLASH_F32 ? launch<float, __nv_bfloat16>(a, n_sm, s) : launch<__nv_bfloat16, __nv_bfloat16>(a, n_sm, s);
+  return in_dtype == DFLASH_F32 ? launch<float, __half>(a, n_sm, s) : launch<__half, __half>(a, n_sm, s);
 }
 
 }  // namespace dfl

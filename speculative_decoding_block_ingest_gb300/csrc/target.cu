@@ -86,12 +86,18 @@ StepView view(const dflash_paged_cache* c, const dflash_step* s) {
   return v;
 }
 
-// One CTA per SM (each takes all of an SM's tensor memory).
-int step_ctas(int* n) {
+// SMs of the current device.
+int sm_count(int* n) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return launched(e, "device SM count");
+  return DFLASH_OK;
+}
+
+// CTAs of the attention: one per SM (each takes all of an SM's tensor memory).
+int step_ctas(int* n) {
+  if (int rc = sm_count(n)) return rc;
   if (*n > kStepStatusWords) *n = kStepStatusWords;
   return DFLASH_OK;
 }
@@ -185,8 +191,15 @@ int dflash_step_append(const dflash_paged_cache* cache, const dflash_step* step,
   a.positions = p->positions;
   a.q_out = p->q_out;
   a.q_out_stride = p->q_out_stride;
-  for (int i = 0; i < p->rot_dim / 2; ++i) a.turns[i] = p->inv_freq[i] / (2.0 * M_PI);
-  return launched(launch_step_append(a, p->dtype, cache->dtype, static_cast<cudaStream_t>(stream)), "step append");
+  for (int i = 0; i < p->rot_dim / 2; ++i) {
+    const double t = p->inv_freq[i] / (2.0 * M_PI);
+    if (!std::isfinite(t)) return invalid("RoPE frequencies");
+    a.turns[i] = (uint64_t)std::ldexp(t - std::floor(t), 64);
+  }
+  int n_sm = 0;
+  if (int rc = sm_count(&n_sm)) return rc;
+  return launched(launch_step_append(a, p->dtype, cache->dtype, n_sm, static_cast<cudaStream_t>(stream)),
+                  "step append");
 }
 
 int dflash_step_attention_workspace(const dflash_paged_cache* cache, int32_t n_rows, int32_t n_heads, size_t* bytes) {
@@ -342,7 +355,9 @@ int dflash_verify_tokens(const dflash_verify_args* p, void* stream) {
   a.u_token = p->u_token;
   a.tokens = p->tokens;
   a.n_accepted = p->n_accepted;
-  return launched(launch_verify(a, p->dtype, static_cast<cudaStream_t>(stream)), "verify tokens");
+  int n_sm = 0;
+  if (int rc = sm_count(&n_sm)) return rc;
+  return launched(launch_verify(a, p->dtype, n_sm, static_cast<cudaStream_t>(stream)), "verify tokens");
 }
 
 }  // extern "C"

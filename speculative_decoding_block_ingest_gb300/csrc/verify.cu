@@ -347,11 +347,7 @@ int cluster_size(int n_seq, int n_sm) {
 }
 
 template <typename T>
-cudaError_t launch(const VerifyArgs& a, cudaStream_t s) {
-  int dev = 0, n_sm = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
+cudaError_t launch(const VerifyArgs& a, int n_sm, cudaStream_t s) {
   const unsigned ctas = cluster_size(a.n_seq, n_sm);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(a.n_seq * ctas);
@@ -369,10 +365,10 @@ cudaError_t launch(const VerifyArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_verify(const VerifyArgs& a, int dtype, cudaStream_t s) {
-  if (dtype == DFLASH_F32) return launch<float>(a, s);
-  if (dtype == DFLASH_BF16) return launch<__nv_bfloat16>(a, s);
-  return launch<__half>(a, s);
+cudaError_t launch_verify(const VerifyArgs& a, int dtype, int n_sm, cudaStream_t s) {
+  if (dtype == DFLASH_F32) return launch<float>(a, n_sm, s);
+  if (dtype == DFLASH_BF16) return launch<__nv_bfloat16>(a, n_sm, s);
+  return launch<__half>(a, n_sm, s);
 }
 
 }  // namespace dfl
