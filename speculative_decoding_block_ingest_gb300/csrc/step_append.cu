@@ -9,7 +9,7 @@
 // flops an element: bytes bound it, for one token the launch and a chain of
 // dependent loads (row -> sequence -> length -> page).
 //
-// A warp takes a whole row, or (few rows) an eighth of its heads: d / 16 lanes
+// A warp takes half of a row's heads, or (few rows) an eighth: d / 16 lanes
 // hold a head row, each the two 8-element chunks that RoPE pairs, so the
 // rotation needs no exchange, the norm three shuffles and no warp waits for
 // another.  Sequence, cache row and angles are found while the first head
@@ -29,39 +29,40 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kFewWarps = 8;      // warps of a row when there are few rows
+constexpr int kManyWarps = 2;     // and when there are many
 
 struct Chunk {
   float v[8];
 };
 
-__device__ __forceinline__ Chunk load8(const float* p) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-}
-__device__ __forceinline__ Chunk load8(const __nv_bfloat16* p) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  Chunk c;
+// Eight elements as loaded (16-bit ones stay packed while in flight).
+template <typename T>
+struct Raw {
+  uint4 u;
+  __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ Chunk get() const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    Chunk c;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(w[i]));
-    c.v[2 * i] = f.x;
-    c.v[2 * i + 1] = f.y;
+    for (int i = 0; i < 4; ++i) {
+      float2 f;
+      if constexpr (std::is_same_v<T, __nv_bfloat16>) f = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(w[i]));
+      else f = __half22float2(reinterpret_cast<const __half2&>(w[i]));
+      c.v[2 * i] = f.x;
+      c.v[2 * i + 1] = f.y;
+    }
+    return c;
   }
-  return c;
-}
-__device__ __forceinline__ Chunk load8(const __half* p) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  Chunk c;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(reinterpret_cast<const __half2&>(w[i]));
-    c.v[2 * i] = f.x;
-    c.v[2 * i + 1] = f.y;
+};
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
   }
-  return c;
-}
+  __device__ __forceinline__ Chunk get() const { return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
+};
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const Chunk& c) {
   uint32_t w[4];
 #pragma unroll
@@ -81,13 +82,19 @@ __device__ __forceinline__ void store8(__half* p, const Chunk& c) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Resident CTAs of an SM.  Many rows: 3, each lane 3 head rows deep (2 in f32):
+// 157 us for 34912 rows of 48 f16 heads, 5.8 TB/s; 4 CTAs of 64 registers spill
+// where there are norms (222 us for 32000 rows against 150), 2 leave the
+// loads' latency open.  Few rows: one wave at any occupancy.
+constexpr int append_ctas(int warps) { return warps == kManyWarps ? 3 : 2; }
+
 template <typename In, typename Out, int D, int WARPS>
-__global__ void __launch_bounds__(kAppendThreads) step_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS)) step_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kLanes = D / 16;               // lanes of a head row
   constexpr int kGroups = 32 / kLanes;         // head rows of a warp at once
-  constexpr int kDepth = sizeof(In) == 4 ? 2 : 4;   // of those, in flight
+  constexpr int kDepth = WARPS == kManyWarps && sizeof(In) == 2 ? 3 : 2;   // of those, in flight
   constexpr int kStep = WARPS * kGroups;       // heads between a lane's
-  __shared__ float2 cs_all[kAppendThreads / 32][D / 2];
+  __shared__ __align__(16) float2 cs_all[kAppendThreads / 32][D / 2];
   pdl_wait();
   pdl_launch_dependents();
   const StepView& s = a.s;
@@ -109,7 +116,7 @@ __global__ void __launch_bounds__(kAppendThreads) step_append_kernel(const __gri
 
   const int stride = gridDim.x * (kAppendThreads / 32) / WARPS;
   for (int row = id / WARPS; row < s.n_rows; row += stride) {
-    Chunk x0[kDepth], x1[kDepth];
+    Raw<In> x0[kDepth], x1[kDepth];
     auto fetch = [&](int h0) {
 #pragma unroll
       for (int i = 0; i < kDepth; ++i) {
@@ -118,8 +125,8 @@ __global__ void __launch_bounds__(kAppendThreads) step_append_kernel(const __gri
           const In* p = h < Hq ? static_cast<const In*>(a.q) + row * a.q_stride + (long)h * D
                         : h < Hq + Hkv ? static_cast<const In*>(a.k) + row * a.k_stride + (long)(h - Hq) * D
                                        : static_cast<const In*>(a.v) + row * a.v_stride + (long)(h - Hq - Hkv) * D;
-          x0[i] = load8(p + c0);
-          x1[i] = load8(p + c1);
+          x0[i].load(p + c0);
+          x1[i].load(p + c1);
         }
       }
     };
@@ -166,7 +173,7 @@ __global__ void __launch_bounds__(kAppendThreads) step_append_kernel(const __gri
         const int h = h0 + i * kStep;
         const bool is_q = h < Hq, is_v = h >= Hq + Hkv;
         const float* gain = is_q ? a.q_gain : (is_v ? nullptr : a.k_gain);
-        Chunk y0 = x0[i], y1 = x1[i];
+        Chunk y0 = x0[i].get(), y1 = x1[i].get();
         if (a.q_gain || a.k_gain) {
           float ss = 0.f;
 #pragma unroll
@@ -175,12 +182,15 @@ __global__ void __launch_bounds__(kAppendThreads) step_append_kernel(const __gri
           for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
           if (h < heads && gain) {
             const float r = rsqrtf(ss * (1.f / D) + a.eps);
-            const Chunk g0 = load8(gain + c0), g1 = load8(gain + c1);
+            Raw<float> g;
+            g.load(gain + c0);
+            Chunk x = g.get();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              y0.v[j] *= r * g0.v[j];
-              y1.v[j] *= r * g1.v[j];
-            }
+            for (int j = 0; j < 8; ++j) y0.v[j] *= r * x.v[j];
+            g.load(gain + c1);
+            x = g.get();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y1.v[j] *= r * x.v[j];
           }
         }
         if (h >= heads || (!is_q && dst < 0)) continue;
@@ -204,14 +214,18 @@ __global__ void __launch_bounds__(kAppendThreads) step_append_kernel(const __gri
 
 template <typename In, typename Out>
 cudaError_t launch(const AppendArgs& a, int n_sm, cudaStream_t s) {
-  // Eight warps a row while they are resident together (32 warps an SM);
-  // beyond, the repeated look-ups cost more than the shorter rows save.
+  // Eight warps a row up to two waves of them (bf16, 48 normed heads: 304 rows
+  // 4.9 us against 6.9 with two warps, 608 rows 6.9 against 7.0, 1000 rows 10.6
+  // against 10.3): beyond, the repeated look-ups cost more than short rows save.
   const bool few = (long)a.s.n_rows * kFewWarps <= 32L * n_sm;
-  const long warps = (long)a.s.n_rows * (few ? kFewWarps : 1);
+  const long warps = (long)a.s.n_rows * (few ? kFewWarps : kManyWarps);
   const long ctas = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
-  const dim3 grid((unsigned)(ctas < 4L * n_sm ? ctas : 4L * n_sm)), block(kAppendThreads);
-  auto* kernel = few ? (a.c.d == 128 ? step_append_kernel<In, Out, 128, kFewWarps> : step_append_kernel<In, Out, 64, kFewWarps>)
-                     : (a.c.d == 128 ? step_append_kernel<In, Out, 128, 1> : step_append_kernel<In, Out, 64, 1>);
+  const long most = (long)append_ctas(few ? kFewWarps : kManyWarps) * n_sm;
+  const dim3 grid((unsigned)(ctas < most ? ctas : most)), block(kAppendThreads);
+  auto* kernel = few ? (a.c.d == 128 ? step_append_kernel<In, Out, 128, kFewWarps>
+                                     : step_append_kernel<In, Out, 64, kFewWarps>)
+                     : (a.c.d == 128 ? step_append_kernel<In, Out, 128, kManyWarps>
+                                     : step_append_kernel<In, Out, 64, kManyWarps>);
   return launch_pdl(kernel, grid, block, 0, s, a);
 }
 
