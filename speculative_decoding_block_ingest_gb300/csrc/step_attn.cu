@@ -703,82 +703,107 @@ __global__ void __launch_bounds__(kStepThreads, 1)
 
 // ---------------------------------------------------------------- merge
 // One warp per (row, head): o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i
-// over the row's fragments, at most one per segment and CTA.
-constexpr int kMergeThreads = 256;
+// over the row's fragments, one per segment and CTA that worked on it.  Few
+// bytes, so latency bounds it: what does not depend on an earlier load is
+// loaded at once, partial rows kAhead at a time.
+constexpr int kMergeThreads = 128, kAhead = 4;
 
 template <int D, typename Out>
-__global__ void __launch_bounds__(kMergeThreads) step_merge_kernel(const __grid_constant__ StepAttnArgs a) {
+__global__ void __launch_bounds__(kMergeThreads, 8) step_merge_kernel(const __grid_constant__ StepAttnArgs a) {
   constexpr int kPer = D / 32;   // elements of a lane
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const long item = (long)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
-  const long row = item / a.Hq;
-  const int head = (int)(item % a.Hq), h = head / a.G;
-  if (row >= a.s.start(a.s.n_seq)) return;   // behind the last sequence: left as it is
+  const unsigned item = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);   // at most 2^31
+  const unsigned row = item / (unsigned)a.Hq;
+  if (row >= (unsigned)a.s.n_rows) return;
+  const int head = (int)(item - row * a.Hq), h = head / a.G;
+  const int rows = a.s.start(a.s.n_seq);
+  // per segment: first CTA, fragments, the row's place in a continued tile pair
+  int c0[2] = {0, 0}, n[2] = {0, 0}, trow[2] = {0, 0};
+  float2 firsts[2];
+#pragma unroll
+  for (int seg = 0; seg < 2; ++seg)
+    if (seg == 1 || a.s.prefix_len > 0) {
+      const int4 meta = a.meta[((long)seg * a.s.n_rows + row) * a.Hkv + h];
+      firsts[seg] = a.seg_ml[seg][item];
+      c0[seg] = min(max(meta.x, 0), a.n_cta - 1);
+      n[seg] = min(max(meta.y, c0[seg]), a.n_cta - 1) - c0[seg] + 1;
+      const int in_tile = min(max(meta.z, 0), 2 * a.tpt - 1);
+      // rows of a pair's second tile lie behind the first's 128
+      trow[seg] = (in_tile < a.tpt ? in_tile * a.G : 128 + (in_tile - a.tpt) * a.G) + head - h * a.G;
+    }
+  if (row >= (unsigned)rows) return;   // behind the last sequence: left as it is
+  const int total = n[0] + n[1];
   float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) o[i] = 0.f;
   bool bad = false;
-  for (int seg = a.s.prefix_len > 0 ? 0 : 1; seg < 2; ++seg) {
-    const int4 meta = a.meta[((long)seg * a.s.n_rows + row) * a.Hkv + h];
-    const int c0 = min(max(meta.x, 0), a.n_cta - 1), c1 = min(max(meta.y, c0), a.n_cta - 1);
-    const int in_tile = min(max(meta.z, 0), 2 * a.tpt - 1);
-    // rows of a pair's second tile lie behind the first's 128
-    const int trow = in_tile < a.tpt ? in_tile * a.G : 128 + (in_tile - a.tpt) * a.G;
-    const int n = c1 - c0 + 1;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      // lane i: fragment i's max and sum
-      const int i = i0 + lane;
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (i < n) {
-        ml = i == 0 ? a.seg_ml[seg][row * a.Hq + head] : a.cta_ml[(long)(c0 + i) * 256 + trow + head - h * a.G];
-        bad |= a.status[c0 + i] != 0;
-      }
-      float mx = ml.x;
+  for (int i0 = 0; i0 < total; i0 += 32) {
+    // lane i: fragment i's max, sum and partial row
+    const int i = i0 + lane, seg = i >= n[0], k = i - (seg ? n[0] : 0);
+    float2 ml = make_float2(-INFINITY, 0.f);
+    const float* src = nullptr;
+    if (i < total) {
+      const int cta = (seg ? c0[1] : c0[0]) + k;
+      const long at = (long)cta * 256 + (seg ? trow[1] : trow[0]);
+      ml = k == 0 ? (seg ? firsts[1] : firsts[0]) : a.cta_ml[at];
+      src = k == 0 ? (seg ? a.seg_o[1] : a.seg_o[0]) + (long)item * D : a.cta_o + at * D;
+      bad |= a.status[cta] != 0;
+    }
+    float mx = ml.x;
 #pragma unroll
-      for (int s = 16; s; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-      const float mn = fmaxf(m, mx);
+    for (int s = 16; s; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    const float mn = fmaxf(m, mx);
+    // a part without a maximum counts nothing, unless its sum is NaN
+    const float wt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_fast(ml.x - mn);
+    float add = wt == 0.f ? 0.f : wt * ml.y;
+#pragma unroll
+    for (int s = 16; s; s >>= 1) add += __shfl_xor_sync(0xffffffffu, add, s);
+    if (i0 > 0) {
       const float keep = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2_fast(m - mn);
-      const float wt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_fast(ml.x - mn);
-      m = mn;
-      float add = wt == 0.f ? 0.f : wt * ml.y;
-#pragma unroll
-      for (int s = 16; s; s >>= 1) add += __shfl_xor_sync(0xffffffffu, add, s);
-      l = (keep == 0.f ? 0.f : l * keep) + add;
+      l = keep == 0.f ? 0.f : l * keep;
 #pragma unroll
       for (int v = 0; v < kPer; ++v) o[v] = keep == 0.f ? 0.f : o[v] * keep;
-      const int cnt = min(32, n - i0);
-#pragma unroll 4
-      for (int f = 0; f < cnt; ++f) {
-        const float g = __shfl_sync(0xffffffffu, wt, f);
-        const float* src = i0 + f == 0 ? a.seg_o[seg] + (row * a.Hq + head) * D
-                                       : a.cta_o + ((long)(c0 + i0 + f) * 256 + trow + head - h * a.G) * D;
-        float x[kPer];
-        if constexpr (kPer == 4) {
-          const float4 q = reinterpret_cast<const float4*>(src)[lane];
-          x[0] = q.x, x[1] = q.y, x[2] = q.z, x[3] = q.w;
-        } else {
-          const float2 q = reinterpret_cast<const float2*>(src)[lane];
-          x[0] = q.x, x[1] = q.y;
-        }
+    }
+    m = mn;
+    l += add;
+    const int cnt = min(32, total - i0);
+    for (int f0 = 0; f0 < cnt; f0 += kAhead) {
+      float x[kAhead][kPer], g[kAhead];
 #pragma unroll
-        for (int v = 0; v < kPer; ++v) o[v] = g == 0.f ? o[v] : fmaf(x[v], g, o[v]);
+      for (int f = 0; f < kAhead; ++f) {
+        g[f] = 0.f;
+        if (f0 + f >= cnt) continue;
+        g[f] = __shfl_sync(0xffffffffu, wt, f0 + f);
+        const float* p = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), f0 + f)) + lane * kPer;
+        if constexpr (kPer == 4) {
+          const float4 q = *reinterpret_cast<const float4*>(p);
+          x[f][0] = q.x, x[f][1] = q.y, x[f][2] = q.z, x[f][3] = q.w;
+        } else {
+          const float2 q = *reinterpret_cast<const float2*>(p);
+          x[f][0] = q.x, x[f][1] = q.y;
+        }
       }
+#pragma unroll
+      for (int f = 0; f < kAhead; ++f)
+        if (g[f] != 0.f)
+#pragma unroll
+          for (int v = 0; v < kPer; ++v) o[v] = fmaf(x[f][v], g[f], o[v]);
     }
   }
   bad = __any_sync(0xffffffffu, bad);
   const float inv = bad ? __int_as_float(0x7fc00000) : (l == 0.f ? 0.f : 1.f / l);
-  Out* dst = static_cast<Out*>(a.out) + row * a.out_stride + (long)head * D + lane * kPer;
+  Out* dst = static_cast<Out*>(a.out) + (long)row * a.out_stride + (long)head * D + lane * kPer;
+  uint32_t y[kPer / 2];
 #pragma unroll
-  for (int v = 0; v < kPer; ++v) o[v] *= inv;
-  Out y[kPer];
-#pragma unroll
-  for (int v = 0; v < kPer; ++v) y[v] = Out(o[v]);
-  if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(y);
-  else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(y);
+  for (int v = 0; v < kPer; v += 2)
+    y[v / 2] = __float_as_uint(pack2<std::is_same_v<Out, __nv_bfloat16>>(make_float2(o[v] * inv, o[v + 1] * inv)));
+  if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+  else *reinterpret_cast<uint32_t*>(dst) = y[0];
   if (a.lse && lane == 0)
-    a.lse[row * a.Hq + head] = bad ? inv : (l == 0.f ? -INFINITY : 0.69314718055994531f * (m + log2f(l)));
+    a.lse[item] = bad ? inv : (l == 0.f ? -INFINITY : 0.69314718055994531f * (m + log2f(l)));
 }
 
 template <int D, bool BF16>

@@ -1,5 +1,6 @@
 // target.cu -- C ABI of the target model's side of a speculative step
 // (include/dflash.h): argument checks, tensor maps and launches.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -86,12 +87,15 @@ StepView view(const dflash_paged_cache* c, const dflash_step* s) {
   return v;
 }
 
-// SMs of the current device.
+// SMs of the current device (asked once for each).
 int sm_count(int* n) {
+  static std::atomic<int> known[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev < 64 && (*n = known[dev].load(std::memory_order_relaxed)) > 0) return DFLASH_OK;
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return launched(e, "device SM count");
+  if (dev < 64) known[dev].store(*n, std::memory_order_relaxed);
   return DFLASH_OK;
 }
 

@@ -46,11 +46,11 @@ def _cuda(device: torch.device, what: str) -> torch.device:
 
 def _vector(device: torch.device, what: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype = torch.int32) -> int:
     """Device pointer of a tensor of this shape whose rows are contiguous."""
-    if t.device != device:
+    if t.get_device() != device.index:
         _refuse(f"{what} is on {t.device}, expected {device}")
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         _refuse(f"{what} is {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape)}")
-    if shape[-1] > 1 and t.stride(-1) != 1:
+    if not t.is_contiguous() and shape[-1] > 1 and t.stride(-1) != 1:
         _refuse(f"{what} must be contiguous in its last dimension")
     return t.data_ptr()
 
@@ -69,8 +69,9 @@ def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
 
 
 def _stream(device: torch.device) -> int:
-    """Handle of the device's current stream (the public call makes a Stream
-    object, 2 us of a 10 us call)."""
+    """Handle of the device's current stream.  (The public calls for this and
+    for the current device take 2 us of a call's 15; tensors on the device
+    exist by now, so CUDA is initialised.)"""
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
@@ -84,7 +85,7 @@ def _used(stream: Optional[torch.cuda.Stream], *tensors):
 
 
 def _elsewhere(device: torch.device, stream: Optional[torch.cuda.Stream]) -> bool:
-    return stream is not None or torch.cuda.current_device() != device.index
+    return stream is not None or torch._C._cuda_getDevice() != device.index
 
 
 class Rope:
@@ -110,6 +111,7 @@ class PagedCache:
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
         self.device = _cuda(k.device, "k cache")
+        self.index = self.device.index
         if k.dim() != 4 or v.device != k.device or v.dtype != k.dtype or k.shape != v.shape or k.stride() != v.stride():
             _refuse("k and v caches must be alike: [n_pages, page_size, n_kv_heads, head_dim], device, dtype, strides")
         if k.stride(3) != 1:
@@ -177,7 +179,7 @@ class Step:
 def _rows(cache: PagedCache, what: str, t: torch.Tensor, n_rows: Optional[int] = None, heads: Optional[int] = None):
     """(rows, heads, row stride) of a [n_rows, heads, head_dim] tensor with contiguous heads."""
     shape, st, d = t.shape, t.stride(), cache.head_dim
-    if t.device != cache.device:
+    if t.get_device() != cache.index:
         _refuse(f"{what} is on {t.device}, the cache on {cache.device}")
     if len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads) or (
             n_rows is not None and shape[0] != n_rows):
@@ -209,14 +211,15 @@ def append(cache: PagedCache, step: Step, q: Optional[torch.Tensor], k: torch.Te
         return q_out
     n, _, ks = _rows(cache, "k", k, None, cache.n_kv_heads)
     _, _, vs = _rows(cache, "v", v, n, cache.n_kv_heads)
-    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+    dt = k.dtype
+    if v.dtype is not dt or (q is not None and q.dtype is not dt):
         _refuse("q, k and v must have one dtype")
     hq = qp = qs = qop = qos = 0
     if q is not None:
         _, hq, qs = _rows(cache, "q", q, n)
         qp = q.data_ptr()
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=cache.dtype, device=dev)
+            q_out = torch.empty_like(q, dtype=cache.dtype, memory_format=torch.contiguous_format)
             qos = hq * cache.head_dim
         else:
             if q_out.dtype != cache.dtype:
@@ -257,13 +260,13 @@ def attention(cache: PagedCache, step: Step, q: torch.Tensor, *, scale: Optional
         _used(stream, cache.k, cache.v, *step.tensors, q, out, lse, workspace)
         return out, lse
     n, hq, qs = _rows(cache, "q", q)
-    if q.dtype != cache.dtype:
+    if q.dtype is not cache.dtype:
         _refuse("q must have the cache's dtype")
     if scale is not None and not scale > 0:
         _refuse("scale must be positive")
     ref, need = step.rows(cache, n), cache.workspace_bytes(n, hq)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         os = hq * cache.head_dim
     else:
         if out.dtype != q.dtype:
