@@ -401,7 +401,8 @@ int dflash_launch_count(dflash_t *h, int64_t *launches);
  *
  * Out-of-range contents of the device arrays cannot be refused by the host;
  * the kernels bound them instead: a row index, length or page outside its
- * range writes nothing, and a page outside [0, n_pages) reads as zeros.
+ * range writes nothing, a page outside [0, n_pages) reads as zeros, and row
+ * starts that decrease leave the rows unspecified, inside their buffers.
  * ------------------------------------------------------------------------ */
 
 /* A paged cache of one target layer.  Key row r of a page, kv head h starts
@@ -504,9 +505,9 @@ int dflash_step_attention(const dflash_paged_cache *cache, const dflash_step *st
  * 2 floor(128 / G) tokens of one kv head (G query heads each), keys in blocks
  * of 128.  The prefix's items come first, then each sequence's (by head, then
  * rows).  An item costs 3 + rows G / 32 units for its ends and 4 (more than
- * floor(128 / G) tokens) or 3 for each block; CTA c of C = min(n_cta,
- * ceil(total / 3)) takes the units [c total / C, (c + 1) total / C) and with
- * them the blocks that start there. */
+ * floor(128 / G) tokens) or 3 for each block; C = min(n_cta, ceil(total / 3))
+ * CTAs take equal runs of units (the first ones a unit more) and with them the
+ * blocks that start there. */
 typedef struct dflash_step_piece {
   int32_t cta;
   int32_t segment;             /* 0: shared prefix, 1: own keys            */

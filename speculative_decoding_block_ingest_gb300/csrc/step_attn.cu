@@ -32,6 +32,8 @@
 //                     the cache's type, over S) read from TMEM
 // V tiles are used as they lie in the cache (rows are keys), as the MN-major
 // operand of the second product.
+#include <atomic>
+
 #include "../../include/dflash.h"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -152,10 +154,9 @@ struct Shared {
   // scheduling: this CTA's fragments, in a ring
   uint64_t ffull[kFrags], fempty[kFrags];
   Frag frag[kFrags];
-  long base;
-  int seq0;
+  int base, seq0;
   union {
-    long warp_units[kStepThreads / 32];   // scheduling
+    int warp_units[kStepThreads / 32];   // scheduling
     float2 ml[2][128];                    // merge of the two streams of a single item
   };
   // first own key whose value element is not finite, per element
@@ -262,27 +263,29 @@ __global__ void __launch_bounds__(kStepThreads, 1)
   {
     const int per = (a.s.n_seq + kStepThreads - 1) / kStepThreads;
     const int i0 = min(tid * per, a.s.n_seq), i1 = min(i0 + per, a.s.n_seq);
-    long mine = 0;
-    for (int i = i0; i < i1; ++i) mine += (long)a.Hkv * w.head_units(i);
-    long inc = mine;
+    int mine = 0;
+    for (int i = i0; i < i1; ++i) mine += a.Hkv * w.head_units(i);
+    int inc = mine;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long x = __shfl_up_sync(0xffffffffu, inc, o);
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += x;
     }
     if (lane == 31) sh.warp_units[warp] = inc;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    long at = w.prefix_units(), total = at;
+    int at = w.prefix_units(), total = at;
+#pragma unroll
     for (int v = 0; v < kStepThreads / 32; ++v) {
       if (v < warp) at += sh.warp_units[v];
       total += sh.warp_units[v];
     }
     at += inc - mine;                    // this thread's first unit
-    share_units(w, total, a.n_cta, blockIdx.x);
+    w.divide(total, a.n_cta, blockIdx.x);
     if (w.ua < w.ub && w.ua >= at && w.ua < at + mine)  // the sequence that holds unit ua
       for (int i = i0; i < i1; ++i) {
-        const long n = (long)a.Hkv * w.head_units(i);
+        const int n = a.Hkv * w.head_units(i);
         if (w.ua < at + n) {
           sh.seq0 = i;
           sh.base = at;
@@ -811,8 +814,16 @@ cudaError_t launch(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMa
                    cudaStream_t s) {
   auto* attn = step_attn_kernel<D, BF16>;
   const size_t smem = step_smem(D, step_stages(D));
-  cudaError_t e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the kernel's shared memory is raised once on every device
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(raised.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) raised.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
   e = launch_pdl(attn, dim3(a.n_cta), dim3(kStepThreads), smem, s, q, k, v, a);
   if (e != cudaSuccess) return e;
   const long warps = (long)a.s.n_rows * a.Hq;

@@ -26,6 +26,9 @@ struct Frag {
   int last_cta;        // and then: the CTA of the item's last unit
 };
 
+// All counts of units are 32-bit (the host refuses more work than that): 64-bit
+// divisions cost 2 us of a 13 us call here.
+//
 // The items in order: the prefix's by kv head and tile pair, then every
 // sequence's.  An item takes end_units, then its blocks' units one block after
 // the other; a CTA runs the blocks that start in its share.
@@ -34,9 +37,9 @@ struct Walk {
   int pair_tok;        // tokens of two tiles
   int rows;            // rows of all sequences
   int pre_blocks, pre_tiles;
-  long ua, ub;         // this CTA's units
-  long total, n_cta;   // all units, and the CTAs that have some
-  long pos;            // first unit of the item at (seg, seq, h, tile)
+  int ua, ub;          // this CTA's units
+  int n_cta, share, more;   // CTAs that have units, a CTA's at least, and how many have one more
+  int pos;             // first unit of the item at (seg, seq, h, tile)
   int seg, seq, h, tile;
 
   __host__ __device__ explicit Walk(const StepAttnArgs& args) : a(args) {
@@ -47,9 +50,7 @@ struct Walk {
   }
   __host__ __device__ int tokens(int i) const { return max(a.s.start(i + 1) - a.s.start(i), 0); }
   __host__ __device__ int weight(int ntok) const { return ntok > a.tpt ? kPairUnits : kSingleUnits; }
-  __host__ __device__ long units(int ntok, int blocks) const {
-    return end_units(ntok * a.G) + (long)blocks * weight(ntok);
-  }
+  __host__ __device__ int units(int ntok, int blocks) const { return end_units(ntok * a.G) + blocks * weight(ntok); }
   // tokens of tile pair j out of T
   __host__ __device__ int pair_tokens(int j, int T) const { return min(pair_tok, T - j * pair_tok); }
   // key blocks that tile pair j of sequence i needs
@@ -59,34 +60,56 @@ struct Walk {
     return (min(max(seen, 0), a.s.room()) + kKeys - 1) / kKeys;
   }
   // units of one kv head: of the prefix, and of sequence i
-  __host__ __device__ long prefix_head() const {
+  __host__ __device__ int prefix_head() const {
     if (!pre_tiles) return 0;
     return (pre_tiles - 1) * units(pair_tok, pre_blocks) + units(pair_tokens(pre_tiles - 1, rows), pre_blocks);
   }
-  __host__ __device__ long prefix_units() const { return a.Hkv * prefix_head(); }
-  __host__ __device__ long head_units(int i) const {
+  __host__ __device__ int prefix_units() const { return a.Hkv * prefix_head(); }
+  __host__ __device__ int head_units(int i) const {
     const int T = tokens(i);
-    long u = 0;
+    int u = 0;
     for (int j = 0; j * pair_tok < T; ++j) u += units(pair_tokens(j, T), blocks(i, j, T));
     return u;
   }
+  // CTA c's share of `total` units.  At most `most` CTAs, none with less than a
+  // block of one tile, so every CTA in use has units and the CTAs of an item
+  // are consecutive (one may find no block starting in its share of it).
+  __host__ __device__ void divide(int total, int most, int c) {
+    n_cta = min(most, (total + kSingleUnits - 1) / kSingleUnits);
+    ua = ub = 0;
+    if (n_cta == 0) return;
+    share = total / n_cta;
+    more = total - share * n_cta;
+    if (c < n_cta) {
+      ua = c * share + min(c, more);
+      ub = ua + share + (c < more);
+    }
+  }
+  __host__ __device__ int cta_of(int unit) const {
+    const int big = more * (share + 1);
+    return unit < big ? unit / (share + 1) : more + (unit - big) / share;
+  }
   // Go to the item that holds unit ua; `seq0` is its sequence (-1: the
   // prefix) and `base` that sequence's first unit.
-  __host__ __device__ void begin(int seq0, long base) {
+  __host__ __device__ void begin(int seq0, int base) {
+    if (seq0 < 0 && ua >= prefix_units()) {   // no sequence holds it: row starts that decrease
+      pos = ub;
+      return;
+    }
     seg = seq0 < 0 ? 0 : 1;
     seq = seq0;
-    const long per_head = seg ? head_units(seq) : prefix_head();
-    h = per_head ? (int)((ua - base) / per_head) : 0;
+    const int per_head = seg ? head_units(seq) : prefix_head();
+    h = per_head ? (ua - base) / per_head : 0;
     pos = base + h * per_head;
     tile = 0;
     if (!seg) {   // every pair but the last is full
-      const long full = units(pair_tok, pre_blocks);
-      tile = (int)min((ua - pos) / full, (long)pre_tiles - 1);
+      const int full = units(pair_tok, pre_blocks);
+      tile = min((ua - pos) / full, pre_tiles - 1);
       pos += tile * full;
     } else {
       const int T = tokens(seq);
       for (; tile * pair_tok < T; ++tile) {
-        const long n = units(pair_tokens(tile, T), blocks(seq, tile, T));
+        const int n = units(pair_tokens(tile, T), blocks(seq, tile, T));
         if (pos + n > ua) break;
         pos += n;
       }
@@ -116,11 +139,11 @@ struct Walk {
       f.keys = seg ? min(a.s.len(seq), a.s.room()) : a.s.prefix_len;
       f.lim0 = seg && a.causal ? a.s.len(seq) - T + tile * pair_tok + 1 : f.keys;
       const int w = weight(f.ntok);
-      const long first_block = pos + end_units(f.ntok * a.G), end = first_block + (long)n * w;
-      f.b0 = (int)min(max(ua - first_block + w - 1, 0L) / w, (long)n);
-      f.b1 = (int)min(max(ub - first_block + w - 1, 0L) / w, (long)n);
+      const int first_block = pos + end_units(f.ntok * a.G), end = first_block + n * w;
+      f.b0 = min((max(ua - first_block, 0) + w - 1) / w, n);
+      f.b1 = min((max(ub - first_block, 0) + w - 1) / w, n);
       f.first = ua <= pos;
-      f.last_cta = (int)min((end * n_cta + total - 1) / total - 1, n_cta - 1);
+      f.last_cta = cta_of(end - 1);
       pos = end;
       ++tile;
       if (seg == 0 && tile == pre_tiles) {
@@ -133,17 +156,13 @@ struct Walk {
   }
 };
 
-// CTA c's share [ua, ub) of `total` units.  At most n_cta CTAs, none with less
-// than a block of one tile, so every CTA in use has units and the CTAs of an
-// item are consecutive (one may find no block starting in its share of it).
-__host__ __device__ inline void share_units(Walk& w, long total, int n_cta, int c) {
-  w.total = total;
-  w.n_cta = min((long)n_cta, (total + kSingleUnits - 1) / kSingleUnits);
-  w.ua = w.ub = 0;
-  if (c < w.n_cta) {
-    w.ua = c * total / w.n_cta;
-    w.ub = (c + 1) * total / w.n_cta;
-  }
+// The units of all sequences' own keys on the host's worst case, and of the
+// prefix: an upper bound that fits 31 bits, or more work than is accepted.
+inline bool step_fits(const StepAttnArgs& a, int max_keys) {
+  const long pairs = ((long)a.s.n_rows + 2 * a.tpt - 1) / (2 * a.tpt);
+  const long blocks = (max_keys + (long)kKeys - 1) / kKeys, pre = (a.s.prefix_len + (long)kKeys - 1) / kKeys;
+  const long most = end_units(2 * a.tpt * a.G) + kPairUnits;   // and one block more than a share may hold
+  return a.Hkv * ((pairs + a.s.n_seq) * (most + blocks * kPairUnits) + pairs * (most + pre * kPairUnits)) < (1L << 31);
 }
 
 }  // namespace dfl

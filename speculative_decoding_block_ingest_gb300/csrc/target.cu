@@ -242,6 +242,7 @@ int dflash_step_attention(const dflash_paged_cache* cache, const dflash_step* st
   set_shape(a, cache, p->n_heads);
   if (int rc = step_ctas(&a.n_cta)) return rc;
   a.causal = p->causal != 0;
+  if (!step_fits(a, a.s.room())) return fail(DFLASH_ERR_UNSUPPORTED, "more work than one call takes: fewer rows");
   const float scale = p->scale > 0 ? p->scale : 1.f / std::sqrt((float)d);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.bf16 = cache->dtype == DFLASH_BF16;
@@ -299,19 +300,19 @@ int dflash_step_attention_plan(const dflash_paged_cache* cache, const dflash_ste
   a.s = view(cache, step);
   set_shape(a, cache, n_heads);
   a.causal = causal != 0;
+  if (!step_fits(a, a.s.room())) return fail(DFLASH_ERR_UNSUPPORTED, "more work than one call takes: fewer rows");
   Walk w(a);
-  long total = w.prefix_units();
-  for (int i = 0; i < step->n_seq; ++i) total += (long)a.Hkv * w.head_units(i);
+  int total = w.prefix_units();
+  for (int i = 0; i < step->n_seq; ++i) total += a.Hkv * w.head_units(i);
   int n = 0;
   for (int c = 0; c < n_cta; ++c) {
-    share_units(w, total, n_cta, c);
+    w.divide(total, n_cta, c);
     if (w.ua >= w.ub) continue;
-    int seq0 = -1;
-    long base = 0;
+    int seq0 = -1, base = 0;
     if (w.ua >= w.prefix_units()) {
       base = w.prefix_units();
       for (seq0 = 0;; ++seq0) {
-        const long u = (long)a.Hkv * w.head_units(seq0);
+        const int u = a.Hkv * w.head_units(seq0);
         if (w.ua < base + u) break;
         base += u;
       }

@@ -71,8 +71,8 @@ def check(rows, kv, n_cta=152, **kw):
         weight[key] = 4 if tokens > 128 // G else 3
         pos += 3 + tokens * G // 32 + weight[key] * blocks
     C = min(n_cta, -(-pos // 3))
-    share = [(c * pos // C, (c + 1) * pos // C) for c in range(C)]
-    assert max(b - a for a, b in share) - min(b - a for a, b in share) <= 1
+    q, more = divmod(pos, C) if C else (0, 0)
+    share = [(c * q + min(c, more), (c + 1) * q + min(c + 1, more)) for c in range(C)]
     got, ctas = {}, {}
     for p in pieces:
         key = (p["segment"], p["seq"], p["kv_head"], p["row0"])
@@ -152,4 +152,8 @@ def test_refusals():
     assert call(heads=3) == dflash.ERR_INVALID_ARG
     assert call(heads=2 * 65) == dflash.ERR_UNSUPPORTED
     assert call(n_cta=0) == dflash.ERR_INVALID_ARG
+    # 2^24 rows over 2^29 keys: more units of work than one call takes
+    big = dflash.StepDesc(n_seq=1, n_rows=1 << 24, row_start=ctypes.addressof(rs), kv_len=ctypes.addressof(kl),
+                          block_table=ctypes.addressof(rs), table_cols=1 << 23, table_stride=1 << 23)
+    assert call(s=big) == dflash.ERR_UNSUPPORTED
     assert lib.dflash_last_error().decode() != ""
