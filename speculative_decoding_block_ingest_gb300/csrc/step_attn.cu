@@ -28,8 +28,8 @@
 //   warps 0..3, 4..7  softmax of stream 0 / 1, one thread per query row
 //   warp 8            TMA: query tiles (ring of 2), K and V tiles (ring)
 //   warp 10, one lane the pieces of items this CTA runs, described in a ring
-//   warp 9, one lane  tcgen05.mma: S = Q K^T into TMEM, O += P V with P (in
-//                     the cache's type, over S) read from TMEM
+//   warp 9            tcgen05.mma: S = Q K^T into TMEM, O += P V with P (in the
+//                     cache's type, over S) read from TMEM
 // V tiles are used as they lie in the cache (rows are keys), as the MN-major
 // operand of the second product.
 #include <atomic>
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
     mbar_init(&sh.drained, 1);
     for (int i = 0; i < kFrags; ++i) {
       mbar_init(&sh.ffull[i], 1);
-      mbar_init(&sh.fempty[i], 10);   // the TMA and MMA warps and the eight softmax warps
+      mbar_init(&sh.fempty[i], 10);   // the TMA and MMA warps and eight softmax warps
     }
     sh.abort = 0;
     sh.any_bad = 0;
@@ -377,15 +377,17 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       // ------------------------------------------------------------------ MMA
       // The warp runs converged and elects a lane only around the tensor
       // instructions: their descriptors then stay in uniform registers (issued
-      // from one lane's branch, each cost about 110 cycles).
+      // from one lane's branch, each cost about 110 cycles).  One warp issues
+      // both streams' products in turn, which keeps the streams half a period
+      // apart (with a warp each they fall into step, softmax against softmax
+      // and product against product: 4140 cycles a pair block).
       bool ok = true;
       uint32_t nq = 0, nb = 0;                         // query tiles and key blocks before this fragment
       uint32_t np[2] = {0, 0};                         // P tiles used by each stream
       const uint64_t q_desc = desc_sw128(smem_u32(sQ)), k_desc = desc_sw128(smem_u32(sKV));
       const uint64_t v_desc = desc_sw128_mn(smem_u32(sKV));
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && !__all_sync(0xffffffffu, pipe_wait(bar, parity, abort))) ok = false;
-        tc_fence_after();
+        if (ok) ok = __all_sync(0xffffffffu, pipe_wait(bar, parity, abort));
         return ok;
       };
       auto landed = [&](uint32_t tile) { return wait(&sh.kvfull[tile % kStages], (tile / kStages) & 1); };
@@ -397,57 +399,56 @@ __global__ void __launch_bounds__(kStepThreads, 1)
         const int cnt[2] = {pair ? n : (n + 1) / 2, pair ? n : n / 2};
         auto tile = [&](int s, int j, int kv) { return 2 * nb + tile_of(pair, pair ? j : 2 * j + s, n, kv); };
         const int slot0 = nq & 1;
-        if (!wait(&sh.qfull[slot0], (nq >> 1) & 1)) continue;
-        if (pair && !wait(&sh.qfull[slot0 ^ 1], ((nq + 1) >> 1) & 1)) continue;
+        // S of a stream's block j; its K tile has landed (one elected lane)
         auto issue_s = [&](int s, int j) {
-          const uint32_t t = tile(s, j, 0);
-          if (!landed(t)) return;
-          const int st = t % kStages, slot = pair ? slot0 ^ s : slot0;
+          const int st = tile(s, j, 0) % kStages, slot = pair ? slot0 ^ s : slot0;
           const uint64_t qd = q_desc + (uint64_t)(slot * (kTile >> 4)), kd = k_desc + (uint64_t)(st * (kTile >> 4));
+#pragma unroll
+          for (int kk = 0; kk < 4 * kDAtoms; ++kk) {
+            const uint64_t at = (uint64_t)((kk >> 2) * (kAtomBytes >> 4) + (kk & 3) * 2);
+            mma_bf16(tmem + 128u * s, qd + at, kd + at, kIdescS, kk > 0);
+          }
+          mma_commit(&sh.sfull[s]);
+          if (!pair || s == 1) mma_commit(&sh.kvempty[st]);
           // the last product on a query tile frees its slot
-          const bool last = j + 1 == cnt[s] && (pair || s == ((n - 1) & 1));
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < 4 * kDAtoms; ++kk) {
-              const uint64_t at = (uint64_t)((kk >> 2) * (kAtomBytes >> 4) + (kk & 3) * 2);
-              mma_bf16(tmem + 128u * s, qd + at, kd + at, kIdescS, kk > 0);
-            }
-            mma_commit(&sh.sfull[s]);
-            if (!pair || s == 1) mma_commit(&sh.kvempty[st]);
-            if (last) mma_commit(&sh.qempty[slot]);
-          }
-          __syncwarp();
+          if (j + 1 == cnt[s] && (pair || s == ((n - 1) & 1))) mma_commit(&sh.qempty[slot]);
         };
-        auto issue_pv = [&](int s, int j) {
-          const uint32_t t = tile(s, j, 1), parity = np[s]++ & 1;
-          if (!landed(t)) return;
-          const int st = t % kStages;
-          const uint64_t vd = v_desc + (uint64_t)(st * (kTile >> 4));
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {   // P arrives in two halves of 64 keys
-            if (!wait(&sh.pfull[s][half], parity)) return;
-            if (elect_one()) {
-#pragma unroll
-              for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                mma_f16_ts(tmem + kColO + 128u * s, tmem + 128u * s + (uint32_t)(kk * 8),
-                           vd + (uint64_t)(kk * (2048 >> 4)), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
-              if (half == 1) {
-                mma_commit(&sh.pvdone[s]);
-                if (!pair || s == 1) mma_commit(&sh.kvempty[st]);
-              }
-            }
-            __syncwarp();
-          }
-        };
+        wait(&sh.qfull[slot0], (nq >> 1) & 1);
+        if (pair) wait(&sh.qfull[slot0 ^ 1], ((nq + 1) >> 1) & 1);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-          if (ok && cnt[s]) issue_s(s, 0);
+          if (cnt[s] && landed(tile(s, 0, 0))) {
+            if (elect_one()) issue_s(s, 0);
+            __syncwarp();
+          }
         for (int j = 0; j < cnt[0] && ok; ++j) {
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            if (!ok || j >= cnt[s]) continue;
-            issue_pv(s, j);
-            if (ok && j + 1 < cnt[s]) issue_s(s, j + 1);
+            if (j >= cnt[s]) continue;
+            const uint32_t t = tile(s, j, 1), parity = np[s]++ & 1;
+            const int st = t % kStages;
+            const uint64_t vd = v_desc + (uint64_t)(st * (kTile >> 4));
+            // the tiles of this product and of the next scores first (a pair
+            // shares them): nothing is waited for between the end of P and
+            // the next scores
+            if ((!pair || s == 0) && (!landed(t) || (j + 1 < cnt[s] && !landed(tile(s, j + 1, 0))))) break;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {   // P arrives in two halves of 64 keys
+              if (!wait(&sh.pfull[s][half], parity)) break;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                  mma_f16_ts(tmem + kColO + 128u * s, tmem + 128u * s + (uint32_t)(kk * 8),
+                             vd + (uint64_t)(kk * (2048 >> 4)), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+                if (half == 1) {
+                  mma_commit(&sh.pvdone[s]);
+                  if (!pair || s == 1) mma_commit(&sh.kvempty[st]);
+                  if (j + 1 < cnt[s]) issue_s(s, j + 1);
+                }
+              }
+              __syncwarp();
+            }
           }
         }
         nq += pair ? 2 : 1;
@@ -508,9 +509,12 @@ __global__ void __launch_bounds__(kStepThreads, 1)
         // elements that are not finite are taken out and remembered.
         const int own0 = causal && f.lim0 < f.keys ? max(f.lim0, 0) : INT_MAX;   // first key not seen by all rows
         if (ok && (st == 0 || !pair) && (key0 + kKeys > f.keys || key0 + kKeys > own0)) {
-          const uint32_t tile = 2 * nb + tile_of(pair, bi, n, 1);
-          if (!__all_sync(0xffffffffu, pipe_wait(&sh.kvfull[tile % kStages], (tile / kStages) & 1, abort))) ok = false;
-          uint8_t* v = sKV + (tile % kStages) * kTile + r * 128;
+          // (a pair shares the tile and its streams' products come in turn, so
+          // stream 0 does it for both; the slot's use before this one is over,
+          // because the scores just read were issued behind its product)
+          const uint32_t tile = 2 * nb + tile_of(pair, bi, n, 1), stage = tile % kStages;
+          if (!__all_sync(0xffffffffu, pipe_wait(&sh.kvfull[stage], (tile / kStages) & 1, abort))) ok = false;
+          uint8_t* v = sKV + stage * kTile + r * 128;
           const int key = key0 + r;
           if (key >= f.keys) {
 #pragma unroll

@@ -7,12 +7,13 @@ namespace dfl {
 
 constexpr int kKeys = 128;   // keys of a block
 
-// What a CTA's work costs, in units of about 900 cycles: a block of keys for
-// two tiles (bound by shared-memory and L2 reads, 3500 cycles measured) or
-// for one (by HBM, 2650), and an item's start and end, which writes up to 128
-// KB of partial rows (2500 cycles for 8 rows, 10600 for 256).
+// What a CTA's work costs, in units of about 800 cycles: a block of keys for
+// two tiles (3250 cycles measured) or for one (1900 from L2, 2700 from HBM, both
+// streams together), and an item's start and end, which fills and drains the
+// pipeline and writes a partial row of each of its rows (5000 cycles for 8 rows,
+// 11000 for 128, 13000 for 256).
 constexpr int kPairUnits = 4, kSingleUnits = 3;
-__host__ __device__ inline int end_units(int rows) { return 3 + rows / 32; }
+__host__ __device__ inline int end_units(int rows) { return 6 + min(rows, 128) / 16; }
 
 // One piece of an item that a CTA runs: key blocks [b0, b1) of the segment.
 struct Frag {

@@ -61,6 +61,10 @@ def items(rows, kv, *, hq, hkv, prefix=0, page=64, causal=True, cols=None):
     return want
 
 
+def ends(rows):
+    return 6 + min(rows, 128) // 16
+
+
 def check(rows, kv, n_cta=152, **kw):
     pieces = plan(rows, kv, n_cta=n_cta, **kw)
     want = items(rows, kv, **kw)
@@ -69,7 +73,7 @@ def check(rows, kv, n_cta=152, **kw):
     for key, (tokens, blocks) in want.items():           # prefix first, then by sequence, head and rows
         start[key] = pos
         weight[key] = 4 if tokens > 128 // G else 3
-        pos += 3 + tokens * G // 32 + weight[key] * blocks
+        pos += ends(tokens * G) + weight[key] * blocks
     C = min(n_cta, -(-pos // 3))
     q, more = divmod(pos, C) if C else (0, 0)
     share = [(c * q + min(c, more), (c + 1) * q + min(c + 1, more)) for c in range(C)]
@@ -80,7 +84,7 @@ def check(rows, kv, n_cta=152, **kw):
         assert p["n_tokens"] == tokens and 0 <= p["block0"] <= p["block1"] <= blocks
         a, b = share[p["cta"]]
         assert p["first"] == (a <= start[key] < b)
-        at = start[key] + 3 + tokens * G // 32            # the blocks that start in the CTA's share
+        at = start[key] + ends(tokens * G)            # the blocks that start in the CTA's share
         starts = [i for i in range(p["block0"], p["block1"])]
         assert all(a <= at + weight[key] * i < b for i in starts)
         got.setdefault(key, []).append((p["block0"], p["block1"], p["first"]))

@@ -214,6 +214,19 @@ def test_attention_random_steps(T):
                                     scale=case[4] ** -0.5))
 
 
+@pytest.mark.parametrize("case", [
+    # enough blocks for every CTA to go round its ring of K and V tiles several times, in every mode
+    ([2], [60000], 8, 8, 128, 64, BF, True, 0, False),
+    ([1, 3], [41000, 20001], 8, 8, 64, 128, HF, True, 1000, True),
+    ([90, 1, 2], [9000, 15000, 11000], 32, 4, 128, 64, BF, True, 3000, False),
+    ([1] * 300, [5 + i % 380 for i in range(300)], 4, 4, 128, 16, BF, True, 0, False),
+], ids=["single", "single-d64", "pair-and-single", "many-short"])
+def test_attention_long(T, case):
+    rows, _, hq, hkv, d, page, dt, causal, prefix, hnd = case
+    (starts, kv, table, pre, kc, vc, q, _), o, lse = attend_case(T, case, seed=40)
+    close(o, lse, R.attend_step(q, kc, vc, starts, kv, table, pre, prefix, page, causal=causal, scale=d ** -0.5))
+
+
 def test_attention_large_scores_scale_and_strided_rows(T):
     """Scores far apart (the running maximum moves often), a scale of the caller's, queries and results inside wider
     rows."""
