@@ -28,6 +28,7 @@
 //   warps 0..3, 4..7  softmax of stream 0 / 1, one thread per query row
 //   warp 8            TMA: query tiles (ring of 2), K and V tiles (ring)
 //   warp 10, one lane the pieces of items this CTA runs, described in a ring
+//   warp 11           waits for the tiles that the MMA warp's next products read
 //   warp 9            tcgen05.mma: S = Q K^T into TMEM, O += P V with P (in the
 //                     cache's type, over S) read from TMEM
 // V tiles are used as they lie in the cache (rows are keys), as the MN-major
@@ -147,7 +148,7 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, uint64_t
 
 struct Shared {
   uint64_t kvfull[kMaxStages], kvempty[kMaxStages];
-  uint64_t qfull[2], qempty[2], sfull[2], pfull[2][2], pvdone[2];
+  uint64_t qfull[2], qempty[2], sfull[2], pfull[2][2], pvdone[2], kfirst[2];
   uint64_t drained;
   uint32_t tmem;
   int abort;
@@ -235,14 +236,15 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       mbar_init(&sh.qfull[i], 1);
       mbar_init(&sh.qempty[i], 1);
       mbar_init(&sh.sfull[i], 1);
-      mbar_init(&sh.pfull[i][0], 128);
+      mbar_init(&sh.pfull[i][0], 129);   // and warp 11
       mbar_init(&sh.pfull[i][1], 128);
       mbar_init(&sh.pvdone[i], 1);
+      mbar_init(&sh.kfirst[i], 1);
     }
     mbar_init(&sh.drained, 1);
     for (int i = 0; i < kFrags; ++i) {
       mbar_init(&sh.ffull[i], 1);
-      mbar_init(&sh.fempty[i], 10);   // the TMA and MMA warps and eight softmax warps
+      mbar_init(&sh.fempty[i], 11);   // warps 8, 9 and 11 and eight softmax warps
     }
     sh.abort = 0;
     sh.any_bad = 0;
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
         if (ok) ok = __all_sync(0xffffffffu, pipe_wait(bar, parity, abort));
         return ok;
       };
-      auto landed = [&](uint32_t tile) { return wait(&sh.kvfull[tile % kStages], (tile / kStages) & 1); };
+      uint32_t nfirst[2] = {0, 0};                     // fragments each stream had a part in
       Frag f;
       while (take(f)) {
         const int n = f.b1 - f.b0;
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
         const int cnt[2] = {pair ? n : (n + 1) / 2, pair ? n : n / 2};
         auto tile = [&](int s, int j, int kv) { return 2 * nb + tile_of(pair, pair ? j : 2 * j + s, n, kv); };
         const int slot0 = nq & 1;
-        // S of a stream's block j; its K tile has landed (one elected lane)
+        // S of a stream's block j (one elected lane)
         auto issue_s = [&](int s, int j) {
           const int st = tile(s, j, 0) % kStages, slot = pair ? slot0 ^ s : slot0;
           const uint64_t qd = q_desc + (uint64_t)(slot * (kTile >> 4)), kd = k_desc + (uint64_t)(st * (kTile >> 4));
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
         if (pair) wait(&sh.qfull[slot0 ^ 1], ((nq + 1) >> 1) & 1);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-          if (cnt[s] && landed(tile(s, 0, 0))) {
+          if (cnt[s] && wait(&sh.kfirst[s], nfirst[s]++ & 1)) {
             if (elect_one()) issue_s(s, 0);
             __syncwarp();
           }
@@ -428,12 +430,10 @@ __global__ void __launch_bounds__(kStepThreads, 1)
             const uint32_t t = tile(s, j, 1), parity = np[s]++ & 1;
             const int st = t % kStages;
             const uint64_t vd = v_desc + (uint64_t)(st * (kTile >> 4));
-            // the tiles of this product and of the next scores first (a pair
-            // shares them): nothing is waited for between the end of P and
-            // the next scores
-            if ((!pair || s == 0) && (!landed(t) || (j + 1 < cnt[s] && !landed(tile(s, j + 1, 0))))) break;
+            // P arrives in two halves of 64 keys; warp 11 holds the first one
+            // back until this product's V and the next scores' K have landed
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {   // P arrives in two halves of 64 keys
+            for (int half = 0; half < 2; ++half) {
               if (!wait(&sh.pfull[s][half], parity)) break;
               tc_fence_after();
               if (elect_one()) {
@@ -460,6 +460,43 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       __syncwarp();
       int none = 0;
       pipe_wait(&sh.drained, 0, &none);
+    } else if (warp == 11) {
+      // ------------------------------------------------------------------ tiles landed
+      // Waits for the tiles in the MMA warp's place: that warp's instructions
+      // bound a pair's blocks, and a wait that is over already costs it 200
+      // cycles.  It waits for every tile, none before the one that had its
+      // slot before, so a barrier's parity is never read a turn early; and it
+      // goes on to a stream's next block only when the last P is complete,
+      // because its arrival would count for that one.
+      bool ok = true;
+      uint32_t nb = 0, np[2] = {0, 0};
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, pipe_wait(bar, parity, abort));
+      };
+      auto landed = [&](uint32_t tile) { wait(&sh.kvfull[tile % kStages], (tile / kStages) & 1); };
+      Frag f;
+      while (take(f)) {
+        const int n = f.b1 - f.b0;
+        if (!ok || n <= 0) continue;
+        const bool pair = f.ntok > a.tpt;
+        const int cnt[2] = {pair ? n : (n + 1) / 2, pair ? n : n / 2};
+        auto tile = [&](int s, int j, int kv) { return 2 * nb + tile_of(pair, pair ? j : 2 * j + s, n, kv); };
+        for (int j = -1; j < cnt[0] && ok; ++j) {   // -1: the first scores' K tiles
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (j >= cnt[s] || cnt[s] == 0) continue;
+            if (!pair || s == 0) {                  // a pair shares its tiles
+              if (j >= 0) landed(tile(s, j, 1));
+              if (j + 1 < cnt[s]) landed(tile(s, j + 1, 0));
+            }
+            if (np[s] > 0) wait(&sh.pfull[s][0], (np[s] - 1) & 1);
+            if (j >= 0) ++np[s];
+            if (ok && lane == 0) mbar_arrive(j < 0 ? &sh.kfirst[s] : &sh.pfull[s][0]);
+          }
+        }
+        nb += (uint32_t)n;
+      }
+      if (!ok) sh.abort = 1;
     } else if (warp == 10) {
       // ------------------------------------------------------------------ fragments
       if (lane == 0) {
