@@ -131,11 +131,16 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS)) step_appen
       }
     };
     fetch(first);
-    // the row's sequence: those that end at or before it lie below
+    // the row's sequence: as many end at or before the row as lie below it
+    // (each lane looks at the end of one 32nd of what is left)
     int seq = 0;
-#pragma unroll 4
-    for (int i = lane; i < s.n_seq; i += 32) seq += s.start(i + 1) <= row;
-    seq = __reduce_add_sync(0xffffffffu, seq);
+    for (int left = s.n_seq; left > 0;) {
+      const int step = (left + 31) / 32;
+      const int end = seq + min((lane + 1) * step, left);
+      const int below = __popc(__ballot_sync(0xffffffffu, s.start(end) <= row)) * step;
+      seq += min(below, left);
+      left = below >= left ? 0 : min(step, left - below) - 1;
+    }
     if (seq >= s.n_seq) break;   // rows behind the last sequence stay as they are
     const int own = s.len(seq) - s.start(seq + 1) + row;   // this row's own key index
     long dst = -1;                                         // its row in the cache

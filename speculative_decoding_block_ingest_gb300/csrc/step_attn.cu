@@ -13,7 +13,7 @@
 // (o, max, sum) of the segments are merged by a second kernel.
 //
 // Balance.  One CTA per SM; the items' key blocks form one line of units that
-// is cut into equal pieces (StepAttnArgs), so a single long sequence, many
+// is cut into equal pieces (step_plan.cuh), so a single long sequence, many
 // short ones and any mixture load the SMs alike, with lengths known only on
 // the device.  A CTA continues at most one item begun by another (its first),
 // which bounds the partials: one per row and segment plus one tile per CTA.
@@ -303,7 +303,10 @@ __global__ void __launch_bounds__(kStepThreads, 1)
   uint32_t nf = 0;
   auto take = [&](Frag& f) -> bool {
     const int i = nf % kFrags;
-    ring_wait(&sh.ffull[i], (nf / kFrags) & 1);
+    if (!__all_sync(0xffffffffu, ring_wait(&sh.ffull[i], (nf / kFrags) & 1))) {
+      sh.abort = 1;
+      return false;
+    }
     f = sh.frag[i];
     ++nf;
     __syncwarp();

@@ -427,3 +427,38 @@ def test_verify_views(T):
     tok, acc = T.verify_tokens(block[:, 1:], wide[..., :V], ua.to(DEV), ut.to(DEV))
     wt, wa = R.verify(draft, tp, ua, ut)
     assert np.array_equal(acc.cpu().numpy(), wa) and np.array_equal(tok.cpu().numpy(), wt)
+
+
+def test_append_many_sequences(T):
+    """More sequences than a warp looks at in one go, most of them without rows."""
+    n, d = 2500, 64
+    rows = [3 if i % 7 == 0 else 0 for i in range(n)]
+    kv = [t + i % 4 for i, t in enumerate(rows)]
+    starts, kv, table, _, n_pages = R.make_step(rows, kv, 16, seed=8)
+    kc, vc = caches(n_pages, 16, 1, d, HF)
+    g = torch.Generator().manual_seed(9)
+    k, v = (torch.randn(starts[-1], 1, d, generator=g).to(HF).to(DEV) for _ in range(2))
+    T.append(T.PagedCache(kc, vc), T.Step(i32(starts), i32(kv), table.to(DEV)), None, k, v)
+    own = [(int(table[i, j // 16]), j % 16) for i, t in enumerate(rows) for j in range(kv[i] - t, kv[i])]
+    p, r = (torch.tensor(x, device=DEV) for x in zip(*own))
+    assert torch.equal(kc[p, r], k) and torch.equal(vc[p, r], v)
+
+
+def test_bad_device_arrays_stay_in_bounds(T):
+    """Lengths, row starts and page ids outside their ranges: nothing outside the buffers is touched, nothing hangs."""
+    d, rows = 64, 8
+    kc, vc = caches(4, 16, 2, d, BF, seed=3)
+    q = torch.randn(rows, 4, d, generator=torch.Generator().manual_seed(4)).to(BF).to(DEV)
+    kv = torch.randn(rows, 2, d, generator=torch.Generator().manual_seed(5)).to(BF).to(DEV)
+    big = 2 ** 31 - 1
+    for starts, lens, pages in [([0, 100, 200], [5, 5], [[0], [1]]), ([0, 8, 3], [5, 5], [[0], [1]]),
+                                ([-5, 4, 8], [-3, big], [[0], [1]]), ([0, 4, 8], [16, 16], [[-1], [big]]),
+                                ([8, 8, 8], [16, 16], [[0], [1]]), ([5, 0, 8], [3, big], [[99], [-big]])]:
+        guard = torch.full((rows + 16, 4, d), 5.0, dtype=BF, device=DEV)
+        cache, step = T.PagedCache(kc, vc), T.Step(i32(starts), i32(lens), i32(pages), i32([7, -1]), 20)
+        T.append(cache, step, q, kv, kv, q_out=guard[:rows])
+        out = torch.full((rows + 16, 4, d), 5.0, dtype=BF, device=DEV)
+        ws = torch.empty(cache.workspace_bytes(rows, 4), dtype=torch.uint8, device=DEV)
+        T.attention(cache, step, q, out=out[:rows], workspace=ws)
+        T.attention_status(ws)
+        assert bool((out[rows:] == 5).all()) and bool((guard[rows:] == 5).all())
