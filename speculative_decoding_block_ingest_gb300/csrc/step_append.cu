@@ -9,7 +9,7 @@
 // flops an element: bytes bound it, for one token the launch and a chain of
 // dependent loads (row -> sequence -> length -> page).
 //
-// A warp takes half of a row's heads, or (few rows) an eighth: d / 16 lanes
+// A warp takes a whole row, or (few rows) an eighth of its heads: d / 16 lanes
 // hold a head row, each the two 8-element chunks that RoPE pairs, so the
 // rotation needs no exchange, the norm three shuffles and no warp waits for
 // another.  Sequence, cache row and angles are found while the first head
@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kFewWarps = 8;      // warps of a row when there are few rows
-constexpr int kManyWarps = 2;     // and when there are many
+constexpr int kManyWarps = 1;     // and when there are many
 
 struct Chunk {
   float v[8];
@@ -82,17 +82,17 @@ __device__ __forceinline__ void store8(__half* p, const Chunk& c) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Resident CTAs of an SM.  Many rows: 3, each lane 3 head rows deep (2 in f32):
-// 157 us for 34912 rows of 48 f16 heads, 5.8 TB/s; 4 CTAs of 64 registers spill
-// where there are norms (222 us for 32000 rows against 150), 2 leave the
-// loads' latency open.  Few rows: one wave at any occupancy.
-constexpr int append_ctas(int warps) { return warps == kManyWarps ? 3 : 2; }
+// Resident CTAs of an SM.  Many rows: four, each lane 2 head rows deep (1 in
+// f32): 34912 rows of 48 f16 heads in 148 us (6.2 TB/s), 32000 normed bf16 rows in
+// 145; three CTAs, two warps a row and 3 deep 148 and 152, deeper ones spill.
+// Few rows: one to four waves at any occupancy.
+constexpr int append_ctas(int warps) { return warps == kManyWarps ? 4 : 2; }
 
 template <typename In, typename Out, int D, int WARPS>
 __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS)) step_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kLanes = D / 16;               // lanes of a head row
   constexpr int kGroups = 32 / kLanes;         // head rows of a warp at once
-  constexpr int kDepth = WARPS == kManyWarps && sizeof(In) == 2 ? 3 : 2;   // of those, in flight
+  constexpr int kDepth = WARPS == kManyWarps && sizeof(In) == 4 ? 1 : 2;   // of those, in flight
   constexpr int kStep = WARPS * kGroups;       // heads between a lane's
   __shared__ __align__(16) float2 cs_all[kAppendThreads / 32][D / 2];
   pdl_wait();
@@ -130,7 +130,9 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS)) step_appen
         }
       }
     };
-    fetch(first);
+    // many rows: other warps cover these loads' latency, and held through the
+    // look-ups below their registers spill
+    if constexpr (WARPS == kFewWarps) fetch(first);
     // the row's sequence: as many end at or before the row as lie below it
     // (each lane looks at the end of one 32nd of what is left)
     int seq = 0;
@@ -149,6 +151,7 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS)) step_appen
       if (page >= 0 && page < s.n_pages)
         dst = page * a.c.page_stride + (long)(own & (s.page_size - 1)) * a.c.row_stride;
     }
+    if constexpr (WARPS == kManyWarps) fetch(first);
     float2 w[8];
     if (a.rot) {
       const long pos = a.positions ? (long)a.positions[row] : (long)s.prefix_len + own;
@@ -219,10 +222,10 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS)) step_appen
 
 template <typename In, typename Out>
 cudaError_t launch(const AppendArgs& a, int n_sm, cudaStream_t s) {
-  // Eight warps a row up to two waves of them (bf16, 48 normed heads: 304 rows
-  // 4.9 us against 6.9 with two warps, 608 rows 6.9 against 7.0, 1000 rows 10.6
-  // against 10.3): beyond, the repeated look-ups cost more than short rows save.
-  const bool few = (long)a.s.n_rows * kFewWarps <= 32L * n_sm;
+  // Eight warps a row up to four waves of them (bf16, 48 normed heads: 300 rows
+  // 4.9 us against 11.0 with one warp, 1200 rows 10.9 against 11.3, 1600 rows 14.5
+  // against 14.0): beyond, the repeated look-ups cost more than short rows save.
+  const bool few = (long)a.s.n_rows * kFewWarps <= 64L * n_sm;
   const long warps = (long)a.s.n_rows * (few ? kFewWarps : kManyWarps);
   const long ctas = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
   const long most = (long)append_ctas(few ? kFewWarps : kManyWarps) * n_sm;
