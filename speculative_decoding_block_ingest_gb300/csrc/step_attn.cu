@@ -27,7 +27,7 @@
 // Either way one stream's products run under the other's softmax.
 //   warps 0..3, 4..7  softmax of stream 0 / 1, one thread per query row
 //   warp 8            TMA: query tiles (ring of 2), K and V tiles (ring)
-//   warp 10, one lane the pieces of items this CTA runs, described in a ring
+//   warp 10           the pieces of items this CTA runs, described in a ring
 //   warp 11           waits for the tiles that the MMA warp's next products read
 //   warp 9            tcgen05.mma: S = Q K^T into TMEM, O += P V with P (in the
 //                     cache's type, over S) read from TMEM
@@ -152,14 +152,10 @@ struct Shared {
   uint64_t drained;
   uint32_t tmem;
   int abort;
-  // scheduling: this CTA's fragments, in a ring
+  // this CTA's fragments, in a ring
   uint64_t ffull[kFrags], fempty[kFrags];
   Frag frag[kFrags];
-  int base, seq0;
-  union {
-    int warp_units[kStepThreads / 32];   // scheduling
-    float2 ml[2][128];                    // merge of the two streams of a single item
-  };
+  float2 ml[2][128];   // merge of the two streams of a single item
   // first own key whose value element is not finite, per element
   int bad[128];
   int any_bad;
@@ -248,8 +244,6 @@ __global__ void __launch_bounds__(kStepThreads, 1)
     }
     sh.abort = 0;
     sh.any_bad = 0;
-    sh.seq0 = -1;
-    sh.base = 0;
     fence_barrier_init();
     tma_prefetch_map(&tmQ);
     tma_prefetch_map(&tmK);
@@ -257,47 +251,13 @@ __global__ void __launch_bounds__(kStepThreads, 1)
   }
   if (tid < 128) sh.bad[tid] = INT_MAX;
   if (warp == 9) tmem_alloc(&sh.tmem, 512);
-  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  pdl_wait();   // the step's arrays, queries and cache may come from the kernel before
   pdl_launch_dependents();
 
-  // ---- this CTA's units: every thread counts a run of sequences
-  Walk w(a);
-  {
-    const int per = (a.s.n_seq + kStepThreads - 1) / kStepThreads;
-    const int i0 = min(tid * per, a.s.n_seq), i1 = min(i0 + per, a.s.n_seq);
-    int mine = 0;
-    for (int i = i0; i < i1; ++i) mine += a.Hkv * w.head_units(i);
-    int inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-    if (lane == 31) sh.warp_units[warp] = inc;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    int at = w.prefix_units(), total = at;
-#pragma unroll
-    for (int v = 0; v < kStepThreads / 32; ++v) {
-      if (v < warp) at += sh.warp_units[v];
-      total += sh.warp_units[v];
-    }
-    at += inc - mine;                    // this thread's first unit
-    w.divide(total, a.n_cta, blockIdx.x);
-    if (w.ua < w.ub && w.ua >= at && w.ua < at + mine)  // the sequence that holds unit ua
-      for (int i = i0; i < i1; ++i) {
-        const int n = a.Hkv * w.head_units(i);
-        if (w.ua < at + n) {
-          sh.seq0 = i;
-          sh.base = at;
-          break;
-        }
-        at += n;
-      }
-    __syncthreads();
-  }
-  const uint32_t tmem = sh.tmem;
   // Every role takes every fragment, also after a failed wait (it then skips
   // the work), so the ring and the named barriers never starve.
   uint32_t nf = 0;
@@ -502,8 +462,39 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       if (!ok) sh.abort = 1;
     } else if (warp == 10) {
       // ------------------------------------------------------------------ fragments
+      // The warp counts all units, 32 sequences at a time, then looks for the
+      // sequence that holds this CTA's first.
+      Walk w(a);
+      const int n = a.s.n_seq, prefix = w.prefix_units();
+      auto units_of = [&](int i) { return i < n ? a.Hkv * w.head_units(i) : 0; };
+      const int mine = units_of(lane);
+      int total = prefix + __reduce_add_sync(0xffffffffu, mine);
+#pragma unroll 4
+      for (int i = 32; i < n; i += 32) total += __reduce_add_sync(0xffffffffu, units_of(i + lane));
+      w.divide(total, a.n_cta, blockIdx.x);
+      int seq0 = -1, base = 0;
+      if (w.ua < w.ub && w.ua >= prefix) {
+        base = prefix;
+        for (int i = 0; i < n; i += 32) {
+          const int u = i ? units_of(i + lane) : mine;
+          int inc = u;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += x;
+          }
+          const unsigned holds = __ballot_sync(0xffffffffu, w.ua < base + inc);
+          if (holds) {
+            const int l = __ffs(holds) - 1;
+            seq0 = i + l;
+            base += __shfl_sync(0xffffffffu, inc - u, l);
+            break;
+          }
+          base += __shfl_sync(0xffffffffu, inc, 31);
+        }
+      }
       if (lane == 0) {
-        if (w.ua < w.ub) w.begin(sh.seq0, sh.base);
+        if (w.ua < w.ub) w.begin(seq0, base);
         else w.pos = w.ub;
         for (uint32_t i = 0, more = 1; more; ++i) {
           Frag f;

@@ -78,7 +78,7 @@ struct Walk {
   __host__ __device__ void divide(int total, int most, int c) {
     n_cta = min(most, (total + kSingleUnits - 1) / kSingleUnits);
     ua = ub = 0;
-    if (n_cta == 0) return;
+    if (n_cta <= 0) return;
     share = total / n_cta;
     more = total - share * n_cta;
     if (c < n_cta) {
