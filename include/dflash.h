@@ -488,8 +488,9 @@ typedef struct dflash_attention_args {
 } dflash_attention_args;
 
 /* out = softmax(scale q K^T) V over each row's keys, lse = log of the sum of
- * exp(scale q.k) over them (natural).  The shared prefix is read once for the
- * whole batch.  A row without keys gives zeros and lse -inf.  What the cache
+ * exp(scale q.k) over them (natural).  The shared prefix is attended by
+ * the batch's rows together: once per 256 of a kv head's query rows, not once
+ * per sequence.  A row without keys gives zeros and lse -inf.  What the cache
  * holds past a sequence's or the prefix's last key has no effect, whatever
  * it is.  A value element of the step's own rows that is not finite makes
  * that element NaN in every row that sees it, and only there; keys and

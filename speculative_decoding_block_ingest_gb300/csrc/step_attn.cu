@@ -24,7 +24,11 @@
 //   single (at most one tile of rows: decoding)  stream 0 takes the even
 //          blocks and stream 1 the odd ones of the same rows, and their
 //          results are merged in tensor memory.
-// Either way one stream's products run under the other's softmax.
+// Either way one stream's products run under the other's softmax.  What bounds
+// it: a pair's block takes 2830 cycles of which the tensor pipe works 2048 (the
+// issue path between them; 32 sequences of 16 rows behind 16384 keys: 115 us, 1.24
+// PFLOP/s with the merge); a single's 2700 are HBM's (one sequence, 131016 keys:
+// 6.7 TB/s in the loop, 96 us in all).
 //   warps 0..3, 4..7  softmax of stream 0 / 1, one thread per query row
 //   warp 8            TMA: query tiles (ring of 2), K and V tiles (ring)
 //   warp 10           the pieces of items this CTA runs, described in a ring
@@ -119,8 +123,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
   return d;
 }
+// Two softmax weights (the lower key in the low half) or results in the
+// cache's type: the product with V takes both operands in one 16-bit type.  The
+// row sums add the unrounded weights, so the rounding (half a step, either way)
+// does not add up in the quotient.
 template <bool BF16>
-__device__ __forceinline__ float pack2(float2 p) {   // two weights in the cache's type (the lower key in the low half)
+__device__ __forceinline__ float pack2(float2 p) {
   if constexpr (BF16) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
     return __uint_as_float(reinterpret_cast<const uint32_t&>(b));
@@ -713,9 +721,8 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       }
       if (live && (pair || st == 0)) {
         *pml = make_float2(m0, l0);
-        if (f.first && head == 0) {
+        if (f.first && head == 0)
           a.meta[((long)f.seg * a.s.n_rows + row) * a.Hkv + f.h] = make_int4(blockIdx.x, f.last_cta, t, 0);
-        }
       }
       tc_fence_before();
       both();                                        // both streams have read O, and the notes on bad values
