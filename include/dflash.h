@@ -506,7 +506,7 @@ int dflash_step_attention(const dflash_paged_cache *cache, const dflash_step *st
  * 2 floor(128 / G) tokens of one kv head (G query heads each), keys in blocks
  * of 128.  The prefix's items come first, then each sequence's (by head, then
  * rows).  An item costs 6 + min(rows G, 128) / 16 units for its ends and 4 (more than
- * floor(128 / G) tokens) or 3 for each block; C = min(n_cta, ceil(total / 3))
+ * floor(128 / G) tokens) or 3 for each block; C = min(n_cta, ceil(total / 6))
  * CTAs take equal runs of units (the first ones a unit more) and with them the
  * blocks that start there. */
 typedef struct dflash_step_piece {

@@ -91,7 +91,8 @@ struct StepAttnArgs {
   float* lse;
   // workspace
   int* status;         // [n_cta]
-  int4* meta;          // [2][n_rows][Hkv]: segment's first and last CTA, row's token within its tile
+  int4* meta;          // [2][n_rows][Hkv]: segment's first and last CTA, row's token within its tiles,
+                       // whether the row's result is written
   float* seg_o[2];     // [n_rows][Hq][d]: a segment's first fragment (prefix, own), unnormalised
   float2* seg_ml[2];   // [n_rows][Hq]: its (max, sum)
   float* cta_o;        // [n_cta][256][d]: the fragment a CTA continues

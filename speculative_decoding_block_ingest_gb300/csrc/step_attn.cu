@@ -10,7 +10,8 @@
 // that run over the rows of the whole batch, so its keys are read once per
 // kv head and 256 rows instead of once per sequence; own keys by tiles of one
 // sequence.  Item = (segment, sequence, kv head, two tiles).  Partial results
-// (o, max, sum) of the segments are merged by a second kernel.
+// (o, max, sum) of the segments and pieces are merged by a second kernel; an
+// item that one CTA ran whole, without a prefix, is finished where it is.
 //
 // Balance.  One CTA per SM; the items' key blocks form one line of units that
 // is cut into equal pieces (step_plan.cuh), so a single long sequence, many
@@ -136,6 +137,11 @@ __device__ __forceinline__ float pack2(float2 p) {
     const __half2 b = __floats2half2_rn(p.x, p.y);
     return __uint_as_float(reinterpret_cast<const uint32_t&>(b));
   }
+}
+
+// log of a row's sum of exponentials from its maximum (in log2 units) and sum
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l == 0.f ? -INFINITY : 0.69314718055994531f * (m + log2f(l));
 }
 
 // Descriptor of an MN-major tile in the 128-byte swizzle: rows are K (keys)
@@ -682,6 +688,9 @@ __global__ void __launch_bounds__(kStepThreads, 1)
         if (e0.x == -INFINITY && e0.y != 0.f) l0 = e0.y, w0 = 1.f;
         if (e1.x == -INFINITY && e1.y != 0.f) l0 = e1.y, w1 = 1.f;
       }
+      // a row whose every key was here needs no merge: its result as it stands
+      const bool whole = f.first && f.last_cta == (int)blockIdx.x && a.s.prefix_len == 0;
+      const float inv = l0 == 0.f ? 0.f : 1.f / l0;
       const bool empty = pair ? cnt == 0 : n == 0;
       const bool poisoned = sh.any_bad;
       // a pair's streams write their own rows; of a single item each writes
@@ -713,16 +722,28 @@ __global__ void __launch_bounds__(kStepThreads, 1)
             for (int i = 0; i < 32; ++i)
               if (sh.bad[c + i] < lim) o[i] = __int_as_float(0x7fc00000);
           }
-          if (live) {
+          if (live && whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.out_stride +
+                                                  (long)(f.h * a.G + head) * D + c);
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t y[4];
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                y[v] = __float_as_uint(pack2<BF16>(make_float2(o[i + 2 * v] * inv, o[i + 2 * v + 1] * inv)));
+              dst[i / 8] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          } else if (live) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) store_sector(po + c + i, o + i);
           }
         }
       }
       if (live && (pair || st == 0)) {
-        *pml = make_float2(m0, l0);
+        if (!whole) *pml = make_float2(m0, l0);
+        else if (a.lse) a.lse[row * a.Hq + f.h * a.G + head] = log_sum(m0, l0);
         if (f.first && head == 0)
-          a.meta[((long)f.seg * a.s.n_rows + row) * a.Hkv + f.h] = make_int4(blockIdx.x, f.last_cta, t, 0);
+          a.meta[((long)f.seg * a.s.n_rows + row) * a.Hkv + f.h] = make_int4(blockIdx.x, f.last_cta, t, whole);
       }
       tc_fence_before();
       both();                                        // both streams have read O, and the notes on bad values
@@ -767,6 +788,7 @@ __global__ void __launch_bounds__(kMergeThreads, 8) step_merge_kernel(const __gr
   // per segment: first CTA, fragments, the row's place in a continued tile pair
   int c0[2] = {0, 0}, n[2] = {0, 0}, trow[2] = {0, 0};
   float2 firsts[2];
+  bool whole = false;
 #pragma unroll
   for (int seg = 0; seg < 2; ++seg)
     if (seg == 1 || a.s.prefix_len > 0) {
@@ -777,8 +799,11 @@ __global__ void __launch_bounds__(kMergeThreads, 8) step_merge_kernel(const __gr
       const int in_tile = min(max(meta.z, 0), 2 * a.tpt - 1);
       // rows of a pair's second tile lie behind the first's 128
       trow[seg] = (in_tile < a.tpt ? in_tile * a.G : 128 + (in_tile - a.tpt) * a.G) + head - h * a.G;
+      whole = meta.w != 0;
     }
   if (row >= (unsigned)rows) return;   // behind the last sequence: left as it is
+  // written by the attention already (and nothing to merge if it failed there)
+  if (whole && a.s.prefix_len == 0 && a.status[c0[1]] == 0) return;
   const int total = n[0] + n[1];
   float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
@@ -848,7 +873,7 @@ __global__ void __launch_bounds__(kMergeThreads, 8) step_merge_kernel(const __gr
   if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
   else *reinterpret_cast<uint32_t*>(dst) = y[0];
   if (a.lse && lane == 0)
-    a.lse[item] = bad ? inv : (l == 0.f ? -INFINITY : 0.69314718055994531f * (m + log2f(l)));
+    a.lse[item] = bad ? inv : log_sum(m, l);
 }
 
 template <int D, bool BF16>

@@ -74,7 +74,7 @@ def check(rows, kv, n_cta=152, **kw):
         start[key] = pos
         weight[key] = 4 if tokens > 128 // G else 3
         pos += ends(tokens * G) + weight[key] * blocks
-    C = min(n_cta, -(-pos // 3))
+    C = min(n_cta, -(-pos // 6))
     q, more = divmod(pos, C) if C else (0, 0)
     share = [(c * q + min(c, more), (c + 1) * q + min(c + 1, more)) for c in range(C)]
     got, ctas = {}, {}
