@@ -91,8 +91,11 @@ struct StepAttnArgs {
   float* lse;
   // workspace
   int* status;         // [n_cta]
+  int by_cta;          // the merge goes by CTA (split), else by row (meta)
   int4* meta;          // [2][n_rows][Hkv]: segment's first and last CTA, row's token within its tiles,
                        // whether the row's result is written
+  int4* split;         // [n_cta]: first row, tokens, kv head and last CTA of the item that
+                       // begins in a CTA and goes on in others (no tokens: none)
   float* seg_o[2];     // [n_rows][Hq][d]: a segment's first fragment (prefix, own), unnormalised
   float2* seg_ml[2];   // [n_rows][Hq]: its (max, sum)
   float* cta_o;        // [n_cta][256][d]: the fragment a CTA continues

@@ -531,6 +531,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
     const int tok = r / a.G, head = r - tok * a.G;
     bool ok = true;
     uint32_t np = 0, nb = 0;
+    int4 split = make_int4(0, 0, 0, 0);              // the item that goes on in another CTA, if any
     auto both = [&]() { asm volatile("barrier.sync %0, %1;" ::"r"(kBarPair), "r"(kSoftThreads) : "memory"); };
     Frag f;
     while (take(f)) {
@@ -677,7 +678,9 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       }
       float m0 = m, l0 = l, w0 = 1.f, w1 = 0.f;      // this stream's part, or the merge of both
       if (!pair) sh.ml[st][r] = make_float2(m, l);
+      if (!ok) sh.abort = 1;
       both();
+      if (*abort) ok = false;
       if (!pair) {
         const float2 e0 = sh.ml[0][r], e1 = sh.ml[1][r];
         m0 = fmaxf(e0.x, e1.x);
@@ -690,7 +693,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       }
       // a row whose every key was here needs no merge: its result as it stands
       const bool whole = f.first && f.last_cta == (int)blockIdx.x && a.s.prefix_len == 0;
-      const float inv = l0 == 0.f ? 0.f : 1.f / l0;
+      const float inv = !ok ? __int_as_float(0x7fc00000) : (l0 == 0.f ? 0.f : 1.f / l0);
       const bool empty = pair ? cnt == 0 : n == 0;
       const bool poisoned = sh.any_bad;
       // a pair's streams write their own rows; of a single item each writes
@@ -701,7 +704,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
           float o[32];
           if (empty || !ok) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;   // (times inv)
           } else {
             const uint32_t oa = tmem + lanes + kColO + c;
             tmem_ld32_async(oa + (pair ? 128u * st : 0u), o);
@@ -741,10 +744,11 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       }
       if (live && (pair || st == 0)) {
         if (!whole) *pml = make_float2(m0, l0);
-        else if (a.lse) a.lse[row * a.Hq + f.h * a.G + head] = log_sum(m0, l0);
-        if (f.first && head == 0)
+        else if (a.lse) a.lse[row * a.Hq + f.h * a.G + head] = ok ? log_sum(m0, l0) : inv;
+        if (f.first && head == 0 && !a.by_cta)
           a.meta[((long)f.seg * a.s.n_rows + row) * a.Hkv + f.h] = make_int4(blockIdx.x, f.last_cta, t, whole);
       }
+      if (tid == 0 && f.first && !whole) split = make_int4(f.tok0, f.ntok, f.h, f.last_cta);
       tc_fence_before();
       both();                                        // both streams have read O, and the notes on bad values
       if (poisoned) {
@@ -754,6 +758,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       }
       tc_fence_after();
     }
+    if (tid == 0 && a.by_cta) a.split[blockIdx.x] = split;
     if (!ok) sh.abort = 1;
   }
   __syncwarp();
@@ -768,57 +773,47 @@ __global__ void __launch_bounds__(kStepThreads, 1)
 }
 
 // ---------------------------------------------------------------- merge
-// One warp per (row, head): o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i
-// over the row's fragments, one per segment and CTA that worked on it.  Few
-// bytes, so latency bounds it: what does not depend on an earlier load is
-// loaded at once, partial rows kAhead at a time.
-constexpr int kMergeThreads = 128, kAhead = 4;
+// o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i over a row's fragments, one
+// per segment and CTA that worked on it; a warp per (row, head).  Few bytes,
+// so latency bounds it: what does not depend on an earlier load is loaded at
+// once, partial rows kAhead at a time (32 verifying sequences, 5 fragments a
+// row: 13 us of 115).
+constexpr int kMergeThreads = 128, kMergeWarps = kMergeThreads / 32, kAhead = 4;
+constexpr int kSplitBlocks = 16;   // blocks for the rows of a CTA's last item
+
+// A segment's fragments of one row: CTAs first .. first + n - 1, of which the
+// first left its part in the row's own place and the others in tile row `trow`
+// of theirs.
+struct Parts {
+  int first, n, trow;
+  float2 ml;   // the first one's max and sum
+};
+// place of (token t of an item, head of its kv head) among a CTA's 256 tile
+// rows: those of a pair's second tile lie behind the first's 128
+__device__ __forceinline__ int tile_row(const StepAttnArgs& a, int t, int head) {
+  return (t < a.tpt ? t * a.G : 128 + (t - a.tpt) * a.G) + head;
+}
 
 template <int D, typename Out>
-__global__ void __launch_bounds__(kMergeThreads, 8) step_merge_kernel(const __grid_constant__ StepAttnArgs a) {
+__device__ __forceinline__ void merge_row(const StepAttnArgs& a, long row, int head, const Parts& pre, const Parts& own,
+                                          int lane) {
   constexpr int kPer = D / 32;   // elements of a lane
-  pdl_wait();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const unsigned item = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);   // at most 2^31
-  const unsigned row = item / (unsigned)a.Hq;
-  if (row >= (unsigned)a.s.n_rows) return;
-  const int head = (int)(item - row * a.Hq), h = head / a.G;
-  const int rows = a.s.start(a.s.n_seq);
-  // per segment: first CTA, fragments, the row's place in a continued tile pair
-  int c0[2] = {0, 0}, n[2] = {0, 0}, trow[2] = {0, 0};
-  float2 firsts[2];
-  bool whole = false;
-#pragma unroll
-  for (int seg = 0; seg < 2; ++seg)
-    if (seg == 1 || a.s.prefix_len > 0) {
-      const int4 meta = a.meta[((long)seg * a.s.n_rows + row) * a.Hkv + h];
-      firsts[seg] = a.seg_ml[seg][item];
-      c0[seg] = min(max(meta.x, 0), a.n_cta - 1);
-      n[seg] = min(max(meta.y, c0[seg]), a.n_cta - 1) - c0[seg] + 1;
-      const int in_tile = min(max(meta.z, 0), 2 * a.tpt - 1);
-      // rows of a pair's second tile lie behind the first's 128
-      trow[seg] = (in_tile < a.tpt ? in_tile * a.G : 128 + (in_tile - a.tpt) * a.G) + head - h * a.G;
-      whole = meta.w != 0;
-    }
-  if (row >= (unsigned)rows) return;   // behind the last sequence: left as it is
-  // written by the attention already (and nothing to merge if it failed there)
-  if (whole && a.s.prefix_len == 0 && a.status[c0[1]] == 0) return;
-  const int total = n[0] + n[1];
+  const long item = row * a.Hq + head;
+  const int total = pre.n + own.n;
   float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) o[i] = 0.f;
   bool bad = false;
   for (int i0 = 0; i0 < total; i0 += 32) {
     // lane i: fragment i's max, sum and partial row
-    const int i = i0 + lane, seg = i >= n[0], k = i - (seg ? n[0] : 0);
+    const int i = i0 + lane, seg = i >= pre.n, k = i - (seg ? pre.n : 0);
     float2 ml = make_float2(-INFINITY, 0.f);
     const float* src = nullptr;
     if (i < total) {
-      const int cta = (seg ? c0[1] : c0[0]) + k;
-      const long at = (long)cta * 256 + (seg ? trow[1] : trow[0]);
-      ml = k == 0 ? (seg ? firsts[1] : firsts[0]) : a.cta_ml[at];
-      src = k == 0 ? (seg ? a.seg_o[1] : a.seg_o[0]) + (long)item * D : a.cta_o + at * D;
+      const int cta = (seg ? own.first : pre.first) + k;
+      const long at = (long)cta * 256 + (seg ? own.trow : pre.trow);
+      ml = k == 0 ? (seg ? own.ml : pre.ml) : a.cta_ml[at];
+      src = k == 0 ? (seg ? a.seg_o[1] : a.seg_o[0]) + item * D : a.cta_o + at * D;
       bad |= a.status[cta] != 0;
     }
     float mx = ml.x;
@@ -865,7 +860,7 @@ __global__ void __launch_bounds__(kMergeThreads, 8) step_merge_kernel(const __gr
   }
   bad = __any_sync(0xffffffffu, bad);
   const float inv = bad ? __int_as_float(0x7fc00000) : (l == 0.f ? 0.f : 1.f / l);
-  Out* dst = static_cast<Out*>(a.out) + (long)row * a.out_stride + (long)head * D + lane * kPer;
+  Out* dst = static_cast<Out*>(a.out) + row * a.out_stride + (long)head * D + lane * kPer;
   uint32_t y[kPer / 2];
 #pragma unroll
   for (int v = 0; v < kPer; v += 2)
@@ -874,6 +869,46 @@ __global__ void __launch_bounds__(kMergeThreads, 8) step_merge_kernel(const __gr
   else *reinterpret_cast<uint32_t*>(dst) = y[0];
   if (a.lse && lane == 0)
     a.lse[item] = bad ? inv : log_sum(m, l);
+}
+
+template <int D, typename Out>
+__global__ void __launch_bounds__(kMergeThreads, 8) step_merge_kernel(const __grid_constant__ StepAttnArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Parts none{0, 0, 0, {-INFINITY, 0.f}};
+  if (a.by_cta) {
+    // only rows of an item that goes on in another CTA: at most one a CTA
+    const int cta = blockIdx.x / kSplitBlocks, part = blockIdx.x % kSplitBlocks;
+    const int4 s = a.split[cta];   // its first row, tokens, kv head and last CTA
+    for (int r = part * kMergeWarps + warp; r < s.y * a.G; r += kSplitBlocks * kMergeWarps) {
+      const int t = r / a.G, sub = r - t * a.G, head = s.z * a.G + sub;
+      const long row = s.x + t;
+      const Parts own{cta, s.w - cta + 1, tile_row(a, t, sub), a.seg_ml[1][row * a.Hq + head]};
+      merge_row<D, Out>(a, row, head, none, own, lane);
+    }
+    return;
+  }
+  const unsigned item = blockIdx.x * kMergeWarps + warp;   // at most 2^31
+  const unsigned row = item / (unsigned)a.Hq;
+  if (row >= (unsigned)a.s.n_rows) return;
+  const int head = (int)(item - row * a.Hq), h = head / a.G;
+  const int rows = a.s.start(a.s.n_seq);
+  Parts p[2] = {none, none};
+  bool whole = false;
+#pragma unroll
+  for (int seg = 0; seg < 2; ++seg)
+    if (seg == 1 || a.s.prefix_len > 0) {
+      const int4 meta = a.meta[((long)seg * a.s.n_rows + row) * a.Hkv + h];
+      p[seg].ml = a.seg_ml[seg][item];
+      p[seg].first = min(max(meta.x, 0), a.n_cta - 1);
+      p[seg].n = min(max(meta.y, p[seg].first), a.n_cta - 1) - p[seg].first + 1;
+      p[seg].trow = tile_row(a, min(max(meta.z, 0), 2 * a.tpt - 1), head - h * a.G);
+      whole = meta.w != 0;
+    }
+  if (whole && a.s.prefix_len == 0) return;   // written already
+  if (row >= (unsigned)rows) return;   // behind the last sequence: left as it is
+  merge_row<D, Out>(a, row, head, p[0], p[1], lane);
 }
 
 template <int D, bool BF16>
@@ -893,8 +928,9 @@ cudaError_t launch(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMa
   }
   e = launch_pdl(attn, dim3(a.n_cta), dim3(kStepThreads), smem, s, q, k, v, a);
   if (e != cudaSuccess) return e;
-  const long warps = (long)a.s.n_rows * a.Hq;
-  const long ctas = (warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
+  // a warp for every (row, head), or sixteen blocks for every CTA's last item
+  const long ctas = a.by_cta ? (long)a.n_cta * kSplitBlocks
+                             : ((long)a.s.n_rows * a.Hq + kMergeWarps - 1) / kMergeWarps;
   auto* merge = step_merge_kernel<D, std::conditional_t<BF16, __nv_bfloat16, __half>>;
   return launch_pdl(merge, dim3((unsigned)ctas), dim3(kMergeThreads), 0, s, a);
 }
