@@ -466,7 +466,8 @@ typedef struct dflash_append_args {
  * each rounded once.  Row pointers start on 16-byte boundaries (bases and
  * strides).  Rows of the caches that no row of the step names stay as they
  * are; a row whose own index would be negative, or past the block table,
- * writes no key or value (its query is written).  One launch. */
+ * writes no key or value (its query is written).  Pages that rows go to belong
+ * to one sequence each.  One launch. */
 int dflash_step_append(const dflash_paged_cache *cache, const dflash_step *step, const dflash_append_args *args,
                        void *stream);
 
@@ -492,11 +493,12 @@ typedef struct dflash_attention_args {
  * the batch's rows together: once per 256 of a kv head's query rows, not once
  * per sequence.  A row without keys gives zeros and lse -inf.  What the cache
  * holds past a sequence's or the prefix's last key has no effect, whatever
- * it is.  A value element of the step's own rows that is not finite makes
- * that element NaN in every row that sees it, and only there; keys and
- * values before the step's rows are finite or spread to the whole sequence
- * (the prefix's to the batch).  Scores and sums are f32; softmax weights are
- * rounded to the cache's type for the product with V.  Two launches. */
+ * it is.  A value element of the step's own rows that is not finite leaves
+ * that element not finite (NaN within a tile of rows) in every row that sees
+ * it, and only there; keys and values before the step's rows are finite or
+ * spread to the whole sequence (the prefix's to the batch).  Scores and sums
+ * are f32; softmax weights are rounded to the cache's type for the product
+ * with V.  Two launches. */
 int dflash_step_attention(const dflash_paged_cache *cache, const dflash_step *step,
                           const dflash_attention_args *args, void *workspace, size_t workspace_bytes, void *stream);
 
@@ -505,10 +507,10 @@ int dflash_step_attention(const dflash_paged_cache *cache, const dflash_step *st
  * and nothing else of them is followed.  Query rows go in items of up to
  * 2 floor(128 / G) tokens of one kv head (G query heads each), keys in blocks
  * of 128.  The prefix's items come first, then each sequence's (by head, then
- * rows).  An item costs 6 + min(rows G, 128) / 16 units for its ends and 4 (more than
- * floor(128 / G) tokens) or 3 for each block; C = min(n_cta, ceil(total / 6))
- * CTAs take equal runs of units (the first ones a unit more) and with them the
- * blocks that start there. */
+ * rows).  An item costs 6 + min(rows G, 128) / 16 units for its ends and 4
+ * (more than floor(128 / G) tokens) or 3 for each block; C = min(n_cta,
+ * ceil(total / 6)) CTAs take equal runs of units (the first ones a unit more)
+ * and with them the blocks that start there. */
 typedef struct dflash_step_piece {
   int32_t cta;
   int32_t segment;             /* 0: shared prefix, 1: own keys            */
@@ -559,7 +561,7 @@ typedef struct dflash_verify_args {
  * Probabilities need not sum to one; NaN, infinite and negative ones count
  * as zero, and a draft outside [0, vocab) is rejected.  Where nothing is left
  * of p_j - q_j the token is drawn from p_j, and without any positive p_j it
- * is 0.  Sums carry 46 bits or more and are taken in a fixed order.  One
+ * is 0.  Sums are kept in two floats (2^-44) and taken in a fixed order.  One
  * launch, no workspace; the rows need no alignment beyond their type's. */
 int dflash_verify_tokens(const dflash_verify_args *args, void *stream);
 

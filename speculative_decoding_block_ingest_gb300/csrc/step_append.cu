@@ -46,8 +46,10 @@ struct Raw {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 f;
-      if constexpr (std::is_same_v<T, __nv_bfloat16>) f = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(w[i]));
-      else f = __half22float2(reinterpret_cast<const __half2&>(w[i]));
+      if constexpr (std::is_same_v<T, __nv_bfloat16>)
+        f = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(w[i]));
+      else
+        f = __half22float2(reinterpret_cast<const __half2&>(w[i]));
       c.v[2 * i] = f.x;
       c.v[2 * i + 1] = f.y;
     }
@@ -89,7 +91,8 @@ __device__ __forceinline__ void store8(__half* p, const Chunk& c) {
 constexpr int append_ctas(int warps) { return warps == kManyWarps ? 4 : 2; }
 
 template <typename In, typename Out, int D, int WARPS>
-__global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS)) step_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
+    step_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kLanes = D / 16;               // lanes of a head row
   constexpr int kGroups = 32 / kLanes;         // head rows of a warp at once
   constexpr int kDepth = WARPS == kManyWarps && sizeof(In) == 4 ? 1 : 2;   // of those, in flight
@@ -241,7 +244,8 @@ cudaError_t launch(const AppendArgs& a, int n_sm, cudaStream_t s) {
 
 cudaError_t launch_step_append(const AppendArgs& a, int in_dtype, int out_dtype, int n_sm, cudaStream_t s) {
   if (out_dtype == DFLASH_BF16)
-    return in_dtype == DFLASH_F32 ? launch<float, __nv_bfloat16>(a, n_sm, s) : launch<__nv_bfloat16, __nv_bfloat16>(a, n_sm, s);
+    return in_dtype == DFLASH_F32 ? launch<float, __nv_bfloat16>(a, n_sm, s)
+                                  : launch<__nv_bfloat16, __nv_bfloat16>(a, n_sm, s);
   return in_dtype == DFLASH_F32 ? launch<float, __half>(a, n_sm, s) : launch<__half, __half>(a, n_sm, s);
 }
 

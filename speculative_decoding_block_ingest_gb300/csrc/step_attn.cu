@@ -54,7 +54,7 @@ constexpr int kSoftRegs = 208, kOtherRegs = 88;
 constexpr int kSoftThreads = 256;        // warps 0..7
 constexpr int kAtomBytes = kKeys * 128;  // 128 rows x 128 bytes
 constexpr int kMaxStages = 11;
-constexpr int kSharedBytes = 3072;       // control block
+constexpr int kSharedBytes = 3 * 1024;   // control block
 constexpr size_t step_smem(int d, int stages) { return (size_t)(2 + stages) * (d / 64) * kAtomBytes + kSharedBytes; }
 // as many K and V tiles as shared memory holds beside two query tiles: 5 at d = 128, 11 at 64
 constexpr int step_stages(int d) {

@@ -131,8 +131,9 @@ class PagedCache:
         key = (n_rows, n_heads)
         if key not in self._ws:
             n = ctypes.c_size_t(0)
+            lib = dflash.load_library()
             with torch.cuda.device(self.device):
-                _check(dflash.load_library().dflash_step_attention_workspace(self.ref, n_rows, n_heads, ctypes.byref(n)))
+                _check(lib.dflash_step_attention_workspace(self.ref, n_rows, n_heads, ctypes.byref(n)))
             if len(self._ws) > 64:
                 self._ws.clear()
             self._ws[key] = n.value

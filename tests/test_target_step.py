@@ -336,6 +336,23 @@ def test_operators_on_another_stream(T):
     o2, l2 = T.attention(T.PagedCache(kc, vc), step, q, stream=s)
     s.synchronize()
     assert torch.equal(o, o2) and torch.equal(lse, l2)
+    # append and verification, with tensors that go out of use before they have run
+    k, v = (torch.randn(q.shape[0], 2, 128, device=DEV).to(BF) for _ in range(2))
+    c = T.PagedCache(kc, vc)
+    want = T.append(c, step, q, k, v, rope=T.Rope(128))
+    args = [t.to(DEV) if t is not None else None for t in verify_case(4, 5, 30000, F4, False, True, seed=2)]
+    ref = T.verify_tokens(*args[:4], draft_probs=args[4], n_draft=args[5])
+    gone = [t.clone() for t in (q, k, v)]
+    gone2 = [t.clone() if t is not None else None for t in args]
+    s.wait_stream(torch.cuda.current_stream())
+    got = T.append(c, step, *gone, rope=T.Rope(128), stream=s)
+    tok = T.verify_tokens(*gone2[:4], draft_probs=gone2[4], n_draft=gone2[5], stream=s)
+    del gone, gone2
+    torch.zeros(1 << 22, device=DEV).fill_(7)      # may take over memory that was let go
+    s.synchronize()
+    assert torch.equal(tok[0], ref[0]) and torch.equal(tok[1], ref[1])
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
 
 
 # ------------------------------------------------------------------ verification
