@@ -507,19 +507,20 @@ __global__ void __launch_bounds__(kStepThreads, 1)
           base += __shfl_sync(0xffffffffu, inc, 31);
         }
       }
-      if (lane == 0) {
-        if (w.ua < w.ub) w.begin(seq0, base);
-        else w.pos = w.ub;
-        for (uint32_t i = 0, more = 1; more; ++i) {
-          Frag f;
-          more = w.next(f);
-          if (!more) f.seg = -1;
-          if (!ring_wait(&sh.fempty[i % kFrags], ((i / kFrags) & 1) ^ 1)) break;
+      if (w.ua < w.ub) w.begin(seq0, base);
+      else w.pos = w.ub;
+      bool more = true;
+      for (uint32_t i = 0; more; ++i) {
+        Frag f;
+        more = w.next(f);
+        if (!more) f.seg = -1;
+        if (!__all_sync(0xffffffffu, ring_wait(&sh.fempty[i % kFrags], ((i / kFrags) & 1) ^ 1))) break;
+        if (lane == 0) {
           sh.frag[i % kFrags] = f;
           mbar_arrive(&sh.ffull[i % kFrags]);
         }
+        __syncwarp();
       }
-      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));

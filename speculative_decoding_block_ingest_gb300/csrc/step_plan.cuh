@@ -32,7 +32,8 @@ struct Frag {
 //
 // The items in order: the prefix's by kv head and tile pair, then every
 // sequence's.  An item takes end_units, then its blocks' units one block after
-// the other; a CTA runs the blocks that start in its share.
+// the other; a CTA runs the blocks that start in its share.  On the device a
+// converged warp walks (it skips sequences without rows 32 at a time).
 struct Walk {
   const StepAttnArgs& a;
   int pair_tok;        // tokens of two tiles
@@ -42,6 +43,7 @@ struct Walk {
   int n_cta, share, more;   // CTAs that have units, a CTA's at least, and how many have one more
   int pos;             // first unit of the item at (seg, seq, h, tile)
   int seg, seq, h, tile;
+  int row0, T, len;    // the sequence's first row, rows and keys
 
   __host__ __device__ explicit Walk(const StepAttnArgs& args) : a(args) {
     pair_tok = 2 * a.tpt;
@@ -54,9 +56,8 @@ struct Walk {
   __host__ __device__ int units(int ntok, int blocks) const { return end_units(ntok * a.G) + blocks * weight(ntok); }
   // tokens of tile pair j out of T
   __host__ __device__ int pair_tokens(int j, int T) const { return min(pair_tok, T - j * pair_tok); }
-  // key blocks that tile pair j of sequence i needs
-  __host__ __device__ int blocks(int i, int j, int T) const {
-    const int len = a.s.len(i);
+  // key blocks that tile pair j needs of a sequence with T rows and len keys
+  __host__ __device__ int blocks(int j, int T, int len) const {
     const int seen = a.causal ? len - T + min((j + 1) * pair_tok, T) : len;
     return (min(max(seen, 0), a.s.room()) + kKeys - 1) / kKeys;
   }
@@ -67,9 +68,9 @@ struct Walk {
   }
   __host__ __device__ int prefix_units() const { return a.Hkv * prefix_head(); }
   __host__ __device__ int head_units(int i) const {
-    const int T = tokens(i);
+    const int T = tokens(i), len = a.s.len(i);
     int u = 0;
-    for (int j = 0; j * pair_tok < T; ++j) u += units(pair_tokens(j, T), blocks(i, j, T));
+    for (int j = 0; j * pair_tok < T; ++j) u += units(pair_tokens(j, T), blocks(j, T, len));
     return u;
   }
   // CTA c's share of `total` units.  At most `most` CTAs, none with much less
@@ -92,6 +93,29 @@ struct Walk {
     const int big = more * (share + 1);
     return unit < big ? unit / (share + 1) : more + (unit - big) / share;
   }
+  __host__ __device__ void enter(int i) {   // sequence i, or the next one with rows
+#ifdef __CUDA_ARCH__
+    const int lane = threadIdx.x & 31;
+    for (; i < a.s.n_seq; i += 32) {
+      const unsigned some = __ballot_sync(0xffffffffu, i + lane < a.s.n_seq && tokens(i + lane) > 0);
+      if (some) {
+        i += __ffs(some) - 1;
+        break;
+      }
+    }
+#else
+    while (i < a.s.n_seq && tokens(i) == 0) ++i;
+#endif
+    seq = i;
+    h = tile = 0;
+    if (i >= a.s.n_seq) {
+      pos = ub;        // nothing left
+      return;
+    }
+    row0 = a.s.start(i);
+    T = tokens(i);
+    len = a.s.len(i);
+  }
   // Go to the item that holds unit ua; `seq0` is its sequence (-1: the
   // prefix) and `base` that sequence's first unit.
   __host__ __device__ void begin(int seq0, int base) {
@@ -101,61 +125,63 @@ struct Walk {
     }
     seg = seq0 < 0 ? 0 : 1;
     seq = seq0;
-    const int per_head = seg ? head_units(seq) : prefix_head();
-    h = per_head ? (ua - base) / per_head : 0;
-    pos = base + h * per_head;
     tile = 0;
-    if (!seg) {   // every pair but the last is full
-      const int full = units(pair_tok, pre_blocks);
-      tile = min((ua - pos) / full, pre_tiles - 1);
+    if (!seg) {
+      const int per_head = prefix_head(), full = units(pair_tok, pre_blocks);
+      h = ua / per_head;
+      pos = h * per_head;
+      tile = min((ua - pos) / full, pre_tiles - 1);   // every pair but the last is full
       pos += tile * full;
-    } else {
-      const int T = tokens(seq);
-      for (; tile * pair_tok < T; ++tile) {
-        const int n = units(pair_tokens(tile, T), blocks(seq, tile, T));
-        if (pos + n > ua) break;
-        pos += n;
-      }
+      return;
+    }
+    pos = base;
+    enter(seq0);
+    if (pos >= ub) return;
+    const int per_head = head_units(seq);
+    h = min((ua - base) / per_head, a.Hkv - 1);
+    pos += h * per_head;
+    for (; (tile + 1) * pair_tok < T; ++tile) {
+      const int n = units(pair_tokens(tile, T), blocks(tile, T, len));
+      if (pos + n > ua) break;
+      pos += n;
     }
   }
   // The next fragment, or false behind the last.
   __host__ __device__ bool next(Frag& f) {
-    while (pos < ub) {
-      int n = pre_blocks, T = rows;
-      if (seg) {
-        T = tokens(seq);
-        if (tile * pair_tok >= T) {   // the next head, or sequence
-          tile = 0;
-          if (T == 0 || ++h == a.Hkv) {
-            h = 0;
-            if (++seq >= a.s.n_seq) return false;
-          }
-          continue;
-        }
-        n = blocks(seq, tile, T);
-      }
-      f.seg = seg;
-      f.seq = seq;
-      f.h = h;
-      f.tok0 = tile * pair_tok + (seg ? a.s.start(seq) : 0);
-      f.ntok = pair_tokens(tile, T);
-      f.keys = seg ? min(a.s.len(seq), a.s.room()) : a.s.prefix_len;
-      f.lim0 = seg && a.causal ? a.s.len(seq) - T + tile * pair_tok + 1 : f.keys;
-      const int w = weight(f.ntok);
-      const int first_block = pos + end_units(f.ntok * a.G), end = first_block + n * w;
-      f.b0 = min((max(ua - first_block, 0) + w - 1) / w, n);
-      f.b1 = min((max(ub - first_block, 0) + w - 1) / w, n);
-      f.first = ua <= pos;
-      f.last_cta = cta_of(end - 1);
-      pos = end;
-      ++tile;
-      if (seg == 0 && tile == pre_tiles) {
+    if (pos >= ub) return false;
+    const int n = seg ? blocks(tile, T, len) : pre_blocks;
+    f.seg = seg;
+    f.seq = seq;
+    f.h = h;
+    f.tok0 = tile * pair_tok + (seg ? row0 : 0);
+    f.ntok = pair_tokens(tile, seg ? T : rows);
+    f.keys = seg ? min(len, a.s.room()) : a.s.prefix_len;
+    f.lim0 = seg && a.causal ? len - T + tile * pair_tok + 1 : f.keys;
+    const int w = weight(f.ntok);
+    const int first_block = pos + end_units(f.ntok * a.G), end = first_block + n * w;
+    auto block_at = [&](int unit) {   // the first block that starts at `unit` or behind
+      const int u = max(unit - first_block, 0) + w - 1;
+      return min(w == kPairUnits ? u / kPairUnits : u / kSingleUnits, n);
+    };
+    f.b0 = block_at(ua);
+    f.b1 = block_at(ub);
+    f.first = ua <= pos;
+    f.last_cta = f.first ? cta_of(end - 1) : -1;
+    pos = end;
+    ++tile;
+    if (seg == 0) {
+      if (tile == pre_tiles) {
         tile = 0;
-        if (++h == a.Hkv) seg = 1, h = 0, seq = 0;
+        if (++h == a.Hkv) {
+          seg = 1;
+          enter(0);
+        }
       }
-      return true;
+    } else if (tile * pair_tok >= T) {
+      tile = 0;
+      if (++h == a.Hkv) enter(seq + 1);
     }
-    return false;
+    return true;
   }
 };
 

@@ -326,7 +326,7 @@ int dflash_step_attention_plan(const dflash_paged_cache* cache, const dflash_ste
     w.begin(seq0, base);
     for (Frag f; w.next(f); ++n)
       if (n < max_pieces)
-        pieces[n] = {c, f.seg, f.seg ? f.seq : -1, f.h, f.tok0, f.ntok, f.b0, f.b1, f.first, f.first ? f.last_cta : -1};
+        pieces[n] = {c, f.seg, f.seg ? f.seq : -1, f.h, f.tok0, f.ntok, f.b0, f.b1, f.first, f.last_cta};
   }
   *n_pieces = n;
   return n > max_pieces ? fail(DFLASH_ERR_CAPACITY, "%d pieces, room for %d", n, max_pieces) : DFLASH_OK;

@@ -220,10 +220,13 @@ def test_attention_random_steps(T):
     ([1, 3], [41000, 20001], 8, 8, 64, 128, HF, True, 1000, True),
     ([90, 1, 2], [9000, 15000, 11000], 32, 4, 128, 64, BF, True, 3000, False),
     ([1] * 300, [5 + i % 380 for i in range(300)], 4, 4, 128, 16, BF, True, 0, False),
+    # a batch of many places, most of them without rows
+    ([2 if i % 97 == 5 else 0 for i in range(4096)], [300 if i % 97 == 5 else i % 3 for i in range(4096)], 8, 2, 64,
+     16, BF, True, 200, False),
     # many more rows than the CTAs' last items have: merged by CTA
     ([1500, 3, 900, 0, 1], [1500, 2000, 950, 10, 1], 32, 4, 64, 64, HF, True, 0, False),
     ([1400, 700], [1400, 900], 24, 2, 128, 16, BF, False, 0, True),
-], ids=["single", "single-d64", "pair-and-single", "many-short", "prompts", "prompts-not-causal"])
+], ids=["single", "single-d64", "pair-and-single", "many-short", "many-empty", "prompts", "prompts-not-causal"])
 def test_attention_long(T, case):
     rows, _, hq, hkv, d, page, dt, causal, prefix, hnd = case
     (starts, kv, table, pre, kc, vc, q, _), o, lse = attend_case(T, case, seed=40)
