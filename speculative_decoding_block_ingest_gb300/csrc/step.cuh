@@ -74,7 +74,7 @@ struct VerifyArgs {
   int* tokens;
   int* n_accepted;
 };
-cudaError_t launch_verify(const VerifyArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_verify(const VerifyArgs& a, int dtype, int n_sm, cudaStream_t s);
 
 // Attention of a step (step_attn.cu; how it is cut into pieces: step_plan.cuh).
 constexpr int kStepStatusWords = 1024;   // most CTAs (one status word each)

@@ -366,7 +366,9 @@ int dflash_verify_tokens(const dflash_verify_args* p, void* stream) {
   a.u_token = p->u_token;
   a.tokens = p->tokens;
   a.n_accepted = p->n_accepted;
-  return launched(launch_verify(a, p->dtype, static_cast<cudaStream_t>(stream)), "verify tokens");
+  int n_sm = 0;
+  if (int rc = sm_count(&n_sm)) return rc;
+  return launched(launch_verify(a, p->dtype, n_sm, static_cast<cudaStream_t>(stream)), "verify tokens");
 }
 
 }  // extern "C"

@@ -8,13 +8,13 @@
 // the accepted drafts is read: 4 (V + V) bytes a sequence bound it, and for
 // one sequence the latency of two gathers, one sweep and a search.
 //
-// One cluster of 8 CTAs per sequence.  The row is cut into 64 runs, one per
+// One cluster of up to 8 CTAs per sequence.  The row is cut into runs, one per
 // warp of the cluster; each warp sums its run, the sums are exchanged through
 // distributed shared memory, every CTA finds the run where u * total falls,
 // and the CTA that holds it searches it (its entries are in L1 / L2).  Small
 // CTAs, four to an SM, hide one sequence's gathers and search behind another's
 // sweep: 256 sequences x 262144 f32 in 91 us (5.9 TB/s) against 103 with CTAs of
-// 512 threads, two to an SM, and 98 without clusters.
+// 512 threads, two to an SM.
 //
 // A cumulative sum is compared with a number, and a vocabulary has 10^5
 // boundaries, so f32 sums (2^-24) would move one draw in a few hundred to a
@@ -38,8 +38,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kVerifyThreads = 256;   // four CTAs to an SM
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kCluster = 8;           // the portable limit
-constexpr int kRuns = kCluster * kVerifyWarps;
+constexpr int kMaxCluster = 8;        // the portable limit
+constexpr int kMaxRuns = kMaxCluster * kVerifyWarps;
 
 __device__ __forceinline__ float as_f32(float x) { return x; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -197,45 +197,87 @@ struct Pack {
   }
 };
 
+// The 16 bytes that start `shift` bytes into lo (a multiple of the type's size).
+template <typename T>
+__device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi, int shift) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
+  if (sizeof(T) == 2 && (shift & 2))
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Adds entries i, i + 1, ... in steps of 32 lanes x DEPTH x 16 bytes while they
+// end at or before b; p + i is aligned, and q + i `shift` bytes behind a
+// 16-byte boundary (entries next to the step, inside the run, are read too).
+template <typename T, bool DIFF, bool SHIFT, int DEPTH>
+__device__ __forceinline__ void add_steps(Sum2 (&s)[2], const Row<T>& r, int& i, int b, int lane, int shift) {
+  constexpr int kVec = Pack<T>::kEntries, kStep = 32 * kVec * DEPTH;
+  for (; i + kStep + (SHIFT ? kVec : 0) <= b; i += kStep) {
+    Pack<T> p[DEPTH], q[DEPTH];
+    uint4 next[DEPTH];
+#pragma unroll
+    for (int u = 0; u < DEPTH; ++u) {
+      const int at = i + (u * 32 + lane) * kVec;
+      p[u].load(r.p + at);
+      if (DIFF) {
+        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(r.q + at) - shift);
+        q[u].u = src[0];
+        if (SHIFT) next[u] = src[1];
+      }
+    }
+    if (!DIFF && r.skip >= i && r.skip < i + kStep)
+#pragma unroll
+      for (int u = 0; u < DEPTH; ++u) p[u].clear(r.skip - (i + (u * 32 + lane) * kVec));
+#pragma unroll
+    for (int u = 0; u < DEPTH; ++u) {
+      if (DIFF && SHIFT) q[u].u = shifted<T>(q[u].u, next[u], shift);
+#pragma unroll
+      for (int v = 0; v < kVec / 2; ++v)
+        add_pair<DIFF>(s[v & 1], p[u].pair(v), DIFF ? q[u].pair(v) : make_float2(0.f, 0.f));
+    }
+  }
+}
+
 // Sum of entries [a, b) over the warp's lanes (every lane gets it).
 template <typename T, bool DIFF>
 __device__ __forceinline__ Sum run_total(const Row<T>& r, int a, int b, int lane) {
-  constexpr int kVec = Pack<T>::kEntries, kDepth = 4, kScalar = 8;
+  constexpr int kVec = Pack<T>::kEntries, kScalar = 4;
   Sum2 s[2];
   const T zero = T(0.f);
-  int i = a;
-  if (((reinterpret_cast<uintptr_t>(r.p + a) | (DIFF ? reinterpret_cast<uintptr_t>(r.q + a) : 0)) & 15) == 0) {
-    for (; i + 32 * kVec * kDepth <= b; i += 32 * kVec * kDepth) {
-      Pack<T> p[kDepth], q[kDepth];
+  auto add_entries = [&](int i, int end) {   // one by one
+    for (; i < end; i += 32 * kScalar) {
+      T p[kScalar], q[kScalar];
 #pragma unroll
-      for (int u = 0; u < kDepth; ++u) {
-        const int at = i + (u * 32 + lane) * kVec;
-        p[u].load(r.p + at);
-        if (DIFF) q[u].load(r.q + at);
+      for (int u = 0; u < kScalar; ++u) {
+        const int at = i + u * 32 + lane;
+        p[u] = at < end && at != r.skip ? r.p[at] : zero;
+        q[u] = DIFF && at < end ? r.q[at] : zero;
       }
-      if (!DIFF && r.skip >= i && r.skip < i + 32 * kVec * kDepth)
 #pragma unroll
-        for (int u = 0; u < kDepth; ++u) p[u].clear(r.skip - (i + (u * 32 + lane) * kVec));
-#pragma unroll
-      for (int u = 0; u < kDepth; ++u)
-#pragma unroll
-        for (int v = 0; v < kVec / 2; ++v)
-          add_pair<DIFF>(s[v & 1], p[u].pair(v), DIFF ? q[u].pair(v) : make_float2(0.f, 0.f));
+      for (int u = 0; u < kScalar; u += 2)
+        add_pair<DIFF>(s[u / 2 & 1], make_float2(as_f32(p[u]), as_f32(p[u + 1])),
+                       make_float2(as_f32(q[u]), as_f32(q[u + 1])));
     }
+  };
+  // from the first aligned entry of p; rows of p and q are seldom aligned
+  // alike, so q's are put together from two aligned loads
+  int i = a + (int)((16 - (reinterpret_cast<uintptr_t>(r.p + a) & 15)) & 15) / (int)sizeof(T);
+  const int shift = DIFF ? (int)(reinterpret_cast<uintptr_t>(r.q + i) & 15) : 0;
+  if (i - shift / (int)sizeof(T) < a) i += kVec;
+  i = min(i, b);
+  add_entries(a, i);
+  if (DIFF && shift) {
+    add_steps<T, DIFF, DIFF, 2>(s, r, i, b, lane, shift);
+  } else {
+    add_steps<T, DIFF, false, 4>(s, r, i, b, lane, 0);
+    add_steps<T, DIFF, false, 1>(s, r, i, b, lane, 0);
   }
-  for (; i < b; i += 32 * kScalar) {
-    T p[kScalar], q[kScalar];
-#pragma unroll
-    for (int u = 0; u < kScalar; ++u) {
-      const int at = i + u * 32 + lane;
-      p[u] = at < b && at != r.skip ? r.p[at] : zero;
-      q[u] = DIFF && at < b ? r.q[at] : zero;
-    }
-#pragma unroll
-    for (int u = 0; u < kScalar; u += 2)
-      add_pair<DIFF>(s[u / 2 & 1], make_float2(as_f32(p[u]), as_f32(p[u + 1])),
-                     make_float2(as_f32(q[u]), as_f32(q[u + 1])));
-  }
+  add_entries(i, b);
   Sum t[4];
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
@@ -246,8 +288,8 @@ __device__ __forceinline__ Sum run_total(const Row<T>& r, int a, int b, int lane
   Sum c = (t[0] + t[1]) + (t[2] + t[3]);
   if (__any_sync(0xffffffffu, !(c.hi < INFINITY))) {
     c = Sum{};
-    for (i = a + lane; i < b; i += 32)
-      if (i != r.skip) add_weight(c, DIFF, as_f32(r.p[i]), DIFF ? as_f32(r.q[i]) : 0.f);
+    for (int k = a + lane; k < b; k += 32)
+      if (k != r.skip) add_weight(c, DIFF, as_f32(r.p[k]), DIFF ? as_f32(r.q[k]) : 0.f);
     c = c.normal();
   }
 #pragma unroll
@@ -257,12 +299,13 @@ __device__ __forceinline__ Sum run_total(const Row<T>& r, int a, int b, int lane
 
 template <typename T>
 __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_constant__ VerifyArgs a) {
-  __shared__ Sum run_sum[kRuns];       // every run's sum, written by the whole cluster
+  __shared__ Sum run_sum[kMaxRuns];       // every run's sum, written by the whole cluster
   __shared__ Sum warp_sum[kVerifyWarps];
   __shared__ Sum sh_base, sh_th;
   __shared__ int sh_acc, sh_run, sh_token;
   cg::cluster_group cl = cg::this_cluster();
-  const int rank = (int)cl.block_rank(), seq = blockIdx.x / kCluster;
+  const int rank = (int)cl.block_rank(), ctas = (int)cl.num_blocks(), seq = blockIdx.x / ctas;
+  const int runs = ctas * kVerifyWarps;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_launch_dependents();
@@ -299,7 +342,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
   const float u = u0 > 0.f ? fminf(u0, 1.f) : 0.f;
   const int V = a.vocab;
   // runs start on multiples of 16 entries
-  const int len = ((V + kRuns - 1) / kRuns + 15) & ~15;
+  const int len = ((V + runs - 1) / runs + 15) & ~15;
   Row<T> r{P + acc * a.p_row, nullptr, -1};
   if (acc < nd) {
     if (Q) r.q = Q + acc * a.q_row;
@@ -310,23 +353,25 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
     const int lo = min(my * len, V), hi = min((my + 1) * len, V);
     const Sum t = r.q ? run_total<T, true>(r, lo, hi, lane) : run_total<T, false>(r, lo, hi, lane);
     cl.sync();   // every CTA runs, and has read the sums of a first try
-    if (lane < kCluster) *cl.map_shared_rank(&run_sum[my], lane) = t;
+    if (lane < ctas) *cl.map_shared_rank(&run_sum[my], lane) = t;
     cl.sync();
     if (warp == 0) {   // where u * total falls among the runs: a few neighbours per lane
-      constexpr int kPer = kRuns / 32;
+      constexpr int kPer = kMaxRuns / 32;
       Sum v[kPer], c;
       int last = -1;   // last run with weight
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int k = lane * kPer + i;
-        c = c + run_sum[k];
-        if (run_sum[k].hi > 0.f) last = k;
+        if (k < runs) {
+          c = c + run_sum[k];
+          if (run_sum[k].hi > 0.f) last = k;
+        }
         v[i] = c;
       }
       Sum before;
       const Sum inc = scan(c, lane, before);
       const Sum th = shfl(inc, 31) * u;
-      int run = kRuns;   // first run past th
+      int run = kMaxRuns;   // first run past th
       Sum base;
 #pragma unroll
       for (int i = kPer - 1; i >= 0; --i)
@@ -334,7 +379,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
           run = lane * kPer + i;
           base = i ? before + v[i - 1] : before;
         }
-      const unsigned hit = __ballot_sync(0xffffffffu, run < kRuns);
+      const unsigned hit = __ballot_sync(0xffffffffu, run < kMaxRuns);
       const int src = hit ? __ffs(hit) - 1 : 0;
       run = __shfl_sync(0xffffffffu, run, src);
       base = shfl(base, src);
@@ -418,14 +463,22 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
 }
 
 template <typename T>
-cudaError_t launch(const VerifyArgs& a, cudaStream_t s) {
+cudaError_t launch(const VerifyArgs& a, int n_sm, cudaStream_t s) {
+  // CTAs of a sequence: enough for 16384 entries each (f32, 250 x 30001: 2 CTAs
+  // 15.5 us, 8 27.9; 172 x 59277: 4 22.0, 8 26.3, 2 24.6; 256 x 262144: 8 91, 4
+  // 94, 2 107), more while the SMs have room for them (one greedy 32768: 8 CTAs
+  // 5.8 us, 2 7.8).
+  unsigned ctas = 1;
+  while (ctas < kMaxCluster && (a.vocab > 16384 * (int)ctas ||
+                                (2L * a.n_seq * ctas <= 4L * n_sm && a.vocab > 2048 * (int)ctas)))
+    ctas *= 2;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.n_seq * kCluster);
+  cfg.gridDim = dim3(a.n_seq * ctas);
   cfg.blockDim = dim3(kVerifyThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {kCluster, 1, 1};
+  attr[0].val.clusterDim = {ctas, 1, 1};
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
@@ -435,10 +488,10 @@ cudaError_t launch(const VerifyArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_verify(const VerifyArgs& a, int dtype, cudaStream_t s) {
-  if (dtype == DFLASH_F32) return launch<float>(a, s);
-  if (dtype == DFLASH_BF16) return launch<__nv_bfloat16>(a, s);
-  return launch<__half>(a, s);
+cudaError_t launch_verify(const VerifyArgs& a, int dtype, int n_sm, cudaStream_t s) {
+  if (dtype == DFLASH_F32) return launch<float>(a, n_sm, s);
+  if (dtype == DFLASH_BF16) return launch<__nv_bfloat16>(a, n_sm, s);
+  return launch<__half>(a, n_sm, s);
 }
 
 }  // namespace dfl

@@ -385,6 +385,8 @@ def run_verify(T, draft, tp, ua, ut, dp=None, nd=None):
     (5, 4, 50001, BF, False, False), (4, 3, 65536, HF, False, True), (2, 40, 517, F4, True, True),
     (9, 1, 1, F4, True, False), (6, 2, 17, F4, False, False), (8, 0, 4099, F4, True, False),
     (2, 1, 262144, BF, True, False), (2, 2, 300001, F4, False, False),
+    (3, 2, 70013, F4, False, False), (3, 2, 70014, F4, False, True), (5, 3, 40007, HF, False, False),
+    (4, 2, 90010, BF, False, False), (300, 2, 3001, F4, False, True), (160, 1, 20011, BF, False, False),
 ])
 def test_verify(T, n, k, V, dt, greedy, ragged):
     args = verify_case(n, k, V, dt, greedy, ragged, seed=n * 1000 + k)
