@@ -507,10 +507,11 @@ int dflash_step_attention(const dflash_paged_cache *cache, const dflash_step *st
  * and nothing else of them is followed.  Query rows go in items of up to
  * 2 floor(128 / G) tokens of one kv head (G query heads each), keys in blocks
  * of 128.  The prefix's items come first, then each sequence's (by head, then
- * rows).  An item costs 6 + min(rows G, 128) / 16 units for its ends and 4
- * (more than floor(128 / G) tokens) or 3 for each block; C = min(n_cta,
- * ceil(total / 6)) CTAs take equal runs of units (the first ones a unit more)
- * and with them the blocks that start there. */
+ * rows).  An item costs 4 units (more than floor(128 / G) tokens) or 3 for each
+ * block, then 6 + min(rows G, 128) / 16 for its ends; C = min(n_cta,
+ * max(floor(total / 6), 1)) CTAs take equal runs of units (the first ones a
+ * unit more) and with them the blocks that start there, the first also the
+ * rows of an item without a block. */
 typedef struct dflash_step_piece {
   int32_t cta;
   int32_t segment;             /* 0: shared prefix, 1: own keys            */

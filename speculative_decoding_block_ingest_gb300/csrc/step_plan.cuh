@@ -24,16 +24,18 @@ struct Frag {
   int lim0;            // own, causal: keys that token tok0 sees (may be <= 0)
   int b0, b1;
   int first;           // holds the item's first unit
-  int last_cta;        // and then: the CTA of the item's last unit
+  int last_cta;        // and then: the CTA of the item's last block
 };
 
 // All counts of units are 32-bit (the host refuses more work than that): 64-bit
 // divisions cost 2 us of a 13 us call here.
 //
 // The items in order: the prefix's by kv head and tile pair, then every
-// sequence's.  An item takes end_units, then its blocks' units one block after
-// the other; a CTA runs the blocks that start in its share.  On the device a
-// converged warp walks (it skips sequences without rows 32 at a time).
+// sequence's.  An item takes its blocks' units one block after the other, then
+// end_units; a CTA runs the blocks that start in its share.  A share holds more
+// than a block, so the CTAs of an item are consecutive, and an item of one block
+// is whole (with the ends in front, 48 such items were 96 pieces).  On the device
+// a converged warp walks (it skips sequences without rows 32 at a time).
 struct Walk {
   const StepAttnArgs& a;
   int pair_tok;        // tokens of two tiles
@@ -75,11 +77,9 @@ struct Walk {
   }
   // CTA c's share of `total` units.  At most `most` CTAs, none with much less
   // than a block of one tile for both its streams (one token behind 4001 keys:
-  // 14.6 us, 17.7 with half of that, 15.5 with 16 units).  Every CTA in use has
-  // units, so the CTAs of an item are consecutive; one may find no block that
-  // starts in its share of it.
+  // 14.6 us, 17.7 with half of that, 15.5 with 16 units).
   __host__ __device__ void divide(int total, int most, int c) {
-    n_cta = min(most, (total + 2 * kSingleUnits - 1) / (2 * kSingleUnits));
+    n_cta = min(most, total > 0 ? max(total / (2 * kSingleUnits), 1) : 0);
     ua = ub = 0;
     if (n_cta <= 0) return;
     share = total / n_cta;
@@ -148,40 +148,42 @@ struct Walk {
   }
   // The next fragment, or false behind the last.
   __host__ __device__ bool next(Frag& f) {
-    if (pos >= ub) return false;
-    const int n = seg ? blocks(tile, T, len) : pre_blocks;
-    f.seg = seg;
-    f.seq = seq;
-    f.h = h;
-    f.tok0 = tile * pair_tok + (seg ? row0 : 0);
-    f.ntok = pair_tokens(tile, seg ? T : rows);
-    f.keys = seg ? min(len, a.s.room()) : a.s.prefix_len;
-    f.lim0 = seg && a.causal ? len - T + tile * pair_tok + 1 : f.keys;
-    const int w = weight(f.ntok);
-    const int first_block = pos + end_units(f.ntok * a.G), end = first_block + n * w;
-    auto block_at = [&](int unit) {   // the first block that starts at `unit` or behind
-      const int u = max(unit - first_block, 0) + w - 1;
-      return min(w == kPairUnits ? u / kPairUnits : u / kSingleUnits, n);
-    };
-    f.b0 = block_at(ua);
-    f.b1 = block_at(ub);
-    f.first = ua <= pos;
-    f.last_cta = f.first ? cta_of(end - 1) : -1;
-    pos = end;
-    ++tile;
-    if (seg == 0) {
-      if (tile == pre_tiles) {
-        tile = 0;
-        if (++h == a.Hkv) {
-          seg = 1;
-          enter(0);
+    for (;;) {
+      if (pos >= ub) return false;
+      const int n = seg ? blocks(tile, T, len) : pre_blocks;
+      f.seg = seg;
+      f.seq = seq;
+      f.h = h;
+      f.tok0 = tile * pair_tok + (seg ? row0 : 0);
+      f.ntok = pair_tokens(tile, seg ? T : rows);
+      f.keys = seg ? min(len, a.s.room()) : a.s.prefix_len;
+      f.lim0 = seg && a.causal ? len - T + tile * pair_tok + 1 : f.keys;
+      const int w = weight(f.ntok);
+      auto block_at = [&](int unit) {   // the first block that starts at `unit` or behind
+        const int u = max(unit - pos, 0) + w - 1;
+        return min(w == kPairUnits ? u / kPairUnits : u / kSingleUnits, n);
+      };
+      f.b0 = block_at(ua);
+      f.b1 = block_at(ub);
+      f.first = ua <= pos;
+      f.last_cta = f.first ? cta_of(pos + max(n - 1, 0) * w) : -1;
+      pos += n * w + end_units(f.ntok * a.G);
+      ++tile;
+      if (seg == 0) {
+        if (tile == pre_tiles) {
+          tile = 0;
+          if (++h == a.Hkv) {
+            seg = 1;
+            enter(0);
+          }
         }
+      } else if (tile * pair_tok >= T) {
+        tile = 0;
+        if (++h == a.Hkv) enter(seq + 1);
       }
-    } else if (tile * pair_tok >= T) {
-      tile = 0;
-      if (++h == a.Hkv) enter(seq + 1);
+      // an item without a block still has its rows written, by its first CTA
+      if (f.first || f.b0 < f.b1) return true;
     }
-    return true;
   }
 };
 

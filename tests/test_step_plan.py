@@ -69,12 +69,12 @@ def check(rows, kv, n_cta=152, **kw):
     pieces = plan(rows, kv, n_cta=n_cta, **kw)
     want = items(rows, kv, **kw)
     G = kw["hq"] // kw["hkv"]
-    start, pos, weight = {}, 0, {}
+    start, pos, weight = {}, 0, {}     # an item's blocks, then its ends
     for key, (tokens, blocks) in want.items():           # prefix first, then by sequence, head and rows
         start[key] = pos
         weight[key] = 4 if tokens > 128 // G else 3
         pos += ends(tokens * G) + weight[key] * blocks
-    C = min(n_cta, -(-pos // 6))
+    C = min(n_cta, max(pos // 6, 1)) if pos else 0
     q, more = divmod(pos, C) if C else (0, 0)
     share = [(c * q + min(c, more), (c + 1) * q + min(c + 1, more)) for c in range(C)]
     got, ctas = {}, {}
@@ -84,23 +84,24 @@ def check(rows, kv, n_cta=152, **kw):
         assert p["n_tokens"] == tokens and 0 <= p["block0"] <= p["block1"] <= blocks
         a, b = share[p["cta"]]
         assert p["first"] == (a <= start[key] < b)
-        at = start[key] + ends(tokens * G)            # the blocks that start in the CTA's share
-        starts = [i for i in range(p["block0"], p["block1"])]
-        assert all(a <= at + weight[key] * i < b for i in starts)
+        assert [i for i in range(blocks) if a <= start[key] + weight[key] * i < b] \
+            == list(range(p["block0"], p["block1"]))      # the blocks that start in the CTA's share
+        assert p["block0"] < p["block1"] or blocks == 0
         got.setdefault(key, []).append((p["block0"], p["block1"], p["first"]))
         ctas.setdefault(key, []).append((p["cta"], p["first"], p["last_cta"]))
     assert set(got) == set(want)
     for key, parts in got.items():
         at = 0
         for i, (b0, b1, first) in enumerate(parts):      # pieces come in CTA order
-            assert first == (i == 0) and (b0 == at or b0 == b1)
-            at = max(at, b1)
+            assert first == (i == 0) and b0 == at
+            at = b1
         assert at == want[key][1]
         c = [x for x, _, _ in ctas[key]]
         assert c == list(range(c[0], c[0] + len(c)))     # one CTA after the other
         assert ctas[key][0][2] == c[-1] and all(x[2] == -1 for x in ctas[key][1:])
-    # every CTA in use has a piece, and continues at most one item (its first)
-    assert sorted({p["cta"] for p in pieces}) == list(range(C))
+        assert len(parts) == 1 or want[key][1] > 1       # one block: one piece
+    # a CTA continues at most one item (its first)
+    assert {p["cta"] for p in pieces} <= set(range(C))
     for c in range(C):
         mine = [p for p in pieces if p["cta"] == c]
         assert all(p["first"] for p in mine[1:])
