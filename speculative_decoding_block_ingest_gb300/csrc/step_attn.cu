@@ -775,10 +775,12 @@ __global__ void __launch_bounds__(kStepThreads, 1)
 
 // ---------------------------------------------------------------- merge
 // o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i over a row's fragments, one
-// per segment and CTA that worked on it; a warp per (row, head).  Few bytes,
-// so latency bounds it: what does not depend on an earlier load is loaded at
-// once, partial rows kAhead at a time (32 verifying sequences, 5 fragments a
-// row: 13 us of 115).
+// per segment and CTA that worked on it; a warp per (row, head), or the four
+// of a block where all of those blocks run at once (19 short sequences behind
+// 15769 keys of one kv head, 100 fragments a row: the call 16.9 us, 24.3 with a
+// warp; 128 rows x 32 heads 28.2 and 25.0).  Few bytes, so latency bounds it: what
+// does not depend on an earlier load is loaded at once, partial rows kAhead at a
+// time (32 verifying sequences, 5 fragments a row: 13 us of 115).
 constexpr int kMergeThreads = 128, kMergeWarps = kMergeThreads / 32, kAhead = 4;
 constexpr int kSplitBlocks = 16;   // blocks for the rows of a CTA's last item
 
@@ -795,17 +797,19 @@ __device__ __forceinline__ int tile_row(const StepAttnArgs& a, int t, int head) 
   return (t < a.tpt ? t * a.G : 128 + (t - a.tpt) * a.G) + head;
 }
 
-template <int D, typename Out>
+// One warp merges a row, or WARPS > 1 a part of its fragments each.
+template <int D, typename Out, int WARPS>
 __device__ __forceinline__ void merge_row(const StepAttnArgs& a, long row, int head, const Parts& pre, const Parts& own,
-                                          int lane) {
+                                          int lane, int warp) {
   constexpr int kPer = D / 32;   // elements of a lane
   const long item = row * a.Hq + head;
-  const int total = pre.n + own.n;
+  const int all = pre.n + own.n, share = (all + WARPS - 1) / WARPS;
+  const int begin = warp * share, total = min(begin + share, all);
   float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) o[i] = 0.f;
   bool bad = false;
-  for (int i0 = 0; i0 < total; i0 += 32) {
+  for (int i0 = begin; i0 < total; i0 += 32) {
     // lane i: fragment i's max, sum and partial row
     const int i = i0 + lane, seg = i >= pre.n, k = i - (seg ? pre.n : 0);
     float2 ml = make_float2(-INFINITY, 0.f);
@@ -826,7 +830,7 @@ __device__ __forceinline__ void merge_row(const StepAttnArgs& a, long row, int h
     float add = wt == 0.f ? 0.f : wt * ml.y;
 #pragma unroll
     for (int s = 16; s; s >>= 1) add += __shfl_xor_sync(0xffffffffu, add, s);
-    if (i0 > 0) {
+    if (i0 > begin) {
       const float keep = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2_fast(m - mn);
       l = keep == 0.f ? 0.f : l * keep;
 #pragma unroll
@@ -860,6 +864,34 @@ __device__ __forceinline__ void merge_row(const StepAttnArgs& a, long row, int h
     }
   }
   bad = __any_sync(0xffffffffu, bad);
+  if constexpr (WARPS > 1) {
+    __shared__ float part[WARPS][D];
+    __shared__ float3 mlb[WARPS];
+#pragma unroll
+    for (int v = 0; v < kPer; ++v) part[warp][lane * kPer + v] = o[v];
+    if (lane == 0) mlb[warp] = make_float3(m, l, bad);
+    __syncthreads();
+    if (warp > 0) return;
+    float mn = m;
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) mn = fmaxf(mn, mlb[w].x);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float3 p = mlb[w];
+      const float wt = p.x == -INFINITY ? (p.y == 0.f ? 0.f : 1.f) : ex2_fast(p.x - mn);
+      if (w == 0) {
+        l = wt == 0.f ? 0.f : l * wt;
+#pragma unroll
+        for (int v = 0; v < kPer; ++v) o[v] = wt == 0.f ? 0.f : o[v] * wt;
+      } else if (wt != 0.f) {
+        l = fmaf(p.y, wt, l);
+#pragma unroll
+        for (int v = 0; v < kPer; ++v) o[v] = fmaf(part[w][lane * kPer + v], wt, o[v]);
+      }
+      bad |= p.z != 0.f;
+    }
+    m = mn;
+  }
   const float inv = bad ? __int_as_float(0x7fc00000) : (l == 0.f ? 0.f : 1.f / l);
   Out* dst = static_cast<Out*>(a.out) + row * a.out_stride + (long)head * D + lane * kPer;
   uint32_t y[kPer / 2];
@@ -872,13 +904,13 @@ __device__ __forceinline__ void merge_row(const StepAttnArgs& a, long row, int h
     a.lse[item] = bad ? inv : log_sum(m, l);
 }
 
-template <int D, typename Out>
+template <int D, typename Out, int WARPS>
 __global__ void __launch_bounds__(kMergeThreads, 8) step_merge_kernel(const __grid_constant__ StepAttnArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Parts none{0, 0, 0, {-INFINITY, 0.f}};
-  if (a.by_cta) {
+  if (WARPS == 1 && a.by_cta) {
     // only rows of an item that goes on in another CTA: at most one a CTA
     const int cta = blockIdx.x / kSplitBlocks, part = blockIdx.x % kSplitBlocks;
     const int4 s = a.split[cta];   // its first row, tokens, kv head and last CTA
@@ -886,11 +918,11 @@ __global__ void __launch_bounds__(kMergeThreads, 8) step_merge_kernel(const __gr
       const int t = r / a.G, sub = r - t * a.G, head = s.z * a.G + sub;
       const long row = s.x + t;
       const Parts own{cta, s.w - cta + 1, tile_row(a, t, sub), a.seg_ml[1][row * a.Hq + head]};
-      merge_row<D, Out>(a, row, head, none, own, lane);
+      merge_row<D, Out, 1>(a, row, head, none, own, lane, 0);
     }
     return;
   }
-  const unsigned item = blockIdx.x * kMergeWarps + warp;   // at most 2^31
+  const unsigned item = WARPS == 1 ? blockIdx.x * kMergeWarps + warp : blockIdx.x;   // at most 2^31
   const unsigned row = item / (unsigned)a.Hq;
   if (row >= (unsigned)a.s.n_rows) return;
   const int head = (int)(item - row * a.Hq), h = head / a.G;
@@ -909,7 +941,7 @@ __global__ void __launch_bounds__(kMergeThreads, 8) step_merge_kernel(const __gr
     }
   if (whole && a.s.prefix_len == 0) return;   // written already
   if (row >= (unsigned)rows) return;   // behind the last sequence: left as it is
-  merge_row<D, Out>(a, row, head, p[0], p[1], lane);
+  merge_row<D, Out, WARPS>(a, row, head, p[0], p[1], lane, WARPS == 1 ? 0 : warp);
 }
 
 template <int D, bool BF16>
@@ -929,11 +961,13 @@ cudaError_t launch(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMa
   }
   e = launch_pdl(attn, dim3(a.n_cta), dim3(kStepThreads), smem, s, q, k, v, a);
   if (e != cudaSuccess) return e;
-  // a warp for every (row, head), or sixteen blocks for every CTA's last item
-  const long ctas = a.by_cta ? (long)a.n_cta * kSplitBlocks
-                             : ((long)a.s.n_rows * a.Hq + kMergeWarps - 1) / kMergeWarps;
-  auto* merge = step_merge_kernel<D, std::conditional_t<BF16, __nv_bfloat16, __half>>;
-  return launch_pdl(merge, dim3((unsigned)ctas), dim3(kMergeThreads), 0, s, a);
+  // a block or a warp for every (row, head), or sixteen blocks for every CTA's last item
+  using Out = std::conditional_t<BF16, __nv_bfloat16, __half>;
+  const long items = (long)a.s.n_rows * a.Hq;
+  if (!a.by_cta && items <= 8L * a.n_cta)   // a block each, while all fit at once
+    return launch_pdl(step_merge_kernel<D, Out, kMergeWarps>, dim3((unsigned)items), dim3(kMergeThreads), 0, s, a);
+  const long ctas = a.by_cta ? (long)a.n_cta * kSplitBlocks : (items + kMergeWarps - 1) / kMergeWarps;
+  return launch_pdl(step_merge_kernel<D, Out, 1>, dim3((unsigned)ctas), dim3(kMergeThreads), 0, s, a);
 }
 
 }  // namespace
