@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
           if (key >= f.keys) {
 #pragma unroll
             for (int c = 0; c < 8 * kDAtoms; ++c)
-              *reinterpret_cast<uint4*>(v + (c >> 3) * kAtomBytes + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(v + (c >> 3) * kAtomBytes + ((c & 7) ^ (r & 7)) * 16) = make_uint4(0, 0, 0, 0);
           } else if (key >= own0) {
             // an exponent of ones carries into the sign's place
             constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;

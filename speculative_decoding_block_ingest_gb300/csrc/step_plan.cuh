@@ -20,7 +20,7 @@ struct Frag {
   int seg;             // 0 prefix, 1 own keys, -1: no further piece
   int seq, h;
   int tok0, ntok;      // first row of the step and tokens of the item's tiles
-  int keys;            // keys of the segment that may be read
+  int keys;            // keys of the segment that its rows see
   int lim0;            // own, causal: keys that token tok0 sees (may be <= 0)
   int b0, b1;
   int first;           // holds the item's first unit
@@ -58,11 +58,12 @@ struct Walk {
   __host__ __device__ int units(int ntok, int blocks) const { return end_units(ntok * a.G) + blocks * weight(ntok); }
   // tokens of tile pair j out of T
   __host__ __device__ int pair_tokens(int j, int T) const { return min(pair_tok, T - j * pair_tok); }
-  // key blocks that tile pair j needs of a sequence with T rows and len keys
-  __host__ __device__ int blocks(int j, int T, int len) const {
-    const int seen = a.causal ? len - T + min((j + 1) * pair_tok, T) : len;
-    return (min(max(seen, 0), a.s.room()) + kKeys - 1) / kKeys;
+  // keys that rows of tile pair j see of a sequence with T rows and len keys
+  __host__ __device__ int seen(int j, int T, int len) const {
+    const int n = a.causal ? len - T + min((j + 1) * pair_tok, T) : len;
+    return min(max(n, 0), a.s.room());
   }
+  __host__ __device__ int blocks(int j, int T, int len) const { return (seen(j, T, len) + kKeys - 1) / kKeys; }
   // units of one kv head: of the prefix, and of sequence i
   __host__ __device__ int prefix_head() const {
     if (!pre_tiles) return 0;
@@ -156,7 +157,7 @@ struct Walk {
       f.h = h;
       f.tok0 = tile * pair_tok + (seg ? row0 : 0);
       f.ntok = pair_tokens(tile, seg ? T : rows);
-      f.keys = seg ? min(len, a.s.room()) : a.s.prefix_len;
+      f.keys = seg ? seen(tile, T, len) : a.s.prefix_len;
       f.lim0 = seg && a.causal ? len - T + tile * pair_tok + 1 : f.keys;
       const int w = weight(f.ntok);
       auto block_at = [&](int unit) {   // the first block that starts at `unit` or behind
