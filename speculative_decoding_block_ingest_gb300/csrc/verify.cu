@@ -464,13 +464,15 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
 
 template <typename T>
 cudaError_t launch(const VerifyArgs& a, int n_sm, cudaStream_t s) {
-  // CTAs of a sequence: enough for 16384 entries each (f32, 250 x 30001: 2 CTAs
-  // 15.5 us, 8 27.9; 172 x 59277: 4 22.0, 8 26.3, 2 24.6; 256 x 262144: 8 91, 4
-  // 94, 2 107), more while the SMs have room for them (one greedy 32768: 8 CTAs
-  // 5.8 us, 2 7.8).
+  // CTAs of a sequence: enough for 40960 entries each (f32: 256 x 262144 91 us
+  // with 8 CTAs, 94 with 4; 256 x 160736 52.9 with 8, 46.3 with 4), for 16384
+  // while not all the SMs' places are taken (172 x 59277: 4 22.0, 8 26.3, 2 24.6;
+  // 256 x 32000: 2 12.9, 4 16.2), and more while half of them are free (100 x
+  // 32000: 4 9.1, 2 10.0; one greedy 32768: 8 5.8, 2 7.8).
   unsigned ctas = 1;
-  while (ctas < kMaxCluster && (a.vocab > 16384 * (int)ctas ||
-                                (2L * a.n_seq * ctas <= 4L * n_sm && a.vocab > 2048 * (int)ctas)))
+  while (ctas < kMaxCluster &&
+         (a.vocab > 40960 * (int)ctas || ((long)a.n_seq * ctas < 4L * n_sm && a.vocab > 16384 * (int)ctas) ||
+          ((long)a.n_seq * ctas <= 2L * n_sm && a.vocab > 2048 * (int)ctas)))
     ctas *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(a.n_seq * ctas);
