@@ -226,7 +226,11 @@ def test_attention_random_steps(T):
     # many more rows than the CTAs' last items have: merged by CTA
     ([1500, 3, 900, 0, 1], [1500, 2000, 950, 10, 1], 32, 4, 64, 64, HF, True, 0, False),
     ([1400, 700], [1400, 900], 24, 2, 128, 16, BF, False, 0, True),
-], ids=["single", "single-d64", "pair-and-single", "many-short", "many-empty", "prompts", "prompts-not-causal"])
+    # one kv head: rows with a part in every CTA, more than 32 for each of a merging block's warps
+    ([3], [50000], 4, 1, 128, 64, BF, True, 0, False),
+    ([1, 0, 2, 1], [400, 7, 300, 1], 2, 1, 64, 32, HF, True, 40000, False),
+], ids=["single", "single-d64", "pair-and-single", "many-short", "many-empty", "prompts", "prompts-not-causal",
+        "one-head", "one-head-prefix"])
 def test_attention_long(T, case):
     rows, _, hq, hkv, d, page, dt, causal, prefix, hnd = case
     (starts, kv, table, pre, kc, vc, q, _), o, lse = attend_case(T, case, seed=40)
