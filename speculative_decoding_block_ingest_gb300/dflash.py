@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -110,6 +111,24 @@ class VerifyArgs(ctypes.Structure):
                 ("n_accepted", ctypes.c_void_p)]
 
 
+def packer(cls):
+    """Function of a structure's fields, in order (pointers as integers), to
+    its bytes, which a call takes in its place: 1.4 us less than an instance."""
+    codes = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_void_p: "P", ctypes.c_float: "f",
+             ctypes.c_double: "d"}
+    fmt = "@" + "".join(codes[t] for _, t in cls._fields_)     # native sizes and alignment
+    fmt += "x" * (ctypes.sizeof(cls) - struct.calcsize(fmt))
+    to_bytes = struct.Struct(fmt).pack
+
+    def pack(*fields):
+        try:
+            return to_bytes(*fields)
+        except (struct.error, OverflowError) as e:
+            raise DflashError(ERR_INVALID_ARG, f"{cls.__name__}: {e}") from None
+
+    return pack
+
+
 _lib = None
 
 
@@ -149,12 +168,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     dbl = ctypes.c_double
     lib.dflash_rope_frequencies.argtypes = [i32, dbl, dbl, i32, dbl, dbl, PDOUBLE, PDOUBLE]
     cache_p, step_p = ctypes.POINTER(PagedCacheDesc), ctypes.POINTER(StepDesc)
-    lib.dflash_step_append.argtypes = [cache_p, step_p, ctypes.POINTER(AppendArgs), vp]
+    lib.dflash_step_append.argtypes = [vp, vp, vp, vp]   # structures by reference, or their bytes (packer)
     lib.dflash_step_attention_workspace.argtypes = [cache_p, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
-    lib.dflash_step_attention.argtypes = [cache_p, step_p, ctypes.POINTER(AttentionArgs), vp, ctypes.c_size_t, vp]
+    lib.dflash_step_attention.argtypes = [vp, vp, vp, vp, ctypes.c_size_t, vp]
     lib.dflash_step_attention_status.argtypes = [vp, vp]
     lib.dflash_step_attention_plan.argtypes = [cache_p, step_p, i32, i32, i32, p32, ctypes.POINTER(StepPiece), i32]
-    lib.dflash_verify_tokens.argtypes = [ctypes.POINTER(VerifyArgs), vp]
+    lib.dflash_verify_tokens.argtypes = [vp, vp]
     lib.dflash_destroy.argtypes = [vp]
     lib.dflash_destroy.restype = None
     lib.dflash_last_error.restype = ctypes.c_char_p

@@ -24,6 +24,8 @@ import torch
 from . import dflash
 from .dflash import BF16, ERR_INVALID_ARG, ERR_UNSUPPORTED, F16, F32, DflashError, _check
 
+_append_args, _attention_args, _verify_args = (
+    dflash.packer(c) for c in (dflash.AppendArgs, dflash.AttentionArgs, dflash.VerifyArgs))
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
@@ -230,13 +232,13 @@ def append(cache: PagedCache, step: Step, q: Optional[torch.Tensor], k: torch.Te
     elif q_out is not None:
         _refuse("q_out without q")
     head = (cache.head_dim,)
-    a = dflash.AppendArgs(
+    a = _append_args(
         _dtype(k, "rows"), hq, qp, k.data_ptr(), v.data_ptr(), qs, ks, vs,
         0 if q_gain is None else _vector(dev, "q_gain", q_gain, head, torch.float32),
         0 if k_gain is None else _vector(dev, "k_gain", k_gain, head, torch.float32), eps,
         0 if rope is None else rope.rot_dim, 0 if rope is None else rope.ptr, 1.0 if rope is None else rope.mscale,
         0 if positions is None else _vector(dev, "positions", positions, (n,)), qop, qos)
-    rc = dflash.load_library().dflash_step_append(cache.ref, step.rows(cache, n), ctypes.byref(a), _stream(dev))
+    rc = dflash.load_library().dflash_step_append(cache.ref, step.rows(cache, n), a, _stream(dev))
     if rc:
         _check(rc)
     return q_out
@@ -283,10 +285,10 @@ def attention(cache: PagedCache, step: Step, q: torch.Tensor, *, scale: Optional
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _vector(dev, "workspace", workspace, (workspace.numel(),), torch.uint8)
-    a = dflash.AttentionArgs(hq, 1 if causal else 0, 0.0 if scale is None else scale, q.data_ptr(), qs, out.data_ptr(),
-                             os, lse.data_ptr())
-    rc = dflash.load_library().dflash_step_attention(cache.ref, ref, ctypes.byref(a), workspace.data_ptr(),
-                                                     workspace.numel(), _stream(dev))
+    a = _attention_args(hq, 1 if causal else 0, 0.0 if scale is None else scale, q.data_ptr(), qs, out.data_ptr(), os,
+                        lse.data_ptr())
+    rc = dflash.load_library().dflash_step_attention(cache.ref, ref, a, workspace.data_ptr(), workspace.numel(),
+                                                     _stream(dev))
     if rc:
         _check(rc)
     return out, lse
@@ -329,13 +331,13 @@ def verify_tokens(draft: torch.Tensor, target_probs: torch.Tensor, u_accept: tor
     ua = _vector(dev, "u_accept", u_accept, (n, k), torch.float32) if k else 0
     tokens = torch.empty((n, k1), dtype=torch.int32, device=dev)
     accepted = torch.empty(n, dtype=torch.int32, device=dev)
-    a = dflash.VerifyArgs(
+    a = _verify_args(
         n, k, vocab, _dtype(target_probs, "target_probs"), d, draft.stride(0),
         0 if n_draft is None else _vector(dev, "n_draft", n_draft, (n,)),
         _vector(dev, "target_probs", target_probs, (n, k1, vocab), dt), ts[0], ts[1] if k else vocab, dp, dss, drs,
         ua, u_accept.stride(0), _vector(dev, "u_token", u_token, (n,), torch.float32), tokens.data_ptr(),
         accepted.data_ptr())
-    rc = dflash.load_library().dflash_verify_tokens(ctypes.byref(a), _stream(dev))
+    rc = dflash.load_library().dflash_verify_tokens(a, _stream(dev))
     if rc:
         _check(rc)
     return tokens, accepted

@@ -168,3 +168,14 @@ def test_binding_refuses_host_tensors(lib):
     with pytest.raises(dflash.DflashError):
         target.verify_tokens(torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, 2, 8), torch.zeros(1, 1),
                              torch.zeros(1))
+
+
+@pytest.mark.parametrize("cls", [dflash.AppendArgs, dflash.AttentionArgs, dflash.VerifyArgs])
+def test_packed_arguments_are_the_structure(cls):
+    floats = (ctypes.c_float, ctypes.c_double)
+    values = [i + 0.5 if t in floats else 1000 + i for i, (_, t) in enumerate(cls._fields_)]
+    got = cls.from_buffer_copy(dflash.packer(cls)(*values))
+    assert [getattr(got, n) for n, _ in cls._fields_] == values
+    with pytest.raises(dflash.DflashError) as e:       # n_seq, n_heads or dtype past 32 bits
+        dflash.packer(cls)(1 << 31, *values[1:])
+    assert e.value.code == dflash.ERR_INVALID_ARG
