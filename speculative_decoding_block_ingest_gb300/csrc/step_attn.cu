@@ -961,6 +961,9 @@ cudaError_t launch(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMa
   }
   e = launch_pdl(attn, dim3(a.n_cta), dim3(kStepThreads), smem, s, q, k, v, a);
   if (e != cudaSuccess) return e;
+  // items of at most one block are whole: nothing to merge (48 single tokens 11.8 -> 10.5 us,
+  // 56 short verifications 32.0 -> 23.7)
+  if (a.s.prefix_len == 0 && a.s.room() <= kKeys) return cudaSuccess;
   // a block or a warp for every (row, head), or sixteen blocks for every CTA's last item
   using Out = std::conditional_t<BF16, __nv_bfloat16, __half>;
   const long items = (long)a.s.n_rows * a.Hq;
