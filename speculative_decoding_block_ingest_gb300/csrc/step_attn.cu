@@ -29,7 +29,7 @@
 // it: a pair's block takes 2830 cycles of which the tensor pipe works 2048 (the
 // issue path between them; 32 sequences of 16 rows behind 16384 keys: 115 us, 1.24
 // PFLOP/s with the merge); a single's 2700 are HBM's (one sequence, 131016 keys:
-// 6.7 TB/s in the loop, 96 us in all).
+// 6.7 TB/s in the loop, 93 us in all).
 //   warps 0..3, 4..7  softmax of stream 0 / 1, one thread per query row
 //   warp 8            TMA: query tiles (ring of 2), K and V tiles (ring)
 //   warp 10           the pieces of items this CTA runs, described in a ring

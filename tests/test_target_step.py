@@ -334,6 +334,44 @@ def test_attention_repeats_bit_for_bit_and_replays(T):
         close(out, lse, want)
 
 
+def test_attention_with_room_for_one_block_of_keys(T):
+    """A block table of at most 128 keys (nothing to merge) and a wider one of the same keys: the same bits."""
+    rows, kv = [1, 0, 17, 4, 2], [128, 3, 17, 2, 0]
+    starts, kv, table, _, n_pages = R.make_step(rows, kv, 32, seed=14)
+    assert table.shape[1] == 4
+    kc, vc = caches(n_pages, 32, 2, 128, BF, seed=15)
+    q = torch.randn(starts[-1] + 2, 10, 128, generator=torch.Generator().manual_seed(16)).to(BF).to(DEV)
+    cache, got = T.PagedCache(kc, vc), []
+    for extra in (0, 1):
+        wide = torch.cat([table, table[:, :extra]], 1)
+        out, lse = torch.full_like(q, 3), torch.full((len(q), 10), 3.0, device=DEV)
+        ws = torch.empty(cache.workspace_bytes(len(q), 10), dtype=torch.uint8, device=DEV)
+        T.attention(cache, T.Step(i32(starts), i32(kv), wide.to(DEV)), q, out=out, lse=lse, workspace=ws)
+        T.attention_status(ws)
+        got.append((out, lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    out, lse = got[0]
+    n = starts[-1]
+    close(out[:n], lse[:n], R.attend_step(q[:n], kc, vc, starts, kv, table, torch.zeros(0, dtype=torch.int32), 0, 32,
+                                          causal=True, scale=128 ** -0.5))
+    assert bool((out[n:] == 3).all()) and bool((lse[n:] == 3).all())
+
+
+def test_two_calls_at_once(T):
+    """Calls on two streams, each with a workspace of its own, as they would run one after the other."""
+    calls = [attend_case(T, ATTEND[i], seed=30 + i) for i in (5, 13)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(8):
+        for i, ((_, _, _, _, kc, vc, q, step), _, _) in enumerate(calls):
+            got[i].append(T.attention(T.PagedCache(kc, vc), step, q, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i, (_, o, lse) in enumerate(calls):
+        assert all(torch.equal(a, o) and torch.equal(b, lse) for a, b in got[i])
+
+
 def test_operators_on_another_stream(T):
     """Inputs made on one stream, the call on another, ordered by the caller."""
     case = ATTEND[4]
