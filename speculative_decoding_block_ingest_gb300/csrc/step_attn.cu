@@ -27,7 +27,7 @@
 //          results are merged in tensor memory.
 // Either way one stream's products run under the other's softmax.  What bounds
 // it: a pair's block takes 2830 cycles of which the tensor pipe works 2048 (the
-// issue path between them; 32 sequences of 16 rows behind 16384 keys: 115 us, 1.24
+// issue path between them; 32 sequences of 16 rows behind 16384 keys: 111 us, 1.28
 // PFLOP/s with the merge); a single's 2700 are HBM's (one sequence, 131016 keys:
 // 6.7 TB/s in the loop, 93 us in all).
 //   warps 0..3, 4..7  softmax of stream 0 / 1, one thread per query row
@@ -775,13 +775,15 @@ __global__ void __launch_bounds__(kStepThreads, 1)
 
 // ---------------------------------------------------------------- merge
 // o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i over a row's fragments, one
-// per segment and CTA that worked on it; a warp per (row, head), or the four
-// of a block where all of those blocks run at once (19 short sequences behind
-// 15769 keys of one kv head, 100 fragments a row: the call 16.9 us, 24.3 with a
-// warp; 128 rows x 32 heads 28.2 and 25.0).  Few bytes, so latency bounds it: what
-// does not depend on an earlier load is loaded at once, partial rows kAhead at a
-// time (32 verifying sequences, 5 fragments a row: 13 us of 115).
-constexpr int kMergeThreads = 128, kMergeWarps = kMergeThreads / 32, kAhead = 4;
+// per segment and CTA that worked on it.  Few bytes, so latency bounds it: what
+// does not depend on an earlier load is loaded at once, and a (row, head) has
+// the four warps of a block where all of those run at once (19 short sequences
+// behind 15769 keys of one kv head, 100 fragments a row: the call 16.9 us, 24.3
+// with a warp; 128 rows x 32 heads 28.2 and 25.0), else a warp (64 rows x 32: the
+// call 191.4 us, 192.7 with half a warp), and half a warp where there are more
+// than run at once (32 verifying sequences, 512 rows x 32 of 5 fragments: 111.6 us,
+// 114.0 with a warp; four prompts of 2000 rows 168.6 and 175.2).
+constexpr int kMergeThreads = 128, kMergeWarps = kMergeThreads / 32;
 constexpr int kSplitBlocks = 16;   // blocks for the rows of a CTA's last item
 
 // A segment's fragments of one row: CTAs first .. first + n - 1, of which the
@@ -797,19 +799,22 @@ __device__ __forceinline__ int tile_row(const StepAttnArgs& a, int t, int head) 
   return (t < a.tpt ? t * a.G : 128 + (t - a.tpt) * a.G) + head;
 }
 
-// One warp merges a row, or WARPS > 1 a part of its fragments each.
-template <int D, typename Out, int WARPS>
-__device__ __forceinline__ void merge_row(const StepAttnArgs& a, long row, int head, const Parts& pre, const Parts& own,
-                                          int lane, int warp) {
-  constexpr int kPer = D / 32;   // elements of a lane
+// LANES lanes merge a row (all groups of a warp come here, `live` or not), or
+// WARPS > 1 warps a part of its fragments each.
+template <int D, typename Out, int WARPS, int LANES>
+__device__ __forceinline__ void merge_row(const StepAttnArgs& a, bool live, long row, int head, const Parts& pre,
+                                          const Parts& own, int lane, int warp) {
+  constexpr int kPer = D / LANES;                // elements of a lane
+  constexpr int kAhead = LANES == 32 ? 4 : 2;    // partial rows in flight
   const long item = row * a.Hq + head;
   const int all = pre.n + own.n, share = (all + WARPS - 1) / WARPS;
-  const int begin = warp * share, total = min(begin + share, all);
+  const int begin = warp * share, total = live ? min(begin + share, all) : 0;
+  const int most = LANES == 32 ? total : __reduce_max_sync(0xffffffffu, total);
   float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) o[i] = 0.f;
   bool bad = false;
-  for (int i0 = begin; i0 < total; i0 += 32) {
+  for (int i0 = begin; i0 < most; i0 += LANES) {
     // lane i: fragment i's max, sum and partial row
     const int i = i0 + lane, seg = i >= pre.n, k = i - (seg ? pre.n : 0);
     float2 ml = make_float2(-INFINITY, 0.f);
@@ -823,13 +828,13 @@ __device__ __forceinline__ void merge_row(const StepAttnArgs& a, long row, int h
     }
     float mx = ml.x;
 #pragma unroll
-    for (int s = 16; s; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    for (int s = LANES / 2; s; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
     const float mn = fmaxf(m, mx);
     // a part without a maximum counts nothing, unless its sum is NaN
     const float wt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_fast(ml.x - mn);
     float add = wt == 0.f ? 0.f : wt * ml.y;
 #pragma unroll
-    for (int s = 16; s; s >>= 1) add += __shfl_xor_sync(0xffffffffu, add, s);
+    for (int s = LANES / 2; s; s >>= 1) add += __shfl_xor_sync(0xffffffffu, add, s);
     if (i0 > begin) {
       const float keep = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2_fast(m - mn);
       l = keep == 0.f ? 0.f : l * keep;
@@ -838,19 +843,23 @@ __device__ __forceinline__ void merge_row(const StepAttnArgs& a, long row, int h
     }
     m = mn;
     l += add;
-    const int cnt = min(32, total - i0);
+    const int cnt = min(LANES, most - i0);
     for (int f0 = 0; f0 < cnt; f0 += kAhead) {
       float x[kAhead][kPer], g[kAhead];
 #pragma unroll
       for (int f = 0; f < kAhead; ++f) {
         g[f] = 0.f;
         if (f0 + f >= cnt) continue;
-        g[f] = __shfl_sync(0xffffffffu, wt, f0 + f);
+        g[f] = __shfl_sync(0xffffffffu, wt, f0 + f, LANES);
         const float* p = reinterpret_cast<const float*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), f0 + f)) + lane * kPer;
-        if constexpr (kPer == 4) {
-          const float4 q = *reinterpret_cast<const float4*>(p);
-          x[f][0] = q.x, x[f][1] = q.y, x[f][2] = q.z, x[f][3] = q.w;
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), f0 + f, LANES)) + lane * kPer;
+        if (LANES < 32 && g[f] == 0.f) continue;
+        if constexpr (kPer >= 4) {
+#pragma unroll
+          for (int v = 0; v < kPer; v += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(p + v);
+            x[f][v] = q.x, x[f][v + 1] = q.y, x[f][v + 2] = q.z, x[f][v + 3] = q.w;
+          }
         } else {
           const float2 q = *reinterpret_cast<const float2*>(p);
           x[f][0] = q.x, x[f][1] = q.y;
@@ -863,7 +872,9 @@ __device__ __forceinline__ void merge_row(const StepAttnArgs& a, long row, int h
           for (int v = 0; v < kPer; ++v) o[v] = fmaf(x[f][v], g[f], o[v]);
     }
   }
-  bad = __any_sync(0xffffffffu, bad);
+  const unsigned any = __ballot_sync(0xffffffffu, bad);
+  bad = LANES == 32 ? any != 0 : (any >> (threadIdx.x & 31 & ~(LANES - 1)) & ((1ull << LANES) - 1)) != 0;
+  if (!live) return;
   if constexpr (WARPS > 1) {
     __shared__ float part[WARPS][D];
     __shared__ float3 mlb[WARPS];
@@ -898,40 +909,44 @@ __device__ __forceinline__ void merge_row(const StepAttnArgs& a, long row, int h
 #pragma unroll
   for (int v = 0; v < kPer; v += 2)
     y[v / 2] = __float_as_uint(pack2<std::is_same_v<Out, __nv_bfloat16>>(make_float2(o[v] * inv, o[v + 1] * inv)));
-  if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+  if constexpr (kPer == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+  else if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
   else *reinterpret_cast<uint32_t*>(dst) = y[0];
   if (a.lse && lane == 0)
     a.lse[item] = bad ? inv : log_sum(m, l);
 }
 
-template <int D, typename Out, int WARPS>
+template <int D, typename Out, int WARPS, int LANES>
 __global__ void __launch_bounds__(kMergeThreads, 8) step_merge_kernel(const __grid_constant__ StepAttnArgs a) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kRows = kMergeThreads / LANES;   // rows of a block at once
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
   const Parts none{0, 0, 0, {-INFINITY, 0.f}};
-  if (WARPS == 1 && a.by_cta) {
+  if (LANES == 16 && a.by_cta) {
     // only rows of an item that goes on in another CTA: at most one a CTA
     const int cta = blockIdx.x / kSplitBlocks, part = blockIdx.x % kSplitBlocks;
     const int4 s = a.split[cta];   // its first row, tokens, kv head and last CTA
-    for (int r = part * kMergeWarps + warp; r < s.y * a.G; r += kSplitBlocks * kMergeWarps) {
-      const int t = r / a.G, sub = r - t * a.G, head = s.z * a.G + sub;
+    const int n = s.y * a.G;
+    for (int r0 = part * kRows; r0 < n; r0 += kSplitBlocks * kRows) {
+      const bool live = r0 + group < n;
+      const int r = live ? r0 + group : 0, t = r / a.G, sub = r - t * a.G, head = s.z * a.G + sub;
       const long row = s.x + t;
       const Parts own{cta, s.w - cta + 1, tile_row(a, t, sub), a.seg_ml[1][row * a.Hq + head]};
-      merge_row<D, Out, 1>(a, row, head, none, own, lane, 0);
+      merge_row<D, Out, 1, LANES>(a, live, row, head, none, own, lane, 0);
     }
     return;
   }
-  const unsigned item = WARPS == 1 ? blockIdx.x * kMergeWarps + warp : blockIdx.x;   // at most 2^31
+  const unsigned item = WARPS == 1 ? blockIdx.x * kRows + group : blockIdx.x;   // at most 2^31
   const unsigned row = item / (unsigned)a.Hq;
-  if (row >= (unsigned)a.s.n_rows) return;
+  bool live = row < (unsigned)a.s.n_rows;
   const int head = (int)(item - row * a.Hq), h = head / a.G;
   const int rows = a.s.start(a.s.n_seq);
   Parts p[2] = {none, none};
   bool whole = false;
 #pragma unroll
   for (int seg = 0; seg < 2; ++seg)
-    if (seg == 1 || a.s.prefix_len > 0) {
+    if (live && (seg == 1 || a.s.prefix_len > 0)) {
       const int4 meta = a.meta[((long)seg * a.s.n_rows + row) * a.Hkv + h];
       p[seg].ml = a.seg_ml[seg][item];
       p[seg].first = min(max(meta.x, 0), a.n_cta - 1);
@@ -939,9 +954,10 @@ __global__ void __launch_bounds__(kMergeThreads, 8) step_merge_kernel(const __gr
       p[seg].trow = tile_row(a, min(max(meta.z, 0), 2 * a.tpt - 1), head - h * a.G);
       whole = meta.w != 0;
     }
-  if (whole && a.s.prefix_len == 0) return;   // written already
-  if (row >= (unsigned)rows) return;   // behind the last sequence: left as it is
-  merge_row<D, Out, WARPS>(a, row, head, p[0], p[1], lane, WARPS == 1 ? 0 : warp);
+  // written already, or behind the last sequence: left as it is
+  if ((whole && a.s.prefix_len == 0) || row >= (unsigned)rows) live = false;
+  if (!__any_sync(0xffffffffu, live)) return;
+  merge_row<D, Out, WARPS, LANES>(a, live, row, head, p[0], p[1], lane, WARPS == 1 ? 0 : group);
 }
 
 template <int D, bool BF16>
@@ -964,13 +980,18 @@ cudaError_t launch(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMa
   // items of at most one block are whole: nothing to merge (48 single tokens 11.8 -> 10.5 us,
   // 56 short verifications 32.0 -> 23.7)
   if (a.s.prefix_len == 0 && a.s.room() <= kKeys) return cudaSuccess;
-  // a block or a warp for every (row, head), or sixteen blocks for every CTA's last item
+  // a block, a warp or half a warp for every (row, head), as many as run at
+  // once; or sixteen blocks for every CTA's last item
   using Out = std::conditional_t<BF16, __nv_bfloat16, __half>;
-  const long items = (long)a.s.n_rows * a.Hq;
-  if (!a.by_cta && items <= 8L * a.n_cta)   // a block each, while all fit at once
-    return launch_pdl(step_merge_kernel<D, Out, kMergeWarps>, dim3((unsigned)items), dim3(kMergeThreads), 0, s, a);
-  const long ctas = a.by_cta ? (long)a.n_cta * kSplitBlocks : (items + kMergeWarps - 1) / kMergeWarps;
-  return launch_pdl(step_merge_kernel<D, Out, 1>, dim3((unsigned)ctas), dim3(kMergeThreads), 0, s, a);
+  const long items = (long)a.s.n_rows * a.Hq, resident = 8L * a.n_cta;
+  auto merge = [&](auto* kernel, long blocks) {
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kMergeThreads), 0, s, a);
+  };
+  if (a.by_cta) return merge(step_merge_kernel<D, Out, 1, 16>, (long)a.n_cta * kSplitBlocks);
+  if (items <= resident) return merge(step_merge_kernel<D, Out, kMergeWarps, 32>, items);
+  if (items <= resident * kMergeWarps)
+    return merge(step_merge_kernel<D, Out, 1, 32>, (items + kMergeWarps - 1) / kMergeWarps);
+  return merge(step_merge_kernel<D, Out, 1, 16>, (items + 2 * kMergeWarps - 1) / (2 * kMergeWarps));
 }
 
 }  // namespace
