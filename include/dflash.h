@@ -429,7 +429,8 @@ typedef struct dflash_step {
   const int32_t *kv_len;        /* device [n_seq]                          */
   const int32_t *block_table;   /* device [n_seq, table_cols] page ids     */
   int32_t table_cols;
-  int64_t table_stride;         /* elements between its rows               */
+  int64_t table_stride;         /* elements between its rows; 0: one row of
+                                   pages for all sequences                 */
   int32_t prefix_len;           /* 0: no shared prefix                     */
   const int32_t *prefix_pages;  /* device, ceil(prefix_len / page_size)    */
 } dflash_step;

@@ -64,7 +64,7 @@ int check_step(const dflash_paged_cache* c, const dflash_step* s) {
   if (s->n_seq < 1 || s->n_seq > kMaxSeqs) return fail(DFLASH_ERR_INVALID_ARG, "n_seq must be 1..%d", kMaxSeqs);
   if (s->n_rows < 0 || s->n_rows > kMaxRows) return invalid("n_rows out of range");
   if (!s->row_start || !s->kv_len || (!s->block_table && s->table_cols > 0)) return invalid("step array is null");
-  if (s->table_cols < 0 || s->table_stride < s->table_cols) return invalid("block table shape");
+  if (s->table_cols < 0 || (s->table_stride < s->table_cols && s->table_stride != 0)) return invalid("block table shape");
   if (s->prefix_len < 0 || (s->prefix_len > 0 && !s->prefix_pages)) return invalid("prefix");
   if ((long)s->prefix_len + (long)s->table_cols * c->page_size >= (1L << 31)) return invalid("more than 2^31 keys");
   return DFLASH_OK;

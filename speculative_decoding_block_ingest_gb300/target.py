@@ -146,7 +146,8 @@ class Step:
     """The rows of a step: sequence i owns rows ``row_start[i] ..
     row_start[i+1]-1`` and, with them, ``kv_len[i]`` keys at the pages
     ``block_table[i]``, behind the ``prefix_len`` keys at ``prefix_pages``
-    that all sequences share.  int32 device tensors."""
+    that all sequences share.  int32 device tensors; block_table may be one
+    row of pages expanded to all sequences, but its rows may not overlap."""
 
     def __init__(self, row_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor,
                  prefix_pages: Optional[torch.Tensor] = None, prefix_len: int = 0):
@@ -161,7 +162,8 @@ class Step:
         pp = _vector(dev, "prefix_pages", prefix_pages, (self.prefix_pages,)) if self.prefix_pages else 0
         self.tensors = (row_start, kv_len, block_table, prefix_pages)
         self.prefix_len = int(prefix_len)
-        self.fields = (rs, kl, bt, cols, max(block_table.stride(0), cols) if n > 1 else cols, self.prefix_len, pp)
+        # the stride of a dimension of one row is never used
+        self.fields = (rs, kl, bt, cols, block_table.stride(0) if n > 1 else cols, self.prefix_len, pp)
         self.n_seq = n
         self._refs = {}
 
