@@ -513,7 +513,7 @@ int dflash_step_attention(const dflash_paged_cache *cache, const dflash_step *st
  * block, then 6 + min(rows G, 128) / 16 for its ends; C = min(n_cta,
  * max(floor(total / 6), 1)) CTAs take equal runs of units (the first ones a
  * unit more) and with them the blocks that start there, the first also the
- * rows of an item without a block. */
+ * rows of an item without a block.  Row starts that decrease make no pieces. */
 typedef struct dflash_step_piece {
   int32_t cta;
   int32_t segment;             /* 0: shared prefix, 1: own keys            */

@@ -482,10 +482,14 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       const int n = a.s.n_seq, prefix = w.prefix_units();
       auto units_of = [&](int i) { return i < n ? a.Hkv * w.head_units(i) : 0; };
       const int mine = units_of(lane);
-      int total = prefix + __reduce_add_sync(0xffffffffu, mine);
+      bool falls = lane < n && w.falls(lane);
+      unsigned total = prefix + __reduce_add_sync(0xffffffffu, (unsigned)mine);
 #pragma unroll 4
-      for (int i = 32; i < n; i += 32) total += __reduce_add_sync(0xffffffffu, units_of(i + lane));
-      w.divide(total, a.n_cta, blockIdx.x);
+      for (int i = 32; i < n; i += 32) {
+        total += __reduce_add_sync(0xffffffffu, (unsigned)units_of(i + lane));
+        falls |= i + lane < n && w.falls(i + lane);
+      }
+      w.divide(__any_sync(0xffffffffu, falls) ? 0 : (int)total, a.n_cta, blockIdx.x);
       int seq0 = -1, base = 0;
       if (w.ua < w.ub && w.ua >= prefix) {
         base = prefix;

@@ -54,6 +54,9 @@ struct Walk {
     pre_tiles = pre_blocks ? (rows + pair_tok - 1) / pair_tok : 0;
   }
   __host__ __device__ int tokens(int i) const { return max(a.s.start(i + 1) - a.s.start(i), 0); }
+  // Row starts that decrease make a plan of no units: step_fits bounds the sum
+  // of rows that do not, and the sum of others can wrap.
+  __host__ __device__ bool falls(int i) const { return a.s.start(i + 1) < a.s.start(i); }
   __host__ __device__ int weight(int ntok) const { return ntok > a.tpt ? kPairUnits : kSingleUnits; }
   __host__ __device__ int units(int ntok, int blocks) const { return end_units(ntok * a.G) + blocks * weight(ntok); }
   // tokens of tile pair j out of T
@@ -120,7 +123,7 @@ struct Walk {
   // Go to the item that holds unit ua; `seq0` is its sequence (-1: the
   // prefix) and `base` that sequence's first unit.
   __host__ __device__ void begin(int seq0, int base) {
-    if (seq0 < 0 && ua >= prefix_units()) {   // no sequence holds it: row starts that decrease
+    if (seq0 < 0 && ua >= prefix_units()) {   // no sequence holds it: arrays written to while the call runs
       pos = ub;
       return;
     }
@@ -189,7 +192,8 @@ struct Walk {
 };
 
 // The units of all sequences' own keys on the host's worst case, and of the
-// prefix: an upper bound that fits 31 bits, or more work than is accepted.
+// prefix: an upper bound that fits 31 bits, or more work than is accepted.  (It
+// holds for row starts that do not decrease: their rows are at most n_rows.)
 inline bool step_fits(const StepAttnArgs& a, int max_keys) {
   const long pairs = ((long)a.s.n_rows + 2 * a.tpt - 1) / (2 * a.tpt);
   const long blocks = (max_keys + (long)kKeys - 1) / kKeys, pre = (a.s.prefix_len + (long)kKeys - 1) / kKeys;

@@ -309,7 +309,13 @@ int dflash_step_attention_plan(const dflash_paged_cache* cache, const dflash_ste
   if (!step_fits(a, a.s.room())) return fail(DFLASH_ERR_UNSUPPORTED, "more work than one call takes: fewer rows");
   Walk w(a);
   int total = w.prefix_units();
-  for (int i = 0; i < step->n_seq; ++i) total += a.Hkv * w.head_units(i);
+  for (int i = 0; i < step->n_seq; ++i) {
+    if (w.falls(i)) {
+      total = 0;
+      break;
+    }
+    total += a.Hkv * w.head_units(i);
+  }
   int n = 0;
   for (int c = 0; c < n_cta; ++c) {
     w.divide(total, n_cta, c);
