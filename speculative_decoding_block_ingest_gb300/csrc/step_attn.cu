@@ -684,7 +684,11 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       float m0 = m, l0 = l, w0 = 1.f, w1 = 0.f;      // this stream's part, or the merge of both
       if (!pair) sh.ml[st][r] = make_float2(m, l);
       if (!ok) sh.abort = 1;
+      // a single item's streams read each other's products, which only their
+      // own stream has waited for
+      tc_fence_before();
       both();
+      tc_fence_after();
       if (*abort) ok = false;
       if (!pair) {
         const float2 e0 = sh.ml[0][r], e1 = sh.ml[1][r];

@@ -1,0 +1,52 @@
+"""More of the step operators on the GPU: the calls their documentation allows and tests/test_target_step.py does not
+make."""
+import numpy as np
+import pytest
+import torch
+
+import _target_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, HF, F4 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def T():
+    from speculative_decoding_block_ingest_gb300 import target
+    return target
+
+
+def i32(x):
+    return torch.as_tensor(x, dtype=torch.int32).to(DEV)
+
+
+def inputs(T, rows, kv, hq, hkv, d, page, dt, prefix=0, seed=0):
+    """(starts, table, prefix pages, k, v, q, step) of random values, all on the GPU but the index lists."""
+    starts, kv, table, pre, n_pages = R.make_step(rows, kv, page, prefix=prefix, seed=seed)
+    g = torch.Generator().manual_seed(seed + 1)
+    k, v = (torch.randn(n_pages, page, hkv, d, generator=g).to(dt).to(DEV) for _ in range(2))
+    q = torch.randn(starts[-1], hq, d, generator=g).to(dt).to(DEV)
+    return starts, table, pre, k, v, q, T.Step(i32(starts), i32(kv), table.to(DEV), pre.to(DEV), prefix)
+
+
+def close(o, lse, want):
+    wo, to, wl, tl = want
+    assert np.all(np.abs(o.double().cpu().numpy() - wo) <= to)
+    assert np.all(np.abs(lse.double().cpu().numpy() - wl) <= tl)
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("d,dt", [(64, HF), (128, BF)])
+def test_items_of_two_streams_merge_the_same_every_time(T, d, dt):
+    """Few rows of many lengths: each item's even and odd blocks are two accumulators, read across the two streams
+    right behind their last product.  Every call gives the same bits, and the right ones."""
+    kv = [129 + 97 * i % 1400 for i in range(150)]
+    rows = [1 + i % 2 for i in range(150)]
+    starts, table, pre, k, v, q, step = inputs(T, rows, kv, 8, 2, d, 64, dt, seed=1)
+    cache = T.PagedCache(k, v)
+    first = T.attention(cache, step, q)
+    for _ in range(60):
+        o, lse = T.attention(cache, step, q)
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    close(*first, R.attend_step(q, k, v, starts, kv, table, pre, 0, 64, causal=True, scale=d ** -0.5))
