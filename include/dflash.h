@@ -420,7 +420,8 @@ typedef struct dflash_paged_cache {
   int64_t page_stride, row_stride, head_stride;
 } dflash_paged_cache;
 
-/* The rows of a step and where their sequences' keys are. */
+/* The rows of a step and where their sequences' keys are.  prefix_len and the
+ * rows of table_cols pages are at most 2^31 - 257 together. */
 typedef struct dflash_step {
   int32_t n_seq;                /* 1 .. 4096                               */
   int32_t n_rows;               /* rows of the step's buffers; those from

@@ -66,7 +66,9 @@ int check_step(const dflash_paged_cache* c, const dflash_step* s) {
   if (!s->row_start || !s->kv_len || (!s->block_table && s->table_cols > 0)) return invalid("step array is null");
   if (s->table_cols < 0 || (s->table_stride < s->table_cols && s->table_stride != 0)) return invalid("block table shape");
   if (s->prefix_len < 0 || (s->prefix_len > 0 && !s->prefix_pages)) return invalid("prefix");
-  if ((long)s->prefix_len + (long)s->table_cols * c->page_size >= (1L << 31)) return invalid("more than 2^31 keys");
+  // the ends of the last block of keys and of the last page have 32-bit indices too
+  if ((long)s->prefix_len + (long)s->table_cols * c->page_size >= (1L << 31) - 256)
+    return invalid("more than 2^31 - 257 keys");
   return DFLASH_OK;
 }
 

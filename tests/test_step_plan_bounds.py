@@ -49,3 +49,25 @@ def test_starts_outside_the_buffer_are_bounded_first(lib):
     rc, pieces = plan(lib, [-5, 4, 200, 300], [9, 9, 9], n_rows=8, hq=4, hkv=2, cols=1)
     assert rc == dflash.OK
     assert {(p.seq, p.row0, p.n_tokens) for p in pieces} == {(0, 0, 4), (1, 4, 4)}
+
+
+@pytest.mark.parametrize("kw", [dict(prefix=2 ** 31 - 1, cols=0), dict(prefix=2 ** 31 - 100, cols=0),
+                                dict(prefix=2 ** 31 - 1 - 64, cols=1), dict(prefix=0, cols=2 ** 25 - 1)])
+def test_key_counts_whose_last_block_passes_31_bits_are_refused(lib, kw):
+    """A block or a page that ends behind key 2^31 - 1 has no 32-bit index."""
+    rc, _ = plan(lib, [0, 1], [2 ** 31 - 1], n_rows=1, hq=1, hkv=1, **kw)
+    assert rc == dflash.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(prefix=2 ** 31 - 257, cols=0), dict(prefix=0, cols=2 ** 25 - 5),
+                                dict(prefix=2 ** 30, cols=2 ** 24 - 5)])
+def test_the_largest_key_counts(lib, kw):
+    kv = kw["cols"] * 64
+    rc, pieces = plan(lib, [0, 1], [2 ** 31 - 1], n_rows=1, hq=1, hkv=1, **kw)
+    assert rc == dflash.OK
+    for seg, keys in ((0, kw["prefix"]), (1, kv)):
+        at = 0
+        for p in (x for x in pieces if x.segment == seg):
+            assert p.block0 == at
+            at = p.block1
+        assert at == -(-keys // 128)
