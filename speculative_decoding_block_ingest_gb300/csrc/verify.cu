@@ -22,6 +22,11 @@
 // here (a search in f64 took 9 us of a 16 us call), so every sum is kept in
 // two floats: p - q and every addition are split into result and rounding
 // error without loss, and the errors are summed beside: 2^-44 or better.
+//
+// The same sum taken in another order can differ in its last bits, so next to
+// the threshold two levels of the search may disagree.  Each level therefore
+// looks only among parts that have weight, and where none of them passes the
+// threshold the last entry with weight stands.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -358,13 +363,17 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
     if (warp == 0) {   // where u * total falls among the runs: a few neighbours per lane
       constexpr int kPer = kMaxRuns / 32;
       Sum v[kPer], c;
-      int last = -1;   // last run with weight
+      int last = -1;       // last run with weight
+      unsigned some = 0;   // which of the lane's runs have any
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int k = lane * kPer + i;
         if (k < runs) {
           c = c + run_sum[k];
-          if (run_sum[k].hi > 0.f) last = k;
+          if (run_sum[k].hi > 0.f) {
+            last = k;
+            some |= 1u << i;
+          }
         }
         v[i] = c;
       }
@@ -375,7 +384,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
       Sum base;
 #pragma unroll
       for (int i = kPer - 1; i >= 0; --i)
-        if (before + v[i] > th) {
+        if (some >> i & 1 && before + v[i] > th) {
           run = lane * kPer + i;
           base = i ? before + v[i - 1] : before;
         }
@@ -383,7 +392,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
       const int src = hit ? __ffs(hit) - 1 : 0;
       run = __shfl_sync(0xffffffffu, run, src);
       base = shfl(base, src);
-      // u * total at or past the total: the last entry that has weight
+      // u * total at or past the total: the last run that has weight
       last = __reduce_max_sync(0xffffffffu, last);
       if (lane == 0) {
         sh_run = hit ? run : last;
@@ -443,8 +452,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
     __syncthreads();
     fallback = max(fallback, sh_token);
     Sum wb;
-    const Sum winc = scan(lane < kVerifyWarps ? warp_sum[lane] : Sum{}, lane, wb);
-    const unsigned past = __ballot_sync(0xffffffffu, base + winc > th);
+    const Sum wsum = lane < kVerifyWarps ? warp_sum[lane] : Sum{};
+    const Sum winc = scan(wsum, lane, wb);
+    const unsigned past = __ballot_sync(0xffffffffu, wsum.hi > 0.f && base + winc > th);
     if (past) {   // the same in every warp
       if (warp != __ffs(past) - 1) return;
       const Sum mine = base + shfl(wb, warp);
@@ -453,7 +463,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
       for (int j = kPer - 1; j >= 0; --j)
         if (mine + (before + w[j]) > th && w[j] > (j ? w[j - 1] : Sum{})) first = i + j;
       first = __reduce_min_sync(0xffffffffu, first);
-      if (lane == 0) out[acc] = first != INT_MAX ? first : (last >= 0 ? last : fallback);
+      if (lane == 0) out[acc] = first != INT_MAX ? first : last;
       return;
     }
     base = base + shfl(winc, 31);

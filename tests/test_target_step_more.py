@@ -50,3 +50,41 @@ def test_items_of_two_streams_merge_the_same_every_time(T, d, dt):
         o, lse = T.attention(cache, step, q)
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
     close(*first, R.attend_step(q, k, v, starts, kv, table, pre, 0, 64, causal=True, scale=d ** -0.5))
+
+
+# ------------------------------------------------------------------ verification
+def drawn(T, tp, ut):
+    """Tokens drawn from the rows of tp [n, V] (no drafts), into memory that holds -7."""
+    import ctypes
+    from speculative_decoding_block_ingest_gb300 import dflash
+    n, V = tp.shape
+    tok, acc = torch.full((n,), -7, dtype=torch.int32, device=DEV), torch.full((n,), -7, dtype=torch.int32, device=DEV)
+    a = dflash.VerifyArgs(n_seq=n, k=0, vocab=V, dtype=dflash.F32, target_probs=tp.data_ptr(), target_seq_stride=V,
+                          target_row_stride=V, u_token=ut.data_ptr(), tokens=tok.data_ptr(), n_accepted=acc.data_ptr())
+    assert dflash.load_library().dflash_verify_tokens(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert bool((acc == 0).all())
+    return tok.cpu().numpy()
+
+
+def check_draws(tp, ut, tok):
+    """Every token has weight, and u * total lies on its step but for the sums' error (2^-44, and 2^-39 of the 64-bit
+    sums here)."""
+    w = tp.double().cpu().numpy()
+    c = np.cumsum(w, 1)
+    i = np.arange(len(w))
+    assert ((tok >= 0) & (tok < w.shape[1])).all(), tok[(tok < 0) | (tok >= w.shape[1])]
+    th, eps = ut.double().cpu().numpy() * c[:, -1], 2.0 ** -38
+    assert (w[i, tok] > 0).all()
+    assert (c[i, tok] >= th * (1 - eps)).all() and (c[i, tok] - w[i, tok] <= th * (1 + eps)).all()
+
+
+def test_verify_thresholds_next_to_the_border_of_a_run(T):
+    """Rows whose halves weigh the same and u = 1/2: sums taken in different orders fall on both sides of the
+    threshold, at the end of the entries that a warp, a CTA or a search step has."""
+    g = torch.Generator().manual_seed(1)
+    x = torch.exp(4 * torch.randn(2048, 4096, generator=g))
+    half = torch.full((2048,), 0.5, device=DEV)
+    for y in (x.flip(1), x, x[:, torch.randperm(4096, generator=g)]):
+        tp = torch.cat([x, y], 1).to(DEV)
+        check_draws(tp, half, drawn(T, tp, half))
