@@ -248,7 +248,8 @@ __device__ __forceinline__ void add_steps(Sum2 (&s)[2], const Row<T>& r, int& i,
   }
 }
 
-// Sum of entries [a, b) over the warp's lanes (every lane gets it).
+// Sum of entries [a, b) over the warp's lanes (every lane gets lane 0's: a sum's
+// last bits depend on the order of its terms, and the CTAs have to agree).
 template <typename T, bool DIFF>
 __device__ __forceinline__ Sum run_total(const Row<T>& r, int a, int b, int lane) {
   constexpr int kVec = Pack<T>::kEntries, kScalar = 4;
@@ -299,7 +300,7 @@ __device__ __forceinline__ Sum run_total(const Row<T>& r, int a, int b, int lane
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) c = c + shfl_xor(c, o);
-  return c;
+  return shfl(c, 0);
 }
 
 template <typename T>

@@ -88,3 +88,17 @@ def test_verify_thresholds_next_to_the_border_of_a_run(T):
     for y in (x.flip(1), x, x[:, torch.randperm(4096, generator=g)]):
         tp = torch.cat([x, y], 1).to(DEV)
         check_draws(tp, half, drawn(T, tp, half))
+
+
+def test_verify_thresholds_next_to_entries_without_weight(T):
+    """The same with nothing but zeros between the halves: the runs there are never drawn from, nor is entry 0."""
+    V = 16384
+    half = torch.full((32,), 0.5, device=DEV)
+    for m in (256, 700, 1536, 2048, 3333, 6000):
+        for seed in range(12):
+            g = torch.Generator().manual_seed(seed)
+            x = torch.exp(4 * torch.randn(32, m, generator=g))
+            tp = torch.zeros(32, V)
+            tp[:, 1:m + 1], tp[:, V - m:] = x, x[:, torch.randperm(m, generator=g)]
+            tp = tp.to(DEV)
+            check_draws(tp, half, drawn(T, tp, half))
