@@ -328,11 +328,16 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
       bool take = false;
       if (j < nd) {
         const int x = draft[j];
-        const float u = a.u_accept[seq * a.u_stride + j];
+        float u = a.u_accept[seq * a.u_stride + j];
         if (x >= 0 && x < a.vocab) {
-          const float p = weight(as_f32(P[j * a.p_row + x]));
+          float p = weight(as_f32(P[j * a.p_row + x]));
           const float q = Q ? weight(as_f32(Q[j * a.q_row + x])) : 1.f;
-          // u q < p, the product with its rounding error
+          // u q < p, the product with its rounding error; next to a tiny p
+          // both sides times 2^64, where that error still is a float
+          if (p < 0x1p-60f) {
+            p *= 0x1p64f;
+            u *= 0x1p64f;
+          }
           const float h = __fmul_rn(u, q);
           take = h < p || (h == p && fmaf(u, q, -h) < 0.f);
         }

@@ -102,3 +102,24 @@ def test_verify_thresholds_next_to_entries_without_weight(T):
             tp[:, 1:m + 1], tp[:, V - m:] = x, x[:, torch.randperm(m, generator=g)]
             tp = tp.to(DEV)
             check_draws(tp, half, drawn(T, tp, half))
+
+
+@pytest.mark.parametrize("dt", [F4, BF, HF])
+def test_verify_accepts_tiny_probabilities_by_their_product(T, dt):
+    """u q < p where u q has bits below the smallest float: equal probabilities are always accepted."""
+    n, V = 400, 64
+    g = torch.Generator().manual_seed(5)
+    one = {F4: 2.0 ** -149, BF: 2.0 ** -133, HF: 2.0 ** -24}[dt]
+    tp = torch.full((n, 2, V), 0.01, dtype=torch.float64)
+    dp = torch.full((n, 1, V), 0.01, dtype=torch.float64)
+    draft = torch.randint(0, V, (n, 1), generator=g).to(torch.int32)
+    i = torch.arange(n)
+    p, q = torch.randint(1, 5, (2, n), generator=g).double() * one
+    q[::2] = p[::2]
+    tp[i, 0, draft[:, 0].long()], dp[i, 0, draft[:, 0].long()] = p, q
+    args = [draft, tp.to(dt), torch.rand(n, 1, generator=g), torch.rand(n, generator=g), dp.to(dt)]
+    args[2][:20] = 1 - 2.0 ** -24
+    tok, acc = T.verify_tokens(*(t.to(DEV) for t in args[:4]), draft_probs=args[4].to(DEV))
+    wt, wa = R.verify(*args)
+    assert bool((wa[::2] == 1).all())
+    assert np.array_equal(acc.cpu().numpy(), wa) and np.array_equal(tok.cpu().numpy(), wt)
