@@ -500,7 +500,8 @@ typedef struct dflash_attention_args {
  * it, and only there; keys and values before the step's rows are finite or
  * spread to the whole sequence (the prefix's to the batch).  Scores and sums
  * are f32; softmax weights are rounded to the cache's type for the product
- * with V.  Two launches; one where there is no prefix and the block table has
+ * with V (f16: at 2^7 times their size, so that a key's share below 2^-32 of
+ * the largest is what can be lost).  Two launches; one where there is no prefix and the block table has
  * room for at most 128 keys of a sequence. */
 int dflash_step_attention(const dflash_paged_cache *cache, const dflash_step *step,
                           const dflash_attention_args *args, void *workspace, size_t workspace_bytes, void *stream);

@@ -127,7 +127,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // Two softmax weights (the lower key in the low half) or results in the
 // cache's type: the product with V takes both operands in one 16-bit type.  The
 // row sums add the unrounded weights, so the rounding (half a step, either way)
-// does not add up in the quotient.
+// does not add up in the quotient.  f16 rounds to zero, always downward, below
+// 2^-25, and loses bits below 2^-14: its weights are taken times 2^7, the most
+// that keeps them (2^8 and less, see kGrow) in its range, so that what is lost
+// of a weight is at most 2^-32 of the row's maximum's.
 template <bool BF16>
 __device__ __forceinline__ float pack2(float2 p) {
   if constexpr (BF16) {
@@ -229,6 +232,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
   constexpr uint32_t kFmt = BF16 ? (1u << 7) | (1u << 10) : 0u;
   constexpr uint32_t kIdescS = (1u << 4) | kFmt | ((128u >> 3) << 17) | ((128u >> 4) << 24);
   constexpr uint32_t kIdescO = (1u << 4) | kFmt | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
+  constexpr float kBias = BF16 ? 0.f : 7.f;            // weights, their sums and products are 2^kBias times as large
   constexpr uint32_t kColO = 256;                      // TMEM: S / P of the streams at 0 and 128, O at 256 and 384
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
@@ -636,7 +640,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
             scores();   // read again rather than kept beside O
           }
           if (grow) m = mj;
-          const float nm = m == -INFINITY ? 0.f : -m;
+          const float nm = m == -INFINITY ? 0.f : kBias - m;
           const float2 neg = make_float2(nm, nm), sc = make_float2(a.scale_log2, a.scale_log2);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -681,6 +685,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
         po = a.cta_o + at * D;
         pml = a.cta_ml + at;
       }
+      m -= kBias;                                    // the maximum that the sum and O go with
       float m0 = m, l0 = l, w0 = 1.f, w1 = 0.f;      // this stream's part, or the merge of both
       if (!pair) sh.ml[st][r] = make_float2(m, l);
       if (!ok) sh.abort = 1;

@@ -1,5 +1,7 @@
 """More of the step operators on the GPU: the calls their documentation allows and tests/test_target_step.py does not
 make."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -50,6 +52,35 @@ def test_items_of_two_streams_merge_the_same_every_time(T, d, dt):
         o, lse = T.attention(cache, step, q)
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
     close(*first, R.attend_step(q, k, v, starts, kv, table, pre, 0, 64, causal=True, scale=d ** -0.5))
+
+
+@pytest.mark.parametrize("rows", [1, 256], ids=["single", "pair"])
+@pytest.mark.parametrize("drop", [20, 22.7, 25.5, 28])
+def test_f16_keys_far_below_the_largest_still_count(T, rows, drop):
+    """One key, then 131071 whose weights are 2^-drop of its own: the tail is up to an eighth of the sum, and half or
+    all of it goes through one running maximum.  (All sequences read the same pages; what they return is one row.)"""
+    n, page, d, n_seq = 131072, 256, 64, 304 // (1 if rows == 1 else 2)
+    k, v = (torch.zeros(n // page, page, 1, d, dtype=HF, device=DEV) for _ in range(2))
+    half = torch.tensor(drop * math.log(2) / 2).to(HF)          # scores a * (+-half) / 8 with a = 8
+    k[..., 0], v[:] = -half, 1
+    v[..., 1::2] = -0.75
+    k[0, 0, 0, 0], v[0, 0] = half, 0
+    q = torch.zeros(n_seq * rows, 1, d, dtype=HF, device=DEV)
+    q[..., 0] = 8
+    table = i32([list(range(n // page))]).expand(n_seq, n // page)
+    step = T.Step(i32([i * rows for i in range(n_seq + 1)]), i32([n] * n_seq), table)
+    o, lse = T.attention(T.PagedCache(k, v), step, q, causal=False)
+    w = math.exp(-2 * float(half))
+    l = 1 + (n - 1) * w
+    tail = (n - 1) * w / l
+    want = torch.where(torch.arange(d) % 2 == 0, tail, -0.75 * tail).double()
+    # the result's rounding and the weights' (2^-11 each, on values of one sign), scores of at most 10 after three
+    # roundings in f32 and their exponentials (2^-17 in all), sums of n terms in f32, 2^-32 of the largest weight a key
+    tol = (2.0 ** -10 * 1.01 + 2.0 ** -17 + (n + 64) * 2.0 ** -23) * want.abs() + n * 2.0 ** -32 / l
+    e = (o[:, 0].double().cpu() - want).abs()
+    assert bool((e <= tol).all()), (float(e.max()), tail)
+    want_lse = float(half) + math.log(l)
+    assert float((lse.double().cpu() - want_lse).abs().max()) <= (n + 64) * 2.0 ** -24 + 2.0 ** -20 * abs(want_lse)
 
 
 # ------------------------------------------------------------------ verification
