@@ -843,16 +843,17 @@ __device__ __forceinline__ void merge_row(const StepAttnArgs& a, bool live, long
 #pragma unroll
     for (int s = LANES / 2; s; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
     const float mn = fmaxf(m, mx);
-    // a part without a maximum counts nothing, unless its sum is NaN
-    const float wt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_fast(ml.x - mn);
-    float add = wt == 0.f ? 0.f : wt * ml.y;
+    // a part without a maximum is left out (< 0), unless its sum is NaN; one
+    // that weighs nothing is not: it can hold NaN
+    const float wt = ml.x == -INFINITY ? (ml.y == 0.f ? -1.f : 1.f) : ex2_fast(ml.x - mn);
+    float add = wt < 0.f ? 0.f : wt * ml.y;
 #pragma unroll
     for (int s = LANES / 2; s; s >>= 1) add += __shfl_xor_sync(0xffffffffu, add, s);
     if (i0 > begin) {
       const float keep = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2_fast(m - mn);
-      l = keep == 0.f ? 0.f : l * keep;
+      l *= keep;
 #pragma unroll
-      for (int v = 0; v < kPer; ++v) o[v] = keep == 0.f ? 0.f : o[v] * keep;
+      for (int v = 0; v < kPer; ++v) o[v] *= keep;
     }
     m = mn;
     l += add;
@@ -861,12 +862,12 @@ __device__ __forceinline__ void merge_row(const StepAttnArgs& a, bool live, long
       float x[kAhead][kPer], g[kAhead];
 #pragma unroll
       for (int f = 0; f < kAhead; ++f) {
-        g[f] = 0.f;
+        g[f] = -1.f;
         if (f0 + f >= cnt) continue;
         g[f] = __shfl_sync(0xffffffffu, wt, f0 + f, LANES);
         const float* p = reinterpret_cast<const float*>(
             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), f0 + f, LANES)) + lane * kPer;
-        if (LANES < 32 && g[f] == 0.f) continue;
+        if (LANES < 32 && g[f] < 0.f) continue;
         if constexpr (kPer >= 4) {
 #pragma unroll
           for (int v = 0; v < kPer; v += 4) {
@@ -880,7 +881,7 @@ __device__ __forceinline__ void merge_row(const StepAttnArgs& a, bool live, long
       }
 #pragma unroll
       for (int f = 0; f < kAhead; ++f)
-        if (g[f] != 0.f)
+        if (!(g[f] < 0.f))
 #pragma unroll
           for (int v = 0; v < kPer; ++v) o[v] = fmaf(x[f][v], g[f], o[v]);
     }
@@ -904,10 +905,10 @@ __device__ __forceinline__ void merge_row(const StepAttnArgs& a, bool live, long
       const float3 p = mlb[w];
       const float wt = p.x == -INFINITY ? (p.y == 0.f ? 0.f : 1.f) : ex2_fast(p.x - mn);
       if (w == 0) {
-        l = wt == 0.f ? 0.f : l * wt;
+        l *= wt;
 #pragma unroll
-        for (int v = 0; v < kPer; ++v) o[v] = wt == 0.f ? 0.f : o[v] * wt;
-      } else if (wt != 0.f) {
+        for (int v = 0; v < kPer; ++v) o[v] *= wt;
+      } else {
         l = fmaf(p.y, wt, l);
 #pragma unroll
         for (int v = 0; v < kPer; ++v) o[v] = fmaf(part[w][lane * kPer + v], wt, o[v]);

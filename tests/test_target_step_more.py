@@ -83,6 +83,44 @@ def test_f16_keys_far_below_the_largest_still_count(T, rows, drop):
     assert float((lse.double().cpu() - want_lse).abs().max()) <= (n + 64) * 2.0 ** -24 + 2.0 ** -20 * abs(want_lse)
 
 
+@pytest.mark.parametrize("rows,kv,hq,hkv,prefix", [
+    ([600], [8000], 1, 1, 0), ([600], [8000], 4, 1, 0), ([2000], [2000], 32, 2, 0),
+    ([16], [300], 4, 1, 700), ([16] * 4, [300] * 4, 32, 4, 700), ([16] * 10, [300] * 10, 32, 4, 700),
+], ids=["block", "warp", "by-cta", "prefix-block", "prefix-warp", "prefix-half-warp"])
+def test_values_that_are_not_finite_reach_rows_through_any_merge(T, rows, kv, hq, hkv, prefix):
+    """A NaN or infinite value, or a NaN key, whose part of the keys weighs nothing beside the rest (120 below the
+    largest score) is seen all the same."""
+    d, page = 64, 64
+    starts, table, pre, k, v, q, step = inputs(T, rows, kv, hq, hkv, d, page, BF, prefix=prefix, seed=3)
+    q[:] = 0
+    q[..., 0] = 8
+    n, t = kv[0], rows[0]
+    # own keys from here on score 120 less than the others and the prefix's
+    turn = 0 if prefix else n - t if n > t else 1000
+    bad = n - t + 5 if n > t else 1100
+    k[pre.long().to(DEV), ..., 0] = 60.0
+    for i in range(len(rows)):
+        j = torch.arange(n)
+        p, r = table[i][j // page].long(), j % page
+        k[p, r, :, 0] = torch.where(j < turn, 60.0, -60.0).to(BF).to(DEV)[:, None]
+    want = R.attend_step(q, k, v, starts, kv, table, pre, prefix, page, causal=True, scale=d ** -0.5)
+    for i in range(len(rows)):
+        at = int(table[i, bad // page]), bad % page
+        v[at][:, 3], v[at][:, 7] = float("nan"), float("inf")
+        k[int(table[i, (n - 1) // page]), (n - 1) % page] = float("nan")     # the last row's own key
+    o, lse = T.attention(T.PagedCache(k, v), step, q)
+    o, lse, (wo, to, wl, tl) = o.double().cpu().numpy(), lse.double().cpu().numpy(), want
+    own = np.concatenate([n - t + np.arange(t)] * len(rows))                 # each row's own key
+    last = own == n - 1
+    assert np.isnan(o[last]).all() and np.isnan(lse[last]).all()
+    assert np.all(np.abs(lse - wl)[~last] <= tl[~last])
+    sees = np.zeros(o.shape, dtype=bool)
+    sees[own >= bad, :, 3] = sees[own >= bad, :, 7] = True
+    assert not np.isfinite(o[sees]).any()
+    sees[last] = True
+    assert np.all(np.abs(o - wo)[~sees] <= to[~sees])
+
+
 # ------------------------------------------------------------------ verification
 def drawn(T, tp, ut):
     """Tokens drawn from the rows of tp [n, V] (no drafts), into memory that holds -7."""
