@@ -450,11 +450,11 @@ typedef struct dflash_append_args {
   int64_t q_stride, k_stride, v_stride;   /* elements between rows         */
   const float *q_gain, *k_gain;  /* device [head_dim] head RMSNorm gains, or
                                     NULL: that side has no norm            */
-  double eps;                /* of the head norms, > 0                     */
+  double eps;                /* of the head norms, > 0 (as a float too)    */
   int32_t rot_dim;           /* rotated leading elements of a head, a
                                 multiple of 16 up to head_dim (0: none)    */
   const double *inv_freq;    /* host [rot_dim / 2], read during the call   */
-  double mscale;             /* factor on cos and sin                      */
+  double mscale;             /* factor on cos and sin, finite as a float   */
   const int32_t *positions;  /* device [n_rows], or NULL: as above         */
   void *q_out;               /* device [n_rows, n_heads, head_dim], cache
                                 dtype; may be q itself when the types and

@@ -166,8 +166,8 @@ int dflash_step_append(const dflash_paged_cache* cache, const dflash_step* step,
   if (p->n_heads < 0 || p->n_heads > kMaxHeads) return invalid("n_heads out of range");
   if (p->rot_dim < 0 || p->rot_dim > cache->head_dim || p->rot_dim % 16)
     return invalid("rot_dim must be a multiple of 16 up to head_dim");
-  if (p->rot_dim > 0 && (!p->inv_freq || !std::isfinite(p->mscale))) return invalid("RoPE frequencies");
-  if ((p->q_gain || p->k_gain) && !(p->eps > 0)) return invalid("eps must be > 0");
+  if (p->rot_dim > 0 && (!p->inv_freq || !std::isfinite((float)p->mscale))) return invalid("RoPE frequencies");
+  if ((p->q_gain || p->k_gain) && !((float)p->eps > 0)) return invalid("eps must be > 0 in f32");
   if (step->n_rows == 0) return DFLASH_OK;
   if (!p->k || !p->v || (p->n_heads > 0 && (!p->q || !p->q_out))) return invalid("row pointer is null");
   const int d = cache->head_dim;

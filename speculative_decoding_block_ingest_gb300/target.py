@@ -57,6 +57,16 @@ def _vector(device: torch.device, what: str, t: torch.Tensor, shape: tuple, dtyp
     return t.data_ptr()
 
 
+def _scale(scale: Optional[float]) -> float:
+    """The attention's scale as the f32 it is passed as, where 0 stands for the default."""
+    if scale is None:
+        return 0.0
+    s = ctypes.c_float(scale).value
+    if not 0 < s < float("inf"):
+        _refuse("scale must be positive, and finite, in f32")
+    return s
+
+
 @contextlib.contextmanager
 def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
     """The device (and the caller's stream, if any) made current."""
@@ -267,8 +277,6 @@ def attention(cache: PagedCache, step: Step, q: torch.Tensor, *, scale: Optional
     n, hq, qs = _rows(cache, "q", q)
     if q.dtype is not cache.dtype:
         _refuse("q must have the cache's dtype")
-    if scale is not None and not scale > 0:
-        _refuse("scale must be positive")
     ref, need = step.rows(cache, n), cache.workspace_bytes(n, hq)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -287,7 +295,7 @@ def attention(cache: PagedCache, step: Step, q: torch.Tensor, *, scale: Optional
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _vector(dev, "workspace", workspace, (workspace.numel(),), torch.uint8)
-    a = _attention_args(hq, 1 if causal else 0, 0.0 if scale is None else scale, q.data_ptr(), qs, out.data_ptr(), os,
+    a = _attention_args(hq, 1 if causal else 0, _scale(scale), q.data_ptr(), qs, out.data_ptr(), os,
                         lse.data_ptr())
     rc = dflash.load_library().dflash_step_attention(cache.ref, ref, a, workspace.data_ptr(), workspace.numel(),
                                                      _stream(dev))
