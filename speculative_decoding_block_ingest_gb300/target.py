@@ -141,15 +141,16 @@ class PagedCache:
     def workspace_bytes(self, n_rows: int, n_heads: int) -> int:
         """Workspace of :func:`attention` for up to n_rows rows."""
         key = (n_rows, n_heads)
-        if key not in self._ws:
+        got = self._ws.get(key)
+        if got is None:
             n = ctypes.c_size_t(0)
             lib = dflash.load_library()
             with torch.cuda.device(self.device):
                 _check(lib.dflash_step_attention_workspace(self.ref, n_rows, n_heads, ctypes.byref(n)))
             if len(self._ws) > 64:
-                self._ws.clear()
-            self._ws[key] = n.value
-        return self._ws[key]
+                self._ws = {}      # another thread may be about to look into the old one
+            got = self._ws[key] = n.value
+        return got
 
 
 class Step:

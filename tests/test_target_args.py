@@ -25,3 +25,41 @@ def test_a_scale_that_is_no_float_is_refused(scale):
 def test_scales():
     assert target._scale(None) == 0.0 and target._scale(0.125) == 0.125
     assert target._scale(1e-40) == ctypes.c_float(1e-40).value > 0
+
+
+def test_two_threads_ask_for_workspaces(lib, monkeypatch):  # noqa: F811
+    """Sizes are kept for some shapes at a time; a thread that makes room takes no other thread's answer away."""
+    import contextlib
+    import threading
+
+    class Lib:
+        def dflash_step_attention_workspace(self, ref, rows, heads, n):
+            n._obj.value = 1000 * rows + heads
+            return 0
+
+    monkeypatch.setattr(target.dflash, "load_library", Lib)
+    monkeypatch.setattr(target.torch.cuda, "device", lambda d: contextlib.nullcontext())
+
+    class Others(dict):
+        """Between storing an answer and reading it, other threads fill the table and clear it."""
+
+        def __setitem__(self, key, value):
+            dict.__setitem__(self, key, value)
+            self.clear()
+
+    c = object.__new__(target.PagedCache)
+    c.device, c.ref, c._ws = None, None, Others()
+    assert c.workspace_bytes(3, 4) == 3004
+    c._ws, bad = {}, []
+
+    def ask(first):
+        for i in range(first, first + 500):
+            if c.workspace_bytes(i, 8) != 1000 * i + 8:
+                bad.append(i)
+
+    threads = [threading.Thread(target=ask, args=(100 * i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert bad == [] and len(c._ws) <= 66 + len(threads)
