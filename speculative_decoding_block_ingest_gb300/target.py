@@ -26,6 +26,7 @@ from .dflash import BF16, ERR_INVALID_ARG, ERR_UNSUPPORTED, F16, F32, DflashErro
 
 _append_args, _attention_args, _verify_args = (
     dflash.packer(c) for c in (dflash.AppendArgs, dflash.AttentionArgs, dflash.VerifyArgs))
+_STATUS_BYTES = 4096     # what every attention workspace starts with
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
@@ -309,6 +310,9 @@ def attention_status(workspace: torch.Tensor, stream: Optional[torch.cuda.Stream
     """Wait for the stream; raise if a bounded device-side wait of the last
     attention on this workspace gave up."""
     dev = _cuda(workspace.device, "workspace")
+    _vector(dev, "workspace", workspace, (workspace.numel(),), torch.uint8)
+    if workspace.numel() < _STATUS_BYTES:
+        _refuse(f"a workspace of {workspace.numel()} bytes is not one of the attention's")
     with _on(dev, stream):
         _check(dflash.load_library().dflash_step_attention_status(workspace.data_ptr(), _stream(dev)))
 

@@ -121,6 +121,19 @@ def test_values_that_are_not_finite_reach_rows_through_any_merge(T, rows, kv, hq
     assert np.all(np.abs(o - wo)[~sees] <= to[~sees])
 
 
+def test_status_of_what_is_no_workspace_is_refused(T):
+    """A tensor shorter than the words it would be read for, or not the bytes a call was given."""
+    from speculative_decoding_block_ingest_gb300.dflash import DflashError
+    ok = torch.zeros(4096, dtype=torch.uint8, device=DEV)
+    T.attention_status(ok)
+    for bad in (ok[:4095], ok[:0], ok.view(torch.int32), ok.view(2, 2048), torch.zeros(16384, dtype=torch.uint8, device=DEV)[::2]):
+        with pytest.raises(DflashError):
+            T.attention_status(bad)
+    # the smallest workspace there is holds them
+    k = torch.zeros(1, 16, 1, 64, dtype=BF, device=DEV)
+    assert T.PagedCache(k, k.clone()).workspace_bytes(0, 1) >= 4096
+
+
 # ------------------------------------------------------------------ verification
 def drawn(T, tp, ut):
     """Tokens drawn from the rows of tp [n, V] (no drafts), into memory that holds -7."""
