@@ -402,7 +402,8 @@ int dflash_launch_count(dflash_t *h, int64_t *launches);
  * Out-of-range contents of the device arrays cannot be refused by the host;
  * the kernels bound them instead: a row index, length or page outside its
  * range writes nothing, a page outside [0, n_pages) reads as zeros, and row
- * starts that decrease leave the rows unspecified, inside their buffers.
+ * starts that decrease, or do not begin at 0, leave the step's results and the
+ * cache rows of the table's pages unspecified, inside their buffers.
  * ------------------------------------------------------------------------ */
 
 /* A paged cache of one target layer.  Key row r of a page, kv head h starts

@@ -134,6 +134,71 @@ def test_status_of_what_is_no_workspace_is_refused(T):
     assert T.PagedCache(k, k.clone()).workspace_bytes(0, 1) >= 4096
 
 
+class Guarded:
+    """Buffers inside larger ones; what lies on either side has to stay."""
+
+    def __init__(self):
+        self.all = []
+
+    def __call__(self, shape, dtype, value):
+        n, pad = math.prod(shape), 512
+        flat = torch.full((n + 2 * pad,), value, dtype=dtype, device=DEV)
+        self.all.append((flat, n, pad, value))
+        return flat[pad:pad + n].view(shape)
+
+    def untouched(self):
+        return all(bool((f[:p] == x).all()) and bool((f[p + n:] == x).all()) for f, n, p, x in self.all)
+
+
+BIG = 2 ** 31 - 1
+BAD_SMALL = [([0, 100, 200], [5, 5], [[0], [1]]), ([0, 8, 3], [5, 5], [[0], [1]]), ([-5, 4, 8], [-3, BIG], [[0], [1]]),
+             ([0, 4, 8], [16, 16], [[-1], [BIG]]), ([8, 8, 8], [16, 16], [[0], [1]]),
+             ([5, 0, 8], [3, BIG], [[99], [-BIG]]), ([0, 4, 8], [16, 3], [[2], [2]])]
+FAR = 5000
+BAD_LARGE = [([0, FAR] * 6 + [0], [200] * 12, [[i % 8, 1, 2, -4] for i in range(12)]),
+             ([-9, 2500, BIG], [BIG, 4000], [[0, 1, 2, 3], [4, 77, 6, 7]]),
+             ([0, 4000, 3999, FAR], [250, 250, 250], [[0, 1, 2, 3]] * 3), ([FAR, 0, 0], [9, 9], [[0, 1, 2, 3]] * 2),
+             ([0, 10, FAR], [-BIG, 256], [[0, 1, 2, 3], [4, 5, 6, 7]])]
+
+
+@pytest.mark.parametrize("starts,lens,pages,prefix,rows,page,heads",
+                         [(*c, p, 8, 16, 4) for c in BAD_SMALL for p in (20, 0)]
+                         + [(*c, p, FAR, 64, 8) for c in BAD_LARGE for p in (0, 150)])
+def test_bad_device_arrays_write_nothing_else(T, starts, lens, pages, prefix, rows, page, heads):
+    """Row starts, lengths and pages out of range, through every way of merging: buffers keep their surroundings, the
+    caches every row that no (sequence, key) in range names."""
+    d, hkv = 64, 2
+    new, g = Guarded(), torch.Generator().manual_seed(6)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(BF).to(DEV)
+    kc, vc = (new((8, page, hkv, d), BF, 5.0) for _ in range(2))
+    kc.copy_(rnd(*kc.shape)), vc.copy_(rnd(*vc.shape))
+    before = kc.clone(), vc.clone()
+    q, kv = rnd(rows, heads, d), rnd(rows, hkv, d)
+    cache, step = T.PagedCache(kc, vc), T.Step(i32(starts), i32(lens), i32(pages), i32([7, -1, BIG]), prefix)
+    T.append(cache, step, q, kv, kv, q_out=new(q.shape, BF, 5.0))
+    torch.cuda.synchronize()
+    s = [min(max(x, 0), rows) for x in starts]
+    falls = s[0] != 0 or any(b < a for a, b in zip(s, s[1:]))      # rows of no known sequence
+    named = torch.zeros(8, page, dtype=torch.bool)
+    for i, n in enumerate(lens):
+        own = range(len(pages[i]) * page) if falls else range(max(n, 0) - (s[i + 1] - s[i]), max(n, 0))
+        for j in own:
+            if 0 <= j < len(pages[i]) * page and 0 <= pages[i][j // page] < 8:
+                named[pages[i][j // page], j % page] = True
+    for c, b in zip((kc, vc), before):
+        assert torch.equal(c[~named.to(DEV)], b[~named.to(DEV)])
+    need = cache.workspace_bytes(rows, heads)
+    ws, out, lse = new((need,), torch.uint8, 90), new(q.shape, BF, 5.0), new((rows, heads), F4, 5.0)
+    kept = kc.clone(), vc.clone()
+    for causal in (True, False):
+        T.attention(cache, step, q, out=out, lse=lse, workspace=ws, causal=causal)
+        T.attention_status(ws)
+    assert torch.equal(kc, kept[0]) and torch.equal(vc, kept[1])
+    assert new.untouched()
+    if not falls:
+        assert bool((out[s[-1]:] == 5).all()) and bool((lse[s[-1]:] == 5).all())
+
+
 # ------------------------------------------------------------------ verification
 def drawn(T, tp, ut):
     """Tokens drawn from the rows of tp [n, V] (no drafts), into memory that holds -7."""
