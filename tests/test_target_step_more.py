@@ -199,6 +199,72 @@ def test_bad_device_arrays_write_nothing_else(T, starts, lens, pages, prefix, ro
         assert bool((out[s[-1]:] == 5).all()) and bool((lse[s[-1]:] == 5).all())
 
 
+# ------------------------------------------------------------------ offsets past 32 bits
+FAR_ROW = 1_200_000_000      # elements between rows: the third starts behind 2^31
+
+
+def test_append_and_attention_far_into_large_pools(T):
+    """Pages, query rows and results whose offsets pass 2^31 elements, both layouts of the pool."""
+    n_pages, page, hkv, d, hq = 20011, 256, 8, 64, 16           # 2.6e9 elements each
+    for hnd in (False, True):
+        shape = (n_pages, hkv, page, d) if hnd else (n_pages, page, hkv, d)
+        kc, vc = (torch.empty(*shape, dtype=BF, device=DEV) for _ in range(2))
+        if hnd:
+            kc, vc = kc.transpose(1, 2), vc.transpose(1, 2)
+        table = torch.tensor([[n_pages - 1, 3, 17000], [16500, 19999, 0]], dtype=torch.int32)
+        rows, kv, starts = [2, 1], [600, 700], [0, 2, 3]
+        g = torch.Generator().manual_seed(11)
+        for p in table.flatten().tolist():
+            kc[p], vc[p] = (torch.randn(page, hkv, d, generator=g).to(BF).to(DEV) for _ in range(2))
+        wide = torch.empty(2 * FAR_ROW + hq * d, dtype=BF, device=DEV)
+        q = wide.as_strided((3, hq, d), (FAR_ROW, d, 1))
+        q.copy_(torch.randn(3, hq, d, generator=g).to(BF))
+        k, v = (torch.randn(3, hkv, d, generator=g).to(BF).to(DEV) for _ in range(2))
+        cache, step = T.PagedCache(kc, vc), T.Step(i32(starts), i32(kv), table.to(DEV))
+        assert T.append(cache, step, q, k, v, q_out=q) is q          # in place, no norm and no rotation
+        for row, (i, own) in enumerate([(0, 598), (0, 599), (1, 699)]):
+            p = int(table[i, own // page])
+            assert torch.equal(kc[p, own % page], k[row]) and torch.equal(vc[p, own % page], v[row])
+        far = torch.empty(2 * FAR_ROW + hq * d, dtype=BF, device=DEV).as_strided((3, hq, d), (FAR_ROW, d, 1))
+        o, lse = T.attention(cache, step, q, out=far)
+        used = table.flatten().tolist()
+        small = torch.arange(6, dtype=torch.int32).view(2, 3)
+        close(o, lse, R.attend_step(q, kc[used], vc[used], starts, kv, small, torch.zeros(0, dtype=torch.int32), 0, page,
+                                    causal=True, scale=d ** -0.5))
+        del kc, vc, cache, wide, far, q, o
+
+
+def test_verify_rows_far_apart(T):
+    n, k, V = 3, 2, 5003
+    g = torch.Generator().manual_seed(12)
+    tp, dp = (torch.softmax(3 * torch.randn(n, m, V, generator=g), -1) for m in (k + 1, k))
+    draft = tp[:, :k].argmax(-1).to(torch.int32)
+    ua, ut = torch.rand(n, k, generator=g), torch.rand(n, generator=g)
+    far = []
+    for x, (s0, s1) in ((tp, (FAR_ROW, 100_000_001)), (dp, (FAR_ROW + 3, 2 ** 27))):
+        buf = torch.empty((n - 1) * s0 + (x.shape[1] - 1) * s1 + V, device=DEV)
+        far.append(buf.as_strided(x.shape, (s0, s1, 1)))
+        far[-1].copy_(x)
+    tok, acc = T.verify_tokens(draft.to(DEV), far[0], ua.to(DEV), ut.to(DEV), draft_probs=far[1])
+    wt, wa = R.verify(draft, tp, ua, ut, dp)
+    assert np.array_equal(acc.cpu().numpy(), wa) and np.array_equal(tok.cpu().numpy(), wt)
+
+
+def test_steps_without_rows(T):
+    """A step of no rows, and buffers whose sequences have none."""
+    kc, vc = (torch.ones(2, 16, 2, 64, dtype=BF, device=DEV) for _ in range(2))
+    cache = T.PagedCache(kc, vc)
+    for n in (0, 5):
+        step = T.Step(i32([0, 0, 0]), i32([3, 0]), i32([[0], [1]]), i32([1]), 7)
+        q, k = torch.ones(n, 4, 64, dtype=BF, device=DEV), torch.zeros(n, 2, 64, dtype=BF, device=DEV)
+        out, lse = torch.full_like(q, 3), torch.full((n, 4), 3.0, device=DEV)
+        ws = torch.full((cache.workspace_bytes(n, 4),), 90, dtype=torch.uint8, device=DEV)
+        T.append(cache, step, q, k, k, rope=T.Rope(64))
+        T.attention(cache, step, q, out=out, lse=lse, workspace=ws)
+        T.attention_status(ws)
+        assert bool((kc == 1).all()) and bool((vc == 1).all()) and bool((out == 3).all()) and bool((lse == 3).all())
+
+
 # ------------------------------------------------------------------ verification
 def drawn(T, tp, ut):
     """Tokens drawn from the rows of tp [n, V] (no drafts), into memory that holds -7."""
