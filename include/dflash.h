@@ -469,8 +469,8 @@ typedef struct dflash_append_args {
  * each rounded once.  Row pointers start on 16-byte boundaries (bases and
  * strides).  Rows of the caches that no row of the step names stay as they
  * are; a row whose own index would be negative, or past the block table,
- * writes no key or value (its query is written).  Pages that rows go to belong
- * to one sequence each.  One launch. */
+ * writes no key or value (its query is written).  No two rows of a step go to
+ * the same row of the cache.  One launch. */
 int dflash_step_append(const dflash_paged_cache *cache, const dflash_step *step, const dflash_append_args *args,
                        void *stream);
 
@@ -564,11 +564,11 @@ typedef struct dflash_verify_args {
  * is drawn from the positive part of p_j - q_j, after n_draft acceptances
  * from p_{n_draft}: the lowest index whose cumulative sum exceeds
  * u_token * total.  The tokens are then distributed as the target's own.
- * Probabilities need not sum to one; NaN, infinite and negative ones count
- * as zero, and a draft outside [0, vocab) is rejected.  Where nothing is left
+ * Probabilities need not sum to one, but to a finite float; NaN, infinite and
+ * negative ones count as zero, and a draft outside [0, vocab) is rejected.  Where nothing is left
  * of p_j - q_j the token is drawn from p_j, and without any positive p_j it
- * is 0.  Sums are kept in two floats (2^-44) and taken in a fixed order.  One
- * launch, no workspace; the rows need no alignment beyond their type's. */
+ * is 0.  Sums are kept in two floats (2^-44) and taken in a fixed order; the
+ * token always has weight where any entry has.  One launch, no workspace; the rows need no alignment beyond their type's. */
 int dflash_verify_tokens(const dflash_verify_args *args, void *stream);
 
 /* Release the handle (the workspace stays the caller's). */
