@@ -464,7 +464,7 @@ typedef struct dflash_append_args {
 } dflash_append_args;
 
 /* Queries and keys of the step's rows: per head x / sqrt(mean x^2 + eps) *
- * gain, then RoPE (pairs j, j + rot_dim / 2; the rest of a head passes
+ * gain (the sum of x^2 a finite float), then RoPE (pairs j, j + rot_dim / 2; the rest of a head passes
  * through); keys and values go to their rows of the cache, queries to q_out,
  * each rounded once.  Row pointers start on 16-byte boundaries (bases and
  * strides).  Rows of the caches that no row of the step names stay as they
@@ -500,10 +500,11 @@ typedef struct dflash_attention_args {
  * that element not finite (NaN within a tile of rows) in every row that sees
  * it, and only there; keys and values before the step's rows are finite or
  * spread to the whole sequence (the prefix's to the batch).  Scores and sums
- * are f32; softmax weights are rounded to the cache's type for the product
+ * are f32, of weights up to 2^8 times the largest's: values times that and the
+ * number of keys are finite floats (f16 ones always are).  Softmax weights are rounded to the cache's type for the product
  * with V (f16: at 2^7 times their size, so that a key's share below 2^-32 of
- * the largest is what can be lost).  Two launches; one where there is no prefix and the block table has
- * room for at most 128 keys of a sequence. */
+ * the largest is what can be lost).  Two launches; one where there is no prefix
+ * and the block table has room for at most 128 keys of a sequence. */
 int dflash_step_attention(const dflash_paged_cache *cache, const dflash_step *step,
                           const dflash_attention_args *args, void *workspace, size_t workspace_bytes, void *stream);
 
@@ -565,10 +566,11 @@ typedef struct dflash_verify_args {
  * from p_{n_draft}: the lowest index whose cumulative sum exceeds
  * u_token * total.  The tokens are then distributed as the target's own.
  * Probabilities need not sum to one, but to a finite float; NaN, infinite and
- * negative ones count as zero, and a draft outside [0, vocab) is rejected.  Where nothing is left
- * of p_j - q_j the token is drawn from p_j, and without any positive p_j it
- * is 0.  Sums are kept in two floats (2^-44) and taken in a fixed order; the
- * token always has weight where any entry has.  One launch, no workspace; the rows need no alignment beyond their type's. */
+ * negative ones count as zero, and a draft outside [0, vocab) is rejected.
+ * Where nothing is left of p_j - q_j the token is drawn from p_j, and without
+ * any positive p_j it is 0.  Sums are kept in two floats (2^-44) and taken in a
+ * fixed order; the token has weight where any entry has.  One launch, no
+ * workspace; the rows need no alignment beyond their type's. */
 int dflash_verify_tokens(const dflash_verify_args *args, void *stream);
 
 /* Release the handle (the workspace stays the caller's). */
