@@ -464,9 +464,9 @@ typedef struct dflash_append_args {
 } dflash_append_args;
 
 /* Queries and keys of the step's rows: per head x / sqrt(mean x^2 + eps) *
- * gain (the sum of x^2 a finite float), then RoPE (pairs j, j + rot_dim / 2; the rest of a head passes
- * through); keys and values go to their rows of the cache, queries to q_out,
- * each rounded once.  Row pointers start on 16-byte boundaries (bases and
+ * gain (the sum of x^2 a finite float), then RoPE (pairs j, j + rot_dim / 2;
+ * the rest of a head passes through); keys and values go to their rows of the
+ * cache, queries to q_out, each rounded once.  Row pointers start on 16-byte boundaries (bases and
  * strides).  Rows of the caches that no row of the step names stay as they
  * are; a row whose own index would be negative, or past the block table,
  * writes no key or value (its query is written).  No two rows of a step go to
@@ -500,11 +500,12 @@ typedef struct dflash_attention_args {
  * that element not finite (NaN within a tile of rows) in every row that sees
  * it, and only there; keys and values before the step's rows are finite or
  * spread to the whole sequence (the prefix's to the batch).  Scores and sums
- * are f32, of weights up to 2^8 times the largest's: values times that and the
- * number of keys are finite floats (f16 ones always are).  Softmax weights are rounded to the cache's type for the product
- * with V (f16: at 2^7 times their size, so that a key's share below 2^-32 of
- * the largest is what can be lost).  Two launches; one where there is no prefix
- * and the block table has room for at most 128 keys of a sequence. */
+ * are f32, of weights up to 2^8: values times that and the number of keys are
+ * finite floats (f16 ones always are).  Softmax weights are rounded to the
+ * cache's type for the product with V (f16: at 2^7 times their size, so that a
+ * key's share below 2^-32 of the largest is what can be lost).  Two launches;
+ * one where there is no prefix and the block table has room for at most 128 keys
+ * of a sequence. */
 int dflash_step_attention(const dflash_paged_cache *cache, const dflash_step *step,
                           const dflash_attention_args *args, void *workspace, size_t workspace_bytes, void *stream);
 
