@@ -78,7 +78,7 @@ def listed():
          "short": False, "shape_seed": 11},
         # a full server: finished sequences give way to prompts, the pool runs out before all of them are in
         {"name": "next-batch-4000", "op": "next", "n_seq": 4000, "page": 16, "prefix": 0, "len_lo": 0,
-         "len_hi": 3000, "prev_lo": 0, "prev_hi": 17, "rows_lo": 0, "rows_hi": 150, "verified": True, "done": 0.3,
+         "len_hi": 3000, "prev_lo": 0, "prev_hi": 17, "rows_lo": 0, "rows_hi": 150, "verified": True, "done": 0.02,
          "short": True, "shape_seed": 12},
     ]
 
@@ -151,7 +151,7 @@ def _next_pool(c):
     cols = max(-(-(n + t) // c["page"]) for n, t in zip(old, rows)) + 1
     held = sum(-(-n // c["page"]) for n in old)
     grow = sum(-(-t // c["page"]) + 1 for t in rows)
-    free = grow // 4 if c["short"] else grow
+    free = grow // 8 if c["short"] else grow
     return cols, held + free + 5, free
 
 
