@@ -343,7 +343,8 @@ def _round4(x):
     # e4m3: 4 significant bits down to 2^-6, then steps of 2^-9; ties to even
     a = (top / 6).clamp(max=448)
     e = torch.frexp(a)[1].clamp(min=-5) - 4
-    sc = torch.ldexp(torch.round(torch.ldexp(a, -e)), e).clamp(max=448)
+    step = ((e.long() + 1023) << 52).view(torch.float64).to(x.dtype)     # 2^e by its bits: pow() is not exact
+    sc = (torch.round(a / step) * step).clamp(max=448)
     fine = torch.isfinite(top)
     sc = torch.where(fine, sc, float("nan"))
     t, u = b.abs(), sc[..., None]
