@@ -461,11 +461,13 @@ typedef struct dflash_append_args {
                                 dtype; may be q itself when the types and
                                 strides are the same                       */
   int64_t q_out_stride;
+  int32_t interleaved;       /* RoPE pairs: 0: elements j, j + rot_dim / 2
+                                (halves), else 2 j, 2 j + 1                */
 } dflash_append_args;
 
 /* Queries and keys of the step's rows: per head x / sqrt(mean x^2 + eps) *
- * gain (the sum of x^2 a finite float), then RoPE (pairs j, j + rot_dim / 2;
- * the rest of a head passes through); keys and values go to their rows of the
+ * gain (the sum of x^2 a finite float), then RoPE (pairs as `interleaved`
+ * says; the rest of a head passes through); keys and values go to their rows of the
  * cache, queries to q_out, each rounded once.  Row pointers start on 16-byte boundaries (bases and
  * strides).  Rows of the caches that no row of the step names stay as they
  * are; a row whose own index would be negative, or past the block table,
@@ -537,6 +539,119 @@ int dflash_step_attention_plan(const dflash_paged_cache *cache, const dflash_ste
  * on this workspace completed: DFLASH_ERR_TIMEOUT when a bounded device-side
  * wait gave up (its rows then hold NaN). */
 int dflash_step_attention_status(const void *workspace, void *stream);
+
+/* ---- A cache held in 4 bits.
+ *
+ * A head row of head_dim elements goes in blocks of 16.  A block has a scale
+ * s (e4m3, one byte) and an element a code c (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * and a sign; two a byte, the even element in the low half); the element's
+ * value is c * s * unit.  72 bytes a row of 128 elements, where 16 bits take
+ * 256. */
+typedef struct dflash_packed_cache {
+  void *k, *v;               /* codes: head row (page, r, h) starts at
+                                page * page_stride + r * row_stride +
+                                h * head_stride, head_dim / 2 bytes        */
+  void *k_scale, *v_scale;   /* e4m3 scales: head_dim / 16 bytes a head row,
+                                by the scale strides                       */
+  int32_t dtype;             /* of queries, results and rounded rows:
+                                DFLASH_BF16 or DFLASH_F16                  */
+  int32_t n_pages;
+  int32_t page_size;         /* rows of a page: 16, 32, 64, 128 or 256     */
+  int32_t n_kv_heads;
+  int32_t head_dim;          /* 64 or 128                                  */
+  int64_t page_stride, row_stride, head_stride;   /* bytes, multiples of 16;
+                                k and v start on 16-byte boundaries        */
+  int64_t scale_page_stride, scale_row_stride, scale_head_stride;   /* bytes,
+                                multiples of head_dim / 16, as the bases   */
+  float k_unit, v_unit;      /* powers of two, 2^-60 .. 2^58: for rows whose
+                                largest elements lie outside 6 times e4m3's
+                                2^-9 .. 448 (1 for normed keys)            */
+} dflash_packed_cache;
+
+typedef struct dflash_packed_append_args {
+  dflash_append_args rows;   /* as of dflash_step_append                   */
+  void *k_values, *v_values; /* device [n_rows, n_kv_heads, head_dim] in the
+                                cache's dtype, or NULL: what the rows stand
+                                for once rounded                           */
+  int64_t k_values_stride, v_values_stride;
+} dflash_packed_append_args;
+
+/* dflash_step_append into a packed cache.  With y a key after norm and RoPE, or
+ * a value: s = max |y| / (6 unit) of the block rounded to e4m3 (nearest, ties to
+ * even, at most 448), c = y / (s unit) rounded to e2m1 (nearest, ties to the even
+ * code, at most 6; the sign kept, also of 0; 0 where s is).  A block with a NaN or an
+ * infinity gets s = NaN.  The codes are those of y in exact arithmetic (eps at
+ * least 2^-80, angles to 2^-40 of a turn at positions below 2^24): they do not
+ * depend on the order of sums, nor on the rows beside them.  Rows of k_values and
+ * v_values whose keys or values are not written stay as they are.  One launch. */
+int dflash_step_append_packed(const dflash_packed_cache *cache, const dflash_step *step,
+                              const dflash_packed_append_args *args, void *stream);
+
+/* dflash_step_attention over a packed cache: the same arguments, results,
+ * workspace rules and status (dflash_step_attention_status), queries and results
+ * in the cache's dtype.  Keys and values are what their codes and scales stand
+ * for, exactly; softmax weights are rounded to f16 (at 2^7 times their size) for
+ * the product with V.  Results are finite floats while unit * 2688 times the
+ * number of keys is.  What the cache holds past a sequence's or the prefix's
+ * last key has no effect.  A NaN scale leaves its block's 16 elements NaN in every row
+ * that sees the key (of a key: the row's whole result) and, in the step's own rows,
+ * only there; before the step's rows it may spread to the whole sequence (the
+ * prefix's to the batch). */
+int dflash_step_attention_packed_workspace(const dflash_packed_cache *cache, int32_t n_rows, int32_t n_heads,
+                                           size_t *bytes);
+int dflash_step_attention_packed(const dflash_packed_cache *cache, const dflash_step *step,
+                                 const dflash_attention_args *args, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/* ---- The tables of the next step, from what stands of the last one.
+ *
+ * Per sequence of n = kv_len keys, T = row_start[i+1] - row_start[i] of them the
+ * last step's rows: kept = min(keep, n) where keep >= 0 (0: the sequence is
+ * over), else n - T + min(T, 1 + n_accepted) where n_accepted >= 0 (the step's
+ * first row and its accepted drafts stand), else n.  It is given the rows[i] it asks
+ * for (less than 1: none; more than its row of the table has pages for: none), in order,
+ * up to the first sequence that the free pages or n_rows do not last for: that one
+ * and those behind it get none.  (Pages to spare: those free before, and those that
+ * become free if all get what they ask for.)
+ *
+ * Outputs: kv_len = kept + rows given, row_start, and the free stack's height
+ * n_free.  Pages a sequence no longer needs go on the stack (free_pages, written
+ * from its old height on), the last sequence's last page first; then the pages
+ * that sequences need come off its top, the first sequence's first page first, into
+ * the block table.  So giving back what the last call took leaves the stack as it
+ * was.  Entries of the table behind a sequence's last page stay as they are. */
+typedef struct dflash_next_step_args {
+  int32_t n_seq;              /* 1 .. 4096                                 */
+  int32_t page_size;          /* 16, 32, 64, 128 or 256                    */
+  int32_t table_cols;
+  int32_t n_pages;            /* places of free_pages                      */
+  int32_t n_rows;             /* most rows of the step                     */
+  int32_t prefix_len;         /* added to positions                        */
+  int64_t table_stride;       /* elements between the table's rows         */
+  const int32_t *kv_len;      /* device [n_seq]                            */
+  const int32_t *row_start;   /* device [n_seq + 1]                        */
+  const int32_t *n_free;      /* device [1]                                */
+  const int32_t *rows;        /* device [n_seq]                            */
+  const int32_t *n_accepted;  /* device [n_seq], or NULL                   */
+  const int32_t *keep;        /* device [n_seq], or NULL                   */
+  int32_t *block_table;       /* device [n_seq, table_cols], in and out    */
+  int32_t *free_pages;        /* device [n_pages], in and out              */
+  int32_t *kv_len_out;        /* may be kv_len                             */
+  int32_t *row_start_out;     /* may be row_start                          */
+  int32_t *n_free_out;        /* may be n_free                             */
+  int64_t *slots;             /* device [n_rows]: page * page_size + row of
+                                 the page; or NULL, like the next two      */
+  int32_t *positions;         /* device [n_rows]: prefix_len + own index   */
+  int32_t *sequences;         /* device [n_rows]: whose row it is          */
+  uint32_t *ticket;           /* device [1], 0 before the first call; calls
+                                 with one ticket must not overlap          */
+} dflash_next_step_args;
+
+/* Rows of slots, positions and sequences behind the last one given stay as they
+ * are.  With other outputs than inputs the call can be repeated: it plans the same
+ * step.  Lengths and heights out of range are bounded to the table and the stack; a
+ * page id is passed on as it is.  One launch, no workspace, no waiting. */
+int dflash_next_step(const dflash_next_step_args *args, void *stream);
 
 typedef struct dflash_verify_args {
   int32_t n_seq;

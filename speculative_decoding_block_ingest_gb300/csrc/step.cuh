@@ -50,6 +50,7 @@ struct AppendArgs {
   const float* k_gain;
   float eps;
   int rot;
+  int interleaved;        // pairs (2j, 2j + 1) instead of (j, j + rot / 2)
   float mscale;
   const int* positions;
   void* q_out;
@@ -58,6 +59,19 @@ struct AppendArgs {
 };
 // in_dtype / out_dtype: dflash_dtype values of q, k, v and of the cache
 cudaError_t launch_step_append(const AppendArgs& a, int in_dtype, int out_dtype, int n_sm, cudaStream_t s);
+
+// The same into a packed cache (fp4.cuh): a.c and sc give the codes' and the
+// scales' places in bytes.
+struct Append4Args {
+  AppendArgs a;
+  CacheView sc;
+  double eps, mscale;   // as given, for what is computed again in 64 bits
+  float k_unit, v_unit, k_inv_unit, v_inv_unit;
+  void* k_values;       // the rounded rows in the queries' type, or null
+  void* v_values;
+  long k_values_stride, v_values_stride;
+};
+cudaError_t launch_step_append4(const Append4Args& a, int in_dtype, int out_dtype, int n_sm, cudaStream_t s);
 
 struct VerifyArgs {
   int n_seq, k, vocab;
@@ -76,6 +90,37 @@ struct VerifyArgs {
 };
 cudaError_t launch_verify(const VerifyArgs& a, int dtype, int n_sm, cudaStream_t s);
 
+struct NextArgs {
+  int n_seq, page_shift, table_cols, n_pages, n_rows, prefix_len;
+  long table_stride;
+  const int* kv_len;
+  const int* row_start;
+  const int* n_free;
+  const int* rows;
+  const int* n_accepted;   // or null
+  const int* keep;         // or null
+  int* block_table;
+  int* free;
+  int* kv_len_out;
+  int* row_start_out;
+  int* n_free_out;
+  long long* slots;        // or null, like the next two
+  int* positions;
+  int* sequences;
+  unsigned* ticket;        // 0 between calls
+};
+cudaError_t launch_next_step(const NextArgs& a, int n_sm, cudaStream_t s);
+
+// A packed cache in bytes (fp4.cuh).
+struct PackedView {
+  const uint8_t* k;
+  const uint8_t* v;
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
+  long page_stride, row_stride, head_stride;
+  long scale_page_stride, scale_row_stride, scale_head_stride;
+};
+
 // Attention of a step (step_attn.cu; how it is cut into pieces: step_plan.cuh).
 constexpr int kStepStatusWords = 1024;   // most CTAs (one status word each)
 struct StepAttnArgs {
@@ -84,6 +129,8 @@ struct StepAttnArgs {
   int tpt;             // tokens of a 128-row tile: floor(128 / G)
   int causal;
   float scale_log2;    // scale * log2(e)
+  float out_scale;     // of the results
+  PackedView packed;   // launch_step_attention4's cache
   int bf16;            // else f16
   int box_rows, boxes; // rows of one cache box (a page, at most 128) and boxes of a 128-key tile
   void* out;
@@ -104,6 +151,9 @@ struct StepAttnArgs {
 };
 cudaError_t launch_step_attention(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMap& k,
                                   const CUtensorMap& v, cudaStream_t s);
+cudaError_t launch_step_attention4(const StepAttnArgs& a, const CUtensorMap& q, cudaStream_t s);
+// o = out_scale sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i over the fragments of every row that is not whole.
+cudaError_t launch_step_merge(const StepAttnArgs& a, cudaStream_t s);
 
 // The calling thread's error message (dflash_last_error); returns code.
 int report_error(int code, const char* message);

@@ -5,6 +5,7 @@
 //   y = x * rsqrt(mean(x^2) + eps) * gain          (where there is a gain)
 //   y_j, y_{j+h} = y_j c_j - y_{j+h} s_j, y_{j+h} c_j + y_j s_j,  h = rot / 2,
 //   c_j, s_j = mscale * cos, sin(p inv_freq_j)
+// (or on y_{2j}, y_{2j+1} where pairs are interleaved)
 // and values pass through.  Everything is read once and written once, a few
 // flops an element: bytes bound it, for one token the launch and a chain of
 // dependent loads (row -> sequence -> length -> page).
@@ -23,6 +24,7 @@
 #include "kernels.cuh"
 #include "ptx.cuh"
 #include "step.cuh"
+#include "step_rows.cuh"
 
 namespace dfl {
 namespace {
@@ -31,66 +33,13 @@ constexpr int kAppendThreads = 256;
 constexpr int kFewWarps = 8;      // warps of a row when there are few rows
 constexpr int kManyWarps = 1;     // and when there are many
 
-struct Chunk {
-  float v[8];
-};
-
-// Eight elements as loaded (16-bit ones stay packed while in flight).
-template <typename T>
-struct Raw {
-  uint4 u;
-  __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ Chunk get() const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    Chunk c;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float2 f;
-      if constexpr (std::is_same_v<T, __nv_bfloat16>)
-        f = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(w[i]));
-      else
-        f = __half22float2(reinterpret_cast<const __half2&>(w[i]));
-      c.v[2 * i] = f.x;
-      c.v[2 * i + 1] = f.y;
-    }
-    return c;
-  }
-};
-template <>
-struct Raw<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ __forceinline__ Chunk get() const { return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
-};
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const Chunk& c) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(c.v[2 * i], c.v[2 * i + 1]);
-    w[i] = reinterpret_cast<const uint32_t&>(b);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void store8(__half* p, const Chunk& c) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 b = __floats2half2_rn(c.v[2 * i], c.v[2 * i + 1]);
-    w[i] = reinterpret_cast<const uint32_t&>(b);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // Resident CTAs of an SM.  Many rows: four, each lane 2 head rows deep (1 in
 // f32): 34912 rows of 48 f16 heads in 148 us (6.2 TB/s), 32000 normed bf16 rows in
 // 145; three CTAs, two warps a row and 3 deep 148 and 152, deeper ones spill.
 // Few rows: one to four waves at any occupancy.
 constexpr int append_ctas(int warps) { return warps == kManyWarps ? 4 : 2; }
 
-template <typename In, typename Out, int D, int WARPS>
+template <typename In, typename Out, int D, int WARPS, bool INTER>
 __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
     step_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kLanes = D / 16;               // lanes of a head row
@@ -170,7 +119,7 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
       if (rot) {
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-          const float4 v = *reinterpret_cast<const float4*>(&cs[8 * l + j]);
+          const float4 v = *reinterpret_cast<const float4*>(pair_angles<INTER>(cs, j, c0, c1));
           w[j] = make_float2(v.x, v.y);
           w[j + 1] = make_float2(v.z, v.w);
         }
@@ -205,14 +154,7 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
           }
         }
         if (h >= heads || (!is_q && dst < 0)) continue;
-        if (rot && !is_v) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float u = y0.v[j], t = y1.v[j];
-            y0.v[j] = u * w[j].x - t * w[j].y;
-            y1.v[j] = t * w[j].x + u * w[j].y;
-          }
-        }
+        if (rot && !is_v) rotate<INTER>(y0, y1, w);
         Out* o = is_q   ? static_cast<Out*>(a.q_out) + row * a.q_out_stride + (long)h * D
                  : is_v ? static_cast<Out*>(a.c.v) + dst + (h - Hq - Hkv) * a.c.head_stride
                         : static_cast<Out*>(a.c.k) + dst + (h - Hq) * a.c.head_stride;
@@ -223,7 +165,7 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
   }
 }
 
-template <typename In, typename Out>
+template <bool INTER, typename In, typename Out>
 cudaError_t launch(const AppendArgs& a, int n_sm, cudaStream_t s) {
   // Eight warps a row up to four waves of them (bf16, 48 normed heads: 300 rows
   // 4.9 us against 11.0 with one warp, 1200 rows 10.9 against 11.3, 1600 rows 14.5
@@ -233,20 +175,25 @@ cudaError_t launch(const AppendArgs& a, int n_sm, cudaStream_t s) {
   const long ctas = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
   const long most = (long)append_ctas(few ? kFewWarps : kManyWarps) * n_sm;
   const dim3 grid((unsigned)(ctas < most ? ctas : most)), block(kAppendThreads);
-  auto* kernel = few ? (a.c.d == 128 ? step_append_kernel<In, Out, 128, kFewWarps>
-                                     : step_append_kernel<In, Out, 64, kFewWarps>)
-                     : (a.c.d == 128 ? step_append_kernel<In, Out, 128, kManyWarps>
-                                     : step_append_kernel<In, Out, 64, kManyWarps>);
+  auto* kernel = few ? (a.c.d == 128 ? step_append_kernel<In, Out, 128, kFewWarps, INTER>
+                                     : step_append_kernel<In, Out, 64, kFewWarps, INTER>)
+                     : (a.c.d == 128 ? step_append_kernel<In, Out, 128, kManyWarps, INTER>
+                                     : step_append_kernel<In, Out, 64, kManyWarps, INTER>);
   return launch_pdl(kernel, grid, block, 0, s, a);
+}
+
+template <bool INTER>
+cudaError_t launch(const AppendArgs& a, int in_dtype, int out_dtype, int n_sm, cudaStream_t s) {
+  if (out_dtype == DFLASH_BF16)
+    return in_dtype == DFLASH_F32 ? launch<INTER, float, __nv_bfloat16>(a, n_sm, s)
+                                  : launch<INTER, __nv_bfloat16, __nv_bfloat16>(a, n_sm, s);
+  return in_dtype == DFLASH_F32 ? launch<INTER, float, __half>(a, n_sm, s) : launch<INTER, __half, __half>(a, n_sm, s);
 }
 
 }  // namespace
 
 cudaError_t launch_step_append(const AppendArgs& a, int in_dtype, int out_dtype, int n_sm, cudaStream_t s) {
-  if (out_dtype == DFLASH_BF16)
-    return in_dtype == DFLASH_F32 ? launch<float, __nv_bfloat16>(a, n_sm, s)
-                                  : launch<__nv_bfloat16, __nv_bfloat16>(a, n_sm, s);
-  return in_dtype == DFLASH_F32 ? launch<float, __half>(a, n_sm, s) : launch<__half, __half>(a, n_sm, s);
+  return a.interleaved ? launch<true>(a, in_dtype, out_dtype, n_sm, s) : launch<false>(a, in_dtype, out_dtype, n_sm, s);
 }
 
 }  // namespace dfl

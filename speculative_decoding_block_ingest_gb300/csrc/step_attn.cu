@@ -41,18 +41,22 @@
 #include <atomic>
 
 #include "../../include/dflash.h"
+#include "fp4.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
+#include "step_attn.cuh"
 #include "step_plan.cuh"
 
 namespace dfl {
 namespace {
 
-constexpr int kStepThreads = 384;
-// registers of a softmax / other thread: 2 x 208 + 88 = 3 x 168, the launch's own
-constexpr int kSoftRegs = 208, kOtherRegs = 88;
+// threads, and registers of a softmax / other / rounding thread; together the
+// launch's own: 2 x 208 + 88 = 3 x 168, 2 x 176 + 72 + 88 = 4 x 128
+constexpr int step_threads(bool packed) { return packed ? 512 : 384; }
+constexpr int soft_regs(bool packed) { return packed ? 176 : 208; }
+constexpr int other_regs(bool packed) { return packed ? 72 : 88; }
+constexpr int kCodeRegs = 88;
 constexpr int kSoftThreads = 256;        // warps 0..7
-constexpr int kAtomBytes = kKeys * 128;  // 128 rows x 128 bytes
 constexpr int kMaxStages = 11;
 constexpr int kSharedBytes = 3 * 1024;   // control block
 constexpr size_t step_smem(int d, int stages) { return (size_t)(2 + stages) * (d / 64) * kAtomBytes + kSharedBytes; }
@@ -62,107 +66,6 @@ constexpr int step_stages(int d) {
   while (step_smem(d, n) > 227 * 1024) --n;
   return n;
 }
-constexpr float kGrow = 8.f;             // O is rescaled when a row's max grows by more than 2^8
-constexpr int kFrags = 2;                // fragments described ahead
-constexpr int kBarPair = 3;              // named barrier of the 256 softmax threads
-
-// ---------------------------------------------------------------- TMEM access
-// 128 columns of a row are loaded at once and waited for once; the wait takes
-// the registers as operands so that no use of them can move above it.
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld_wait32(float* v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
-                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
-                 "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
-                 "+f"(v[30]), "+f"(v[31])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16};" ::"r"(taddr),
-      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
-      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// 32 aligned bytes at once: rows of a tile lie far apart, so a lane's store
-// fills whole sectors by itself.
-__device__ __forceinline__ void store_sector(float* p, const float* v) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float m;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
-  return m;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-  return d;
-}
-// Two softmax weights (the lower key in the low half) or results in the
-// cache's type: the product with V takes both operands in one 16-bit type.  The
-// row sums add the unrounded weights, so the rounding (half a step, either way)
-// does not add up in the quotient.  f16 rounds to zero, always downward, below
-// 2^-25, and loses bits below 2^-14: its weights are taken times 2^7, the most
-// that keeps them (2^8 and less, see kGrow) in its range, so that what is lost
-// of a weight is at most 2^-32 of the row's maximum's.
-template <bool BF16>
-__device__ __forceinline__ float pack2(float2 p) {
-  if constexpr (BF16) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
-    return __uint_as_float(reinterpret_cast<const uint32_t&>(b));
-  } else {
-    const __half2 b = __floats2half2_rn(p.x, p.y);
-    return __uint_as_float(reinterpret_cast<const uint32_t&>(b));
-  }
-}
-
-// log of a row's sum of exponentials from its maximum (in log2 units) and sum
-__device__ __forceinline__ float log_sum(float m, float l) {
-  return l == 0.f ? -INFINITY : 0.69314718055994531f * (m + log2f(l));
-}
-
-// Descriptor of an MN-major tile in the 128-byte swizzle: rows are K (keys)
-// of 128 B (64 MN elements), 8-key atoms 1024 B apart along K, the next 64
-// MN elements one tile of 128 keys further.
-__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kAtomBytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-__device__ __forceinline__ void tma_load_4d(void* dst, const void* map, uint64_t* bar, int x, int y, int z, int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
-      "[%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
-}
-
 struct Shared {
   uint64_t kvfull[kMaxStages], kvempty[kMaxStages];
   uint64_t qfull[2], qempty[2], sfull[2], pfull[2][2], pvdone[2], kfirst[2];
@@ -179,60 +82,68 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= kSharedBytes, "control block of the attention kernel");
 
-// One lane of a converged warp, the same in every call.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-  return p != 0;
-}
-
-// Wait for the phase of `parity` of a pipeline barrier; false once `abort` is
-// raised or kWaitNs have passed (the clock is read once in 64 tries).
-__device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63) == 0) {
-      if (*abort) return false;
-      const uint64_t t = globaltimer();
-      if (t0 == 0) t0 = t;
-      else if (t - t0 > kWaitNs) return false;
+// ---------------------------------------------------------------- a packed cache
+// A head row of codes and scales on its way to a 16-bit tile.
+template <int D>
+struct CodeRow {
+  uint4 code[D / 32];
+  uint32_t scale[D / 64];
+  __device__ __forceinline__ void load(const void* c, const void* s) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) code[i] = static_cast<const uint4*>(c)[i];
+    if constexpr (D == 128) {
+      const uint2 t = *static_cast<const uint2*>(s);
+      scale[0] = t.x, scale[1] = t.y;
+    } else {
+      scale[0] = *static_cast<const uint32_t*>(s);
     }
   }
-}
-
-// Place of a K (kv = 0) or V (1) tile of a fragment's block among its 2 n
-// tiles.  A single item's two streams each hold a V tile while its softmax
-// runs, so the K tiles of both blocks go first: the next pair's keys land
-// meanwhile.
-__device__ __forceinline__ uint32_t tile_of(bool pair, int block, int n, int kv) {
-  if (pair) return 2 * block + kv;
-  const int first = block & ~1;
-  return 2 * first + (block & 1) + kv * min(2, n - first);
-}
-
-// Waits on the fragment ring outlast any one fragment; a failed wait
-// elsewhere ends the others within kWaitNs, so this limit is not met.
-__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity))
-    if (globaltimer() - t0 > 10 * kWaitNs) return false;
-  return true;
-}
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) code[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) scale[i] = 0;
+  }
+  // Row r of a swizzled K-major tile.  A code times its scale is exact in either type.
+  template <bool BF16>
+  __device__ __forceinline__ void put(uint8_t* tile, int r) const {
+#pragma unroll
+    for (int b = 0; b < D / 16; ++b) {
+      const uint4 c = code[b / 2];
+      const __half2 two = e4m3_to2(scale[b / 4] >> (16 * ((b / 2) & 1)) & 0xFFFF);
+      const __half2 f = b & 1 ? __high2half2(two) : __low2half2(two);
+      uint32_t h[8];
+      e2m1_to8(b & 1 ? c.z : c.x, h);
+      e2m1_to8(b & 1 ? c.w : c.y, h + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[i] = as_u32(__hmul2(as_half2(h[i]), f));
+        if constexpr (BF16) h[i] = __float_as_uint(pack2<true>(__half22float2(as_half2(h[i]))));
+      }
+      uint8_t* atom = tile + b / 4 * kAtomBytes + r * 128;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<uint4*>(atom + (((2 * b + i) & 7) ^ (r & 7)) * 16) =
+            make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+    }
+  }
+};
 
 // ---------------------------------------------------------------- the kernel
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kStepThreads, 1)
+// PACKED: the cache holds codes and scales, which four more warps turn into the
+// tiles that are loaded as they lie otherwise: K in the queries' type, V in f16.
+template <int D, bool BF16, bool PACKED>
+__global__ void __launch_bounds__(step_threads(PACKED), 1)
     step_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ StepAttnArgs a) {
   constexpr int kDAtoms = D / 64;
   constexpr int kTile = kDAtoms * kAtomBytes;          // a Q, K or V tile
   constexpr int kStages = step_stages(D);              // K and V tiles in flight
-  constexpr uint32_t kFmt = BF16 ? (1u << 7) | (1u << 10) : 0u;
-  constexpr uint32_t kIdescS = (1u << 4) | kFmt | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-  constexpr uint32_t kIdescO = (1u << 4) | kFmt | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
-  constexpr float kBias = BF16 ? 0.f : 7.f;            // weights, their sums and products are 2^kBias times as large
+  constexpr bool kVBF16 = BF16 && !PACKED;             // type of V and of the softmax weights
+  constexpr uint32_t kFmtS = BF16 ? (1u << 7) | (1u << 10) : 0u, kFmtO = kVBF16 ? kFmtS : 0u;
+  constexpr uint32_t kIdescS = (1u << 4) | kFmtS | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+  constexpr uint32_t kIdescO = (1u << 4) | kFmtO | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((128u >> 4) << 24);
+  constexpr float kBias = kVBF16 ? 0.f : 7.f;          // weights, their sums and products are 2^kBias times as large
   constexpr uint32_t kColO = 256;                      // TMEM: S / P of the streams at 0 and 128, O at 256 and 384
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
@@ -243,7 +154,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.kvfull[i], 1);
+      mbar_init(&sh.kvfull[i], PACKED ? 4 : 1);
       mbar_init(&sh.kvempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -258,14 +169,16 @@ __global__ void __launch_bounds__(kStepThreads, 1)
     mbar_init(&sh.drained, 1);
     for (int i = 0; i < kFrags; ++i) {
       mbar_init(&sh.ffull[i], 1);
-      mbar_init(&sh.fempty[i], 11);   // warps 8, 9 and 11 and eight softmax warps
+      mbar_init(&sh.fempty[i], PACKED ? 15 : 11);   // all warps but 10
     }
     sh.abort = 0;
     sh.any_bad = 0;
     fence_barrier_init();
     tma_prefetch_map(&tmQ);
-    tma_prefetch_map(&tmK);
-    tma_prefetch_map(&tmV);
+    if constexpr (!PACKED) {
+      tma_prefetch_map(&tmK);
+      tma_prefetch_map(&tmV);
+    }
   }
   if (tid < 128) sh.bad[tid] = INT_MAX;
   if (warp == 9) tmem_alloc(&sh.tmem, 512);
@@ -292,8 +205,80 @@ __global__ void __launch_bounds__(kStepThreads, 1)
     return f.seg >= 0;
   };
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (PACKED && warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCodeRegs));
+    // ------------------------------------------------------------------ codes to tiles
+    // A thread has a row of every tile, and the next two tiles' codes in flight.
+    bool ok = true;
+    uint32_t nkv = 0;
+    const int r = tid & 127;
+    Frag f;
+    while (take(f)) {
+      const int n = f.b1 - f.b0;
+      if (!ok || n <= 0) continue;
+      const bool pair = f.ntok > a.tpt;
+      const int* table = f.seg ? a.s.block_table + f.seq * a.s.table_stride : a.s.prefix_pages;
+      // the page of this row's key in a block of the fragment (-1: no such key, or page)
+      auto page_of = [&](int block) -> int {
+        const long key = (long)(f.b0 + block) * kKeys + r;
+        const int page = block < n && key < f.keys ? table[key >> a.s.page_shift] : -1;
+        return page < a.s.n_pages ? page : -1;
+      };
+      // pages of two blocks, and of the two behind them
+      int even = page_of(0), odd = page_of(1), even2 = page_of(2), odd2 = page_of(3);
+      auto block_of = [&](int t, int& kv) {   // the inverse of tile_of
+        if (pair) {
+          kv = t & 1;
+          return t >> 1;
+        }
+        const int first = t >> 2 << 1, m = min(2, n - first), w = t & 3;
+        kv = w >= m;
+        return first + w - kv * m;
+      };
+      auto load = [&](CodeRow<D>& x, int t) {
+        if (t >= 2 * n) return;
+        if (t > 0 && (t & 3) == 0) {
+          even = even2, odd = odd2;
+          even2 = page_of((t >> 1) + 2), odd2 = page_of((t >> 1) + 3);
+        }
+        int kv;
+        const int block = block_of(t, kv), page = block & 1 ? odd : even;
+        if (page >= 0) {
+          const long at = ((f.b0 + block) * kKeys + r) & (a.s.page_size - 1);
+          const PackedView& c = a.packed;
+          x.load((kv ? c.v : c.k) + page * c.page_stride + at * c.row_stride + f.h * c.head_stride,
+                 (kv ? c.v_scale : c.k_scale) + page * c.scale_page_stride + at * c.scale_row_stride +
+                     f.h * c.scale_head_stride);
+        } else {
+          x.clear();
+        }
+      };
+      auto put = [&](const CodeRow<D>& x, int t) {
+        const uint32_t tile = nkv + t, st = tile % kStages;
+        if (ok) ok = __all_sync(0xffffffffu, pipe_wait(&sh.kvempty[st], ((tile / kStages) & 1) ^ 1, abort));
+        if (!ok) return;
+        int kv;
+        block_of(t, kv);
+        if (kv) x.template put<false>(sKV + st * kTile, r);
+        else x.template put<BF16>(sKV + st * kTile, r);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.kvfull[st]);
+      };
+      CodeRow<D> x0, x1;
+      load(x0, 0);
+      load(x1, 1);
+      for (int t = 0; t < 2 * n && ok; t += 2) {
+        put(x0, t);
+        load(x0, t + 2);
+        put(x1, t + 1);
+        load(x1, t + 3);
+      }
+      nkv += 2 * n;
+    }
+    if (!ok) sh.abort = 1;
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(PACKED)));
     if (warp == 8) {
       // ------------------------------------------------------------------ TMA
       bool ok = true;
@@ -317,6 +302,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
           }
           __syncwarp();
         }
+        if constexpr (PACKED) continue;
         // page ids: one lane per box of the next 32, the following 32 in flight
         const int* table = f.seg ? a.s.block_table + f.seq * a.s.table_stride : a.s.prefix_pages;
         const int n_box = (f.keys + a.box_rows - 1) >> box_shift;
@@ -531,7 +517,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(soft_regs(PACKED)));
     // ------------------------------------------------------------------ softmax
     const int st = warp >> 2;                        // stream
     const int r = tid & 127;                         // row of its tile
@@ -559,11 +545,12 @@ __global__ void __launch_bounds__(kStepThreads, 1)
         const int key0 = (f.b0 + bi) * kKeys;
         if (ok && !__all_sync(0xffffffffu, pipe_wait(&sh.sfull[st], np & 1, abort))) ok = false;
         tc_fence_after();
-        // V rows behind the last key hold anything: zero them.  Own keys that
+        // V rows behind the last key hold anything: zero them (rounding threads
+        // put zeros there).  Own keys that
         // some row of the step must not see may hold anything too: their
         // elements that are not finite are taken out and remembered.
         const int own0 = causal && f.lim0 < f.keys ? max(f.lim0, 0) : INT_MAX;   // first key not seen by all rows
-        if (ok && (st == 0 || !pair) && (key0 + kKeys > f.keys || key0 + kKeys > own0)) {
+        if (ok && (st == 0 || !pair) && ((!PACKED && key0 + kKeys > f.keys) || key0 + kKeys > own0)) {
           // (a pair shares the tile and its streams' products come in turn, so
           // stream 0 does it for both; the slot's use before this one is over,
           // because the scores just read were issued behind its product)
@@ -571,13 +558,13 @@ __global__ void __launch_bounds__(kStepThreads, 1)
           if (!__all_sync(0xffffffffu, pipe_wait(&sh.kvfull[stage], (tile / kStages) & 1, abort))) ok = false;
           uint8_t* v = sKV + stage * kTile + r * 128;
           const int key = key0 + r;
-          if (key >= f.keys) {
+          if (!PACKED && key >= f.keys) {
 #pragma unroll
             for (int c = 0; c < 8 * kDAtoms; ++c)
               *reinterpret_cast<uint4*>(v + (c >> 3) * kAtomBytes + ((c & 7) ^ (r & 7)) * 16) = make_uint4(0, 0, 0, 0);
-          } else if (key >= own0) {
+          } else if (key >= own0 && key < f.keys) {
             // an exponent of ones carries into the sign's place
-            constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
+            constexpr uint32_t kExp = kVBF16 ? 0x7F807F80u : 0x7C007C00u, kOne = kVBF16 ? 0x00800080u : 0x04000400u;
             auto odd = [&](uint32_t x) { return ((x & kExp) + kOne) & 0x80008000u; };
 #pragma unroll 4
             for (int c = 0; c < 8 * kDAtoms; ++c) {
@@ -652,7 +639,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
               p.x = ex2_fast(p.x);
               p.y = ex2_fast(p.y);
               sum[v & 1] = add2(sum[v & 1], p);
-              pw[v] = pack2<BF16>(p);
+              pw[v] = pack2<kVBF16>(p);
             }
             tmem_st16(s_addr + i / 2, pw);
             if (i % 64 == 32) {
@@ -707,7 +694,7 @@ __global__ void __launch_bounds__(kStepThreads, 1)
       }
       // a row whose every key was here needs no merge: its result as it stands
       const bool whole = f.first && f.last_cta == (int)blockIdx.x && a.s.prefix_len == 0;
-      const float inv = !ok ? __int_as_float(0x7fc00000) : (l0 == 0.f ? 0.f : 1.f / l0);
+      const float inv = !ok ? __int_as_float(0x7fc00000) : (l0 == 0.f ? 0.f : (PACKED ? a.out_scale : 1.f) / l0);
       const bool empty = pair ? cnt == 0 : n == 0;
       const bool poisoned = sh.any_bad;
       // a pair's streams write their own rows; of a single item each writes
@@ -917,7 +904,7 @@ __device__ __forceinline__ void merge_row(const StepAttnArgs& a, bool live, long
     }
     m = mn;
   }
-  const float inv = bad ? __int_as_float(0x7fc00000) : (l == 0.f ? 0.f : 1.f / l);
+  const float inv = bad ? __int_as_float(0x7fc00000) : (l == 0.f ? 0.f : a.out_scale / l);
   Out* dst = static_cast<Out*>(a.out) + row * a.out_stride + (long)head * D + lane * kPer;
   uint32_t y[kPer / 2];
 #pragma unroll
@@ -975,9 +962,28 @@ __global__ void __launch_bounds__(kMergeThreads, 8) step_merge_kernel(const __gr
 }
 
 template <int D, bool BF16>
+cudaError_t merge(const StepAttnArgs& a, cudaStream_t s) {
+  // items of at most one block are whole: nothing to merge (48 single tokens 11.8 -> 10.5 us,
+  // 56 short verifications 32.0 -> 23.7)
+  if (a.s.prefix_len == 0 && a.s.room() <= kKeys) return cudaSuccess;
+  // a block, a warp or half a warp for every (row, head), as many as run at
+  // once; or sixteen blocks for every CTA's last item
+  using Out = std::conditional_t<BF16, __nv_bfloat16, __half>;
+  const long items = (long)a.s.n_rows * a.Hq, resident = 8L * a.n_cta;
+  auto run = [&](auto* kernel, long blocks) {
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kMergeThreads), 0, s, a);
+  };
+  if (a.by_cta) return run(step_merge_kernel<D, Out, 1, 16>, (long)a.n_cta * kSplitBlocks);
+  if (items <= resident) return run(step_merge_kernel<D, Out, kMergeWarps, 32>, items);
+  if (items <= resident * kMergeWarps)
+    return run(step_merge_kernel<D, Out, 1, 32>, (items + kMergeWarps - 1) / kMergeWarps);
+  return run(step_merge_kernel<D, Out, 1, 16>, (items + 2 * kMergeWarps - 1) / (2 * kMergeWarps));
+}
+
+template <int D, bool BF16, bool PACKED>
 cudaError_t launch(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                    cudaStream_t s) {
-  auto* attn = step_attn_kernel<D, BF16>;
+  auto* attn = step_attn_kernel<D, BF16, PACKED>;
   const size_t smem = step_smem(D, step_stages(D));
   // the kernel's shared memory is raised once on every device
   static std::atomic<uint64_t> raised{0};
@@ -989,31 +995,27 @@ cudaError_t launch(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMa
     if (e != cudaSuccess) return e;
     if (dev < 64) raised.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
-  e = launch_pdl(attn, dim3(a.n_cta), dim3(kStepThreads), smem, s, q, k, v, a);
+  e = launch_pdl(attn, dim3(a.n_cta), dim3(step_threads(PACKED)), smem, s, q, k, v, a);
   if (e != cudaSuccess) return e;
-  // items of at most one block are whole: nothing to merge (48 single tokens 11.8 -> 10.5 us,
-  // 56 short verifications 32.0 -> 23.7)
-  if (a.s.prefix_len == 0 && a.s.room() <= kKeys) return cudaSuccess;
-  // a block, a warp or half a warp for every (row, head), as many as run at
-  // once; or sixteen blocks for every CTA's last item
-  using Out = std::conditional_t<BF16, __nv_bfloat16, __half>;
-  const long items = (long)a.s.n_rows * a.Hq, resident = 8L * a.n_cta;
-  auto merge = [&](auto* kernel, long blocks) {
-    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kMergeThreads), 0, s, a);
-  };
-  if (a.by_cta) return merge(step_merge_kernel<D, Out, 1, 16>, (long)a.n_cta * kSplitBlocks);
-  if (items <= resident) return merge(step_merge_kernel<D, Out, kMergeWarps, 32>, items);
-  if (items <= resident * kMergeWarps)
-    return merge(step_merge_kernel<D, Out, 1, 32>, (items + kMergeWarps - 1) / kMergeWarps);
-  return merge(step_merge_kernel<D, Out, 1, 16>, (items + 2 * kMergeWarps - 1) / (2 * kMergeWarps));
+  return merge<D, BF16>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_step_attention(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMap& k,
                                   const CUtensorMap& v, cudaStream_t s) {
-  if (a.d == 128) return a.bf16 ? launch<128, true>(a, q, k, v, s) : launch<128, false>(a, q, k, v, s);
-  return a.bf16 ? launch<64, true>(a, q, k, v, s) : launch<64, false>(a, q, k, v, s);
+  if (a.d == 128) return a.bf16 ? launch<128, true, false>(a, q, k, v, s) : launch<128, false, false>(a, q, k, v, s);
+  return a.bf16 ? launch<64, true, false>(a, q, k, v, s) : launch<64, false, false>(a, q, k, v, s);
+}
+
+cudaError_t launch_step_attention4(const StepAttnArgs& a, const CUtensorMap& q, cudaStream_t s) {
+  if (a.d == 128) return a.bf16 ? launch<128, true, true>(a, q, q, q, s) : launch<128, false, true>(a, q, q, q, s);
+  return a.bf16 ? launch<64, true, true>(a, q, q, q, s) : launch<64, false, true>(a, q, q, q, s);
+}
+
+cudaError_t launch_step_merge(const StepAttnArgs& a, cudaStream_t s) {
+  if (a.d == 128) return a.bf16 ? merge<128, true>(a, s) : merge<128, false>(a, s);
+  return a.bf16 ? merge<64, true>(a, s) : merge<64, false>(a, s);
 }
 
 }  // namespace dfl

@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <utility>
 
 #include "../../include/dflash.h"
 #include "dflash_internal.cuh"
@@ -151,15 +152,11 @@ void set_shape(StepAttnArgs& a, const dflash_paged_cache* c, int n_heads) {
   a.tpt = 128 / a.G;
 }
 
-}  // namespace
+bool rows_ok(const void* ptr, long stride, long elements, long v) {
+  return aligned(ptr, 16) && stride >= elements && stride % v == 0;
+}
 
-extern "C" {
-
-int dflash_step_append(const dflash_paged_cache* cache, const dflash_step* step, const dflash_append_args* p,
-                       void* stream) {
-  report_error(DFLASH_OK, "");
-  if (int rc = check_cache(cache)) return rc;
-  if (int rc = check_step(cache, step)) return rc;
+int check_append(const dflash_paged_cache* cache, const dflash_step* step, const dflash_append_args* p) {
   if (!p) return invalid("args is null");
   if (p->dtype != DFLASH_F32 && p->dtype != cache->dtype)
     return fail(DFLASH_ERR_UNSUPPORTED, "rows must be DFLASH_F32 or of the cache's dtype");
@@ -170,19 +167,19 @@ int dflash_step_append(const dflash_paged_cache* cache, const dflash_step* step,
   if ((p->q_gain || p->k_gain) && !((float)p->eps > 0)) return invalid("eps must be > 0 in f32");
   if (step->n_rows == 0) return DFLASH_OK;
   if (!p->k || !p->v || (p->n_heads > 0 && (!p->q || !p->q_out))) return invalid("row pointer is null");
-  const int d = cache->head_dim;
-  const long vec = p->dtype == DFLASH_F32 ? 4 : 8;
-  auto rows_ok = [&](const void* ptr, long stride, long heads, long v) {
-    return aligned(ptr, 16) && stride >= heads * d && stride % v == 0;
-  };
-  if (!rows_ok(p->k, p->k_stride, cache->n_kv_heads, vec) || !rows_ok(p->v, p->v_stride, cache->n_kv_heads, vec) ||
-      (p->n_heads > 0 &&
-       (!rows_ok(p->q, p->q_stride, p->n_heads, vec) || !rows_ok(p->q_out, p->q_out_stride, p->n_heads, 8))))
+  const long v = p->dtype == DFLASH_F32 ? 4 : 8, kv = (long)cache->n_kv_heads * cache->head_dim,
+             q = (long)p->n_heads * cache->head_dim;
+  if (!rows_ok(p->k, p->k_stride, kv, v) || !rows_ok(p->v, p->v_stride, kv, v) ||
+      (p->n_heads > 0 && (!rows_ok(p->q, p->q_stride, q, v) || !rows_ok(p->q_out, p->q_out_stride, q, 8))))
     return invalid("rows must start on 16-byte boundaries and strides hold a row");
   if (!aligned(p->q_gain, 16) || !aligned(p->k_gain, 16)) return invalid("gains must start on a 16-byte boundary");
-  AppendArgs a{};
+  return DFLASH_OK;
+}
+
+// All of an append's arguments but the cache's.
+int append_args(AppendArgs& a, const dflash_paged_cache* cache, const dflash_step* step,
+                const dflash_append_args* p) {
   a.s = view(cache, step);
-  a.c = {cache->k, cache->v, cache->page_stride, cache->row_stride, cache->head_stride, cache->n_kv_heads, d};
   a.q = p->q;
   a.k = p->k;
   a.v = p->v;
@@ -194,6 +191,7 @@ int dflash_step_append(const dflash_paged_cache* cache, const dflash_step* step,
   a.k_gain = p->k_gain;
   a.eps = (float)p->eps;
   a.rot = p->rot_dim;
+  a.interleaved = p->interleaved != 0;
   a.mscale = (float)p->mscale;
   a.positions = p->positions;
   a.q_out = p->q_out;
@@ -203,10 +201,155 @@ int dflash_step_append(const dflash_paged_cache* cache, const dflash_step* step,
     if (!std::isfinite(t)) return invalid("RoPE frequencies");
     a.turns[i] = (uint64_t)std::ldexp(t - std::floor(t), 64);
   }
+  return DFLASH_OK;
+}
+
+// A packed cache's shape, for the checks that know the other kind.
+dflash_paged_cache shape_of(const dflash_packed_cache* c) {
+  dflash_paged_cache s{};
+  s.dtype = c->dtype;
+  s.n_pages = c->n_pages;
+  s.page_size = c->page_size;
+  s.n_kv_heads = c->n_kv_heads;
+  s.head_dim = c->head_dim;
+  return s;
+}
+
+int check_packed_shape(const dflash_packed_cache* c) {
+  if (!c) return invalid("cache is null");
+  const dflash_paged_cache s = shape_of(c);
+  return check_cache_shape(&s);
+}
+
+// a power of two whose products and quotients with codes stay floats
+bool is_unit(float u) {
+  int e = 0;
+  return std::isfinite(u) && u > 0 && std::frexp(u, &e) == 0.5f && e > -60 && e < 60;
+}
+
+int check_packed(const dflash_packed_cache* c) {
+  if (int rc = check_packed_shape(c)) return rc;
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return invalid("cache pointer is null");
+  if (c->n_pages < 1) return invalid("n_pages must be positive");
+  const long row = c->head_dim / 2, sc = c->head_dim / 16;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, sc) || !aligned(c->v_scale, sc))
+    return invalid("codes must start on a 16-byte boundary, scales on a head row's");
+  for (long st : {(long)c->page_stride, (long)c->row_stride, (long)c->head_stride})
+    if (st < row || st % 16 || st >= (1L << 38)) return invalid("code strides must be multiples of 16 bytes that hold a head row");
+  for (long st : {(long)c->scale_page_stride, (long)c->scale_row_stride, (long)c->scale_head_stride})
+    if (st < sc || st % sc || st >= (1L << 38)) return invalid("scale strides must be multiples of a head row's scales");
+  if (!is_unit(c->k_unit) || !is_unit(c->v_unit)) return invalid("units must be powers of two between 2^-60 and 2^58");
+  return DFLASH_OK;
+}
+
+int check_attention(const dflash_paged_cache* cache, const dflash_step* step, const dflash_attention_args* p,
+                    const void* workspace) {
+  if (!p) return invalid("args is null");
+  if (int rc = check_heads(cache, p->n_heads)) return rc;
+  if (int rc = check_rows(step->n_rows, p->n_heads)) return rc;
+  if (!std::isfinite(p->scale) || p->scale < 0) return invalid("scale must be finite and not negative");
+  if (!workspace || !aligned(workspace, 256)) return invalid("workspace must start on a 256-byte boundary");
+  const int d = cache->head_dim;
+  if (step->n_rows > 0) {
+    if (!p->q || !p->out) return invalid("row pointer is null");
+    if (!aligned(p->q, 16) || !aligned(p->out, 16) || p->q_stride % 8 || p->out_stride % 8 ||
+        p->q_stride < (long)p->n_heads * d || p->out_stride < (long)p->n_heads * d || p->q_stride >= (1L << 38))
+      return invalid("rows must start on 16-byte boundaries and strides hold a row");
+  }
+  return DFLASH_OK;
+}
+
+// All of an attention's arguments but the cache's.
+int attention_args(StepAttnArgs& a, const dflash_paged_cache* cache, const dflash_step* step,
+                   const dflash_attention_args* p) {
+  a.s = view(cache, step);
+  set_shape(a, cache, p->n_heads);
+  if (int rc = step_ctas(&a.n_cta)) return rc;
+  a.causal = p->causal != 0;
+  if (!step_fits(a, a.s.room())) return fail(DFLASH_ERR_UNSUPPORTED, "more work than one call takes: fewer rows");
+  const float scale = p->scale > 0 ? p->scale : 1.f / std::sqrt((float)cache->head_dim);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.out_scale = 1.f;
+  a.bf16 = cache->dtype == DFLASH_BF16;
+  a.box_rows = cache->page_size < kKeys ? cache->page_size : kKeys;
+  a.boxes = kKeys / a.box_rows;
+  a.out = p->out;
+  a.out_stride = p->out_stride;
+  a.lse = p->lse;
+  // Without a prefix only the rows of items that go on in another CTA have
+  // something to merge, at most 256 a CTA: worth looking for them there where
+  // there are many more (four prompts of 2000 rows: 178 us against 223; 32
+  // single tokens 24.9 against 22.8).
+  a.by_cta = step->prefix_len == 0 && (long)step->n_rows * p->n_heads > 256L * a.n_cta;
+  return DFLASH_OK;
+}
+
+int has_workspace(size_t bytes, size_t need) {
+  if (bytes < need) return fail(DFLASH_ERR_CAPACITY, "workspace holds %zu bytes, %zu needed", bytes, need);
+  return DFLASH_OK;
+}
+
+bool encode_queries(CUtensorMap* m, const StepAttnArgs& a, const dflash_attention_args* p, int dtype) {
+  const uint64_t dims[3] = {(uint64_t)a.d, (uint64_t)p->n_heads, (uint64_t)a.s.n_rows};
+  const uint64_t strides[2] = {(uint64_t)a.d * 2, (uint64_t)p->q_stride * 2};
+  const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.tpt};
+  return encode_tiled_map(m, dtype, 3, p->q, dims, strides, box);
+}
+
+}  // namespace
+
+extern "C" {
+
+int dflash_step_append(const dflash_paged_cache* cache, const dflash_step* step, const dflash_append_args* p,
+                       void* stream) {
+  report_error(DFLASH_OK, "");
+  if (int rc = check_cache(cache)) return rc;
+  if (int rc = check_step(cache, step)) return rc;
+  if (int rc = check_append(cache, step, p)) return rc;
+  if (step->n_rows == 0) return DFLASH_OK;
+  AppendArgs a{};
+  if (int rc = append_args(a, cache, step, p)) return rc;
+  a.c = {cache->k, cache->v, cache->page_stride, cache->row_stride, cache->head_stride, cache->n_kv_heads,
+         cache->head_dim};
   int n_sm = 0;
   if (int rc = sm_count(&n_sm)) return rc;
   return launched(launch_step_append(a, p->dtype, cache->dtype, n_sm, static_cast<cudaStream_t>(stream)),
                   "step append");
+}
+
+int dflash_step_append_packed(const dflash_packed_cache* cache, const dflash_step* step,
+                              const dflash_packed_append_args* p, void* stream) {
+  report_error(DFLASH_OK, "");
+  if (int rc = check_packed(cache)) return rc;
+  const dflash_paged_cache shape = shape_of(cache);
+  if (int rc = check_step(&shape, step)) return rc;
+  if (!p) return invalid("args is null");
+  if (int rc = check_append(&shape, step, &p->rows)) return rc;
+  if (step->n_rows == 0) return DFLASH_OK;
+  for (auto [ptr, stride] : {std::pair<const void*, long>{p->k_values, p->k_values_stride},
+                             {p->v_values, p->v_values_stride}})
+    if (ptr && !rows_ok(ptr, stride, (long)cache->n_kv_heads * cache->head_dim, 8))
+      return invalid("rows must start on 16-byte boundaries and strides hold a row");
+  Append4Args a{};
+  if (int rc = append_args(a.a, &shape, step, &p->rows)) return rc;
+  a.a.c = {cache->k, cache->v, cache->page_stride, cache->row_stride, cache->head_stride, cache->n_kv_heads,
+           cache->head_dim};
+  a.sc = {cache->k_scale, cache->v_scale, cache->scale_page_stride, cache->scale_row_stride,
+          cache->scale_head_stride, cache->n_kv_heads, cache->head_dim};
+  a.eps = p->rows.eps;
+  a.mscale = p->rows.mscale;
+  a.k_unit = cache->k_unit;
+  a.v_unit = cache->v_unit;
+  a.k_inv_unit = 1.f / cache->k_unit;
+  a.v_inv_unit = 1.f / cache->v_unit;
+  a.k_values = p->k_values;
+  a.v_values = p->v_values;
+  a.k_values_stride = p->k_values_stride;
+  a.v_values_stride = p->v_values_stride;
+  int n_sm = 0;
+  if (int rc = sm_count(&n_sm)) return rc;
+  return launched(launch_step_append4(a, p->rows.dtype, cache->dtype, n_sm, static_cast<cudaStream_t>(stream)),
+                  "packed step append");
 }
 
 int dflash_step_attention_workspace(const dflash_paged_cache* cache, int32_t n_rows, int32_t n_heads, size_t* bytes) {
@@ -228,56 +371,56 @@ int dflash_step_attention(const dflash_paged_cache* cache, const dflash_step* st
   report_error(DFLASH_OK, "");
   if (int rc = check_cache(cache)) return rc;
   if (int rc = check_step(cache, step)) return rc;
-  if (!p) return invalid("args is null");
-  if (int rc = check_heads(cache, p->n_heads)) return rc;
-  if (int rc = check_rows(step->n_rows, p->n_heads)) return rc;
-  if (!std::isfinite(p->scale) || p->scale < 0) return invalid("scale must be finite and not negative");
-  if (!workspace || !aligned(workspace, 256)) return invalid("workspace must start on a 256-byte boundary");
-  const int d = cache->head_dim;
-  if (step->n_rows > 0) {
-    if (!p->q || !p->out) return invalid("row pointer is null");
-    if (!aligned(p->q, 16) || !aligned(p->out, 16) || p->q_stride % 8 || p->out_stride % 8 ||
-        p->q_stride < (long)p->n_heads * d || p->out_stride < (long)p->n_heads * d || p->q_stride >= (1L << 38))
-      return invalid("rows must start on 16-byte boundaries and strides hold a row");
-  }
+  if (int rc = check_attention(cache, step, p, workspace)) return rc;
   StepAttnArgs a{};
-  a.s = view(cache, step);
-  set_shape(a, cache, p->n_heads);
-  if (int rc = step_ctas(&a.n_cta)) return rc;
-  a.causal = p->causal != 0;
-  if (!step_fits(a, a.s.room())) return fail(DFLASH_ERR_UNSUPPORTED, "more work than one call takes: fewer rows");
-  const float scale = p->scale > 0 ? p->scale : 1.f / std::sqrt((float)d);
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.bf16 = cache->dtype == DFLASH_BF16;
-  a.box_rows = cache->page_size < kKeys ? cache->page_size : kKeys;
-  a.boxes = kKeys / a.box_rows;
-  a.out = p->out;
-  a.out_stride = p->out_stride;
-  a.lse = p->lse;
-  // Without a prefix only the rows of items that go on in another CTA have
-  // something to merge, at most 256 a CTA: worth looking for them there where
-  // there are many more (four prompts of 2000 rows: 178 us against 223; 32
-  // single tokens 24.9 against 22.8).
-  a.by_cta = step->prefix_len == 0 && (long)step->n_rows * p->n_heads > 256L * a.n_cta;
-  const size_t need = carve(a, static_cast<char*>(workspace));
-  if (workspace_bytes < need)
-    return fail(DFLASH_ERR_CAPACITY, "workspace holds %zu bytes, %zu needed", workspace_bytes, need);
+  if (int rc = attention_args(a, cache, step, p)) return rc;
+  if (int rc = has_workspace(workspace_bytes, carve(a, static_cast<char*>(workspace)))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (step->n_rows == 0) return launched(cudaMemsetAsync(a.status, 0, kStepStatusWords * 4, s), "step attention");
   CUtensorMap mq, mk, mv;
-  const uint64_t qdims[3] = {(uint64_t)d, (uint64_t)p->n_heads, (uint64_t)step->n_rows};
-  const uint64_t qstr[2] = {(uint64_t)d * 2, (uint64_t)p->q_stride * 2};
-  const uint32_t qbox[3] = {64, (uint32_t)a.G, (uint32_t)a.tpt};
-  const uint64_t cdims[4] = {(uint64_t)d, (uint64_t)cache->n_kv_heads, (uint64_t)cache->page_size,
+  const uint64_t cdims[4] = {(uint64_t)a.d, (uint64_t)cache->n_kv_heads, (uint64_t)cache->page_size,
                              (uint64_t)cache->n_pages};
   const uint64_t cstr[3] = {(uint64_t)cache->head_stride * 2, (uint64_t)cache->row_stride * 2,
                             (uint64_t)cache->page_stride * 2};
   const uint32_t cbox[4] = {64, 1, (uint32_t)a.box_rows, 1};
-  if (!encode_tiled_map(&mq, cache->dtype, 3, p->q, qdims, qstr, qbox) ||
+  if (!encode_queries(&mq, a, p, cache->dtype) ||
       !encode_tiled_map(&mk, cache->dtype, 4, cache->k, cdims, cstr, cbox) ||
       !encode_tiled_map(&mv, cache->dtype, 4, cache->v, cdims, cstr, cbox))
     return fail(DFLASH_ERR_CUDA, "tensor map of the queries or the cache was refused");
   return launched(launch_step_attention(a, mq, mk, mv, s), "step attention");
+}
+
+int dflash_step_attention_packed_workspace(const dflash_packed_cache* cache, int32_t n_rows, int32_t n_heads,
+                                           size_t* bytes) {
+  report_error(DFLASH_OK, "");
+  if (int rc = check_packed_shape(cache)) return rc;
+  const dflash_paged_cache shape = shape_of(cache);
+  return dflash_step_attention_workspace(&shape, n_rows, n_heads, bytes);
+}
+
+int dflash_step_attention_packed(const dflash_packed_cache* cache, const dflash_step* step,
+                                 const dflash_attention_args* p, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  report_error(DFLASH_OK, "");
+  if (int rc = check_packed(cache)) return rc;
+  const dflash_paged_cache shape = shape_of(cache);
+  if (int rc = check_step(&shape, step)) return rc;
+  if (int rc = check_attention(&shape, step, p, workspace)) return rc;
+  StepAttnArgs a{};
+  if (int rc = attention_args(a, &shape, step, p)) return rc;
+  a.scale_log2 *= cache->k_unit;
+  if (!std::isfinite(a.scale_log2) || a.scale_log2 < 1e-37f) return invalid("scale times the keys' unit must be a normal float");
+  a.out_scale = cache->v_unit;
+  a.packed = {static_cast<const uint8_t*>(cache->k),       static_cast<const uint8_t*>(cache->v),
+              static_cast<const uint8_t*>(cache->k_scale), static_cast<const uint8_t*>(cache->v_scale),
+              cache->page_stride,       cache->row_stride,       cache->head_stride,
+              cache->scale_page_stride, cache->scale_row_stride, cache->scale_head_stride};
+  if (int rc = has_workspace(workspace_bytes, carve(a, static_cast<char*>(workspace)))) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (step->n_rows == 0) return launched(cudaMemsetAsync(a.status, 0, kStepStatusWords * 4, s), "step attention");
+  CUtensorMap mq;
+  if (!encode_queries(&mq, a, p, cache->dtype)) return fail(DFLASH_ERR_CUDA, "tensor map of the queries was refused");
+  return launched(launch_step_attention4(a, mq, s), "packed step attention");
 }
 
 int dflash_step_attention_status(const void* workspace, void* stream) {
@@ -377,6 +520,49 @@ int dflash_verify_tokens(const dflash_verify_args* p, void* stream) {
   int n_sm = 0;
   if (int rc = sm_count(&n_sm)) return rc;
   return launched(launch_verify(a, p->dtype, n_sm, static_cast<cudaStream_t>(stream)), "verify tokens");
+}
+
+int dflash_next_step(const dflash_next_step_args* p, void* stream) {
+  report_error(DFLASH_OK, "");
+  if (!p) return invalid("args is null");
+  if (p->n_seq < 1 || p->n_seq > kMaxSeqs) return fail(DFLASH_ERR_INVALID_ARG, "n_seq must be 1..%d", kMaxSeqs);
+  if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1)))
+    return fail(DFLASH_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256");
+  if (p->n_rows < 0 || p->n_rows > kMaxRows) return invalid("n_rows out of range");
+  if (p->n_pages < 0 || p->table_cols < 0 || p->prefix_len < 0) return invalid("sizes must not be negative");
+  if ((long)p->prefix_len + (long)p->table_cols * p->page_size >= (1L << 31) - 256)
+    return invalid("more than 2^31 - 257 keys");
+  if ((long)p->n_seq * p->table_cols >= (1L << 31)) return invalid("block table of 2^31 pages or more");
+  if (p->n_seq > 1 && p->table_stride < p->table_cols) return invalid("the rows of the block table overlap");
+  if (!p->kv_len || !p->row_start || !p->n_free || !p->rows || !p->kv_len_out || !p->row_start_out ||
+      !p->n_free_out || !p->ticket || (p->table_cols > 0 && !p->block_table) || (p->n_pages > 0 && !p->free_pages))
+    return invalid("null argument");
+  NextArgs a{};
+  a.n_seq = p->n_seq;
+  a.page_shift = __builtin_ctz(p->page_size);
+  a.table_cols = p->table_cols;
+  a.n_pages = p->n_pages;
+  a.n_rows = p->n_rows;
+  a.prefix_len = p->prefix_len;
+  a.table_stride = p->table_stride;
+  a.kv_len = p->kv_len;
+  a.row_start = p->row_start;
+  a.n_free = p->n_free;
+  a.rows = p->rows;
+  a.n_accepted = p->n_accepted;
+  a.keep = p->keep;
+  a.block_table = p->block_table;
+  a.free = p->free_pages;
+  a.kv_len_out = p->kv_len_out;
+  a.row_start_out = p->row_start_out;
+  a.n_free_out = p->n_free_out;
+  a.slots = reinterpret_cast<long long*>(p->slots);
+  a.positions = p->positions;
+  a.sequences = p->sequences;
+  a.ticket = p->ticket;
+  int n_sm = 0;
+  if (int rc = sm_count(&n_sm)) return rc;
+  return launched(launch_next_step(a, n_sm, static_cast<cudaStream_t>(stream)), "next step");
 }
 
 }  // extern "C"

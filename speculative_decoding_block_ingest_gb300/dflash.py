@@ -31,7 +31,8 @@ EXPORTS = ("dflash_workspace_bytes", "dflash_create", "dflash_ingest_ctx", "dfla
            "dflash_profile_read", "dflash_launch_count", "dflash_trace_begin", "dflash_trace_launches",
            "dflash_selftest_wait_timeout", "dflash_attention_plan", "dflash_rope_frequencies", "dflash_step_append",
            "dflash_step_attention_workspace", "dflash_step_attention", "dflash_step_attention_status",
-           "dflash_step_attention_plan", "dflash_verify_tokens")
+           "dflash_step_attention_plan", "dflash_verify_tokens", "dflash_step_append_packed",
+           "dflash_step_attention_packed_workspace", "dflash_step_attention_packed", "dflash_next_step")
 TRACE_WORDS = 16   # u64 words per traced CTA (see dflash_trace_begin)
 KERNEL_KINDS = ("gemm", "attention", "combine", "init", "norm", "finish")
 
@@ -86,7 +87,23 @@ class AppendArgs(ctypes.Structure):
                 ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("q_gain", ctypes.c_void_p),
                 ("k_gain", ctypes.c_void_p), ("eps", ctypes.c_double), ("rot_dim", ctypes.c_int32),
                 ("inv_freq", ctypes.c_void_p), ("mscale", ctypes.c_double), ("positions", ctypes.c_void_p),
-                ("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_int64)]
+                ("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_int64), ("interleaved", ctypes.c_int32)]
+
+
+class PackedCacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64), ("scale_row_stride", ctypes.c_int64),
+                ("scale_head_stride", ctypes.c_int64), ("k_unit", ctypes.c_float), ("v_unit", ctypes.c_float)]
+
+
+class PackedAppendArgs(ctypes.Structure):
+    # (the rows' fields, padded as the structure they are in the header)
+    _fields_ = AppendArgs._fields_ + [("_pad", ctypes.c_int32), ("k_values", ctypes.c_void_p),
+                                      ("v_values", ctypes.c_void_p), ("k_values_stride", ctypes.c_int64),
+                                      ("v_values_stride", ctypes.c_int64)]
 
 
 class AttentionArgs(ctypes.Structure):
@@ -98,6 +115,14 @@ class AttentionArgs(ctypes.Structure):
 class StepPiece(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("cta", "segment", "seq", "kv_head", "row0", "n_tokens", "block0",
                                                "block1", "first", "last_cta")]
+
+
+class NextStepArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_seq", "page_size", "table_cols", "n_pages", "n_rows", "prefix_len")]
+                + [("table_stride", ctypes.c_int64)]
+                + [(n, ctypes.c_void_p) for n in ("kv_len", "row_start", "n_free", "rows", "n_accepted", "keep",
+                                                  "block_table", "free_pages", "kv_len_out", "row_start_out",
+                                                  "n_free_out", "slots", "positions", "sequences", "ticket")])
 
 
 class VerifyArgs(ctypes.Structure):
@@ -174,6 +199,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dflash_step_attention_status.argtypes = [vp, vp]
     lib.dflash_step_attention_plan.argtypes = [cache_p, step_p, i32, i32, i32, p32, ctypes.POINTER(StepPiece), i32]
     lib.dflash_verify_tokens.argtypes = [vp, vp]
+    lib.dflash_step_append_packed.argtypes = [vp, vp, vp, vp]
+    lib.dflash_step_attention_packed_workspace.argtypes = [vp, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
+    lib.dflash_step_attention_packed.argtypes = [vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.dflash_next_step.argtypes = [vp, vp]
     lib.dflash_destroy.argtypes = [vp]
     lib.dflash_destroy.restype = None
     lib.dflash_last_error.restype = ctypes.c_char_p
