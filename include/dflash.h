@@ -552,7 +552,8 @@ typedef struct dflash_packed_cache {
                                 page * page_stride + r * row_stride +
                                 h * head_stride, head_dim / 2 bytes        */
   void *k_scale, *v_scale;   /* e4m3 scales: head_dim / 16 bytes a head row,
-                                by the scale strides                       */
+                                by the scale strides; a head's rows of a
+                                page lie together                          */
   int32_t dtype;             /* of queries, results and rounded rows:
                                 DFLASH_BF16 or DFLASH_F16                  */
   int32_t n_pages;
@@ -561,8 +562,9 @@ typedef struct dflash_packed_cache {
   int32_t head_dim;          /* 64 or 128                                  */
   int64_t page_stride, row_stride, head_stride;   /* bytes, multiples of 16;
                                 k and v start on 16-byte boundaries        */
-  int64_t scale_page_stride, scale_row_stride, scale_head_stride;   /* bytes,
-                                multiples of head_dim / 16, as the bases   */
+  int64_t scale_page_stride, scale_row_stride, scale_head_stride;   /* bytes:
+                                the rows' head_dim / 16, the others
+                                multiples of 16, like the bases            */
   float k_unit, v_unit;      /* powers of two, 2^-60 .. 2^58: for rows whose
                                 largest elements lie outside 6 times e4m3's
                                 2^-9 .. 448 (1 for normed keys)            */

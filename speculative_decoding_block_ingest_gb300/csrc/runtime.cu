@@ -315,18 +315,35 @@ int report_error(int code, const char* message) {
   return code;
 }
 
-bool encode_tiled_map(CUtensorMap* m, int dtype, uint32_t rank, const void* base, const uint64_t* dims,
-                      const uint64_t* strides, const uint32_t* box) {
+namespace {
+bool encode_map(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, uint32_t rank, const void* base,
+                const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   try {
-    return tensor_map_encoder()(m,
-                                dtype == DFLASH_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                                rank, const_cast<void*>(base), dims, strides, box, estr,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return tensor_map_encoder()(m, type, rank, const_cast<void*>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   } catch (const CudaError&) {
     return false;
   }
+}
+}  // namespace
+
+bool encode_tiled_map(CUtensorMap* m, int dtype, uint32_t rank, const void* base, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box) {
+  return encode_map(m, dtype == DFLASH_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    CU_TENSOR_MAP_SWIZZLE_128B, rank, base, dims, strides, box);
+}
+
+bool encode_packed_map(CUtensorMap* m, int element_bytes, uint32_t rank, const void* base, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box) {
+  const auto type = element_bytes == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                    : element_bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_INT32
+                                         : CU_TENSOR_MAP_DATA_TYPE_INT64;
+  const auto swizzle = element_bytes > 1 ? CU_TENSOR_MAP_SWIZZLE_NONE
+                       : box[0] == 64    ? CU_TENSOR_MAP_SWIZZLE_64B
+                                         : CU_TENSOR_MAP_SWIZZLE_32B;
+  return encode_map(m, type, swizzle, rank, base, dims, strides, box);
 }
 
 }  // namespace dfl

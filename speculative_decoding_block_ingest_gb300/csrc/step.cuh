@@ -111,14 +111,10 @@ struct NextArgs {
 };
 cudaError_t launch_next_step(const NextArgs& a, int n_sm, cudaStream_t s);
 
-// A packed cache in bytes (fp4.cuh).
-struct PackedView {
-  const uint8_t* k;
-  const uint8_t* v;
-  const uint8_t* k_scale;
-  const uint8_t* v_scale;
-  long page_stride, row_stride, head_stride;
-  long scale_page_stride, scale_row_stride, scale_head_stride;
+// Boxes of a packed cache (fp4.cuh): codes [rows of a page][head_dim / 2 bytes],
+// swizzled by their length, and the scales of as many rows.
+struct PackedMaps {
+  CUtensorMap k, v, k_scale, v_scale;
 };
 
 // Attention of a step (step_attn.cu; how it is cut into pieces: step_plan.cuh).
@@ -130,7 +126,6 @@ struct StepAttnArgs {
   int causal;
   float scale_log2;    // scale * log2(e)
   float out_scale;     // of the results
-  PackedView packed;   // launch_step_attention4's cache
   int bf16;            // else f16
   int box_rows, boxes; // rows of one cache box (a page, at most 128) and boxes of a 128-key tile
   void* out;
@@ -151,7 +146,7 @@ struct StepAttnArgs {
 };
 cudaError_t launch_step_attention(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMap& k,
                                   const CUtensorMap& v, cudaStream_t s);
-cudaError_t launch_step_attention4(const StepAttnArgs& a, const CUtensorMap& q, cudaStream_t s);
+cudaError_t launch_step_attention4(const StepAttnArgs& a, const CUtensorMap& q, const PackedMaps& m, cudaStream_t s);
 // o = out_scale sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i over the fragments of every row that is not whole.
 cudaError_t launch_step_merge(const StepAttnArgs& a, cudaStream_t s);
 
@@ -160,5 +155,9 @@ int report_error(int code, const char* message);
 // Tiled tensor map of 16-bit elements, 128-byte swizzle; false on failure.
 bool encode_tiled_map(CUtensorMap* m, int dtype, uint32_t rank, const void* base, const uint64_t* dims,
                       const uint64_t* strides, const uint32_t* box);
+// The same of bytes in rows of 32 or 64 (swizzled by that) or of 4- or 8-byte
+// elements that lie as they are.
+bool encode_packed_map(CUtensorMap* m, int element_bytes, uint32_t rank, const void* base, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box);
 
 }  // namespace dfl

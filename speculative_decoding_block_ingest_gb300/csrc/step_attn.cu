@@ -50,26 +50,41 @@
 namespace dfl {
 namespace {
 
-// threads, and registers of a softmax / other / rounding thread; together the
-// launch's own: 2 x 208 + 88 = 3 x 168, 2 x 176 + 72 + 88 = 4 x 128
-constexpr int step_threads(bool packed) { return packed ? 512 : 384; }
-constexpr int soft_regs(bool packed) { return packed ? 176 : 208; }
-constexpr int other_regs(bool packed) { return packed ? 72 : 88; }
-constexpr int kCodeRegs = 88;
+// threads, and registers of a softmax / other / converting thread; together the
+// launch's own: 2 x 208 + 88 = 3 x 168, 2 x 136 + 80 + 2 x 64 = 5 x 96
+constexpr int step_threads(bool packed) { return packed ? 640 : 384; }
+constexpr int soft_regs(bool packed) { return packed ? 136 : 208; }
+constexpr int other_regs(bool packed) { return packed ? 80 : 88; }
+constexpr int kCodeRegs = 64;
 constexpr int kSoftThreads = 256;        // warps 0..7
 constexpr int kMaxStages = 11;
 constexpr int kSharedBytes = 3 * 1024;   // control block
-constexpr size_t step_smem(int d, int stages) { return (size_t)(2 + stages) * (d / 64) * kAtomBytes + kSharedBytes; }
+// a packed cache's tiles as they lie there: codes and scales of 128 head rows.  A
+// copy ends on a 128-byte boundary, and 16 rows' scales at d = 64 are 64 bytes: those
+// of a page take 128.
+constexpr int kCodeTiles = 3;
+constexpr int scale_bytes(int d) { return d == 128 ? kKeys * 8 : kKeys / 16 * 128; }
+constexpr int code_tile(int d) { return kKeys * (d / 2) + scale_bytes(d); }
+template <int D>
+__device__ __forceinline__ int scale_place(int r, int box_rows) {
+  return r * (D / 16) + (D == 64 && box_rows == 16 ? (r >> 4) * 64 : 0);
+}
+static_assert(code_tile(128) % 512 == 0 && code_tile(64) % 512 == 0, "swizzled tiles");
+constexpr size_t step_smem(int d, int stages, bool packed) {
+  return (size_t)(2 + stages) * (d / 64) * kAtomBytes + kSharedBytes + (packed ? kCodeTiles * code_tile(d) : 0);
+}
 // as many K and V tiles as shared memory holds beside two query tiles: 5 at d = 128, 11 at 64
-constexpr int step_stages(int d) {
+// (packed 4 and 10)
+constexpr int step_stages(int d, bool packed) {
   int n = kMaxStages;
-  while (step_smem(d, n) > 227 * 1024) --n;
+  while (step_smem(d, n, packed) > 227 * 1024) --n;
   return n;
 }
 struct Shared {
   uint64_t kvfull[kMaxStages], kvempty[kMaxStages];
   uint64_t qfull[2], qempty[2], sfull[2], pfull[2][2], pvdone[2], kfirst[2];
   uint64_t drained;
+  uint64_t codefull[kCodeTiles], codeempty[kCodeTiles];
   uint32_t tmem;
   int abort;
   // this CTA's fragments, in a ring
@@ -83,51 +98,42 @@ struct Shared {
 static_assert(sizeof(Shared) <= kSharedBytes, "control block of the attention kernel");
 
 // ---------------------------------------------------------------- a packed cache
-// A head row of codes and scales on its way to a 16-bit tile.
-template <int D>
-struct CodeRow {
-  uint4 code[D / 32];
-  uint32_t scale[D / 64];
-  __device__ __forceinline__ void load(const void* c, const void* s) {
+// Half a head row of a tile of codes on its way to row r of a swizzled 16-bit tile
+// (zeros where there is no such key).  A code times its scale is exact in either
+// type.  A short loop: the roles' code shares the instruction caches.
+template <int D, bool BF16>
+__device__ __forceinline__ void convert_row(uint8_t* tile, const uint8_t* codes, int r, int half, int box_rows,
+                                            bool there) {
+  const uint8_t* sc = codes + kKeys * (D / 2) + scale_place<D>(r, box_rows) + half * (D / 32);
+  uint32_t scale;
+  if constexpr (D == 128) scale = *reinterpret_cast<const uint32_t*>(sc);
+  else scale = *reinterpret_cast<const uint16_t*>(sc);
+  if (!there) scale = 0;
+  const uint8_t* row = codes + r * (D / 2);
+  uint8_t* out = tile + r * 128;
+  const int flip = D == 128 ? r >> 1 & 3 : r >> 2 & 1;   // as a TMA box of rows of this length lies
+#pragma unroll 1
+  for (int i = half * (D / 64); i < (half + 1) * (D / 64); ++i) {   // two blocks
+    uint4 c = *reinterpret_cast<const uint4*>(row + (i ^ flip) * 16);
+    if (!there) c = make_uint4(0, 0, 0, 0);
+    const __half2 two = e4m3_to2(scale & 0xFFFF), f[2] = {__low2half2(two), __high2half2(two)};
+    scale >>= 16;
+    uint32_t h[16];
+    e2m1_to8(c.x, h);
+    e2m1_to8(c.y, h + 4);
+    e2m1_to8(c.z, h + 8);
+    e2m1_to8(c.w, h + 12);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) code[i] = static_cast<const uint4*>(c)[i];
-    if constexpr (D == 128) {
-      const uint2 t = *static_cast<const uint2*>(s);
-      scale[0] = t.x, scale[1] = t.y;
-    } else {
-      scale[0] = *static_cast<const uint32_t*>(s);
+    for (int j = 0; j < 16; ++j) {
+      h[j] = as_u32(__hmul2(as_half2(h[j]), f[j / 8]));
+      if constexpr (BF16) h[j] = __float_as_uint(pack2<true>(__half22float2(as_half2(h[j]))));
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint4*>(out + (i >> 1) * kAtomBytes + (((4 * i + j) & 7) ^ (r & 7)) * 16) =
+          make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
   }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) code[i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) scale[i] = 0;
-  }
-  // Row r of a swizzled K-major tile.  A code times its scale is exact in either type.
-  template <bool BF16>
-  __device__ __forceinline__ void put(uint8_t* tile, int r) const {
-#pragma unroll
-    for (int b = 0; b < D / 16; ++b) {
-      const uint4 c = code[b / 2];
-      const __half2 two = e4m3_to2(scale[b / 4] >> (16 * ((b / 2) & 1)) & 0xFFFF);
-      const __half2 f = b & 1 ? __high2half2(two) : __low2half2(two);
-      uint32_t h[8];
-      e2m1_to8(b & 1 ? c.z : c.x, h);
-      e2m1_to8(b & 1 ? c.w : c.y, h + 4);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        h[i] = as_u32(__hmul2(as_half2(h[i]), f));
-        if constexpr (BF16) h[i] = __float_as_uint(pack2<true>(__half22float2(as_half2(h[i]))));
-      }
-      uint8_t* atom = tile + b / 4 * kAtomBytes + r * 128;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        *reinterpret_cast<uint4*>(atom + (((2 * b + i) & 7) ^ (r & 7)) * 16) =
-            make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-    }
-  }
-};
+}
 
 // ---------------------------------------------------------------- the kernel
 // PACKED: the cache holds codes and scales, which four more warps turn into the
@@ -135,10 +141,11 @@ struct CodeRow {
 template <int D, bool BF16, bool PACKED>
 __global__ void __launch_bounds__(step_threads(PACKED), 1)
     step_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ StepAttnArgs a) {
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKScale,
+                     const __grid_constant__ CUtensorMap tmVScale, const __grid_constant__ StepAttnArgs a) {
   constexpr int kDAtoms = D / 64;
   constexpr int kTile = kDAtoms * kAtomBytes;          // a Q, K or V tile
-  constexpr int kStages = step_stages(D);              // K and V tiles in flight
+  constexpr int kStages = step_stages(D, PACKED);      // K and V tiles in flight
   constexpr bool kVBF16 = BF16 && !PACKED;             // type of V and of the softmax weights
   constexpr uint32_t kFmtS = BF16 ? (1u << 7) | (1u << 10) : 0u, kFmtO = kVBF16 ? kFmtS : 0u;
   constexpr uint32_t kIdescS = (1u << 4) | kFmtS | ((128u >> 3) << 17) | ((128u >> 4) << 24);
@@ -148,13 +155,14 @@ __global__ void __launch_bounds__(step_threads(PACKED), 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + 2 * kTile;
-  Shared& sh = *reinterpret_cast<Shared*>(sKV + kStages * kTile);
+  uint8_t* sCode = sKV + kStages * kTile;              // (packed) codes and scales in flight
+  Shared& sh = *reinterpret_cast<Shared*>(sCode + (PACKED ? kCodeTiles * code_tile(D) : 0));
   volatile int* abort = &sh.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.kvfull[i], PACKED ? 4 : 1);
+      mbar_init(&sh.kvfull[i], PACKED ? 8 : 1);
       mbar_init(&sh.kvempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -167,17 +175,23 @@ __global__ void __launch_bounds__(step_threads(PACKED), 1)
       mbar_init(&sh.kfirst[i], 1);
     }
     mbar_init(&sh.drained, 1);
+    for (int i = 0; PACKED && i < kCodeTiles; ++i) {
+      mbar_init(&sh.codefull[i], 1);
+      mbar_init(&sh.codeempty[i], 8);
+    }
     for (int i = 0; i < kFrags; ++i) {
       mbar_init(&sh.ffull[i], 1);
-      mbar_init(&sh.fempty[i], PACKED ? 15 : 11);   // all warps but 10
+      mbar_init(&sh.fempty[i], PACKED ? 19 : 11);   // all warps but 10
     }
     sh.abort = 0;
     sh.any_bad = 0;
     fence_barrier_init();
     tma_prefetch_map(&tmQ);
-    if constexpr (!PACKED) {
-      tma_prefetch_map(&tmK);
-      tma_prefetch_map(&tmV);
+    tma_prefetch_map(&tmK);
+    tma_prefetch_map(&tmV);
+    if constexpr (PACKED) {
+      tma_prefetch_map(&tmKScale);
+      tma_prefetch_map(&tmVScale);
     }
   }
   if (tid < 128) sh.bad[tid] = INT_MAX;
@@ -208,73 +222,36 @@ __global__ void __launch_bounds__(step_threads(PACKED), 1)
   if (PACKED && warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCodeRegs));
     // ------------------------------------------------------------------ codes to tiles
-    // A thread has a row of every tile, and the next two tiles' codes in flight.
+    // A thread has half a row of every tile.  Every warp takes every tile, so its waits
+    // on a slot follow each other and none reads a barrier's parity a turn early.
     bool ok = true;
     uint32_t nkv = 0;
-    const int r = tid & 127;
+    const int r = tid & 127, half = tid >= 512;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, pipe_wait(bar, parity, abort));
+      return ok;
+    };
     Frag f;
     while (take(f)) {
       const int n = f.b1 - f.b0;
       if (!ok || n <= 0) continue;
       const bool pair = f.ntok > a.tpt;
-      const int* table = f.seg ? a.s.block_table + f.seq * a.s.table_stride : a.s.prefix_pages;
-      // the page of this row's key in a block of the fragment (-1: no such key, or page)
-      auto page_of = [&](int block) -> int {
-        const long key = (long)(f.b0 + block) * kKeys + r;
-        const int page = block < n && key < f.keys ? table[key >> a.s.page_shift] : -1;
-        return page < a.s.n_pages ? page : -1;
-      };
-      // pages of two blocks, and of the two behind them
-      int even = page_of(0), odd = page_of(1), even2 = page_of(2), odd2 = page_of(3);
-      auto block_of = [&](int t, int& kv) {   // the inverse of tile_of
-        if (pair) {
-          kv = t & 1;
-          return t >> 1;
-        }
-        const int first = t >> 2 << 1, m = min(2, n - first), w = t & 3;
-        kv = w >= m;
-        return first + w - kv * m;
-      };
-      auto load = [&](CodeRow<D>& x, int t) {
-        if (t >= 2 * n) return;
-        if (t > 0 && (t & 3) == 0) {
-          even = even2, odd = odd2;
-          even2 = page_of((t >> 1) + 2), odd2 = page_of((t >> 1) + 3);
-        }
+      for (int t = 0; t < 2 * n && ok; ++t, ++nkv) {
+        const uint32_t in = nkv % kCodeTiles, st = nkv % kStages;
+        if (!wait(&sh.codefull[in], (nkv / kCodeTiles) & 1)) break;
+        if (!wait(&sh.kvempty[st], ((nkv / kStages) & 1) ^ 1)) break;
         int kv;
-        const int block = block_of(t, kv), page = block & 1 ? odd : even;
-        if (page >= 0) {
-          const long at = ((f.b0 + block) * kKeys + r) & (a.s.page_size - 1);
-          const PackedView& c = a.packed;
-          x.load((kv ? c.v : c.k) + page * c.page_stride + at * c.row_stride + f.h * c.head_stride,
-                 (kv ? c.v_scale : c.k_scale) + page * c.scale_page_stride + at * c.scale_row_stride +
-                     f.h * c.scale_head_stride);
-        } else {
-          x.clear();
-        }
-      };
-      auto put = [&](const CodeRow<D>& x, int t) {
-        const uint32_t tile = nkv + t, st = tile % kStages;
-        if (ok) ok = __all_sync(0xffffffffu, pipe_wait(&sh.kvempty[st], ((tile / kStages) & 1) ^ 1, abort));
-        if (!ok) return;
-        int kv;
-        block_of(t, kv);
-        if (kv) x.template put<false>(sKV + st * kTile, r);
-        else x.template put<BF16>(sKV + st * kTile, r);
+        const bool there = (f.b0 + block_of(pair, t, n, kv)) * kKeys + r < f.keys;
+        const uint8_t* codes = sCode + in * code_tile(D);
+        if (BF16 && kv == 0) convert_row<D, true>(sKV + st * kTile, codes, r, half, a.box_rows, there);
+        else convert_row<D, false>(sKV + st * kTile, codes, r, half, a.box_rows, there);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.kvfull[st]);
-      };
-      CodeRow<D> x0, x1;
-      load(x0, 0);
-      load(x1, 1);
-      for (int t = 0; t < 2 * n && ok; t += 2) {
-        put(x0, t);
-        load(x0, t + 2);
-        put(x1, t + 1);
-        load(x1, t + 3);
+        if (lane == 0) {
+          mbar_arrive(&sh.codeempty[in]);
+          mbar_arrive(&sh.kvfull[st]);
+        }
       }
-      nkv += 2 * n;
     }
     if (!ok) sh.abort = 1;
   } else if (warp >= 8) {
@@ -302,7 +279,6 @@ __global__ void __launch_bounds__(step_threads(PACKED), 1)
           }
           __syncwarp();
         }
-        if constexpr (PACKED) continue;
         // page ids: one lane per box of the next 32, the following 32 in flight
         const int* table = f.seg ? a.s.block_table + f.seq * a.s.table_stride : a.s.prefix_pages;
         const int n_box = (f.keys + a.box_rows - 1) >> box_shift;
@@ -321,6 +297,23 @@ __global__ void __launch_bounds__(step_threads(PACKED), 1)
           const int blocks = min(step, f.b1 - b);
           for (int i = 0; i < 2 * blocks && ok; ++i, ++nkv) {
             const int kv = i >= blocks, box0 = (b + i - kv * blocks) * a.boxes, n = min(a.boxes, n_box - box0);
+            if constexpr (PACKED) {   // codes by even lanes, scales by odd ones
+              const int in = (int)(nkv % kCodeTiles), bi = lane >> 1;
+              ok = __all_sync(0xffffffffu, pipe_wait(&sh.codeempty[in], ((nkv / kCodeTiles) & 1) ^ 1, abort));
+              if (!ok) break;
+              if (lane == 0) mbar_arrive_expect_tx(&sh.codefull[in], (uint32_t)(n * a.box_rows * (D / 2 + D / 16)));
+              __syncwarp();
+              uint8_t* tile = sCode + in * code_tile(D);
+              const int page = __shfl_sync(0xffffffffu, cur, min(box0 - win + bi, 31));
+              const int at = (int)(((long)(box0 + bi) << box_shift) & (a.s.page_size - 1));
+              if (bi < n && lane & 1)
+                tma_load_3d(tile + kKeys * (D / 2) + scale_place<D>(bi * a.box_rows, a.box_rows), kv ? &tmVScale : &tmKScale,
+                            &sh.codefull[in], at, f.h, page);
+              else if (bi < n)
+                tma_load_4d(tile + bi * a.box_rows * (D / 2), kv ? &tmV : &tmK, &sh.codefull[in], 0, f.h, at, page);
+              __syncwarp();
+              continue;
+            }
             const int st = (int)(nkv % kStages);
             ok = __all_sync(0xffffffffu, pipe_wait(&sh.kvempty[st], ((nkv / kStages) & 1) ^ 1, abort));
             if (!ok) break;
@@ -338,8 +331,9 @@ __global__ void __launch_bounds__(step_threads(PACKED), 1)
       if (!ok) {   // leave no copy in flight behind
         sh.abort = 1;
         int none = 0;
-        for (uint32_t i = nkv > (uint32_t)kStages ? nkv - kStages : 0; i < nkv; ++i)
-          pipe_wait(&sh.kvfull[i % kStages], (i / kStages) & 1, &none);
+        constexpr uint32_t kRing = PACKED ? kCodeTiles : kStages;
+        for (uint32_t i = nkv > kRing ? nkv - kRing : 0; i < nkv; ++i)
+          pipe_wait(PACKED ? &sh.codefull[i % kRing] : &sh.kvfull[i % kRing], (i / kRing) & 1, &none);
         for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) pipe_wait(&sh.qfull[i & 1], (i >> 1) & 1, &none);
       }
     } else if (warp == 9) {
@@ -584,27 +578,32 @@ __global__ void __launch_bounds__(step_threads(PACKED), 1)
           fence_proxy_async_smem();
         }
         if (ok && any_live) {
-          float x[kKeys];
+          // A packed cache's softmax reads the scores twice, 32 keys at a time: in code as
+          // long as below, which the converting warps' competes with for the instruction
+          // caches, a block took 4600 cycles, and 3900 like this.
+          constexpr int kAtOnce = PACKED ? 32 : kKeys;
+          float x[kAtOnce];
           const int seen = lim - key0;
           const bool whole = __all_sync(0xffffffffu, seen >= kKeys);
-          auto scores = [&]() {
+          auto scores = [&](int c) {
 #pragma unroll
-            for (int i = 0; i < kKeys; i += 32) tmem_ld32_async(s_addr + i, x + i);
+            for (int i = 0; i < kAtOnce; i += 32) tmem_ld32_async(s_addr + c + i, x + i);
 #pragma unroll
-            for (int i = 0; i < kKeys; i += 32) tmem_ld_wait32(x + i);
+            for (int i = 0; i < kAtOnce; i += 32) tmem_ld_wait32(x + i);
             if (!whole) {
 #pragma unroll
-              for (int i = 0; i < kKeys; ++i) x[i] = i < seen ? x[i] : -INFINITY;
+              for (int i = 0; i < kAtOnce; ++i) x[i] = c + i < seen ? x[i] : -INFINITY;
             }
           };
-          scores();
-          float mx[4];
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += kAtOnce) {
+            scores(c);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(x[i], x[i + 4]);
+            for (int i = 0; i < kAtOnce; i += 8)
 #pragma unroll
-          for (int i = 8; i < kKeys; i += 8)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) mx[v] = max3(mx[v], x[i + v], x[i + v + 4]);
+              for (int v = 0; v < 4; ++v) mx[v] = max3(mx[v], x[i + v], x[i + v + 4]);
+          }
           const float mj = a.scale_log2 * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           // the running maximum moves only when it grows by more than 2^8:
           // weights stay below 2^8 and the final division uses the same one
@@ -624,28 +623,32 @@ __global__ void __launch_bounds__(step_threads(PACKED), 1)
               tmem_st32(oa, o);
             }
             l *= f0;
-            scores();   // read again rather than kept beside O
+            if constexpr (!PACKED) scores(0);   // read again rather than kept beside O
           }
           if (grow) m = mj;
           const float nm = m == -INFINITY ? 0.f : kBias - m;
           const float2 neg = make_float2(nm, nm), sc = make_float2(a.scale_log2, a.scale_log2);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += kAtOnce) {
+            if constexpr (PACKED) scores(c);
 #pragma unroll
-          for (int i = 0; i < kKeys; i += 32) {
-            float pw[16];
+            for (int i = 0; i < kAtOnce; i += 32) {
+              float pw[16];
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-              float2 p = fma2(make_float2(x[i + 2 * v], x[i + 2 * v + 1]), sc, neg);
-              p.x = ex2_fast(p.x);
-              p.y = ex2_fast(p.y);
-              sum[v & 1] = add2(sum[v & 1], p);
-              pw[v] = pack2<kVBF16>(p);
-            }
-            tmem_st16(s_addr + i / 2, pw);
-            if (i % 64 == 32) {
-              tmem_st_wait();
-              tc_fence_before();
-              mbar_arrive(&sh.pfull[st][i / 64]);
+              for (int v = 0; v < 16; ++v) {
+                float2 p = fma2(make_float2(x[i + 2 * v], x[i + 2 * v + 1]), sc, neg);
+                p.x = ex2_fast(p.x);
+                p.y = ex2_fast(p.y);
+                sum[v & 1] = add2(sum[v & 1], p);
+                pw[v] = pack2<kVBF16>(p);
+              }
+              tmem_st16(s_addr + (c + i) / 2, pw);
+              if ((c + i) % 64 == 32) {
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&sh.pfull[st][(c + i) / 64]);
+              }
             }
           }
           const float2 tot = add2(sum[0], sum[1]);
@@ -982,9 +985,9 @@ cudaError_t merge(const StepAttnArgs& a, cudaStream_t s) {
 
 template <int D, bool BF16, bool PACKED>
 cudaError_t launch(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                   cudaStream_t s) {
+                   const CUtensorMap& ks, const CUtensorMap& vs, cudaStream_t s) {
   auto* attn = step_attn_kernel<D, BF16, PACKED>;
-  const size_t smem = step_smem(D, step_stages(D));
+  const size_t smem = step_smem(D, step_stages(D, PACKED), PACKED);
   // the kernel's shared memory is raised once on every device
   static std::atomic<uint64_t> raised{0};
   int dev = 0;
@@ -995,7 +998,7 @@ cudaError_t launch(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMa
     if (e != cudaSuccess) return e;
     if (dev < 64) raised.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
-  e = launch_pdl(attn, dim3(a.n_cta), dim3(step_threads(PACKED)), smem, s, q, k, v, a);
+  e = launch_pdl(attn, dim3(a.n_cta), dim3(step_threads(PACKED)), smem, s, q, k, v, ks, vs, a);
   if (e != cudaSuccess) return e;
   return merge<D, BF16>(a, s);
 }
@@ -1004,13 +1007,15 @@ cudaError_t launch(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMa
 
 cudaError_t launch_step_attention(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMap& k,
                                   const CUtensorMap& v, cudaStream_t s) {
-  if (a.d == 128) return a.bf16 ? launch<128, true, false>(a, q, k, v, s) : launch<128, false, false>(a, q, k, v, s);
-  return a.bf16 ? launch<64, true, false>(a, q, k, v, s) : launch<64, false, false>(a, q, k, v, s);
+  auto* run = a.d == 128 ? (a.bf16 ? launch<128, true, false> : launch<128, false, false>)
+                         : (a.bf16 ? launch<64, true, false> : launch<64, false, false>);
+  return run(a, q, k, v, q, q, s);
 }
 
-cudaError_t launch_step_attention4(const StepAttnArgs& a, const CUtensorMap& q, cudaStream_t s) {
-  if (a.d == 128) return a.bf16 ? launch<128, true, true>(a, q, q, q, s) : launch<128, false, true>(a, q, q, q, s);
-  return a.bf16 ? launch<64, true, true>(a, q, q, q, s) : launch<64, false, true>(a, q, q, q, s);
+cudaError_t launch_step_attention4(const StepAttnArgs& a, const CUtensorMap& q, const PackedMaps& m, cudaStream_t s) {
+  auto* run = a.d == 128 ? (a.bf16 ? launch<128, true, true> : launch<128, false, true>)
+                         : (a.bf16 ? launch<64, true, true> : launch<64, false, true>);
+  return run(a, q, m.k, m.v, m.k_scale, m.v_scale, s);
 }
 
 cudaError_t launch_step_merge(const StepAttnArgs& a, cudaStream_t s) {

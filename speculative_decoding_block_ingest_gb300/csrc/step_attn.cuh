@@ -144,6 +144,17 @@ __device__ __forceinline__ uint32_t tile_of(bool pair, int block, int n, int kv)
   return 2 * first + (block & 1) + kv * min(2, n - first);
 }
 
+// The inverse: block (and kv) of tile t of a fragment of n blocks.
+__device__ __forceinline__ int block_of(bool pair, int t, int n, int& kv) {
+  if (pair) {
+    kv = t & 1;
+    return t >> 1;
+  }
+  const int first = t >> 2 << 1, m = min(2, n - first), w = t & 3;
+  kv = w >= m;
+  return first + w - kv * m;
+}
+
 // Waits on the fragment ring outlast any one fragment; a failed wait
 // elsewhere ends the others within kWaitNs, so this limit is not met.
 __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {

@@ -232,12 +232,15 @@ int check_packed(const dflash_packed_cache* c) {
   if (!c->k || !c->v || !c->k_scale || !c->v_scale) return invalid("cache pointer is null");
   if (c->n_pages < 1) return invalid("n_pages must be positive");
   const long row = c->head_dim / 2, sc = c->head_dim / 16;
-  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, sc) || !aligned(c->v_scale, sc))
-    return invalid("codes must start on a 16-byte boundary, scales on a head row's");
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
+    return invalid("codes and scales must start on 16-byte boundaries");
   for (long st : {(long)c->page_stride, (long)c->row_stride, (long)c->head_stride})
-    if (st < row || st % 16 || st >= (1L << 38)) return invalid("code strides must be multiples of 16 bytes that hold a head row");
-  for (long st : {(long)c->scale_page_stride, (long)c->scale_row_stride, (long)c->scale_head_stride})
-    if (st < sc || st % sc || st >= (1L << 38)) return invalid("scale strides must be multiples of a head row's scales");
+    if (st < row || st % 16 || st >= (1L << 38))
+      return invalid("code strides must be multiples of 16 bytes that hold a head row");
+  if (c->scale_row_stride != sc) return fail(DFLASH_ERR_UNSUPPORTED, "the scales of a head's rows of a page must lie together");
+  for (long st : {(long)c->scale_page_stride, (long)c->scale_head_stride})
+    if (st < sc * c->page_size || st % 16 || st >= (1L << 38))
+      return invalid("scale strides must be multiples of 16 bytes that hold a page's rows");
   if (!is_unit(c->k_unit) || !is_unit(c->v_unit)) return invalid("units must be powers of two between 2^-60 and 2^58");
   return DFLASH_OK;
 }
@@ -411,16 +414,23 @@ int dflash_step_attention_packed(const dflash_packed_cache* cache, const dflash_
   a.scale_log2 *= cache->k_unit;
   if (!std::isfinite(a.scale_log2) || a.scale_log2 < 1e-37f) return invalid("scale times the keys' unit must be a normal float");
   a.out_scale = cache->v_unit;
-  a.packed = {static_cast<const uint8_t*>(cache->k),       static_cast<const uint8_t*>(cache->v),
-              static_cast<const uint8_t*>(cache->k_scale), static_cast<const uint8_t*>(cache->v_scale),
-              cache->page_stride,       cache->row_stride,       cache->head_stride,
-              cache->scale_page_stride, cache->scale_row_stride, cache->scale_head_stride};
   if (int rc = has_workspace(workspace_bytes, carve(a, static_cast<char*>(workspace)))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (step->n_rows == 0) return launched(cudaMemsetAsync(a.status, 0, kStepStatusWords * 4, s), "step attention");
   CUtensorMap mq;
-  if (!encode_queries(&mq, a, p, cache->dtype)) return fail(DFLASH_ERR_CUDA, "tensor map of the queries was refused");
-  return launched(launch_step_attention4(a, mq, s), "packed step attention");
+  PackedMaps m;
+  const uint64_t n_heads = cache->n_kv_heads, page = cache->page_size, n_pages = cache->n_pages, sc = a.d / 16;
+  const uint64_t dims[4] = {(uint64_t)a.d / 2, n_heads, page, n_pages}, sdims[3] = {page, n_heads, n_pages};
+  const uint64_t strides[3] = {(uint64_t)cache->head_stride, (uint64_t)cache->row_stride,
+                               (uint64_t)cache->page_stride};
+  const uint64_t sstrides[2] = {(uint64_t)cache->scale_head_stride, (uint64_t)cache->scale_page_stride};
+  const uint32_t box[4] = {(uint32_t)a.d / 2, 1, (uint32_t)a.box_rows, 1}, sbox[3] = {(uint32_t)a.box_rows, 1, 1};
+  if (!encode_queries(&mq, a, p, cache->dtype) || !encode_packed_map(&m.k, 1, 4, cache->k, dims, strides, box) ||
+      !encode_packed_map(&m.v, 1, 4, cache->v, dims, strides, box) ||
+      !encode_packed_map(&m.k_scale, (int)sc, 3, cache->k_scale, sdims, sstrides, sbox) ||
+      !encode_packed_map(&m.v_scale, (int)sc, 3, cache->v_scale, sdims, sstrides, sbox))
+    return fail(DFLASH_ERR_CUDA, "tensor map of the queries or the cache was refused");
+  return launched(launch_step_attention4(a, mq, m, s), "packed step attention");
 }
 
 int dflash_step_attention_status(const void* workspace, void* stream) {

@@ -183,8 +183,9 @@ class PagedCache4:
     """A target layer's paged cache in 4 bits: codes k and v uint8 ``[n_pages,
     page_size, n_kv_heads, head_dim / 2]`` (two a byte, the even element in the low
     half) and scales ``[n_pages, page_size, n_kv_heads, head_dim / 16]``
-    (float8_e4m3fn, or uint8), each any strides whose last is 1.  An element is
-    e2m1 code x e4m3 scale of its 16 x ``unit`` (powers of two).  ``dtype``: of
+    (float8_e4m3fn, or uint8), each any strides whose last is 1; the scales of a
+    head's rows of a page lie together (``[n_pages, n_kv_heads, page_size,
+    head_dim / 16]`` pools pass their transposes).  An element is e2m1 code x e4m3 scale of its 16 x ``unit`` (powers of two).  ``dtype``: of
     queries, results and rounded rows."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, *,
@@ -210,7 +211,7 @@ class PagedCache4:
             _refuse(f"dtype {dtype} is not supported", ERR_UNSUPPORTED)
         # the stride of a dimension of one element is never used
         st = [s if n > 1 else max(d // 2, 16) for s, n in zip(k.stride(), k.shape)]
-        sc = [s if n > 1 else max(d // 16, 1) for s, n in zip(k_scale.stride(), k.shape)]
+        sc = [s if n > 1 else max(d // 16 * k.shape[1], 16) for s, n in zip(k_scale.stride(), k.shape)]
         try:
             units = ctypes.c_float(k_unit), ctypes.c_float(v_unit)
         except TypeError:

@@ -24,13 +24,18 @@ def i32(x):
 
 
 def pools(n_pages, page, hkv, d, *, hnd=False, pad=0, seed=0):
-    """Random bytes of the four pools as [n_pages, page, hkv, bytes] views, `pad` unused bytes behind a head's codes."""
+    """Random bytes of the four pools as [n_pages, page, hkv, bytes] views: `pad` unused bytes behind a head's codes, and
+    behind its scales of a page."""
     g = torch.Generator().manual_seed(seed)
     out = []
-    for n, extra in ((d // 2, pad), (d // 2, pad), (d // 16, d // 16 if pad else 0), (d // 16, d // 16 if pad else 0)):
-        shape = (n_pages, hkv, page, n + extra) if hnd else (n_pages, page, hkv, n + extra)
-        x = torch.randint(0, 256, shape, generator=g, dtype=torch.uint8).to(DEV)[..., :n]
+    for _ in range(2):
+        shape = (n_pages, hkv, page, d // 2 + pad) if hnd else (n_pages, page, hkv, d // 2 + pad)
+        x = torch.randint(0, 256, shape, generator=g, dtype=torch.uint8).to(DEV)[..., :d // 2]
         out.append(x.transpose(1, 2) if hnd else x)
+    for _ in range(2):
+        n = page * d // 16
+        x = torch.randint(0, 256, (n_pages, hkv, n + pad), generator=g, dtype=torch.uint8).to(DEV)[..., :n]
+        out.append(x.unflatten(2, (page, d // 16)).transpose(1, 2))
     return out
 
 
@@ -274,7 +279,8 @@ def test_offsets_past_32_bits(T):
     """A pool of more than 2^32 bytes of codes."""
     page, hkv, d = 256, 8, 128
     n_pages = (1 << 32) // (page * hkv * 64) + 40
-    mem = [torch.zeros(n_pages, page, hkv, n, dtype=torch.uint8, device=DEV) for n in (64, 64, 8, 8)]
+    mem = [torch.zeros(n_pages, page, hkv, 64, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    mem += [torch.zeros(n_pages, hkv, page, 8, dtype=torch.uint8, device=DEV).transpose(1, 2) for _ in range(2)]
     g = torch.Generator().manual_seed(6)
     k = torch.randn(3, hkv, d, generator=g).to(BF).to(DEV)
     T.append(T.PagedCache4(*mem), T.Step(i32([0, 3]), i32([3]), i32([[n_pages - 1]])), None, k, k)

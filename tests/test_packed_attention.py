@@ -24,19 +24,22 @@ def i32(x):
 
 
 def pools(n_pages, page, hkv, d, *, hnd=False, pad=0, seed=0):
-    """Codes and scales of normal rows, as [n_pages, page, hkv, bytes] views (`pad` bytes behind a head's codes)."""
+    """Codes and scales of normal rows, as [n_pages, page, hkv, bytes] views (`pad` bytes behind a head's codes, and its
+    scales of a page)."""
     rng = np.random.default_rng(seed)
     out = []
     for _ in range(2):
         c, s, _ = P.pack(rng.standard_normal((n_pages, page, hkv, d), dtype=np.float32))
         out.append((c, s))
     mem = []
-    for i, extra in ((0, pad), (1, d // 16 if pad else 0)):
-        for c in out:
-            x = np.pad(c[i], [(0, 0)] * 3 + [(0, extra)])
-            n = x.shape[-1] - extra
-            x = torch.from_numpy(np.ascontiguousarray(x.transpose(0, 2, 1, 3) if hnd else x)).to(DEV)[..., :n]
-            mem.append(x.transpose(1, 2) if hnd else x)
+    for c, _ in out:
+        x = np.pad(c, [(0, 0)] * 3 + [(0, pad)])
+        x = torch.from_numpy(np.ascontiguousarray(x.transpose(0, 2, 1, 3) if hnd else x)).to(DEV)[..., :d // 2]
+        mem.append(x.transpose(1, 2) if hnd else x)
+    for _, s in out:      # a head's rows of a page together
+        x = np.pad(s.transpose(0, 2, 1, 3).reshape(n_pages, hkv, -1), [(0, 0)] * 2 + [(0, pad)])
+        x = torch.from_numpy(x).to(DEV)[..., :page * d // 16]
+        mem.append(x.unflatten(2, (page, d // 16)).transpose(1, 2))
     return mem      # k, v, k_scale, v_scale
 
 
@@ -299,7 +302,8 @@ def test_offsets_past_32_bits(T):
     """Pools of more than 2^32 bytes of codes."""
     page, hkv, d = 256, 8, 128
     n_pages = (1 << 32) // (page * hkv * 64) + 40
-    mem = [torch.zeros(n_pages, page, hkv, n, dtype=torch.uint8, device=DEV) for n in (64, 64, 8, 8)]
+    mem = [torch.zeros(n_pages, page, hkv, 64, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    mem += [torch.zeros(n_pages, hkv, page, 8, dtype=torch.uint8, device=DEV).transpose(1, 2) for _ in range(2)]
     small = pools(4, page, hkv, d, seed=3)
     for m, x in zip(mem, small):
         m[-4:] = x

@@ -17,8 +17,8 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 def packed(**kw):
     a = dict(k=P, v=P, k_scale=P, v_scale=P, dtype=dflash.BF16, n_pages=4, page_size=64, n_kv_heads=2, head_dim=128,
-             page_stride=64 * 128, row_stride=128, head_stride=64, scale_page_stride=64 * 16, scale_row_stride=16,
-             scale_head_stride=8, k_unit=1.0, v_unit=1.0)
+             page_stride=64 * 128, row_stride=128, head_stride=64, scale_page_stride=64 * 16, scale_row_stride=8,
+             scale_head_stride=512, k_unit=1.0, v_unit=1.0)
     a.update(kw)
     return dflash.PackedCacheDesc(**a)
 
@@ -41,8 +41,8 @@ def next_args(**kw):
 CACHE = [(dict(dtype=dflash.F32), UNS), (dict(head_dim=96), UNS), (dict(head_dim=32), UNS), (dict(page_size=8), UNS),
          (dict(page_size=48), UNS), (dict(n_kv_heads=0), INV), (dict(n_pages=0), INV), (dict(k=None), INV),
          (dict(v_scale=None), INV), (dict(v=P + 8), INV), (dict(k_scale=P + 4), INV), (dict(row_stride=120), INV),
-         (dict(head_stride=48), INV), (dict(page_stride=0), INV), (dict(scale_row_stride=12), INV),
-         (dict(scale_head_stride=4), INV), (dict(scale_page_stride=-8), INV), (dict(k_unit=0.0), INV),
+         (dict(head_stride=48), INV), (dict(page_stride=0), INV), (dict(scale_row_stride=16), UNS),
+         (dict(scale_head_stride=504), INV), (dict(scale_head_stride=256), INV), (dict(scale_page_stride=-8), INV), (dict(k_unit=0.0), INV),
          (dict(k_unit=0.75), INV), (dict(v_unit=float("nan")), INV), (dict(v_unit=2.0 ** 90), INV),
          (dict(k_unit=2.0 ** -80), INV), (dict(k_unit=-1.0), INV)]
 
