@@ -111,7 +111,15 @@ struct NextArgs {
 };
 cudaError_t launch_next_step(const NextArgs& a, int n_sm, cudaStream_t s);
 
-// Boxes of a packed cache (fp4.cuh): codes [rows of a page][head_dim / 2 bytes],
+// A packed cache in bytes (fp4.cuh); a head's scales of a page lie together.
+struct PackedView {
+  const uint8_t* k;
+  const uint8_t* v;
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
+  long page_stride, row_stride, head_stride, scale_page_stride, scale_head_stride;
+};
+// Boxes of a packed cache: codes [rows of a page][head_dim / 2 bytes],
 // swizzled by their length, and the scales of as many rows.
 struct PackedMaps {
   CUtensorMap k, v, k_scale, v_scale;
@@ -140,13 +148,26 @@ struct StepAttnArgs {
                        // begins in a CTA and goes on in others (no tokens: none)
   float* seg_o[2];     // [n_rows][Hq][d]: a segment's first fragment (prefix, own), unnormalised
   float2* seg_ml[2];   // [n_rows][Hq]: its (max, sum)
-  float* cta_o;        // [n_cta][256][d]: the fragment a CTA continues
-  float2* cta_ml;      // [n_cta][256]
-  int n_cta;
+  float* cta_o;        // [cta_row][d]: the fragment a CTA continues
+  float2* cta_ml;      // [cta_row]
+  int n_sm;
+  int n_cta;           // CTAs that leave partial results: n_wide of step_attn.cu, whose rows come
+  int n_wide;          // first, then those of step_attn_few.cu (16 rows each)
+  // a packed cache's, for step_attn_few.cu
+  PackedView packed;
+  const void* q;
+  long q_stride;
 };
+// A CTA's partial row among all CTAs'.
+__host__ __device__ inline long cta_row(const StepAttnArgs& a, int cta, int row) {
+  return cta < a.n_wide ? cta * 256L + row : a.n_wide * 256L + (cta - a.n_wide) * 16L + row;
+}
 cudaError_t launch_step_attention(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMap& k,
                                   const CUtensorMap& v, cudaStream_t s);
 cudaError_t launch_step_attention4(const StepAttnArgs& a, const CUtensorMap& q, const PackedMaps& m, cudaStream_t s);
+// wide_ran: launch_step_attention4 went before with the items of many rows, and has
+// set the status words; else this does all of them.
+cudaError_t launch_step_attention_few(const StepAttnArgs& a, bool wide_ran, cudaStream_t s);
 // o = out_scale sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i over the fragments of every row that is not whole.
 cudaError_t launch_step_merge(const StepAttnArgs& a, cudaStream_t s);
 

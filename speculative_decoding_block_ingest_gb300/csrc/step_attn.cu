@@ -460,55 +460,8 @@ __global__ void __launch_bounds__(step_threads(PACKED), 1)
       if (!ok) sh.abort = 1;
     } else if (warp == 10) {
       // ------------------------------------------------------------------ fragments
-      // The warp counts all units, 32 sequences at a time, then looks for the
-      // sequence that holds this CTA's first.
-      Walk w(a);
-      const int n = a.s.n_seq, prefix = w.prefix_units();
-      auto units_of = [&](int i) { return i < n ? a.Hkv * w.head_units(i) : 0; };
-      const int mine = units_of(lane);
-      bool falls = lane < n && w.falls(lane);
-      unsigned total = prefix + __reduce_add_sync(0xffffffffu, (unsigned)mine);
-#pragma unroll 4
-      for (int i = 32; i < n; i += 32) {
-        total += __reduce_add_sync(0xffffffffu, (unsigned)units_of(i + lane));
-        falls |= i + lane < n && w.falls(i + lane);
-      }
-      w.divide(__any_sync(0xffffffffu, falls) ? 0 : (int)total, a.n_cta, blockIdx.x);
-      int seq0 = -1, base = 0;
-      if (w.ua < w.ub && w.ua >= prefix) {
-        base = prefix;
-        for (int i = 0; i < n; i += 32) {
-          const int u = i ? units_of(i + lane) : mine;
-          int inc = u;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += x;
-          }
-          const unsigned holds = __ballot_sync(0xffffffffu, w.ua < base + inc);
-          if (holds) {
-            const int l = __ffs(holds) - 1;
-            seq0 = i + l;
-            base += __shfl_sync(0xffffffffu, inc - u, l);
-            break;
-          }
-          base += __shfl_sync(0xffffffffu, inc, 31);
-        }
-      }
-      if (w.ua < w.ub) w.begin(seq0, base);
-      else w.pos = w.ub;
-      bool more = true;
-      for (uint32_t i = 0; more; ++i) {
-        Frag f;
-        more = w.next(f);
-        if (!more) f.seg = -1;
-        if (!__all_sync(0xffffffffu, ring_wait(&sh.fempty[i % kFrags], ((i / kFrags) & 1) ^ 1))) break;
-        if (lane == 0) {
-          sh.frag[i % kFrags] = f;
-          mbar_arrive(&sh.ffull[i % kFrags]);
-        }
-        __syncwarp();
-      }
+      plan_pieces<WideCosts>(Walk(a, PACKED && a.n_cta > a.n_wide ? kManyRows : kAnyRows), a.n_wide, sh.frag, sh.ffull,
+                             sh.fempty, kFrags, lane);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(soft_regs(PACKED)));
@@ -671,7 +624,7 @@ __global__ void __launch_bounds__(step_threads(PACKED), 1)
         po = a.seg_o[f.seg] + at * D;
         pml = a.seg_ml[f.seg] + at;
       } else {
-        const long at = (long)blockIdx.x * 256 + (pair ? st * 128 : 0) + r;
+        const long at = cta_row(a, blockIdx.x, (pair ? st * 128 : 0) + r);
         po = a.cta_o + at * D;
         pml = a.cta_ml + at;
       }
@@ -824,10 +777,10 @@ __device__ __forceinline__ void merge_row(const StepAttnArgs& a, bool live, long
     const float* src = nullptr;
     if (i < total) {
       const int cta = (seg ? own.first : pre.first) + k;
-      const long at = (long)cta * 256 + (seg ? own.trow : pre.trow);
+      const long at = cta_row(a, cta, seg ? own.trow : pre.trow);
       ml = k == 0 ? (seg ? own.ml : pre.ml) : a.cta_ml[at];
       src = k == 0 ? (seg ? a.seg_o[1] : a.seg_o[0]) + item * D : a.cta_o + at * D;
-      bad |= a.status[cta] != 0;
+      bad |= a.status[cta < a.n_wide ? cta : cta - a.n_wide] != 0;
     }
     float mx = ml.x;
 #pragma unroll
@@ -972,7 +925,7 @@ cudaError_t merge(const StepAttnArgs& a, cudaStream_t s) {
   // a block, a warp or half a warp for every (row, head), as many as run at
   // once; or sixteen blocks for every CTA's last item
   using Out = std::conditional_t<BF16, __nv_bfloat16, __half>;
-  const long items = (long)a.s.n_rows * a.Hq, resident = 8L * a.n_cta;
+  const long items = (long)a.s.n_rows * a.Hq, resident = 8L * a.n_sm;
   auto run = [&](auto* kernel, long blocks) {
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kMergeThreads), 0, s, a);
   };
@@ -998,9 +951,7 @@ cudaError_t launch(const StepAttnArgs& a, const CUtensorMap& q, const CUtensorMa
     if (e != cudaSuccess) return e;
     if (dev < 64) raised.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
-  e = launch_pdl(attn, dim3(a.n_cta), dim3(step_threads(PACKED)), smem, s, q, k, v, ks, vs, a);
-  if (e != cudaSuccess) return e;
-  return merge<D, BF16>(a, s);
+  return launch_pdl(attn, dim3(a.n_wide), dim3(step_threads(PACKED)), smem, s, q, k, v, ks, vs, a);
 }
 
 }  // namespace
@@ -1009,7 +960,8 @@ cudaError_t launch_step_attention(const StepAttnArgs& a, const CUtensorMap& q, c
                                   const CUtensorMap& v, cudaStream_t s) {
   auto* run = a.d == 128 ? (a.bf16 ? launch<128, true, false> : launch<128, false, false>)
                          : (a.bf16 ? launch<64, true, false> : launch<64, false, false>);
-  return run(a, q, k, v, q, q, s);
+  const cudaError_t e = run(a, q, k, v, q, q, s);
+  return e == cudaSuccess ? launch_step_merge(a, s) : e;
 }
 
 cudaError_t launch_step_attention4(const StepAttnArgs& a, const CUtensorMap& q, const PackedMaps& m, cudaStream_t s) {

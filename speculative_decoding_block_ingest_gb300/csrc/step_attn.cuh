@@ -164,4 +164,60 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
+// This CTA's pieces of n_cta CTAs' work, described in a ring; seg -1 ends them.  A
+// warp's work.
+template <class Costs>
+__device__ __forceinline__ void plan_pieces(WalkT<Costs> w, int n_cta, Frag* frag, uint64_t* ffull, uint64_t* fempty,
+                                            uint32_t n_frags, int lane) {
+  // The warp counts all units, 32 sequences at a time, then looks for the
+  // sequence that holds this CTA's first.
+  const StepAttnArgs& a = w.a;
+  const int n = a.s.n_seq, prefix = w.prefix_units();
+  auto units_of = [&](int i) { return i < n ? a.Hkv * w.head_units(i) : 0; };
+  const int mine = units_of(lane);
+  bool falls = lane < n && w.falls(lane);
+  unsigned total = prefix + __reduce_add_sync(0xffffffffu, (unsigned)mine);
+#pragma unroll 4
+  for (int i = 32; i < n; i += 32) {
+    total += __reduce_add_sync(0xffffffffu, (unsigned)units_of(i + lane));
+    falls |= i + lane < n && w.falls(i + lane);
+  }
+  w.divide(__any_sync(0xffffffffu, falls) ? 0 : (int)total, n_cta, blockIdx.x);
+  int seq0 = -1, base = 0;
+  if (w.ua < w.ub && w.ua >= prefix) {
+    base = prefix;
+    for (int i = 0; i < n; i += 32) {
+      const int u = i ? units_of(i + lane) : mine;
+      int inc = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      const unsigned holds = __ballot_sync(0xffffffffu, w.ua < base + inc);
+      if (holds) {
+        const int l = __ffs(holds) - 1;
+        seq0 = i + l;
+        base += __shfl_sync(0xffffffffu, inc - u, l);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  if (w.ua < w.ub) w.begin(seq0, base);
+  else w.pos = w.ub;
+  bool more = true;
+  for (uint32_t i = 0; more; ++i) {
+    Frag f;
+    more = w.next(f);
+    if (!more) f.seg = -1;
+    if (!__all_sync(0xffffffffu, ring_wait(&fempty[i % n_frags], ((i / n_frags) & 1) ^ 1))) break;
+    if (lane == 0) {
+      frag[i % n_frags] = f;
+      mbar_arrive(&ffull[i % n_frags]);
+    }
+    __syncwarp();
+  }
+}
+
 }  // namespace dfl

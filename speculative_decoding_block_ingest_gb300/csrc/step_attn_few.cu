@@ -1,0 +1,548 @@
+// step_attn_few.cu -- attention of a step over a packed cache where a kv head has
+// at most 16 query rows of a sequence (or of the batch, for the prefix): single
+// tokens and short drafts.  (More rows than that are right here too, 16 at a time.)
+// The formula, the items and their pieces are those of
+// step_attn.cu; what is different is that the keys' bytes bound it, and that codes
+// have to become f16 on the way: 144 bytes a key, 256 values.
+//
+// On the 5th-generation tensor cores an operand comes from shared memory, so every
+// value would be written there as f16 and read again: 1600 cycles for a block of
+// 128 keys that HBM delivers in 790, for 128 query rows of which 16 exist.  Here codes
+// go from shared memory to registers, become f16 there and are a warp-wide product's
+// operand at once (mma.sync, 16 keys or elements by 8 query rows).
+//
+// For 16 keys of a warp and N tiles of 8 query rows (keys and elements may come in
+// any order, as long as both operands agree):
+//   S^T [16 keys x 8 rows] += K [16 x 16 elements] Q^T    d / 16 times
+//   P^T = 2^(S^T - m), to f16, transposed in registers (movmatrix)
+//   O^T [16 elements x 8 rows] += V^T [16 x 16 keys] P^T  d / 16 times
+// A lane's codes of K are 32 elements in a row of two keys (one 16-byte load each),
+// those of V 16 elements of four keys, whose nibbles are paired key by key before
+// they become f16.
+//
+// A CTA has 11 such warps, each with every eleventh 16 keys of a piece, its own ring
+// of loads (no barrier between warps) that runs on into the next pieces, and its own
+// running maximum; at a piece's end their parts are summed in a fixed order.  A 12th
+// warp plans.
+#include <atomic>
+
+#include "../../include/dflash.h"
+#include "fp4.cuh"
+#include "kernels.cuh"
+#include "ptx.cuh"
+#include "step_attn.cuh"
+#include "step_plan.cuh"
+
+namespace dfl {
+namespace {
+
+constexpr int kWarps = 11;
+constexpr int kFewThreads = (kWarps + 1) * 32;
+constexpr int kGroup = 16;                  // keys of a load
+constexpr int kFewFrags = 4;                // pieces described ahead
+constexpr int kBarParts = 1;                // named barrier of those warps
+constexpr float kFewBias = 7.f;             // weights are 2^7 times as large (see pack2)
+
+template <int D>
+struct Few {
+  static constexpr int kCode = D / 2, kScale = D / 16;                 // bytes of a head row
+  static constexpr int kStage = 2 * kGroup * (kCode + kScale);         // K codes, V codes, K scales, V scales
+  static constexpr int kAhead = D == 128 ? 5 : 10;                      // loads in flight, a warp's
+  static constexpr int kRow = D + 4;                                   // floats of a partial row
+};
+struct FewShared {
+  uint64_t ffull[kFewFrags], fempty[kFewFrags];
+  Frag frag[kFewFrags];
+  float2 ml[kWarps][kFewRows];
+  int bad[8];            // first own key whose scale is NaN, by block
+  int any_bad, abort;
+};
+template <int D>
+constexpr size_t few_smem() {
+  return (size_t)kWarps * Few<D>::kAhead * Few<D>::kStage + (size_t)kWarps * kFewRows * Few<D>::kRow * 4 +
+         sizeof(FewShared);
+}
+
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint32_t* b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// n bytes and zeros behind them
+__device__ __forceinline__ void cp_async_part(void* dst, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+// The key that row n of a product's operand is: with rows of 64 bytes swizzled like
+// this, the loads below take all banks.
+__device__ __forceinline__ int key_of(int n) { return (n & ~3) | ((0x9C >> (2 * (n & 3))) & 3); }
+template <int D>
+__device__ __forceinline__ int flip(int row) { return D == 128 ? row >> 1 & 3 : row >> 2 & 1; }
+
+// A warp's walk over the 16-key groups of the CTA's pieces, ahead of their use.
+template <int D>
+struct Loader {
+  const StepAttnArgs& a;
+  FewShared& sh;
+  uint8_t* ring;
+  const int warp, lane;
+  uint32_t piece = 0, slot = 0;
+  int ahead = 0;               // groups on their way, or there and not used yet
+  bool done = false;
+  int i = 0, n = 0;            // group of this warp in the piece
+  int keys, b0, h, pages;      // pages: of the next 32 groups, one a lane
+  const int* table;
+
+  __device__ __forceinline__ Loader(const StepAttnArgs& args, FewShared& s, uint8_t* r, int w, int l)
+      : a(args), sh(s), ring(r), warp(w), lane(l) {}
+  __device__ __forceinline__ int key0(int j) const { return b0 * kKeys + (warp + kWarps * j) * kGroup; }
+  __device__ __forceinline__ void look(int first) {
+    const int j = first + lane;
+    pages = j < n ? table[key0(j) >> a.s.page_shift] : -1;
+    if (pages >= a.s.n_pages) pages = -1;
+  }
+  // Loads until the ring is full or the pieces before `end` are done: the ring of
+  // pieces goes on when every warp has taken the oldest.
+  __device__ __forceinline__ void fill(uint32_t end) {
+    while (ahead < Few<D>::kAhead && next(end)) {
+    }
+  }
+  __device__ __forceinline__ bool next(uint32_t end) {
+    while (!done && i >= n) {
+      if (piece >= end) return false;
+      if (!__all_sync(0xffffffffu, ring_wait(&sh.ffull[piece % kFewFrags], (piece / kFewFrags) & 1))) {
+        sh.abort = 1;
+        done = true;
+        break;
+      }
+      const Frag& f = sh.frag[piece % kFewFrags];
+      ++piece;
+      if (f.seg < 0) {
+        done = true;
+        break;
+      }
+      keys = f.keys, b0 = f.b0, h = f.h;
+      table = f.seg ? a.s.block_table + f.seq * a.s.table_stride : a.s.prefix_pages;
+      const int groups = min((f.b1 - f.b0) * (kKeys / kGroup), (keys - b0 * kKeys + kGroup - 1) / kGroup);
+      n = groups > warp ? (groups - warp + kWarps - 1) / kWarps : 0;
+      i = 0;
+      look(0);
+    }
+    if (done) return false;
+    if (i > 0 && (i & 31) == 0) look(i);
+    const int page = __shfl_sync(0xffffffffu, pages, i & 31), k0 = key0(i), at = k0 & (a.s.page_size - 1);
+    const int left = page < 0 ? 0 : min(keys - k0, kGroup);         // rows that exist
+    uint8_t* st = ring + slot * Few<D>::kStage;
+    const PackedView& c = a.packed;
+    const long from = page < 0 ? 0 : page * c.page_stride + at * c.row_stride + h * c.head_stride;
+    const long sfrom = page < 0 ? 0 : page * c.scale_page_stride + (long)at * Few<D>::kScale + h * c.scale_head_stride;
+    constexpr int kChunks = D / 32;                                 // of a row of codes
+    constexpr int kRows = 32 / kChunks;
+#pragma unroll
+    for (int r0 = 0; r0 < kGroup; r0 += kRows) {
+      const int r = r0 + lane / kChunks, ch = lane % kChunks;
+      const long src = r < left ? from + r * c.row_stride + ch * 16 : 0;
+      uint8_t* dst = st + r * Few<D>::kCode + (ch ^ flip<D>(r)) * 16;
+      cp_async_part(dst, c.k + src, r < left ? 16 : 0);
+      cp_async_part(dst + kGroup * Few<D>::kCode, c.v + src, r < left ? 16 : 0);
+    }
+    constexpr int kBytes = kGroup * Few<D>::kScale;                 // of either's scales
+    if (lane < 2 * kBytes / 16) {
+      const int v = lane >= kBytes / 16, off = (lane - (v ? kBytes / 16 : 0)) * 16;
+      const int some = min(max(left * Few<D>::kScale - off, 0), 16);
+      cp_async_part(st + 2 * kGroup * Few<D>::kCode + v * kBytes + off,
+                    (v ? c.v_scale : c.k_scale) + (some ? sfrom + off : 0), some);
+    }
+    ++i;
+    ++ahead;
+    slot = slot + 1 == Few<D>::kAhead ? 0 : slot + 1;
+    cp_async_commit();
+    return true;
+  }
+  // The oldest group is there.
+  __device__ __forceinline__ void wait() const {
+    constexpr int kHalf = Few<D>::kAhead / 2;
+    if (ahead == Few<D>::kAhead) asm volatile("cp.async.wait_group %0;" ::"n"(Few<D>::kAhead - 1) : "memory");
+    else if (ahead > kHalf) asm volatile("cp.async.wait_group %0;" ::"n"(kHalf) : "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+  }
+};
+
+// One piece's rows of a warp: NT tiles of 8.
+template <int D, bool BF16, int NT>
+struct Rows {
+  static constexpr int kSteps = D / 16;
+  uint32_t q[NT][kSteps][2];     // Q^T operands, every row times a power of two
+  float o[NT][kSteps][4];
+  float sc[NT][2], m[NT][2], l[NT][2];   // of rows 8 nt + 2 t, + 1
+  int lim[NT][2], least;         // keys those see, and the fewest that one sees
+
+  __device__ __forceinline__ void start(const StepAttnArgs& a, const Frag& f, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + g, tok = r / a.G, head = r - tok * a.G;
+      uint32_t w[D / 8];          // D / 4 16-bit elements: 4-element runs a quarter each
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (f.tok0 + tok) * a.q_stride +
+                                                        (long)(f.h * a.G + head) * D + t * (D / 4));
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 x = tok < f.ntok ? src[i] : make_uint4(0, 0, 0, 0);
+        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+      }
+      float up = 1.f;             // what the row's scores are to be multiplied by
+      if constexpr (BF16) {
+        // bf16's range in f16: the row times 2^-e, its largest element in [2^14, 2^15); what is
+        // below 2^-24 then is less than 2^-38 of that
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) top = max(top, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = max((int)(top >> 7), 1) - 127 - 14;             // (127 + 14 - e stays within 1 .. 254)
+        const int ec = min(max(e, -126), 113);
+        const float down = __uint_as_float((uint32_t)(127 - ec) << 23);
+        up = __uint_as_float((uint32_t)(127 + ec) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const float2 v = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(w[i]));
+          w[i] = __float_as_uint(pack2<false>(make_float2(v.x * down, v.y * down)));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) q[nt][j][0] = w[2 * j], q[nt][j][1] = w[2 * j + 1];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        sc[nt][c] = a.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * t + c) * 4);
+        const int at = (8 * nt + 2 * t + c) / a.G;
+        lim[nt][c] = at >= f.ntok ? INT_MAX : f.seg == 1 && a.causal ? min(max(f.lim0 + at, 0), f.keys) : f.keys;
+        m[nt][c] = -INFINITY;
+        l[nt][c] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[nt][j][c] = 0.f;
+    }
+    least = f.seg == 1 && a.causal ? min(max(f.lim0, 0), f.keys) : f.keys;
+  }
+
+  // 16 keys from key0 on
+  __device__ __forceinline__ void keys(const uint8_t* st, int key0, int n_keys, FewShared& sh, int lane) {
+    constexpr int kCode = Few<D>::kCode, kScale = Few<D>::kScale;
+    const int g = lane >> 2, t = lane & 3;
+    const uint8_t* scales = st + 2 * kGroup * kCode;
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[nt][c] = 0.f;
+    {
+      // K: a quarter of two keys' elements
+      const int k = key_of(g);
+      constexpr int kWords = D / 32;
+      uint32_t x[2][kWords];
+      __half2 f[2][2];           // scales of the words' blocks
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = k + 8 * i;
+        if constexpr (D == 128) {
+          const uint4 v = *reinterpret_cast<const uint4*>(st + row * kCode + (t ^ flip<D>(row)) * 16);
+          x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+          const __half2 two = e4m3_to2(*reinterpret_cast<const uint16_t*>(scales + row * kScale + 2 * t));
+          f[i][0] = __low2half2(two), f[i][1] = __high2half2(two);
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(st + row * kCode + ((t >> 1) ^ flip<D>(row)) * 16 + (t & 1) * 8);
+          x[i][0] = v.x, x[i][1] = v.y;
+          f[i][0] = f[i][1] = __low2half2(e4m3_to2(scales[row * kScale + t]));
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        uint32_t p[4], r[4];
+        e2m1_to8(x[0][w], p);
+        e2m1_to8(x[1][w], r);
+        const __half2 f0 = f[0][w * 2 / kWords], f1 = f[1][w * 2 / kWords];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[i] = as_u32(__hmul2(as_half2(p[i]), f0));
+          r[i] = as_u32(__hmul2(as_half2(r[i]), f1));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t op[4] = {p[2 * i], r[2 * i], p[2 * i + 1], r[2 * i + 1]};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], op, q[nt][2 * w + i]);
+        }
+      }
+    }
+    if (key0 + kGroup > least) {
+      const int k = key0 + key_of(g);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (k + 8 * (c >> 1) >= lim[nt][c & 1]) s[nt][c] = -INFINITY;
+    }
+    // the running maximum moves only when it grows by more than 2^8 (kGrow), as in step_attn.cu
+    bool grow = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) grow |= fmaxf(s[nt][c], s[nt][c + 2]) * sc[nt][c] > m[nt][c] + kGrow;
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float mx = fmaxf(s[nt][c], s[nt][c + 2]) * sc[nt][c];
+#pragma unroll
+          for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+          if (mx > m[nt][c] + kGrow) {
+            const float f = ex2_fast(m[nt][c] - mx);
+            m[nt][c] = mx;
+            l[nt][c] *= f;
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j) o[nt][j][c] *= f, o[nt][j][c + 2] *= f;
+          }
+        }
+    }
+    uint32_t p[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float w[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float mc = m[nt][c & 1];
+        w[c] = ex2_fast(fmaf(s[nt][c], sc[nt][c & 1], mc == -INFINITY ? 0.f : kFewBias - mc));
+      }
+      l[nt][0] += w[0] + w[2];
+      l[nt][1] += w[1] + w[3];
+      p[nt][0] = transpose8(__float_as_uint(pack2<false>(make_float2(w[0], w[1]))));
+      p[nt][1] = transpose8(__float_as_uint(pack2<false>(make_float2(w[2], w[3]))));
+    }
+    {
+      // V: an eighth of the elements of four keys
+      const int k[4] = {key_of(2 * t), key_of(2 * t + 1), key_of(2 * t) + 8, key_of(2 * t + 1) + 8};
+      constexpr int kWords = D / 64;
+      uint32_t x[4][kWords], sv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* row = st + kGroup * kCode + k[i] * kCode;
+        if constexpr (D == 128) {
+          const uint2 v = *reinterpret_cast<const uint2*>(row + ((g >> 1) ^ flip<D>(k[i])) * 16 + (g & 1) * 8);
+          x[i][0] = v.x, x[i][1] = v.y;
+          sv[i] = scales[kGroup * kScale + k[i] * kScale + g];
+        } else {
+          x[i][0] = *reinterpret_cast<const uint32_t*>(row + ((g >> 2) ^ flip<D>(k[i])) * 16 + (g & 3) * 4);
+          sv[i] = scales[kGroup * kScale + k[i] * kScale + (g >> 1)];
+        }
+      }
+      // NaN scales of the step's own rows that some row must not see: remembered
+      if (key0 + kGroup > least && n_keys > least) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((sv[i] & 0x7F) == kScaleNaN && key0 + k[i] >= least) {
+            sv[i] = 0;
+            atomicMin(&sh.bad[D == 128 ? g : g >> 1], key0 + k[i]);
+            sh.any_bad = 1;
+          }
+      }
+      const __half2 f0 = e4m3_to2(sv[0] | sv[1] << 8), f1 = e4m3_to2(sv[2] | sv[3] << 8);
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        // two keys' nibbles side by side: the even elements, then the odd ones
+        uint32_t v[4][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t lo = x[2 * i][w], hi = x[2 * i + 1][w];
+          e2m1_to8((lo & 0x0F0F0F0Fu) | (hi << 4 & 0xF0F0F0F0u), v[2 * i]);
+          e2m1_to8((lo >> 4 & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u), v[2 * i + 1]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t op[4] = {as_u32(__hmul2(as_half2(v[0][j]), f0)), as_u32(__hmul2(as_half2(v[1][j]), f0)),
+                                  as_u32(__hmul2(as_half2(v[2][j]), f1)), as_u32(__hmul2(as_half2(v[3][j]), f1))};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][4 * w + j], op, p[nt]);
+        }
+      }
+    }
+  }
+
+  // This warp's part into shared memory.
+  __device__ __forceinline__ void finish(float* part, float2* ml, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float sum = l[nt][c];
+#pragma unroll
+        for (int i = 4; i < 32; i <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+        if (g == 0) ml[8 * nt + 2 * t + c] = make_float2(m[nt][c] - kFewBias, sum);
+        float* to = part + (8 * nt + 2 * t + c) * Few<D>::kRow + g * (D / 8);
+#pragma unroll
+        for (int j = 0; j < kSteps; j += 2)
+          *reinterpret_cast<float4*>(to + 2 * j) =
+              make_float4(o[nt][j][c], o[nt][j][c + 2], o[nt][j + 1][c], o[nt][j + 1][c + 2]);
+      }
+  }
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __grid_constant__ StepAttnArgs a,
+                                                                       const bool wide_ran) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  using F = Few<D>;
+  float* parts = reinterpret_cast<float*>(smem + kWarps * F::kAhead * F::kStage);
+  FewShared& sh = *reinterpret_cast<FewShared*>(parts + kWarps * kFewRows * F::kRow);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kFewFrags; ++i) {
+      mbar_init(&sh.ffull[i], 1);
+      mbar_init(&sh.fempty[i], kWarps);
+    }
+    sh.abort = sh.any_bad = 0;
+    for (int i = 0; i < 8; ++i) sh.bad[i] = INT_MAX;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------------ plan
+    plan_pieces<FewCosts>(WalkT<FewCosts>(a, wide_ran ? kOnlyFewRows : kAnyRows), a.n_cta - a.n_wide, sh.frag, sh.ffull, sh.fempty, kFewFrags,
+                          lane);
+  } else {
+    uint8_t* ring = smem + warp * F::kAhead * F::kStage;
+    Loader<D> loader(a, sh, ring, warp, lane);
+    uint32_t slot = 0;
+    int4 split = make_int4(0, 0, 0, 0);
+    auto all = [&]() { asm volatile("barrier.sync %0, %1;" ::"n"(kBarParts), "n"(kWarps * 32) : "memory"); };
+    const int cta = a.n_wide + blockIdx.x;
+    for (uint32_t nf = 0;; ++nf) {
+      // (also where this warp has no group of a piece: the loader reads every piece's
+      // description before the warp lets go of it below)
+      loader.fill(nf + kFewFrags);
+      if (!__all_sync(0xffffffffu, ring_wait(&sh.ffull[nf % kFewFrags], (nf / kFewFrags) & 1))) {
+        sh.abort = 1;      // (the others' waits on this piece fail alike)
+        break;
+      }
+      const Frag f = sh.frag[nf % kFewFrags];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.fempty[nf % kFewFrags]);
+      if (f.seg < 0) break;
+      const int groups = min((f.b1 - f.b0) * (kKeys / kGroup), (f.keys - f.b0 * kKeys + kGroup - 1) / kGroup);
+      const int rows = f.ntok * a.G;
+      float* part = parts + warp * kFewRows * F::kRow;
+      auto run = [&](auto& r) {
+        r.start(a, f, lane);
+        for (int j = warp; j < groups; j += kWarps) {
+          loader.fill(nf + kFewFrags);
+          loader.wait();
+          r.keys(ring + slot * F::kStage, f.b0 * kKeys + j * kGroup, f.keys, sh, lane);
+          slot = slot + 1 == F::kAhead ? 0 : slot + 1;
+          --loader.ahead;
+          __syncwarp();    // all lanes are done with the slot that is filled next
+        }
+        r.finish(part, sh.ml[warp], lane);
+      };
+      if (rows <= 8) {
+        Rows<D, BF16, 1> r;
+        run(r);
+      } else {
+        Rows<D, BF16, 2> r;
+        run(r);
+      }
+      all();
+      // ---- the warps' parts, in order; four elements a thread
+      const bool whole = f.first && f.last_cta == (int)blockIdx.x && a.s.prefix_len == 0;
+      const bool poisoned = sh.any_bad, ok = !*(volatile int*)&sh.abort;
+      for (int e = tid; e < rows * (D / 4); e += kWarps * 32) {
+        const int r = e / (D / 4), c = e % (D / 4) * 4, tok = r / a.G, head = f.h * a.G + r - tok * a.G;
+        float mx = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh.ml[w][r].x);
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 ml = sh.ml[w][r];
+          // a part without a maximum is left out, unless its sum is NaN
+          const float wt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_fast(ml.x - mx);
+          if (ml.x == -INFINITY && ml.y == 0.f) continue;
+          const float4 x = *reinterpret_cast<const float4*>(parts + (w * kFewRows + r) * F::kRow + c);
+          l = fmaf(ml.y, wt, l);
+          o[0] = fmaf(x.x, wt, o[0]), o[1] = fmaf(x.y, wt, o[1]), o[2] = fmaf(x.z, wt, o[2]), o[3] = fmaf(x.w, wt, o[3]);
+        }
+        const int lim = f.seg == 1 && a.causal ? min(max(f.lim0 + tok, 0), f.keys) : f.keys;
+        if (poisoned && sh.bad[c / 16] < lim) o[0] = o[1] = o[2] = o[3] = __int_as_float(0x7fc00000);
+        const long row = f.tok0 + tok, item = row * a.Hq + head;
+        if (whole) {
+          const float inv = !ok ? __int_as_float(0x7fc00000) : l == 0.f ? 0.f : a.out_scale / l;
+          uint32_t y[2];
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+            y[v] = __float_as_uint(pack2<BF16>(make_float2(o[2 * v] * inv, o[2 * v + 1] * inv)));
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.out_stride + (long)head * D + c) =
+              make_uint2(y[0], y[1]);
+          if (c == 0 && a.lse) a.lse[item] = ok ? log_sum(mx, l) : inv;
+        } else {
+          const long at = f.first ? item : cta_row(a, cta, r);
+          *reinterpret_cast<float4*>((f.first ? a.seg_o[f.seg] : a.cta_o) + at * D + c) =
+              make_float4(o[0], o[1], o[2], o[3]);
+          if (c == 0) (f.first ? a.seg_ml[f.seg] : a.cta_ml)[at] = make_float2(mx, l);
+        }
+        if (c == 0 && f.first && r == tok * a.G && !a.by_cta)
+          a.meta[((long)f.seg * a.s.n_rows + row) * a.Hkv + f.h] = make_int4(cta, a.n_wide + f.last_cta, tok, whole);
+      }
+      if (tid == 0 && f.first && !whole) split = make_int4(f.tok0, f.ntok, f.h, a.n_wide + f.last_cta);
+      all();
+      if (poisoned) {
+        if (tid < 8) sh.bad[tid] = INT_MAX;
+        if (tid == 8) sh.any_bad = 0;
+        all();
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (tid == 0 && a.by_cta) a.split[cta] = split;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    const int bad = sh.abort ? DERR_TIMEOUT : 0;
+    a.status[blockIdx.x] = wide_ran && a.status[blockIdx.x] ? a.status[blockIdx.x] : bad;
+  }
+}
+
+template <int D, bool BF16>
+cudaError_t launch(const StepAttnArgs& a, bool wide_ran, cudaStream_t s) {
+  auto* kernel = step_attn_few_kernel<D, BF16>;
+  // the kernel's shared memory is raised once on every device
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(raised.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem<D>());
+    if (e != cudaSuccess) return e;
+    if (dev < 64) raised.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
+  return launch_pdl(kernel, dim3(a.n_cta - a.n_wide), dim3(kFewThreads), few_smem<D>(), s, a, wide_ran);
+}
+
+}  // namespace
+
+cudaError_t launch_step_attention_few(const StepAttnArgs& a, bool wide_ran, cudaStream_t s) {
+  if (a.d == 128) return a.bf16 ? launch<128, true>(a, wide_ran, s) : launch<128, false>(a, wide_ran, s);
+  return a.bf16 ? launch<64, true>(a, wide_ran, s) : launch<64, false>(a, wide_ran, s);
+}
+
+}  // namespace dfl

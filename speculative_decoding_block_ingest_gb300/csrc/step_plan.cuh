@@ -14,6 +14,24 @@ constexpr int kKeys = 128;   // keys of a block
 // 11000 for 128, 13000 for 256).
 constexpr int kPairUnits = 4, kSingleUnits = 3;
 __host__ __device__ inline int end_units(int rows) { return 6 + min(rows, 128) / 16; }
+struct WideCosts {
+  static constexpr int kPair = kPairUnits, kSingle = kSingleUnits;
+  __host__ __device__ static int ends(int rows) { return end_units(rows); }
+  // tokens of an item, at most
+  __host__ __device__ static int tokens(const StepAttnArgs& a) { return 2 * a.tpt; }
+};
+// The same of items of at most kFewRows query rows over a packed cache
+// (step_attn_few.cu), in units of about 450 cycles: a block 900 from HBM, an item's
+// ends 3500.
+constexpr int kFewRows = 16;
+struct FewCosts {
+  static constexpr int kPair = 2, kSingle = 2;
+  __host__ __device__ static int ends(int) { return 8; }
+  __host__ __device__ static int tokens(const StepAttnArgs& a) { return kFewRows / a.G; }
+};
+// Which sequences' items (and whether the prefix's) a kernel takes: all, or those of
+// more / at most kFewRows query rows of a kv head.
+enum RowKind { kAnyRows, kManyRows, kOnlyFewRows };
 
 // One piece of an item that a CTA runs: key blocks [b0, b1) of the segment.
 struct Frag {
@@ -36,9 +54,11 @@ struct Frag {
 // than a block, so the CTAs of an item are consecutive, and an item of one block
 // is whole (with the ends in front, 48 such items were 96 pieces).  On the device
 // a converged warp walks (it skips sequences without rows 32 at a time).
-struct Walk {
+template <class Costs>
+struct WalkT {
   const StepAttnArgs& a;
-  int pair_tok;        // tokens of two tiles
+  const RowKind kind;
+  int pair_tok;        // tokens of an item: two tiles
   int rows;            // rows of all sequences
   int pre_blocks, pre_tiles;
   int ua, ub;          // this CTA's units
@@ -47,18 +67,23 @@ struct Walk {
   int seg, seq, h, tile;
   int row0, T, len;    // the sequence's first row, rows and keys
 
-  __host__ __device__ explicit Walk(const StepAttnArgs& args) : a(args) {
-    pair_tok = 2 * a.tpt;
+  __host__ __device__ explicit WalkT(const StepAttnArgs& args, RowKind k = kAnyRows) : a(args), kind(k) {
+    pair_tok = Costs::tokens(a);
     rows = a.s.start(a.s.n_seq);
     pre_blocks = (a.s.prefix_len + kKeys - 1) / kKeys;
-    pre_tiles = pre_blocks ? (rows + pair_tok - 1) / pair_tok : 0;
+    pre_tiles = pre_blocks && mine(rows) ? (rows + pair_tok - 1) / pair_tok : 0;
   }
-  __host__ __device__ int tokens(int i) const { return max(a.s.start(i + 1) - a.s.start(i), 0); }
+  __host__ __device__ bool mine(int T) const { return kind == kAnyRows || (T * (long)a.G <= kFewRows) == (kind == kOnlyFewRows); }
+  // rows of sequence i (none where its items are another kernel's)
+  __host__ __device__ int tokens(int i) const {
+    const int T = max(a.s.start(i + 1) - a.s.start(i), 0);
+    return mine(T) ? T : 0;
+  }
   // Row starts that decrease make a plan of no units: step_fits bounds the sum
   // of rows that do not, and the sum of others can wrap.
   __host__ __device__ bool falls(int i) const { return a.s.start(i + 1) < a.s.start(i); }
-  __host__ __device__ int weight(int ntok) const { return ntok > a.tpt ? kPairUnits : kSingleUnits; }
-  __host__ __device__ int units(int ntok, int blocks) const { return end_units(ntok * a.G) + blocks * weight(ntok); }
+  __host__ __device__ int weight(int ntok) const { return ntok > a.tpt ? Costs::kPair : Costs::kSingle; }
+  __host__ __device__ int units(int ntok, int blocks) const { return Costs::ends(ntok * a.G) + blocks * weight(ntok); }
   // tokens of tile pair j out of T
   __host__ __device__ int pair_tokens(int j, int T) const { return min(pair_tok, T - j * pair_tok); }
   // keys that rows of tile pair j see of a sequence with T rows and len keys
@@ -83,7 +108,7 @@ struct Walk {
   // than a block of one tile for both its streams (one token behind 4001 keys:
   // 14.6 us, 17.7 with half of that, 15.5 with 16 units).
   __host__ __device__ void divide(int total, int most, int c) {
-    n_cta = min(most, total > 0 ? max(total / (2 * kSingleUnits), 1) : 0);
+    n_cta = min(most, total > 0 ? max(total / (2 * Costs::kSingle), 1) : 0);
     ua = ub = 0;
     if (n_cta <= 0) return;
     share = total / n_cta;
@@ -165,13 +190,13 @@ struct Walk {
       const int w = weight(f.ntok);
       auto block_at = [&](int unit) {   // the first block that starts at `unit` or behind
         const int u = max(unit - pos, 0) + w - 1;
-        return min(w == kPairUnits ? u / kPairUnits : u / kSingleUnits, n);
+        return min(w == Costs::kPair ? u / Costs::kPair : u / Costs::kSingle, n);
       };
       f.b0 = block_at(ua);
       f.b1 = block_at(ub);
       f.first = ua <= pos;
       f.last_cta = f.first ? cta_of(pos + max(n - 1, 0) * w) : -1;
-      pos += n * w + end_units(f.ntok * a.G);
+      pos += n * w + Costs::ends(f.ntok * a.G);
       ++tile;
       if (seg == 0) {
         if (tile == pre_tiles) {
@@ -191,14 +216,19 @@ struct Walk {
   }
 };
 
+using Walk = WalkT<WideCosts>;
+
 // The units of all sequences' own keys on the host's worst case, and of the
 // prefix: an upper bound that fits 31 bits, or more work than is accepted.  (It
 // holds for row starts that do not decrease: their rows are at most n_rows.)
+template <class Costs = WideCosts>
 inline bool step_fits(const StepAttnArgs& a, int max_keys) {
-  const long pairs = ((long)a.s.n_rows + 2 * a.tpt - 1) / (2 * a.tpt);
+  const int tok = Costs::tokens(a);
+  const long pairs = ((long)a.s.n_rows + tok - 1) / tok;
   const long blocks = (max_keys + (long)kKeys - 1) / kKeys, pre = (a.s.prefix_len + (long)kKeys - 1) / kKeys;
-  const long most = end_units(2 * a.tpt * a.G) + kPairUnits;   // and one block more than a share may hold
-  return a.Hkv * ((pairs + a.s.n_seq) * (most + blocks * kPairUnits) + pairs * (most + pre * kPairUnits)) < (1L << 31);
+  const long most = Costs::ends(tok * a.G) + Costs::kPair;   // and one block more than a share may hold
+  return a.Hkv * ((pairs + a.s.n_seq) * (most + blocks * Costs::kPair) + pairs * (most + pre * Costs::kPair)) <
+         (1L << 31);
 }
 
 }  // namespace dfl

@@ -102,10 +102,25 @@ int sm_count(int* n) {
   return DFLASH_OK;
 }
 
-// CTAs of the attention: one per SM (each takes all of an SM's tensor memory).
+void set_shape(StepAttnArgs& a, const dflash_paged_cache* c, int n_heads) {
+  a.Hq = n_heads;
+  a.Hkv = c->n_kv_heads;
+  a.G = a.Hq / a.Hkv;
+  a.d = c->head_dim;
+  a.tpt = 128 / a.G;
+}
+
+// CTAs of an attention kernel: one per SM (each takes all of an SM's tensor memory).
 int step_ctas(int* n) {
   if (int rc = sm_count(n)) return rc;
   if (*n > kStepStatusWords) *n = kStepStatusWords;
+  return DFLASH_OK;
+}
+// Those of all kernels of a call; over a packed cache few rows have one of their own.
+int set_ctas(StepAttnArgs& a, bool packed) {
+  if (int rc = step_ctas(&a.n_sm)) return rc;
+  a.n_wide = a.n_sm;
+  a.n_cta = packed && a.G <= kFewRows ? 2 * a.n_sm : a.n_sm;
   return DFLASH_OK;
 }
 
@@ -139,17 +154,10 @@ size_t carve(StepAttnArgs& a, char* base) {
     a.seg_o[i] = reinterpret_cast<float*>(take(rows * a.Hq * a.d * 4));
     a.seg_ml[i] = reinterpret_cast<float2*>(take(rows * a.Hq * 8));
   }
-  a.cta_o = reinterpret_cast<float*>(take((size_t)a.n_cta * 256 * a.d * 4));
-  a.cta_ml = reinterpret_cast<float2*>(take((size_t)a.n_cta * 256 * 8));
+  const size_t parts = cta_row(a, a.n_cta, 0);
+  a.cta_o = reinterpret_cast<float*>(take(parts * a.d * 4));
+  a.cta_ml = reinterpret_cast<float2*>(take(parts * 8));
   return off;
-}
-
-void set_shape(StepAttnArgs& a, const dflash_paged_cache* c, int n_heads) {
-  a.Hq = n_heads;
-  a.Hkv = c->n_kv_heads;
-  a.G = a.Hq / a.Hkv;
-  a.d = c->head_dim;
-  a.tpt = 128 / a.G;
 }
 
 bool rows_ok(const void* ptr, long stride, long elements, long v) {
@@ -264,10 +272,10 @@ int check_attention(const dflash_paged_cache* cache, const dflash_step* step, co
 
 // All of an attention's arguments but the cache's.
 int attention_args(StepAttnArgs& a, const dflash_paged_cache* cache, const dflash_step* step,
-                   const dflash_attention_args* p) {
+                   const dflash_attention_args* p, bool packed) {
   a.s = view(cache, step);
   set_shape(a, cache, p->n_heads);
-  if (int rc = step_ctas(&a.n_cta)) return rc;
+  if (int rc = set_ctas(a, packed)) return rc;
   a.causal = p->causal != 0;
   if (!step_fits(a, a.s.room())) return fail(DFLASH_ERR_UNSUPPORTED, "more work than one call takes: fewer rows");
   const float scale = p->scale > 0 ? p->scale : 1.f / std::sqrt((float)cache->head_dim);
@@ -283,7 +291,20 @@ int attention_args(StepAttnArgs& a, const dflash_paged_cache* cache, const dflas
   // something to merge, at most 256 a CTA: worth looking for them there where
   // there are many more (four prompts of 2000 rows: 178 us against 223; 32
   // single tokens 24.9 against 22.8).
-  a.by_cta = step->prefix_len == 0 && (long)step->n_rows * p->n_heads > 256L * a.n_cta;
+  a.by_cta = step->prefix_len == 0 && (long)step->n_rows * p->n_heads > 256L * a.n_sm;
+  return DFLASH_OK;
+}
+
+int attention_workspace(const dflash_paged_cache* cache, int32_t n_rows, int32_t n_heads, size_t* bytes, bool packed) {
+  if (!bytes) return invalid("bytes is null");
+  if (int rc = check_cache_shape(cache)) return rc;
+  if (int rc = check_heads(cache, n_heads)) return rc;
+  if (int rc = check_rows(n_rows, n_heads)) return rc;
+  StepAttnArgs a{};
+  set_shape(a, cache, n_heads);
+  a.s.n_rows = n_rows;
+  if (int rc = set_ctas(a, packed)) return rc;
+  *bytes = carve(a, nullptr);
   return DFLASH_OK;
 }
 
@@ -357,16 +378,7 @@ int dflash_step_append_packed(const dflash_packed_cache* cache, const dflash_ste
 
 int dflash_step_attention_workspace(const dflash_paged_cache* cache, int32_t n_rows, int32_t n_heads, size_t* bytes) {
   report_error(DFLASH_OK, "");
-  if (!bytes) return invalid("bytes is null");
-  if (int rc = check_cache_shape(cache)) return rc;
-  if (int rc = check_heads(cache, n_heads)) return rc;
-  if (int rc = check_rows(n_rows, n_heads)) return rc;
-  StepAttnArgs a{};
-  set_shape(a, cache, n_heads);
-  a.s.n_rows = n_rows;
-  if (int rc = step_ctas(&a.n_cta)) return rc;
-  *bytes = carve(a, nullptr);
-  return DFLASH_OK;
+  return attention_workspace(cache, n_rows, n_heads, bytes, false);
 }
 
 int dflash_step_attention(const dflash_paged_cache* cache, const dflash_step* step, const dflash_attention_args* p,
@@ -376,7 +388,7 @@ int dflash_step_attention(const dflash_paged_cache* cache, const dflash_step* st
   if (int rc = check_step(cache, step)) return rc;
   if (int rc = check_attention(cache, step, p, workspace)) return rc;
   StepAttnArgs a{};
-  if (int rc = attention_args(a, cache, step, p)) return rc;
+  if (int rc = attention_args(a, cache, step, p, false)) return rc;
   if (int rc = has_workspace(workspace_bytes, carve(a, static_cast<char*>(workspace)))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (step->n_rows == 0) return launched(cudaMemsetAsync(a.status, 0, kStepStatusWords * 4, s), "step attention");
@@ -398,7 +410,7 @@ int dflash_step_attention_packed_workspace(const dflash_packed_cache* cache, int
   report_error(DFLASH_OK, "");
   if (int rc = check_packed_shape(cache)) return rc;
   const dflash_paged_cache shape = shape_of(cache);
-  return dflash_step_attention_workspace(&shape, n_rows, n_heads, bytes);
+  return attention_workspace(&shape, n_rows, n_heads, bytes, true);
 }
 
 int dflash_step_attention_packed(const dflash_packed_cache* cache, const dflash_step* step,
@@ -410,10 +422,16 @@ int dflash_step_attention_packed(const dflash_packed_cache* cache, const dflash_
   if (int rc = check_step(&shape, step)) return rc;
   if (int rc = check_attention(&shape, step, p, workspace)) return rc;
   StepAttnArgs a{};
-  if (int rc = attention_args(a, &shape, step, p)) return rc;
+  if (int rc = attention_args(a, &shape, step, p, true)) return rc;
   a.scale_log2 *= cache->k_unit;
   if (!std::isfinite(a.scale_log2) || a.scale_log2 < 1e-37f) return invalid("scale times the keys' unit must be a normal float");
   a.out_scale = cache->v_unit;
+  a.packed = {static_cast<const uint8_t*>(cache->k),       static_cast<const uint8_t*>(cache->v),
+              static_cast<const uint8_t*>(cache->k_scale), static_cast<const uint8_t*>(cache->v_scale),
+              cache->page_stride,       cache->row_stride, cache->head_stride,
+              cache->scale_page_stride, cache->scale_head_stride};
+  a.q = p->q;
+  a.q_stride = p->q_stride;
   if (int rc = has_workspace(workspace_bytes, carve(a, static_cast<char*>(workspace)))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (step->n_rows == 0) return launched(cudaMemsetAsync(a.status, 0, kStepStatusWords * 4, s), "step attention");
@@ -430,7 +448,18 @@ int dflash_step_attention_packed(const dflash_packed_cache* cache, const dflash_
       !encode_packed_map(&m.k_scale, (int)sc, 3, cache->k_scale, sdims, sstrides, sbox) ||
       !encode_packed_map(&m.v_scale, (int)sc, 3, cache->v_scale, sdims, sstrides, sbox))
     return fail(DFLASH_ERR_CUDA, "tensor map of the queries or the cache was refused");
-  return launched(launch_step_attention4(a, mq, m, s), "packed step attention");
+  // Which kernels: where a sequence has few rows on average, the one for that, alone
+  // where there is no prefix that many rows share (64 single tokens behind a prefix of 4096
+  // 364 -> 220 us); else the other one for all (with a launch more that finds
+  // nothing to do, 8 ragged verifications 16 -> 25 us).
+  const bool some = a.n_cta > a.n_wide && (long)step->n_rows * a.G <= (long)kFewRows * step->n_seq;
+  const bool alone = some && (step->prefix_len == 0 || (long)step->n_rows * a.G <= kFewRows) && !a.by_cta &&
+                     step_fits<FewCosts>(a, a.s.room());
+  if (!some) a.n_cta = a.n_wide;
+  cudaError_t e = alone ? cudaSuccess : launch_step_attention4(a, mq, m, s);
+  if (e == cudaSuccess && some) e = launch_step_attention_few(a, !alone, s);
+  if (e == cudaSuccess) e = launch_step_merge(a, s);
+  return launched(e, "packed step attention");
 }
 
 int dflash_step_attention_status(const void* workspace, void* stream) {
