@@ -111,14 +111,6 @@ struct NextArgs {
 };
 cudaError_t launch_next_step(const NextArgs& a, int n_sm, cudaStream_t s);
 
-// A packed cache in bytes (fp4.cuh); a head's scales of a page lie together.
-struct PackedView {
-  const uint8_t* k;
-  const uint8_t* v;
-  const uint8_t* k_scale;
-  const uint8_t* v_scale;
-  long page_stride, row_stride, head_stride, scale_page_stride, scale_head_stride;
-};
 // Boxes of a packed cache: codes [rows of a page][head_dim / 2 bytes],
 // swizzled by their length, and the scales of as many rows.
 struct PackedMaps {
@@ -153,9 +145,7 @@ struct StepAttnArgs {
   int n_sm;
   int n_cta;           // CTAs that leave partial results: n_wide of step_attn.cu, whose rows come
   int n_wide;          // first, then those of step_attn_few.cu (16 rows each)
-  // a packed cache's, for step_attn_few.cu
-  PackedView packed;
-  const void* q;
+  const void* q;       // (step_attn_few.cu; the other kernel loads boxes)
   long q_stride;
 };
 // A CTA's partial row among all CTAs'.
@@ -167,7 +157,7 @@ cudaError_t launch_step_attention(const StepAttnArgs& a, const CUtensorMap& q, c
 cudaError_t launch_step_attention4(const StepAttnArgs& a, const CUtensorMap& q, const PackedMaps& m, cudaStream_t s);
 // wide_ran: launch_step_attention4 went before with the items of many rows, and has
 // set the status words; else this does all of them.
-cudaError_t launch_step_attention_few(const StepAttnArgs& a, bool wide_ran, cudaStream_t s);
+cudaError_t launch_step_attention_few(const StepAttnArgs& a, const PackedMaps& m, bool wide_ran, cudaStream_t s);
 // o = out_scale sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i over the fragments of every row that is not whole.
 cudaError_t launch_step_merge(const StepAttnArgs& a, cudaStream_t s);
 

@@ -59,17 +59,7 @@ constexpr int kCodeRegs = 64;
 constexpr int kSoftThreads = 256;        // warps 0..7
 constexpr int kMaxStages = 11;
 constexpr int kSharedBytes = 3 * 1024;   // control block
-// a packed cache's tiles as they lie there: codes and scales of 128 head rows.  A
-// copy ends on a 128-byte boundary, and 16 rows' scales at d = 64 are 64 bytes: those
-// of a page take 128.
-constexpr int kCodeTiles = 3;
-constexpr int scale_bytes(int d) { return d == 128 ? kKeys * 8 : kKeys / 16 * 128; }
-constexpr int code_tile(int d) { return kKeys * (d / 2) + scale_bytes(d); }
-template <int D>
-__device__ __forceinline__ int scale_place(int r, int box_rows) {
-  return r * (D / 16) + (D == 64 && box_rows == 16 ? (r >> 4) * 64 : 0);
-}
-static_assert(code_tile(128) % 512 == 0 && code_tile(64) % 512 == 0, "swizzled tiles");
+constexpr int kCodeTiles = 3;            // of a packed cache, codes and scales in flight
 constexpr size_t step_smem(int d, int stages, bool packed) {
   return (size_t)(2 + stages) * (d / 64) * kAtomBytes + kSharedBytes + (packed ? kCodeTiles * code_tile(d) : 0);
 }
@@ -461,7 +451,7 @@ __global__ void __launch_bounds__(step_threads(PACKED), 1)
     } else if (warp == 10) {
       // ------------------------------------------------------------------ fragments
       plan_pieces<WideCosts>(Walk(a, PACKED && a.n_cta > a.n_wide ? kManyRows : kAnyRows), a.n_wide, sh.frag, sh.ffull,
-                             sh.fempty, kFrags, lane);
+                             sh.fempty, kFrags, lane, [](const Frag&) {});
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(soft_regs(PACKED)));

@@ -10,6 +10,18 @@
 namespace dfl {
 
 constexpr int kAtomBytes = kKeys * 128;  // 128 rows x 128 bytes
+
+// A packed cache's tiles in shared memory: codes and scales of 128 head rows.  A
+// copy ends on a 128-byte boundary, and 16 rows' scales at d = 64 are 64 bytes: those
+// of a page take 128.
+constexpr int scale_bytes(int d) { return d == 128 ? kKeys * 8 : kKeys / 16 * 128; }
+constexpr int code_tile(int d) { return kKeys * (d / 2) + scale_bytes(d); }
+template <int D>
+__device__ __forceinline__ int scale_place(int r, int box_rows) {
+  return r * (D / 16) + (D == 64 && box_rows == 16 ? (r >> 4) * 64 : 0);
+}
+static_assert(code_tile(128) % 512 == 0 && code_tile(64) % 512 == 0, "swizzled tiles");
+
 constexpr float kGrow = 8.f;             // O is rescaled when a row's max grows by more than 2^8
 constexpr int kFrags = 2;                // fragments described ahead
 constexpr int kBarPair = 3;              // named barrier of the 256 softmax threads
@@ -164,11 +176,11 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
-// This CTA's pieces of n_cta CTAs' work, described in a ring; seg -1 ends them.  A
-// warp's work.
-template <class Costs>
+// This CTA's pieces of n_cta CTAs' work, described in a ring (and then given to
+// `each`); seg -1 ends them.  A warp's work.
+template <class Costs, class Each>
 __device__ __forceinline__ void plan_pieces(WalkT<Costs> w, int n_cta, Frag* frag, uint64_t* ffull, uint64_t* fempty,
-                                            uint32_t n_frags, int lane) {
+                                            uint32_t n_frags, int lane, Each&& each) {
   // The warp counts all units, 32 sequences at a time, then looks for the
   // sequence that holds this CTA's first.
   const StepAttnArgs& a = w.a;
@@ -217,6 +229,7 @@ __device__ __forceinline__ void plan_pieces(WalkT<Costs> w, int n_cta, Frag* fra
       mbar_arrive(&ffull[i % n_frags]);
     }
     __syncwarp();
+    if (more) each(f);
   }
 }
 

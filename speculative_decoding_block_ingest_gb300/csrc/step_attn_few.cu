@@ -20,10 +20,11 @@
 // those of V 16 elements of four keys, whose nibbles are paired key by key before
 // they become f16.
 //
-// A CTA has 11 such warps, each with every eleventh 16 keys of a piece, its own ring
-// of loads (no barrier between warps) that runs on into the next pieces, and its own
-// running maximum; at a piece's end their parts are summed in a fixed order.  A 12th
-// warp plans.
+// A CTA has 11 such warps, each with every eleventh 16 keys and a running maximum of
+// its own; at a piece's end their parts are summed in a fixed order.  A 12th warp plans
+// the pieces and loads their blocks, ahead into the next ones.  (With a ring of
+// 16-key loads for every warp, 32 TMA boxes for 128 keys bounded it: 231 us for 64
+// decoding sequences, by cp.async 220.)
 #include <atomic>
 
 #include "../../include/dflash.h"
@@ -38,20 +39,22 @@ namespace {
 
 constexpr int kWarps = 11;
 constexpr int kFewThreads = (kWarps + 1) * 32;
-constexpr int kGroup = 16;                  // keys of a load
+constexpr int kGroup = 16;                  // keys of a warp at a time
 constexpr int kFewFrags = 4;                // pieces described ahead
 constexpr int kBarParts = 1;                // named barrier of those warps
 constexpr float kFewBias = 7.f;             // weights are 2^7 times as large (see pack2)
+constexpr float kNoMax = 1e30f;             // bias minus a maximum below any
 
 template <int D>
 struct Few {
-  static constexpr int kCode = D / 2, kScale = D / 16;                 // bytes of a head row
-  static constexpr int kStage = 2 * kGroup * (kCode + kScale);         // K codes, V codes, K scales, V scales
-  static constexpr int kAhead = D == 128 ? 5 : 10;                      // loads in flight, a warp's
-  static constexpr int kRow = D + 4;                                   // floats of a partial row
+  static constexpr int kCode = D / 2, kScale = D / 16;   // bytes of a head row
+  static constexpr int kStage = 2 * code_tile(D);        // a block: K codes, V codes, K scales, V scales
+  static constexpr int kAhead = D == 128 ? 7 : 13;       // blocks in flight
+  static constexpr int kRow = D + 4;                     // floats of a partial row
 };
 struct FewShared {
   uint64_t ffull[kFewFrags], fempty[kFewFrags];
+  uint64_t full[13], empty[13];
   Frag frag[kFewFrags];
   float2 ml[kWarps][kFewRows];
   int bad[8];            // first own key whose scale is NaN, by block
@@ -59,7 +62,7 @@ struct FewShared {
 };
 template <int D>
 constexpr size_t few_smem() {
-  return (size_t)kWarps * Few<D>::kAhead * Few<D>::kStage + (size_t)kWarps * kFewRows * Few<D>::kRow * 4 +
+  return (size_t)Few<D>::kAhead * Few<D>::kStage + (size_t)kWarps * kFewRows * Few<D>::kRow * 4 +
          sizeof(FewShared);
 }
 
@@ -75,103 +78,61 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// n bytes and zeros behind them
-__device__ __forceinline__ void cp_async_part(void* dst, const void* src, int n) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
-}
 // The key that row n of a product's operand is: with rows of 64 bytes swizzled like
 // this, the loads below take all banks.
 __device__ __forceinline__ int key_of(int n) { return (n & ~3) | ((0x9C >> (2 * (n & 3))) & 3); }
 template <int D>
 __device__ __forceinline__ int flip(int row) { return D == 128 ? row >> 1 & 3 : row >> 2 & 1; }
 
-// A warp's walk over the 16-key groups of the CTA's pieces, ahead of their use.
+// The loading warp: a piece's blocks into the ring; false where a wait gave up.
 template <int D>
-struct Loader {
+struct BlockLoader {
   const StepAttnArgs& a;
+  const PackedMaps& maps;
   FewShared& sh;
   uint8_t* ring;
-  const int warp, lane;
-  uint32_t piece = 0, slot = 0;
-  int ahead = 0;               // groups on their way, or there and not used yet
-  bool done = false;
-  int i = 0, n = 0;            // group of this warp in the piece
-  int keys, b0, h, pages;      // pages: of the next 32 groups, one a lane
-  const int* table;
+  const int lane;
+  uint32_t issued = 0;
 
-  __device__ __forceinline__ Loader(const StepAttnArgs& args, FewShared& s, uint8_t* r, int w, int l)
-      : a(args), sh(s), ring(r), warp(w), lane(l) {}
-  __device__ __forceinline__ int key0(int j) const { return b0 * kKeys + (warp + kWarps * j) * kGroup; }
-  __device__ __forceinline__ void look(int first) {
-    const int j = first + lane;
-    pages = j < n ? table[key0(j) >> a.s.page_shift] : -1;
-    if (pages >= a.s.n_pages) pages = -1;
-  }
-  // Loads until the ring is full or the pieces before `end` are done: the ring of
-  // pieces goes on when every warp has taken the oldest.
-  __device__ __forceinline__ void fill(uint32_t end) {
-    while (ahead < Few<D>::kAhead && next(end)) {
-    }
-  }
-  __device__ __forceinline__ bool next(uint32_t end) {
-    while (!done && i >= n) {
-      if (piece >= end) return false;
-      if (!__all_sync(0xffffffffu, ring_wait(&sh.ffull[piece % kFewFrags], (piece / kFewFrags) & 1))) {
+  __device__ __forceinline__ void piece(const Frag& f) {
+    const int* table = f.seg ? a.s.block_table + f.seq * a.s.table_stride : a.s.prefix_pages;
+    const int shift = __ffs(a.box_rows) - 1, n_box = (f.keys + a.box_rows - 1) >> shift;
+    // page ids: one lane per box of the next 32, the following 32 in flight
+    auto page_of = [&](int box) -> int {
+      return box < n_box ? table[(int)(((long)box << shift) >> a.s.page_shift)] : 0;
+    };
+    int win = f.b0 * a.boxes, cur = page_of(win + lane), nxt = page_of(win + 32 + lane);
+    const int kind = lane & 3, bi = lane >> 2;           // K codes, V codes, K scales, V scales
+    const bool sc = kind >= 2, v = kind & 1;
+    const CUtensorMap* map = sc ? (v ? &maps.v_scale : &maps.k_scale) : v ? &maps.v : &maps.k;
+    const int to = sc ? 2 * kKeys * (D / 2) + v * scale_bytes(D) + scale_place<D>(bi * a.box_rows, a.box_rows)
+                      : v * kKeys * (D / 2) + bi * a.box_rows * (D / 2);
+    for (int b = f.b0; b < f.b1; ++b, ++issued) {
+      const int box0 = b * a.boxes, n = min(a.boxes, n_box - box0);
+      if (box0 >= win + 32) {                             // boxes of a block never straddle a window
+        cur = nxt;
+        win += 32;
+        nxt = page_of(win + 32 + lane);
+      }
+      const uint32_t slot = issued % Few<D>::kAhead;
+      if (!__all_sync(0xffffffffu, pipe_wait(&sh.empty[slot], ((issued / Few<D>::kAhead) & 1) ^ 1, &sh.abort))) {
         sh.abort = 1;
-        done = true;
-        break;
+        return;
       }
-      const Frag& f = sh.frag[piece % kFewFrags];
-      ++piece;
-      if (f.seg < 0) {
-        done = true;
-        break;
-      }
-      keys = f.keys, b0 = f.b0, h = f.h;
-      table = f.seg ? a.s.block_table + f.seq * a.s.table_stride : a.s.prefix_pages;
-      const int groups = min((f.b1 - f.b0) * (kKeys / kGroup), (keys - b0 * kKeys + kGroup - 1) / kGroup);
-      n = groups > warp ? (groups - warp + kWarps - 1) / kWarps : 0;
-      i = 0;
-      look(0);
+      if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], (uint32_t)(n * a.box_rows * 2 * (D / 2 + D / 16)));
+      __syncwarp();
+      const int page = __shfl_sync(0xffffffffu, cur, min(box0 - win + bi, 31));
+      const int at = (int)(((long)(box0 + bi) << shift) & (a.s.page_size - 1));
+      uint8_t* dst = ring + slot * Few<D>::kStage + to;
+      if (bi < n && sc) tma_load_3d(dst, map, &sh.full[slot], at, f.h, page);
+      else if (bi < n) tma_load_4d(dst, map, &sh.full[slot], 0, f.h, at, page);
+      __syncwarp();
     }
-    if (done) return false;
-    if (i > 0 && (i & 31) == 0) look(i);
-    const int page = __shfl_sync(0xffffffffu, pages, i & 31), k0 = key0(i), at = k0 & (a.s.page_size - 1);
-    const int left = page < 0 ? 0 : min(keys - k0, kGroup);         // rows that exist
-    uint8_t* st = ring + slot * Few<D>::kStage;
-    const PackedView& c = a.packed;
-    const long from = page < 0 ? 0 : page * c.page_stride + at * c.row_stride + h * c.head_stride;
-    const long sfrom = page < 0 ? 0 : page * c.scale_page_stride + (long)at * Few<D>::kScale + h * c.scale_head_stride;
-    constexpr int kChunks = D / 32;                                 // of a row of codes
-    constexpr int kRows = 32 / kChunks;
-#pragma unroll
-    for (int r0 = 0; r0 < kGroup; r0 += kRows) {
-      const int r = r0 + lane / kChunks, ch = lane % kChunks;
-      const long src = r < left ? from + r * c.row_stride + ch * 16 : 0;
-      uint8_t* dst = st + r * Few<D>::kCode + (ch ^ flip<D>(r)) * 16;
-      cp_async_part(dst, c.k + src, r < left ? 16 : 0);
-      cp_async_part(dst + kGroup * Few<D>::kCode, c.v + src, r < left ? 16 : 0);
-    }
-    constexpr int kBytes = kGroup * Few<D>::kScale;                 // of either's scales
-    if (lane < 2 * kBytes / 16) {
-      const int v = lane >= kBytes / 16, off = (lane - (v ? kBytes / 16 : 0)) * 16;
-      const int some = min(max(left * Few<D>::kScale - off, 0), 16);
-      cp_async_part(st + 2 * kGroup * Few<D>::kCode + v * kBytes + off,
-                    (v ? c.v_scale : c.k_scale) + (some ? sfrom + off : 0), some);
-    }
-    ++i;
-    ++ahead;
-    slot = slot + 1 == Few<D>::kAhead ? 0 : slot + 1;
-    cp_async_commit();
-    return true;
   }
-  // The oldest group is there.
-  __device__ __forceinline__ void wait() const {
-    constexpr int kHalf = Few<D>::kAhead / 2;
-    if (ahead == Few<D>::kAhead) asm volatile("cp.async.wait_group %0;" ::"n"(Few<D>::kAhead - 1) : "memory");
-    else if (ahead > kHalf) asm volatile("cp.async.wait_group %0;" ::"n"(kHalf) : "memory");
-    else asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncwarp();
+  __device__ __forceinline__ void drain() {   // leave no copy in flight behind
+    int none = 0;
+    for (uint32_t i = issued > (uint32_t)Few<D>::kAhead ? issued - Few<D>::kAhead : 0; i < issued; ++i)
+      pipe_wait(&sh.full[i % Few<D>::kAhead], (i / Few<D>::kAhead) & 1, &none);
   }
 };
 
@@ -181,7 +142,7 @@ struct Rows {
   static constexpr int kSteps = D / 16;
   uint32_t q[NT][kSteps][2];     // Q^T operands, every row times a power of two
   float o[NT][kSteps][4];
-  float sc[NT][2], m[NT][2], l[NT][2];   // of rows 8 nt + 2 t, + 1
+  float sc[NT][2], nm[NT][2], l[NT][2];   // of rows 8 nt + 2 t, + 1; nm: 7 minus the running maximum
   int lim[NT][2], least;         // keys those see, and the fewest that one sees
 
   __device__ __forceinline__ void start(const StepAttnArgs& a, const Frag& f, int lane) {
@@ -222,8 +183,8 @@ struct Rows {
       for (int c = 0; c < 2; ++c) {
         sc[nt][c] = a.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * t + c) * 4);
         const int at = (8 * nt + 2 * t + c) / a.G;
-        lim[nt][c] = at >= f.ntok ? INT_MAX : f.seg == 1 && a.causal ? min(max(f.lim0 + at, 0), f.keys) : f.keys;
-        m[nt][c] = -INFINITY;
+        lim[nt][c] = at < f.ntok && f.seg == 1 && a.causal ? min(max(f.lim0 + at, 0), f.keys) : f.keys;
+        nm[nt][c] = kNoMax;
         l[nt][c] = 0.f;
       }
 #pragma unroll
@@ -234,11 +195,12 @@ struct Rows {
     least = f.seg == 1 && a.causal ? min(max(f.lim0, 0), f.keys) : f.keys;
   }
 
-  // 16 keys from key0 on
-  __device__ __forceinline__ void keys(const uint8_t* st, int key0, int n_keys, FewShared& sh, int lane) {
+  // 16 keys from key0 on: K's codes, V's a tile behind, and their scales
+  __device__ __forceinline__ void keys(const uint8_t* st, const uint8_t* scales, int key0, int n_keys, FewShared& sh,
+                                       int lane) {
     constexpr int kCode = Few<D>::kCode, kScale = Few<D>::kScale;
     const int g = lane >> 2, t = lane & 3;
-    const uint8_t* scales = st + 2 * kGroup * kCode;
+    const uint8_t* v_scales = scales + scale_bytes(D);
     float s[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -292,11 +254,14 @@ struct Rows {
           if (k + 8 * (c >> 1) >= lim[nt][c & 1]) s[nt][c] = -INFINITY;
     }
     // the running maximum moves only when it grows by more than 2^8 (kGrow), as in step_attn.cu
+    float x[NT][4];
     bool grow = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) grow |= fmaxf(s[nt][c], s[nt][c + 2]) * sc[nt][c] > m[nt][c] + kGrow;
+      for (int c = 0; c < 4; ++c) x[nt][c] = fmaf(s[nt][c], sc[nt][c & 1], nm[nt][c & 1]);
+      grow |= fmaxf(fmaxf(x[nt][0], x[nt][1]), fmaxf(x[nt][2], x[nt][3])) > kGrow + kFewBias;
+    }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -305,24 +270,25 @@ struct Rows {
           float mx = fmaxf(s[nt][c], s[nt][c + 2]) * sc[nt][c];
 #pragma unroll
           for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
-          if (mx > m[nt][c] + kGrow) {
-            const float f = ex2_fast(m[nt][c] - mx);
-            m[nt][c] = mx;
+          if (mx + nm[nt][c] > kGrow + kFewBias) {
+            const float to = kFewBias - mx, f = ex2_fast(to - nm[nt][c]);
+            nm[nt][c] = to;
             l[nt][c] *= f;
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) o[nt][j][c] *= f, o[nt][j][c + 2] *= f;
           }
         }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[nt][c] = fmaf(s[nt][c], sc[nt][c & 1], nm[nt][c & 1]);
     }
     uint32_t p[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float w[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float mc = m[nt][c & 1];
-        w[c] = ex2_fast(fmaf(s[nt][c], sc[nt][c & 1], mc == -INFINITY ? 0.f : kFewBias - mc));
-      }
+      for (int c = 0; c < 4; ++c) w[c] = ex2_fast(x[nt][c]);
       l[nt][0] += w[0] + w[2];
       l[nt][1] += w[1] + w[3];
       p[nt][0] = transpose8(__float_as_uint(pack2<false>(make_float2(w[0], w[1]))));
@@ -335,21 +301,23 @@ struct Rows {
       uint32_t x[4][kWords], sv[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint8_t* row = st + kGroup * kCode + k[i] * kCode;
+        const uint8_t* row = st + kKeys * kCode + k[i] * kCode;
         if constexpr (D == 128) {
           const uint2 v = *reinterpret_cast<const uint2*>(row + ((g >> 1) ^ flip<D>(k[i])) * 16 + (g & 1) * 8);
           x[i][0] = v.x, x[i][1] = v.y;
-          sv[i] = scales[kGroup * kScale + k[i] * kScale + g];
+          sv[i] = v_scales[k[i] * kScale + g];
         } else {
           x[i][0] = *reinterpret_cast<const uint32_t*>(row + ((g >> 2) ^ flip<D>(k[i])) * 16 + (g & 3) * 4);
-          sv[i] = scales[kGroup * kScale + k[i] * kScale + (g >> 1)];
+          sv[i] = v_scales[k[i] * kScale + (g >> 1)];
         }
       }
-      // NaN scales of the step's own rows that some row must not see: remembered
-      if (key0 + kGroup > least && n_keys > least) {
+      // behind the last key lies anything; NaN scales of the step's own rows that some row
+      // must not see are remembered
+      if (key0 + kGroup > least) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if ((sv[i] & 0x7F) == kScaleNaN && key0 + k[i] >= least) {
+          if (key0 + k[i] >= n_keys) sv[i] = 0;
+          else if ((sv[i] & 0x7F) == kScaleNaN && key0 + k[i] >= least) {
             sv[i] = 0;
             atomicMin(&sh.bad[D == 128 ? g : g >> 1], key0 + k[i]);
             sh.any_bad = 1;
@@ -387,7 +355,8 @@ struct Rows {
         float sum = l[nt][c];
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-        if (g == 0) ml[8 * nt + 2 * t + c] = make_float2(m[nt][c] - kFewBias, sum);
+        // (the sum and O are 2^7 times theirs, and so go with a maximum less 7)
+        if (g == 0) ml[8 * nt + 2 * t + c] = make_float2(nm[nt][c] == kNoMax ? -INFINITY : -nm[nt][c], sum);
         float* to = part + (8 * nt + 2 * t + c) * Few<D>::kRow + g * (D / 8);
 #pragma unroll
         for (int j = 0; j < kSteps; j += 2)
@@ -398,11 +367,12 @@ struct Rows {
 };
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __grid_constant__ StepAttnArgs a,
+__global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __grid_constant__ PackedMaps maps,
+                                                                       const __grid_constant__ StepAttnArgs a,
                                                                        const bool wide_ran) {
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   using F = Few<D>;
-  float* parts = reinterpret_cast<float*>(smem + kWarps * F::kAhead * F::kStage);
+  float* parts = reinterpret_cast<float*>(smem + F::kAhead * F::kStage);
   FewShared& sh = *reinterpret_cast<FewShared*>(parts + kWarps * kFewRows * F::kRow);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -410,6 +380,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __g
       mbar_init(&sh.ffull[i], 1);
       mbar_init(&sh.fempty[i], kWarps);
     }
+    for (int i = 0; i < F::kAhead; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], kWarps);
+    }
+    for (const CUtensorMap* m : {&maps.k, &maps.v, &maps.k_scale, &maps.v_scale}) tma_prefetch_map(m);
     sh.abort = sh.any_bad = 0;
     for (int i = 0; i < 8; ++i) sh.bad[i] = INT_MAX;
     fence_barrier_init();
@@ -419,20 +394,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __g
   pdl_launch_dependents();
 
   if (warp == kWarps) {
-    // ------------------------------------------------------------------ plan
-    plan_pieces<FewCosts>(WalkT<FewCosts>(a, wide_ran ? kOnlyFewRows : kAnyRows), a.n_cta - a.n_wide, sh.frag, sh.ffull, sh.fempty, kFewFrags,
-                          lane);
+    // ------------------------------------------------------------------ plan and loads
+    BlockLoader<D> loader{a, maps, sh, smem, lane};
+    plan_pieces<FewCosts>(WalkT<FewCosts>(a, wide_ran ? kOnlyFewRows : kAnyRows), a.n_cta - a.n_wide, sh.frag, sh.ffull,
+                          sh.fempty, kFewFrags, lane, [&](const Frag& f) { loader.piece(f); });
+    loader.drain();
   } else {
-    uint8_t* ring = smem + warp * F::kAhead * F::kStage;
-    Loader<D> loader(a, sh, ring, warp, lane);
-    uint32_t slot = 0;
+    uint32_t used = 0;                                   // blocks so far
+    bool ok = true;
     int4 split = make_int4(0, 0, 0, 0);
     auto all = [&]() { asm volatile("barrier.sync %0, %1;" ::"n"(kBarParts), "n"(kWarps * 32) : "memory"); };
     const int cta = a.n_wide + blockIdx.x;
     for (uint32_t nf = 0;; ++nf) {
-      // (also where this warp has no group of a piece: the loader reads every piece's
-      // description before the warp lets go of it below)
-      loader.fill(nf + kFewFrags);
       if (!__all_sync(0xffffffffu, ring_wait(&sh.ffull[nf % kFewFrags], (nf / kFewFrags) & 1))) {
         sh.abort = 1;      // (the others' waits on this piece fail alike)
         break;
@@ -441,19 +414,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __g
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.fempty[nf % kFewFrags]);
       if (f.seg < 0) break;
-      const int groups = min((f.b1 - f.b0) * (kKeys / kGroup), (f.keys - f.b0 * kKeys + kGroup - 1) / kGroup);
       const int rows = f.ntok * a.G;
       float* part = parts + warp * kFewRows * F::kRow;
       auto run = [&](auto& r) {
         r.start(a, f, lane);
-        for (int j = warp; j < groups; j += kWarps) {
-          loader.fill(nf + kFewFrags);
-          loader.wait();
-          r.keys(ring + slot * F::kStage, f.b0 * kKeys + j * kGroup, f.keys, sh, lane);
-          slot = slot + 1 == F::kAhead ? 0 : slot + 1;
-          --loader.ahead;
-          __syncwarp();    // all lanes are done with the slot that is filled next
+        for (int b = f.b0; b < f.b1; ++b, ++used) {
+          const uint32_t slot = used % F::kAhead;
+          // (every warp waits for every block, so a barrier's parity is read in turn)
+          if (ok) ok = __all_sync(0xffffffffu, pipe_wait(&sh.full[slot], (used / F::kAhead) & 1, &sh.abort));
+          const int j = (warp + 3 * (int)(used % kWarps)) % kWarps;   // every eleventh group, across blocks too
+          const int key0 = b * kKeys + j * kGroup;
+          const uint8_t* st = smem + slot * F::kStage;
+          if (ok && j < kKeys / kGroup && key0 < f.keys)
+            r.keys(st + j * kGroup * F::kCode, st + 2 * kKeys * F::kCode + scale_place<D>(j * kGroup, a.box_rows), key0,
+                   f.keys, sh, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.empty[slot]);
         }
+        if (!ok) sh.abort = 1;
         r.finish(part, sh.ml[warp], lane);
       };
       if (rows <= 8) {
@@ -466,7 +444,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __g
       all();
       // ---- the warps' parts, in order; four elements a thread
       const bool whole = f.first && f.last_cta == (int)blockIdx.x && a.s.prefix_len == 0;
-      const bool poisoned = sh.any_bad, ok = !*(volatile int*)&sh.abort;
+      const bool poisoned = sh.any_bad;
+      if (*(volatile int*)&sh.abort) ok = false;
       for (int e = tid; e < rows * (D / 4); e += kWarps * 32) {
         const int r = e / (D / 4), c = e % (D / 4) * 4, tok = r / a.G, head = f.h * a.G + r - tok * a.G;
         float mx = -INFINITY, l = 0.f;
@@ -512,7 +491,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __g
         all();
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
     if (tid == 0 && a.by_cta) a.split[cta] = split;
   }
   __syncthreads();
@@ -523,7 +501,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __g
 }
 
 template <int D, bool BF16>
-cudaError_t launch(const StepAttnArgs& a, bool wide_ran, cudaStream_t s) {
+cudaError_t launch(const StepAttnArgs& a, const PackedMaps& m, bool wide_ran, cudaStream_t s) {
   auto* kernel = step_attn_few_kernel<D, BF16>;
   // the kernel's shared memory is raised once on every device
   static std::atomic<uint64_t> raised{0};
@@ -535,14 +513,15 @@ cudaError_t launch(const StepAttnArgs& a, bool wide_ran, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 64) raised.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
-  return launch_pdl(kernel, dim3(a.n_cta - a.n_wide), dim3(kFewThreads), few_smem<D>(), s, a, wide_ran);
+  return launch_pdl(kernel, dim3(a.n_cta - a.n_wide), dim3(kFewThreads), few_smem<D>(), s, m, a, wide_ran);
 }
 
 }  // namespace
 
-cudaError_t launch_step_attention_few(const StepAttnArgs& a, bool wide_ran, cudaStream_t s) {
-  if (a.d == 128) return a.bf16 ? launch<128, true>(a, wide_ran, s) : launch<128, false>(a, wide_ran, s);
-  return a.bf16 ? launch<64, true>(a, wide_ran, s) : launch<64, false>(a, wide_ran, s);
+cudaError_t launch_step_attention_few(const StepAttnArgs& a, const PackedMaps& m, bool wide_ran, cudaStream_t s) {
+  auto* run = a.d == 128 ? (a.bf16 ? launch<128, true> : launch<128, false>)
+                         : (a.bf16 ? launch<64, true> : launch<64, false>);
+  return run(a, m, wide_ran, s);
 }
 
 }  // namespace dfl

@@ -313,6 +313,20 @@ int has_workspace(size_t bytes, size_t need) {
   return DFLASH_OK;
 }
 
+// Maps of boxes of `rows` rows of a page.
+bool encode_packed(PackedMaps* m, const dflash_packed_cache* c, int rows) {
+  const uint64_t heads = c->n_kv_heads, page = c->page_size, n_pages = c->n_pages;
+  const uint64_t dims[4] = {(uint64_t)c->head_dim / 2, heads, page, n_pages}, sdims[3] = {page, heads, n_pages};
+  const uint64_t strides[3] = {(uint64_t)c->head_stride, (uint64_t)c->row_stride, (uint64_t)c->page_stride};
+  const uint64_t sstrides[2] = {(uint64_t)c->scale_head_stride, (uint64_t)c->scale_page_stride};
+  const uint32_t box[4] = {(uint32_t)c->head_dim / 2, 1, (uint32_t)rows, 1}, sbox[3] = {(uint32_t)rows, 1, 1};
+  const int sc = c->head_dim / 16;   // a row's scales are one element
+  return encode_packed_map(&m->k, 1, 4, c->k, dims, strides, box) &&
+         encode_packed_map(&m->v, 1, 4, c->v, dims, strides, box) &&
+         encode_packed_map(&m->k_scale, sc, 3, c->k_scale, sdims, sstrides, sbox) &&
+         encode_packed_map(&m->v_scale, sc, 3, c->v_scale, sdims, sstrides, sbox);
+}
+
 bool encode_queries(CUtensorMap* m, const StepAttnArgs& a, const dflash_attention_args* p, int dtype) {
   const uint64_t dims[3] = {(uint64_t)a.d, (uint64_t)p->n_heads, (uint64_t)a.s.n_rows};
   const uint64_t strides[2] = {(uint64_t)a.d * 2, (uint64_t)p->q_stride * 2};
@@ -426,28 +440,11 @@ int dflash_step_attention_packed(const dflash_packed_cache* cache, const dflash_
   a.scale_log2 *= cache->k_unit;
   if (!std::isfinite(a.scale_log2) || a.scale_log2 < 1e-37f) return invalid("scale times the keys' unit must be a normal float");
   a.out_scale = cache->v_unit;
-  a.packed = {static_cast<const uint8_t*>(cache->k),       static_cast<const uint8_t*>(cache->v),
-              static_cast<const uint8_t*>(cache->k_scale), static_cast<const uint8_t*>(cache->v_scale),
-              cache->page_stride,       cache->row_stride, cache->head_stride,
-              cache->scale_page_stride, cache->scale_head_stride};
   a.q = p->q;
   a.q_stride = p->q_stride;
   if (int rc = has_workspace(workspace_bytes, carve(a, static_cast<char*>(workspace)))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (step->n_rows == 0) return launched(cudaMemsetAsync(a.status, 0, kStepStatusWords * 4, s), "step attention");
-  CUtensorMap mq;
-  PackedMaps m;
-  const uint64_t n_heads = cache->n_kv_heads, page = cache->page_size, n_pages = cache->n_pages, sc = a.d / 16;
-  const uint64_t dims[4] = {(uint64_t)a.d / 2, n_heads, page, n_pages}, sdims[3] = {page, n_heads, n_pages};
-  const uint64_t strides[3] = {(uint64_t)cache->head_stride, (uint64_t)cache->row_stride,
-                               (uint64_t)cache->page_stride};
-  const uint64_t sstrides[2] = {(uint64_t)cache->scale_head_stride, (uint64_t)cache->scale_page_stride};
-  const uint32_t box[4] = {(uint32_t)a.d / 2, 1, (uint32_t)a.box_rows, 1}, sbox[3] = {(uint32_t)a.box_rows, 1, 1};
-  if (!encode_queries(&mq, a, p, cache->dtype) || !encode_packed_map(&m.k, 1, 4, cache->k, dims, strides, box) ||
-      !encode_packed_map(&m.v, 1, 4, cache->v, dims, strides, box) ||
-      !encode_packed_map(&m.k_scale, (int)sc, 3, cache->k_scale, sdims, sstrides, sbox) ||
-      !encode_packed_map(&m.v_scale, (int)sc, 3, cache->v_scale, sdims, sstrides, sbox))
-    return fail(DFLASH_ERR_CUDA, "tensor map of the queries or the cache was refused");
   // Which kernels: where a sequence has few rows on average, the one for that, alone
   // where there is no prefix that many rows share (64 single tokens behind a prefix of 4096
   // 364 -> 220 us); else the other one for all (with a launch more that finds
@@ -456,8 +453,12 @@ int dflash_step_attention_packed(const dflash_packed_cache* cache, const dflash_
   const bool alone = some && (step->prefix_len == 0 || (long)step->n_rows * a.G <= kFewRows) && !a.by_cta &&
                      step_fits<FewCosts>(a, a.s.room());
   if (!some) a.n_cta = a.n_wide;
+  CUtensorMap mq;
+  PackedMaps m;
+  if (!encode_packed(&m, cache, a.box_rows) || (!alone && !encode_queries(&mq, a, p, cache->dtype)))
+    return fail(DFLASH_ERR_CUDA, "tensor map of the queries or the cache was refused");
   cudaError_t e = alone ? cudaSuccess : launch_step_attention4(a, mq, m, s);
-  if (e == cudaSuccess && some) e = launch_step_attention_few(a, !alone, s);
+  if (e == cudaSuccess && some) e = launch_step_attention_few(a, m, !alone, s);
   if (e == cudaSuccess) e = launch_step_merge(a, s);
   return launched(e, "packed step attention");
 }
