@@ -20,11 +20,11 @@
 // those of V 16 elements of four keys, whose nibbles are paired key by key before
 // they become f16.
 //
-// A CTA has 11 such warps, each with every eleventh 16 keys and a running maximum of
+// A CTA has 11 such warps, each with every eleventh 32 keys and a running maximum of
 // its own; at a piece's end their parts are summed in a fixed order.  A 12th warp plans
-// the pieces and loads their blocks, ahead into the next ones.  (With a ring of
-// 16-key loads for every warp, 32 TMA boxes for 128 keys bounded it: 231 us for 64
-// decoding sequences, by cp.async 220.)
+// the pieces and loads their blocks, ahead into the next ones.  (Smaller loads for a
+// warp each are too many: 64 decoding sequences took 231 us with TMA boxes of 16 keys,
+// 247 with 32, 220 with cp.async.)
 #include <atomic>
 
 #include "../../include/dflash.h"
@@ -39,7 +39,8 @@ namespace {
 
 constexpr int kWarps = 11;
 constexpr int kFewThreads = (kWarps + 1) * 32;
-constexpr int kGroup = 16;                  // keys of a warp at a time
+constexpr int kGroup = 16;                  // keys of a product
+constexpr int kUnit = 2 * kGroup;           // and of a warp at a time
 constexpr int kFewFrags = 4;                // pieces described ahead
 constexpr int kBarParts = 1;                // named barrier of those warps
 constexpr float kFewBias = 7.f;             // weights are 2^7 times as large (see pack2)
@@ -48,7 +49,8 @@ constexpr float kNoMax = 1e30f;             // bias minus a maximum below any
 template <int D>
 struct Few {
   static constexpr int kCode = D / 2, kScale = D / 16;   // bytes of a head row
-  static constexpr int kStage = 2 * code_tile(D);        // a block: K codes, V codes, K scales, V scales
+  static constexpr int kCodes = kKeys * kCode;           // a block's K codes, V codes, K scales, V scales
+  static constexpr int kStage = 2 * code_tile(D);
   static constexpr int kAhead = D == 128 ? 7 : 13;       // blocks in flight
   static constexpr int kRow = D + 4;                     // floats of a partial row
 };
@@ -67,7 +69,7 @@ constexpr size_t few_smem() {
 }
 
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint32_t* b) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
       "%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -75,7 +77,7 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 // The key that row n of a product's operand is: with rows of 64 bytes swizzled like
@@ -195,37 +197,38 @@ struct Rows {
     least = f.seg == 1 && a.causal ? min(max(f.lim0, 0), f.keys) : f.keys;
   }
 
-  // 16 keys from key0 on: K's codes, V's a tile behind, and their scales
-  __device__ __forceinline__ void keys(const uint8_t* st, const uint8_t* scales, int key0, int n_keys, FewShared& sh,
+  // 32 keys, from key0 and row r0 of a block on.
+  __device__ __forceinline__ void keys(const uint8_t* st, int r0, int key0, int n_keys, int box_rows, FewShared& sh,
                                        int lane) {
     constexpr int kCode = Few<D>::kCode, kScale = Few<D>::kScale;
     const int g = lane >> 2, t = lane & 3;
-    const uint8_t* v_scales = scales + scale_bytes(D);
-    float s[NT][4];
+    float s[2][NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) s[nt][c] = 0.f;
-    {
+    for (int u = 0; u < 2; ++u) {
       // K: a quarter of two keys' elements
-      const int k = key_of(g);
+      const uint8_t* codes = st + (r0 + u * kGroup) * kCode;
+      const uint8_t* scales = st + 2 * Few<D>::kCodes + scale_place<D>(r0 + u * kGroup, box_rows);
       constexpr int kWords = D / 32;
       uint32_t x[2][kWords];
       __half2 f[2][2];           // scales of the words' blocks
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int row = k + 8 * i;
+        const int row = key_of(g) + 8 * i;
         if constexpr (D == 128) {
-          const uint4 v = *reinterpret_cast<const uint4*>(st + row * kCode + (t ^ flip<D>(row)) * 16);
+          const uint4 v = *reinterpret_cast<const uint4*>(codes + row * kCode + (t ^ flip<D>(row)) * 16);
           x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
           const __half2 two = e4m3_to2(*reinterpret_cast<const uint16_t*>(scales + row * kScale + 2 * t));
           f[i][0] = __low2half2(two), f[i][1] = __high2half2(two);
         } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(st + row * kCode + ((t >> 1) ^ flip<D>(row)) * 16 + (t & 1) * 8);
+          const uint2 v = *reinterpret_cast<const uint2*>(codes + row * kCode + ((t >> 1) ^ flip<D>(row)) * 16 + (t & 1) * 8);
           x[i][0] = v.x, x[i][1] = v.y;
           f[i][0] = f[i][1] = __low2half2(e4m3_to2(scales[row * kScale + t]));
         }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[u][nt][c] = 0.f;
 #pragma unroll
       for (int w = 0; w < kWords; ++w) {
         uint32_t p[4], r[4];
@@ -241,33 +244,41 @@ struct Rows {
         for (int i = 0; i < 2; ++i) {
           const uint32_t op[4] = {p[2 * i], r[2 * i], p[2 * i + 1], r[2 * i + 1]};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], op, q[nt][2 * w + i]);
+          for (int nt = 0; nt < NT; ++nt) mma16816(s[u][nt], op, q[nt][2 * w + i]);
         }
       }
     }
-    if (key0 + kGroup > least) {
-      const int k = key0 + key_of(g);
+    if (key0 + kUnit > least) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (k + 8 * (c >> 1) >= lim[nt][c & 1]) s[nt][c] = -INFINITY;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (key0 + u * kGroup + key_of(g) + 8 * (c >> 1) >= lim[nt][c & 1]) s[u][nt][c] = -INFINITY;
     }
     // the running maximum moves only when it grows by more than 2^8 (kGrow), as in step_attn.cu
-    float x[NT][4];
+    float x[2][NT][4];
     bool grow = false;
+    auto shift = [&]() {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[nt][c] = fmaf(s[nt][c], sc[nt][c & 1], nm[nt][c & 1]);
-      grow |= fmaxf(fmaxf(x[nt][0], x[nt][1]), fmaxf(x[nt][2], x[nt][3])) > kGrow + kFewBias;
-    }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[u][nt][c] = fmaf(s[u][nt][c], sc[nt][c & 1], nm[nt][c & 1]);
+    };
+    shift();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      grow |= max3(max3(fmaxf(x[0][nt][0], x[0][nt][1]), x[0][nt][2], x[0][nt][3]),
+                   max3(x[1][nt][0], x[1][nt][1], x[1][nt][2]), x[1][nt][3]) > kGrow + kFewBias;
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float mx = fmaxf(s[nt][c], s[nt][c + 2]) * sc[nt][c];
+          float mx = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2])) * sc[nt][c];
 #pragma unroll
           for (int i = 4; i < 32; i <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
           if (mx + nm[nt][c] > kGrow + kFewBias) {
@@ -278,50 +289,55 @@ struct Rows {
             for (int j = 0; j < kSteps; ++j) o[nt][j][c] *= f, o[nt][j][c + 2] *= f;
           }
         }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) x[nt][c] = fmaf(s[nt][c], sc[nt][c & 1], nm[nt][c & 1]);
+      shift();
     }
-    uint32_t p[NT][2];
+    uint32_t p[2][NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float w[4];
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) w[c] = ex2_fast(x[nt][c]);
-      l[nt][0] += w[0] + w[2];
-      l[nt][1] += w[1] + w[3];
-      p[nt][0] = transpose8(__float_as_uint(pack2<false>(make_float2(w[0], w[1]))));
-      p[nt][1] = transpose8(__float_as_uint(pack2<false>(make_float2(w[2], w[3]))));
-    }
-    {
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = ex2_fast(x[u][nt][c]);
+        l[nt][0] += w[0] + w[2];
+        l[nt][1] += w[1] + w[3];
+        p[u][nt][0] = transpose8(__float_as_uint(pack2<false>(make_float2(w[0], w[1]))));
+        p[u][nt][1] = transpose8(__float_as_uint(pack2<false>(make_float2(w[2], w[3]))));
+      }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
       // V: an eighth of the elements of four keys
       const int k[4] = {key_of(2 * t), key_of(2 * t + 1), key_of(2 * t) + 8, key_of(2 * t + 1) + 8};
+      const uint8_t* codes = st + Few<D>::kCodes + (r0 + u * kGroup) * kCode;
+      const uint8_t* scales = st + 2 * Few<D>::kCodes + scale_bytes(D) + scale_place<D>(r0 + u * kGroup, box_rows);
       constexpr int kWords = D / 64;
-      uint32_t x[4][kWords], sv[4];
+      uint32_t y[4][kWords], sv[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint8_t* row = st + kKeys * kCode + k[i] * kCode;
+        const uint8_t* row = codes + k[i] * kCode;
         if constexpr (D == 128) {
           const uint2 v = *reinterpret_cast<const uint2*>(row + ((g >> 1) ^ flip<D>(k[i])) * 16 + (g & 1) * 8);
-          x[i][0] = v.x, x[i][1] = v.y;
-          sv[i] = v_scales[k[i] * kScale + g];
+          y[i][0] = v.x, y[i][1] = v.y;
+          sv[i] = scales[k[i] * kScale + g];
         } else {
-          x[i][0] = *reinterpret_cast<const uint32_t*>(row + ((g >> 2) ^ flip<D>(k[i])) * 16 + (g & 3) * 4);
-          sv[i] = v_scales[k[i] * kScale + (g >> 1)];
+          y[i][0] = *reinterpret_cast<const uint32_t*>(row + ((g >> 2) ^ flip<D>(k[i])) * 16 + (g & 3) * 4);
+          sv[i] = scales[k[i] * kScale + (g >> 1)];
         }
       }
       // behind the last key lies anything; NaN scales of the step's own rows that some row
       // must not see are remembered
-      if (key0 + kGroup > least) {
+      if (key0 + kUnit > least) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (key0 + k[i] >= n_keys) sv[i] = 0;
-          else if ((sv[i] & 0x7F) == kScaleNaN && key0 + k[i] >= least) {
+        for (int i = 0; i < 4; ++i) {
+          const int key = key0 + u * kGroup + k[i];
+          if (key >= n_keys) {
             sv[i] = 0;
-            atomicMin(&sh.bad[D == 128 ? g : g >> 1], key0 + k[i]);
+          } else if ((sv[i] & 0x7F) == kScaleNaN && key >= least) {
+            sv[i] = 0;
+            atomicMin(&sh.bad[D == 128 ? g : g >> 1], key);
             sh.any_bad = 1;
           }
+        }
       }
       const __half2 f0 = e4m3_to2(sv[0] | sv[1] << 8), f1 = e4m3_to2(sv[2] | sv[3] << 8);
 #pragma unroll
@@ -330,7 +346,7 @@ struct Rows {
         uint32_t v[4][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t lo = x[2 * i][w], hi = x[2 * i + 1][w];
+          const uint32_t lo = y[2 * i][w], hi = y[2 * i + 1][w];
           e2m1_to8((lo & 0x0F0F0F0Fu) | (hi << 4 & 0xF0F0F0F0u), v[2 * i]);
           e2m1_to8((lo >> 4 & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u), v[2 * i + 1]);
         }
@@ -339,7 +355,7 @@ struct Rows {
           const uint32_t op[4] = {as_u32(__hmul2(as_half2(v[0][j]), f0)), as_u32(__hmul2(as_half2(v[1][j]), f0)),
                                   as_u32(__hmul2(as_half2(v[2][j]), f1)), as_u32(__hmul2(as_half2(v[3][j]), f1))};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][4 * w + j], op, p[nt]);
+          for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][4 * w + j], op, p[u][nt]);
         }
       }
     }
@@ -400,7 +416,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __g
                           sh.fempty, kFewFrags, lane, [&](const Frag& f) { loader.piece(f); });
     loader.drain();
   } else {
-    uint32_t used = 0;                                   // blocks so far
+    int slot = 0, mine = warp;                           // this warp's next unit, from the next block on
+    uint32_t parity = 0;
+    const int box_rows = a.box_rows;
     bool ok = true;
     int4 split = make_int4(0, 0, 0, 0);
     auto all = [&]() { asm volatile("barrier.sync %0, %1;" ::"n"(kBarParts), "n"(kWarps * 32) : "memory"); };
@@ -418,18 +436,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __g
       float* part = parts + warp * kFewRows * F::kRow;
       auto run = [&](auto& r) {
         r.start(a, f, lane);
-        for (int b = f.b0; b < f.b1; ++b, ++used) {
-          const uint32_t slot = used % F::kAhead;
+        for (int b = f.b0; b < f.b1; ++b) {
           // (every warp waits for every block, so a barrier's parity is read in turn)
-          if (ok) ok = __all_sync(0xffffffffu, pipe_wait(&sh.full[slot], (used / F::kAhead) & 1, &sh.abort));
-          const int j = (warp + 3 * (int)(used % kWarps)) % kWarps;   // every eleventh group, across blocks too
-          const int key0 = b * kKeys + j * kGroup;
-          const uint8_t* st = smem + slot * F::kStage;
-          if (ok && j < kKeys / kGroup && key0 < f.keys)
-            r.keys(st + j * kGroup * F::kCode, st + 2 * kKeys * F::kCode + scale_place<D>(j * kGroup, a.box_rows), key0,
-                   f.keys, sh, lane);
+          if (ok) ok = __all_sync(0xffffffffu, pipe_wait(&sh.full[slot], parity, &sh.abort));
+          if (mine < kKeys / kUnit) {
+            const int key0 = b * kKeys + mine * kUnit;
+            if (ok && key0 < f.keys) r.keys(smem + slot * F::kStage, mine * kUnit, key0, f.keys, box_rows, sh, lane);
+            mine += kWarps;
+          }
+          mine -= kKeys / kUnit;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.empty[slot]);
+          if (++slot == F::kAhead) slot = 0, parity ^= 1;
         }
         if (!ok) sh.abort = 1;
         r.finish(part, sh.ml[warp], lane);
