@@ -116,6 +116,11 @@ cudaError_t launch_next_step(const NextArgs& a, int n_sm, cudaStream_t s);
 struct PackedMaps {
   CUtensorMap k, v, k_scale, v_scale;
 };
+// The same of K and V in one box, the one that lies lower in memory first.
+struct PairMaps {
+  CUtensorMap codes, scales;
+  int v_first[2];
+};
 
 // Attention of a step (step_attn.cu; how it is cut into pieces: step_plan.cuh).
 constexpr int kStepStatusWords = 1024;   // most CTAs (one status word each)
@@ -142,6 +147,7 @@ struct StepAttnArgs {
   float2* seg_ml[2];   // [n_rows][Hq]: its (max, sum)
   float* cta_o;        // [cta_row][d]: the fragment a CTA continues
   float2* cta_ml;      // [cta_row]
+  int few_rows;        // most query rows of an item of step_attn_few.cu: 8 or kFewRows
   int n_sm;
   int n_cta;           // CTAs that leave partial results: n_wide of step_attn.cu, whose rows come
   int n_wide;          // first, then those of step_attn_few.cu (16 rows each)
@@ -157,7 +163,7 @@ cudaError_t launch_step_attention(const StepAttnArgs& a, const CUtensorMap& q, c
 cudaError_t launch_step_attention4(const StepAttnArgs& a, const CUtensorMap& q, const PackedMaps& m, cudaStream_t s);
 // wide_ran: launch_step_attention4 went before with the items of many rows, and has
 // set the status words; else this does all of them.
-cudaError_t launch_step_attention_few(const StepAttnArgs& a, const PackedMaps& m, bool wide_ran, cudaStream_t s);
+cudaError_t launch_step_attention_few(const StepAttnArgs& a, const PairMaps& m, bool wide_ran, cudaStream_t s);
 // o = out_scale sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i over the fragments of every row that is not whole.
 cudaError_t launch_step_merge(const StepAttnArgs& a, cudaStream_t s);
 

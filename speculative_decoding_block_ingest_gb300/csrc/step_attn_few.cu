@@ -20,11 +20,12 @@
 // those of V 16 elements of four keys, whose nibbles are paired key by key before
 // they become f16.
 //
-// A CTA has 11 such warps, each with every eleventh 32 keys and a running maximum of
-// its own; at a piece's end their parts are summed in a fixed order.  A 12th warp plans
-// the pieces and loads their blocks, ahead into the next ones.  (Smaller loads for a
-// warp each are too many: 64 decoding sequences took 231 us with TMA boxes of 16 keys,
-// 247 with 32, 220 with cp.async.)
+// A CTA has 15 such warps for 8 rows (N = 1), or 11 with the registers that 16 need,
+// each with every fifteenth (eleventh) 32 keys and a running maximum of its own; at a
+// piece's end their parts are summed in a fixed order.  A further warp plans the pieces
+// and loads their blocks, ahead into the next ones.  (Smaller loads for a warp each are
+// too many: 64 decoding sequences took 231 us with TMA boxes of 16 keys, 247 with 32,
+// 220 with cp.async; 185 with 11 warps for 8 rows too.)
 #include <atomic>
 
 #include "../../include/dflash.h"
@@ -37,8 +38,6 @@
 namespace dfl {
 namespace {
 
-constexpr int kWarps = 11;
-constexpr int kFewThreads = (kWarps + 1) * 32;
 constexpr int kGroup = 16;                  // keys of a product
 constexpr int kUnit = 2 * kGroup;           // and of a warp at a time
 constexpr int kFewFrags = 4;                // pieces described ahead
@@ -46,27 +45,35 @@ constexpr int kBarParts = 1;                // named barrier of those warps
 constexpr float kFewBias = 7.f;             // weights are 2^7 times as large (see pack2)
 constexpr float kNoMax = 1e30f;             // bias minus a maximum below any
 
-template <int D>
+template <int D, int NT>
 struct Few {
+  static constexpr int kWarps = NT == 1 ? 15 : 11, kThreads = (kWarps + 1) * 32;
+  static constexpr int kTile = 8 * NT;                   // query rows of an item
   static constexpr int kCode = D / 2, kScale = D / 16;   // bytes of a head row
-  static constexpr int kCodes = kKeys * kCode;           // a block's K codes, V codes, K scales, V scales
-  static constexpr int kStage = 2 * code_tile(D);
-  static constexpr int kAhead = D == 128 ? 7 : 13;       // blocks in flight
+  // of a block: by page (of 128 rows at most) K's codes and V's, then by page their scales
+  static constexpr int kCodes = 2 * kKeys * kCode;
+  static constexpr int kStage = kCodes + 2 * kKeys * kScale;
+  static constexpr int kAhead = D == 64 ? 13 : NT == 1 ? 8 : 7;   // blocks in flight
   static constexpr int kRow = D + 4;                     // floats of a partial row
 };
+template <int WARPS, int TILE>
 struct FewShared {
   uint64_t ffull[kFewFrags], fempty[kFewFrags];
   uint64_t full[13], empty[13];
   Frag frag[kFewFrags];
-  float2 ml[kWarps][kFewRows];
+  float2 ml[WARPS][TILE];
   int bad[8];            // first own key whose scale is NaN, by block
   int any_bad, abort;
 };
-template <int D>
+template <int D, int NT>
+using FewState = FewShared<Few<D, NT>::kWarps, Few<D, NT>::kTile>;
+template <int D, int NT>
 constexpr size_t few_smem() {
-  return (size_t)Few<D>::kAhead * Few<D>::kStage + (size_t)kWarps * kFewRows * Few<D>::kRow * 4 +
-         sizeof(FewShared);
+  using F = Few<D, NT>;
+  return (size_t)F::kAhead * F::kStage + (size_t)F::kWarps * F::kTile * F::kRow * 4 + sizeof(FewState<D, NT>);
 }
+static_assert(few_smem<128, 1>() <= 227 * 1024 && few_smem<128, 2>() <= 227 * 1024 && few_smem<64, 1>() <= 227 * 1024 &&
+              few_smem<64, 2>() <= 227 * 1024, "shared memory of the kernel for few rows");
 
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint32_t* b) {
   asm(
@@ -86,12 +93,22 @@ __device__ __forceinline__ int key_of(int n) { return (n & ~3) | ((0x9C >> (2 * 
 template <int D>
 __device__ __forceinline__ int flip(int row) { return D == 128 ? row >> 1 & 3 : row >> 2 & 1; }
 
-// The loading warp: a piece's blocks into the ring; false where a wait gave up.
-template <int D>
+__device__ __forceinline__ void tma_load_5d(void* dst, const void* map, uint64_t* bar, int x, int y, int z, int w, int v) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
+      : "memory");
+}
+
+// The loading warp: a piece's blocks into the ring.  A box has a page's rows of K and
+// of V: issuing the boxes bounds a warp (8 for a block of 64-row pages 159 us, 4 TODO).
+template <int D, int NT>
 struct BlockLoader {
+  using F = Few<D, NT>;
   const StepAttnArgs& a;
-  const PackedMaps& maps;
-  FewShared& sh;
+  const PairMaps& maps;
+  FewState<D, NT>& sh;
   uint8_t* ring;
   const int lane;
   uint32_t issued = 0;
@@ -104,11 +121,9 @@ struct BlockLoader {
       return box < n_box ? table[(int)(((long)box << shift) >> a.s.page_shift)] : 0;
     };
     int win = f.b0 * a.boxes, cur = page_of(win + lane), nxt = page_of(win + 32 + lane);
-    const int kind = lane & 3, bi = lane >> 2;           // K codes, V codes, K scales, V scales
-    const bool sc = kind >= 2, v = kind & 1;
-    const CUtensorMap* map = sc ? (v ? &maps.v_scale : &maps.k_scale) : v ? &maps.v : &maps.k;
-    const int to = sc ? 2 * kKeys * (D / 2) + v * scale_bytes(D) + scale_place<D>(bi * a.box_rows, a.box_rows)
-                      : v * kKeys * (D / 2) + bi * a.box_rows * (D / 2);
+    const bool sc = lane & 1;
+    const int bi = lane >> 1;
+    const int to = (sc ? F::kCodes : 0) + bi * a.box_rows * 2 * (sc ? F::kScale : F::kCode);
     for (int b = f.b0; b < f.b1; ++b, ++issued) {
       const int box0 = b * a.boxes, n = min(a.boxes, n_box - box0);
       if (box0 >= win + 32) {                             // boxes of a block never straddle a window
@@ -116,31 +131,32 @@ struct BlockLoader {
         win += 32;
         nxt = page_of(win + 32 + lane);
       }
-      const uint32_t slot = issued % Few<D>::kAhead;
-      if (!__all_sync(0xffffffffu, pipe_wait(&sh.empty[slot], ((issued / Few<D>::kAhead) & 1) ^ 1, &sh.abort))) {
+      const uint32_t slot = issued % F::kAhead;
+      if (!__all_sync(0xffffffffu, pipe_wait(&sh.empty[slot], ((issued / F::kAhead) & 1) ^ 1, &sh.abort))) {
         sh.abort = 1;
         return;
       }
-      if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], (uint32_t)(n * a.box_rows * 2 * (D / 2 + D / 16)));
+      if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], (uint32_t)(n * a.box_rows * 2 * (F::kCode + F::kScale)));
       __syncwarp();
       const int page = __shfl_sync(0xffffffffu, cur, min(box0 - win + bi, 31));
       const int at = (int)(((long)(box0 + bi) << shift) & (a.s.page_size - 1));
-      uint8_t* dst = ring + slot * Few<D>::kStage + to;
-      if (bi < n && sc) tma_load_3d(dst, map, &sh.full[slot], at, f.h, page);
-      else if (bi < n) tma_load_4d(dst, map, &sh.full[slot], 0, f.h, at, page);
+      uint8_t* dst = ring + slot * F::kStage + to;
+      if (bi < n && sc) tma_load_4d(dst, &maps.scales, &sh.full[slot], at, f.h, page, 0);
+      else if (bi < n) tma_load_5d(dst, &maps.codes, &sh.full[slot], 0, f.h, at, page, 0);
       __syncwarp();
     }
   }
   __device__ __forceinline__ void drain() {   // leave no copy in flight behind
     int none = 0;
-    for (uint32_t i = issued > (uint32_t)Few<D>::kAhead ? issued - Few<D>::kAhead : 0; i < issued; ++i)
-      pipe_wait(&sh.full[i % Few<D>::kAhead], (i / Few<D>::kAhead) & 1, &none);
+    for (uint32_t i = issued > (uint32_t)F::kAhead ? issued - F::kAhead : 0; i < issued; ++i)
+      pipe_wait(&sh.full[i % F::kAhead], (i / F::kAhead) & 1, &none);
   }
 };
 
 // One piece's rows of a warp: NT tiles of 8.
 template <int D, bool BF16, int NT>
 struct Rows {
+  using F = Few<D, NT>;
   static constexpr int kSteps = D / 16;
   uint32_t q[NT][kSteps][2];     // Q^T operands, every row times a power of two
   float o[NT][kSteps][4];
@@ -197,17 +213,19 @@ struct Rows {
     least = f.seg == 1 && a.causal ? min(max(f.lim0, 0), f.keys) : f.keys;
   }
 
-  // 32 keys, from key0 and row r0 of a block on.
-  __device__ __forceinline__ void keys(const uint8_t* st, int r0, int key0, int n_keys, int box_rows, FewShared& sh,
-                                       int lane) {
-    constexpr int kCode = Few<D>::kCode, kScale = Few<D>::kScale;
+  // 32 keys, from key0 and row r0 of a block on; rows of a box, and whether V's codes (scales)
+  // lie first in it.
+  __device__ __forceinline__ void keys(const uint8_t* st, int r0, int key0, int n_keys, int rows, const int* v_first,
+                                       FewState<D, NT>& sh, int lane) {
+    constexpr int kCode = F::kCode, kScale = F::kScale;
     const int g = lane >> 2, t = lane & 3;
     float s[2][NT][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       // K: a quarter of two keys' elements
-      const uint8_t* codes = st + (r0 + u * kGroup) * kCode;
-      const uint8_t* scales = st + 2 * Few<D>::kCodes + scale_place<D>(r0 + u * kGroup, box_rows);
+      const int at = (r0 + u * kGroup) + ((r0 + u * kGroup) & ~(rows - 1));
+      const uint8_t* codes = st + (at + (v_first[0] ? rows : 0)) * kCode;
+      const uint8_t* scales = st + F::kCodes + (at + (v_first[1] ? rows : 0)) * kScale;
       constexpr int kWords = D / 32;
       uint32_t x[2][kWords];
       __half2 f[2][2];           // scales of the words' blocks
@@ -308,8 +326,9 @@ struct Rows {
     for (int u = 0; u < 2; ++u) {
       // V: an eighth of the elements of four keys
       const int k[4] = {key_of(2 * t), key_of(2 * t + 1), key_of(2 * t) + 8, key_of(2 * t + 1) + 8};
-      const uint8_t* codes = st + Few<D>::kCodes + (r0 + u * kGroup) * kCode;
-      const uint8_t* scales = st + 2 * Few<D>::kCodes + scale_bytes(D) + scale_place<D>(r0 + u * kGroup, box_rows);
+      const int at = (r0 + u * kGroup) + ((r0 + u * kGroup) & ~(rows - 1));
+      const uint8_t* codes = st + (at + (v_first[0] ? 0 : rows)) * kCode;
+      const uint8_t* scales = st + F::kCodes + (at + (v_first[1] ? 0 : rows)) * kScale;
       constexpr int kWords = D / 64;
       uint32_t y[4][kWords], sv[4];
 #pragma unroll
@@ -373,7 +392,7 @@ struct Rows {
         for (int i = 4; i < 32; i <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
         // (the sum and O are 2^7 times theirs, and so go with a maximum less 7)
         if (g == 0) ml[8 * nt + 2 * t + c] = make_float2(nm[nt][c] == kNoMax ? -INFINITY : -nm[nt][c], sum);
-        float* to = part + (8 * nt + 2 * t + c) * Few<D>::kRow + g * (D / 8);
+        float* to = part + (8 * nt + 2 * t + c) * F::kRow + g * (D / 8);
 #pragma unroll
         for (int j = 0; j < kSteps; j += 2)
           *reinterpret_cast<float4*>(to + 2 * j) =
@@ -382,14 +401,15 @@ struct Rows {
   }
 };
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __grid_constant__ PackedMaps maps,
-                                                                       const __grid_constant__ StepAttnArgs a,
-                                                                       const bool wide_ran) {
+template <int D, bool BF16, int NT>
+__global__ void __launch_bounds__(Few<D, NT>::kThreads, 1)
+    step_attn_few_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ StepAttnArgs a,
+                         const bool wide_ran) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  using F = Few<D>;
+  using F = Few<D, NT>;
+  constexpr int kWarps = F::kWarps;
   float* parts = reinterpret_cast<float*>(smem + F::kAhead * F::kStage);
-  FewShared& sh = *reinterpret_cast<FewShared*>(parts + kWarps * kFewRows * F::kRow);
+  auto& sh = *reinterpret_cast<FewState<D, NT>*>(parts + kWarps * F::kTile * F::kRow);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kFewFrags; ++i) {
@@ -400,7 +420,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __g
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], kWarps);
     }
-    for (const CUtensorMap* m : {&maps.k, &maps.v, &maps.k_scale, &maps.v_scale}) tma_prefetch_map(m);
+    tma_prefetch_map(&maps.codes);
+    tma_prefetch_map(&maps.scales);
     sh.abort = sh.any_bad = 0;
     for (int i = 0; i < 8; ++i) sh.bad[i] = INT_MAX;
     fence_barrier_init();
@@ -411,7 +432,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __g
 
   if (warp == kWarps) {
     // ------------------------------------------------------------------ plan and loads
-    BlockLoader<D> loader{a, maps, sh, smem, lane};
+    BlockLoader<D, NT> loader{a, maps, sh, smem, lane};
     plan_pieces<FewCosts>(WalkT<FewCosts>(a, wide_ran ? kOnlyFewRows : kAnyRows), a.n_cta - a.n_wide, sh.frag, sh.ffull,
                           sh.fempty, kFewFrags, lane, [&](const Frag& f) { loader.piece(f); });
     loader.drain();
@@ -433,50 +454,42 @@ __global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __g
       if (lane == 0) mbar_arrive(&sh.fempty[nf % kFewFrags]);
       if (f.seg < 0) break;
       const int rows = f.ntok * a.G;
-      float* part = parts + warp * kFewRows * F::kRow;
-      auto run = [&](auto& r) {
-        r.start(a, f, lane);
-        for (int b = f.b0; b < f.b1; ++b) {
-          // (every warp waits for every block, so a barrier's parity is read in turn)
-          if (ok) ok = __all_sync(0xffffffffu, pipe_wait(&sh.full[slot], parity, &sh.abort));
-          if (mine < kKeys / kUnit) {
-            const int key0 = b * kKeys + mine * kUnit;
-            if (ok && key0 < f.keys) r.keys(smem + slot * F::kStage, mine * kUnit, key0, f.keys, box_rows, sh, lane);
-            mine += kWarps;
-          }
-          mine -= kKeys / kUnit;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.empty[slot]);
-          if (++slot == F::kAhead) slot = 0, parity ^= 1;
+      float* part = parts + warp * F::kTile * F::kRow;
+      Rows<D, BF16, NT> r;
+      r.start(a, f, lane);
+      for (int b = f.b0; b < f.b1; ++b) {
+        // (every warp waits for every block, so a barrier's parity is read in turn)
+        if (ok) ok = __all_sync(0xffffffffu, pipe_wait(&sh.full[slot], parity, &sh.abort));
+        if (mine < kKeys / kUnit) {
+          const int key0 = b * kKeys + mine * kUnit;
+          if (ok && key0 < f.keys) r.keys(smem + slot * F::kStage, mine * kUnit, key0, f.keys, box_rows, maps.v_first, sh, lane);
+          mine += kWarps;
         }
-        if (!ok) sh.abort = 1;
-        r.finish(part, sh.ml[warp], lane);
-      };
-      if (rows <= 8) {
-        Rows<D, BF16, 1> r;
-        run(r);
-      } else {
-        Rows<D, BF16, 2> r;
-        run(r);
+        mine -= kKeys / kUnit;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[slot]);
+        if (++slot == F::kAhead) slot = 0, parity ^= 1;
       }
+      if (!ok) sh.abort = 1;
+      r.finish(part, sh.ml[warp], lane);
       all();
       // ---- the warps' parts, in order; four elements a thread
       const bool whole = f.first && f.last_cta == (int)blockIdx.x && a.s.prefix_len == 0;
       const bool poisoned = sh.any_bad;
       if (*(volatile int*)&sh.abort) ok = false;
       for (int e = tid; e < rows * (D / 4); e += kWarps * 32) {
-        const int r = e / (D / 4), c = e % (D / 4) * 4, tok = r / a.G, head = f.h * a.G + r - tok * a.G;
+        const int i = e / (D / 4), c = e % (D / 4) * 4, tok = i / a.G, head = f.h * a.G + i - tok * a.G;
         float mx = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh.ml[w][r].x);
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh.ml[w][i].x);
         float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float2 ml = sh.ml[w][r];
+          const float2 ml = sh.ml[w][i];
           // a part without a maximum is left out, unless its sum is NaN
           const float wt = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_fast(ml.x - mx);
           if (ml.x == -INFINITY && ml.y == 0.f) continue;
-          const float4 x = *reinterpret_cast<const float4*>(parts + (w * kFewRows + r) * F::kRow + c);
+          const float4 x = *reinterpret_cast<const float4*>(parts + (w * F::kTile + i) * F::kRow + c);
           l = fmaf(ml.y, wt, l);
           o[0] = fmaf(x.x, wt, o[0]), o[1] = fmaf(x.y, wt, o[1]), o[2] = fmaf(x.z, wt, o[2]), o[3] = fmaf(x.w, wt, o[3]);
         }
@@ -493,12 +506,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __g
               make_uint2(y[0], y[1]);
           if (c == 0 && a.lse) a.lse[item] = ok ? log_sum(mx, l) : inv;
         } else {
-          const long at = f.first ? item : cta_row(a, cta, r);
+          const long at = f.first ? item : cta_row(a, cta, i);
           *reinterpret_cast<float4*>((f.first ? a.seg_o[f.seg] : a.cta_o) + at * D + c) =
               make_float4(o[0], o[1], o[2], o[3]);
           if (c == 0) (f.first ? a.seg_ml[f.seg] : a.cta_ml)[at] = make_float2(mx, l);
         }
-        if (c == 0 && f.first && r == tok * a.G && !a.by_cta)
+        if (c == 0 && f.first && i == tok * a.G && !a.by_cta)
           a.meta[((long)f.seg * a.s.n_rows + row) * a.Hkv + f.h] = make_int4(cta, a.n_wide + f.last_cta, tok, whole);
       }
       if (tid == 0 && f.first && !whole) split = make_int4(f.tok0, f.ntok, f.h, a.n_wide + f.last_cta);
@@ -518,27 +531,29 @@ __global__ void __launch_bounds__(kFewThreads, 1) step_attn_few_kernel(const __g
   }
 }
 
-template <int D, bool BF16>
-cudaError_t launch(const StepAttnArgs& a, const PackedMaps& m, bool wide_ran, cudaStream_t s) {
-  auto* kernel = step_attn_few_kernel<D, BF16>;
+template <int D, bool BF16, int NT>
+cudaError_t launch(const StepAttnArgs& a, const PairMaps& m, bool wide_ran, cudaStream_t s) {
+  auto* kernel = step_attn_few_kernel<D, BF16, NT>;
   // the kernel's shared memory is raised once on every device
   static std::atomic<uint64_t> raised{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(raised.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem<D>());
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem<D, NT>());
     if (e != cudaSuccess) return e;
     if (dev < 64) raised.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
-  return launch_pdl(kernel, dim3(a.n_cta - a.n_wide), dim3(kFewThreads), few_smem<D>(), s, m, a, wide_ran);
+  return launch_pdl(kernel, dim3(a.n_cta - a.n_wide), dim3(Few<D, NT>::kThreads), few_smem<D, NT>(), s, m, a, wide_ran);
 }
 
 }  // namespace
 
-cudaError_t launch_step_attention_few(const StepAttnArgs& a, const PackedMaps& m, bool wide_ran, cudaStream_t s) {
-  auto* run = a.d == 128 ? (a.bf16 ? launch<128, true> : launch<128, false>)
-                         : (a.bf16 ? launch<64, true> : launch<64, false>);
+cudaError_t launch_step_attention_few(const StepAttnArgs& a, const PairMaps& m, bool wide_ran, cudaStream_t s) {
+  auto* run = a.few_rows == 8 ? a.d == 128 ? (a.bf16 ? launch<128, true, 1> : launch<128, false, 1>)
+                                           : (a.bf16 ? launch<64, true, 1> : launch<64, false, 1>)
+              : a.d == 128    ? (a.bf16 ? launch<128, true, 2> : launch<128, false, 2>)
+                              : (a.bf16 ? launch<64, true, 2> : launch<64, false, 2>);
   return run(a, m, wide_ran, s);
 }
 

@@ -20,17 +20,17 @@ struct WideCosts {
   // tokens of an item, at most
   __host__ __device__ static int tokens(const StepAttnArgs& a) { return 2 * a.tpt; }
 };
-// The same of items of at most kFewRows query rows over a packed cache
-// (step_attn_few.cu), in units of about 450 cycles: a block 900 from HBM, an item's
-// ends 3500.
+// The same of items of at most few_rows (8, or kFewRows) query rows over a packed
+// cache (step_attn_few.cu), in units of about 450 cycles: a block 900 from HBM, an
+// item's ends 3500.
 constexpr int kFewRows = 16;
 struct FewCosts {
   static constexpr int kPair = 2, kSingle = 2;
   __host__ __device__ static int ends(int) { return 8; }
-  __host__ __device__ static int tokens(const StepAttnArgs& a) { return kFewRows / a.G; }
+  __host__ __device__ static int tokens(const StepAttnArgs& a) { return a.few_rows / a.G; }
 };
 // Which sequences' items (and whether the prefix's) a kernel takes: all, or those of
-// more / at most kFewRows query rows of a kv head.
+// more / at most few_rows query rows of a kv head.
 enum RowKind { kAnyRows, kManyRows, kOnlyFewRows };
 
 // One piece of an item that a CTA runs: key blocks [b0, b1) of the segment.
@@ -73,7 +73,7 @@ struct WalkT {
     pre_blocks = (a.s.prefix_len + kKeys - 1) / kKeys;
     pre_tiles = pre_blocks && mine(rows) ? (rows + pair_tok - 1) / pair_tok : 0;
   }
-  __host__ __device__ bool mine(int T) const { return kind == kAnyRows || (T * (long)a.G <= kFewRows) == (kind == kOnlyFewRows); }
+  __host__ __device__ bool mine(int T) const { return kind == kAnyRows || (T * (long)a.G <= a.few_rows) == (kind == kOnlyFewRows); }
   // rows of sequence i (none where its items are another kernel's)
   __host__ __device__ int tokens(int i) const {
     const int T = max(a.s.start(i + 1) - a.s.start(i), 0);

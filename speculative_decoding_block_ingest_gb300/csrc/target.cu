@@ -1,9 +1,11 @@
 // target.cu -- C ABI of the target model's side of a speculative step
 // (include/dflash.h): argument checks, tensor maps and launches.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <utility>
 
 #include "../../include/dflash.h"
@@ -327,6 +329,25 @@ bool encode_packed(PackedMaps* m, const dflash_packed_cache* c, int rows) {
          encode_packed_map(&m->v_scale, sc, 3, c->v_scale, sdims, sstrides, sbox);
 }
 
+// And of K and V together; false where they do not lie like that.
+bool encode_pair(PairMaps* m, const dflash_packed_cache* c, int rows) {
+  const char *k = static_cast<char*>(c->k), *v = static_cast<char*>(c->v);
+  const char *ks = static_cast<char*>(c->k_scale), *vs = static_cast<char*>(c->v_scale);
+  const long apart = v - k, sapart = vs - ks;
+  m->v_first[0] = apart < 0;
+  m->v_first[1] = sapart < 0;
+  if (apart == 0 || sapart == 0 || std::abs(apart) >= (1L << 40) || std::abs(sapart) >= (1L << 40)) return false;
+  const uint64_t heads = c->n_kv_heads, page = c->page_size, n_pages = c->n_pages;
+  const uint64_t dims[5] = {(uint64_t)c->head_dim / 2, heads, page, n_pages, 2}, sdims[4] = {page, heads, n_pages, 2};
+  const uint64_t strides[4] = {(uint64_t)c->head_stride, (uint64_t)c->row_stride, (uint64_t)c->page_stride,
+                               (uint64_t)std::abs(apart)};
+  const uint64_t sstrides[3] = {(uint64_t)c->scale_head_stride, (uint64_t)c->scale_page_stride,
+                                (uint64_t)std::abs(sapart)};
+  const uint32_t box[5] = {(uint32_t)c->head_dim / 2, 1, (uint32_t)rows, 1, 2}, sbox[4] = {(uint32_t)rows, 1, 1, 2};
+  return encode_packed_map(&m->codes, 1, 5, std::min(k, v), dims, strides, box) &&
+         encode_packed_map(&m->scales, c->head_dim / 16, 4, std::min(ks, vs), sdims, sstrides, sbox);
+}
+
 bool encode_queries(CUtensorMap* m, const StepAttnArgs& a, const dflash_attention_args* p, int dtype) {
   const uint64_t dims[3] = {(uint64_t)a.d, (uint64_t)p->n_heads, (uint64_t)a.s.n_rows};
   const uint64_t strides[2] = {(uint64_t)a.d * 2, (uint64_t)p->q_stride * 2};
@@ -447,18 +468,21 @@ int dflash_step_attention_packed(const dflash_packed_cache* cache, const dflash_
   if (step->n_rows == 0) return launched(cudaMemsetAsync(a.status, 0, kStepStatusWords * 4, s), "step attention");
   // Which kernels: where a sequence has few rows on average, the one for that, alone
   // where there is no prefix that many rows share (64 single tokens behind a prefix of 4096
-  // 364 -> 220 us); else the other one for all (with a launch more that finds
+  // 364 us without it); else the other one for all (with a launch more that finds
   // nothing to do, 8 ragged verifications 16 -> 25 us).
-  const bool some = a.n_cta > a.n_wide && (long)step->n_rows * a.G <= (long)kFewRows * step->n_seq;
-  const bool alone = some && (step->prefix_len == 0 || (long)step->n_rows * a.G <= kFewRows) && !a.by_cta &&
+  const long mean = ((long)step->n_rows * a.G + step->n_seq - 1) / step->n_seq;
+  PairMaps pair;
+  const bool some = a.n_cta > a.n_wide && mean <= kFewRows && encode_pair(&pair, cache, a.box_rows);
+  a.few_rows = mean <= 8 && a.G <= 8 ? 8 : kFewRows;
+  const bool alone = some && (step->prefix_len == 0 || (long)step->n_rows * a.G <= a.few_rows) && !a.by_cta &&
                      step_fits<FewCosts>(a, a.s.room());
   if (!some) a.n_cta = a.n_wide;
   CUtensorMap mq;
   PackedMaps m;
-  if (!encode_packed(&m, cache, a.box_rows) || (!alone && !encode_queries(&mq, a, p, cache->dtype)))
+  if (!alone && (!encode_queries(&mq, a, p, cache->dtype) || !encode_packed(&m, cache, a.box_rows)))
     return fail(DFLASH_ERR_CUDA, "tensor map of the queries or the cache was refused");
   cudaError_t e = alone ? cudaSuccess : launch_step_attention4(a, mq, m, s);
-  if (e == cudaSuccess && some) e = launch_step_attention_few(a, m, !alone, s);
+  if (e == cudaSuccess && some) e = launch_step_attention_few(a, pair, !alone, s);
   if (e == cudaSuccess) e = launch_step_merge(a, s);
   return launched(e, "packed step attention");
 }
