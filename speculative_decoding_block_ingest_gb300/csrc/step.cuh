@@ -116,10 +116,11 @@ cudaError_t launch_next_step(const NextArgs& a, int n_sm, cudaStream_t s);
 struct PackedMaps {
   CUtensorMap k, v, k_scale, v_scale;
 };
-// The same of K and V in one box, the one that lies lower in memory first.
+// The same of K and V in one box, the one that lies lower in memory first, or of K
+// and of V where they lie too far apart; of codes and of scales.
 struct PairMaps {
-  CUtensorMap codes, scales;
-  int v_first[2];
+  CUtensorMap codes[2], scales[2];
+  int pair[2], v_first[2];
 };
 
 // Attention of a step (step_attn.cu; how it is cut into pieces: step_plan.cuh).

@@ -52,7 +52,9 @@ struct Few {
   static constexpr int kCode = D / 2, kScale = D / 16;   // bytes of a head row
   // of a block: by page (of 128 rows at most) K's codes and V's, then by page their scales
   static constexpr int kCodes = 2 * kKeys * kCode;
-  static constexpr int kStage = kCodes + 2 * kKeys * kScale;
+  static constexpr int kStage = kCodes + 2 * 1024;
+  // a page's scales take 128 bytes at least: a TMA copy starts on such a boundary
+  static __device__ __forceinline__ int scale_pitch(int rows) { return max(rows * kScale, 128); }
   static constexpr int kAhead = D == 64 ? 13 : NT == 1 ? 8 : 7;   // blocks in flight
   static constexpr int kRow = D + 4;                     // floats of a partial row
 };
@@ -102,7 +104,9 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const void* map, uint64_t
 }
 
 // The loading warp: a piece's blocks into the ring.  A box has a page's rows of K and
-// of V: issuing the boxes bounds a warp (8 for a block of 64-row pages 159 us, 4 TODO).
+// of V where one tensor map can reach both: issuing boxes is what takes this warp's
+// time (8 for a block of 64-row pages instead of 4: 187 us for 64 decoding sequences,
+// not 181).
 template <int D, int NT>
 struct BlockLoader {
   using F = Few<D, NT>;
@@ -121,9 +125,10 @@ struct BlockLoader {
       return box < n_box ? table[(int)(((long)box << shift) >> a.s.page_shift)] : 0;
     };
     int win = f.b0 * a.boxes, cur = page_of(win + lane), nxt = page_of(win + 32 + lane);
-    const bool sc = lane & 1;
-    const int bi = lane >> 1;
-    const int to = (sc ? F::kCodes : 0) + bi * a.box_rows * 2 * (sc ? F::kScale : F::kCode);
+    const int sc = lane & 1, second = lane >> 1 & 1, bi = lane >> 2;
+    const bool pair = maps.pair[sc], mine = !(second && pair);
+    const int to = (sc ? F::kCodes : 0) + (2 * bi + second) * (sc ? F::scale_pitch(a.box_rows) : a.box_rows * F::kCode);
+    const CUtensorMap* map = sc ? &maps.scales[second] : &maps.codes[second];
     for (int b = f.b0; b < f.b1; ++b, ++issued) {
       const int box0 = b * a.boxes, n = min(a.boxes, n_box - box0);
       if (box0 >= win + 32) {                             // boxes of a block never straddle a window
@@ -141,8 +146,12 @@ struct BlockLoader {
       const int page = __shfl_sync(0xffffffffu, cur, min(box0 - win + bi, 31));
       const int at = (int)(((long)(box0 + bi) << shift) & (a.s.page_size - 1));
       uint8_t* dst = ring + slot * F::kStage + to;
-      if (bi < n && sc) tma_load_4d(dst, &maps.scales, &sh.full[slot], at, f.h, page, 0);
-      else if (bi < n) tma_load_5d(dst, &maps.codes, &sh.full[slot], 0, f.h, at, page, 0);
+      if (bi < n && mine) {
+        if (sc && pair) tma_load_4d(dst, map, &sh.full[slot], at, f.h, page, 0);
+        else if (sc) tma_load_3d(dst, map, &sh.full[slot], at, f.h, page);
+        else if (pair) tma_load_5d(dst, map, &sh.full[slot], 0, f.h, at, page, 0);
+        else tma_load_4d(dst, map, &sh.full[slot], 0, f.h, at, page);
+      }
       __syncwarp();
     }
   }
@@ -213,19 +222,20 @@ struct Rows {
     least = f.seg == 1 && a.causal ? min(max(f.lim0, 0), f.keys) : f.keys;
   }
 
-  // 32 keys, from key0 and row r0 of a block on; rows of a box, and whether V's codes (scales)
+  // 32 keys, from key0 and row r0 of a block on; rows of a box (their
+  // logarithm), and whether V's codes (scales)
   // lie first in it.
-  __device__ __forceinline__ void keys(const uint8_t* st, int r0, int key0, int n_keys, int rows, const int* v_first,
+  __device__ __forceinline__ void keys(const uint8_t* st, int r0, int key0, int n_keys, int box_shift, const int* v_first,
                                        FewState<D, NT>& sh, int lane) {
     constexpr int kCode = F::kCode, kScale = F::kScale;
-    const int g = lane >> 2, t = lane & 3;
+    const int g = lane >> 2, t = lane & 3, rows = 1 << box_shift;
     float s[2][NT][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       // K: a quarter of two keys' elements
-      const int at = (r0 + u * kGroup) + ((r0 + u * kGroup) & ~(rows - 1));
-      const uint8_t* codes = st + (at + (v_first[0] ? rows : 0)) * kCode;
-      const uint8_t* scales = st + F::kCodes + (at + (v_first[1] ? rows : 0)) * kScale;
+      const int r = r0 + u * kGroup, box = r >> box_shift, in = r & (rows - 1);
+      const uint8_t* codes = st + ((2 * box + v_first[0]) * rows + in) * kCode;
+      const uint8_t* scales = st + F::kCodes + (2 * box + v_first[1]) * F::scale_pitch(rows) + in * kScale;
       constexpr int kWords = D / 32;
       uint32_t x[2][kWords];
       __half2 f[2][2];           // scales of the words' blocks
@@ -326,9 +336,9 @@ struct Rows {
     for (int u = 0; u < 2; ++u) {
       // V: an eighth of the elements of four keys
       const int k[4] = {key_of(2 * t), key_of(2 * t + 1), key_of(2 * t) + 8, key_of(2 * t + 1) + 8};
-      const int at = (r0 + u * kGroup) + ((r0 + u * kGroup) & ~(rows - 1));
-      const uint8_t* codes = st + (at + (v_first[0] ? 0 : rows)) * kCode;
-      const uint8_t* scales = st + F::kCodes + (at + (v_first[1] ? 0 : rows)) * kScale;
+      const int r = r0 + u * kGroup, box = r >> box_shift, in = r & (rows - 1);
+      const uint8_t* codes = st + ((2 * box + 1 - v_first[0]) * rows + in) * kCode;
+      const uint8_t* scales = st + F::kCodes + (2 * box + 1 - v_first[1]) * F::scale_pitch(rows) + in * kScale;
       constexpr int kWords = D / 64;
       uint32_t y[4][kWords], sv[4];
 #pragma unroll
@@ -420,8 +430,10 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1)
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], kWarps);
     }
-    tma_prefetch_map(&maps.codes);
-    tma_prefetch_map(&maps.scales);
+    for (int i = 0; i < 2; ++i) {
+      if (i == 0 || !maps.pair[0]) tma_prefetch_map(&maps.codes[i]);
+      if (i == 0 || !maps.pair[1]) tma_prefetch_map(&maps.scales[i]);
+    }
     sh.abort = sh.any_bad = 0;
     for (int i = 0; i < 8; ++i) sh.bad[i] = INT_MAX;
     fence_barrier_init();
@@ -439,7 +451,7 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1)
   } else {
     int slot = 0, mine = warp;                           // this warp's next unit, from the next block on
     uint32_t parity = 0;
-    const int box_rows = a.box_rows;
+    const int box_shift = __ffs(a.box_rows) - 1;
     bool ok = true;
     int4 split = make_int4(0, 0, 0, 0);
     auto all = [&]() { asm volatile("barrier.sync %0, %1;" ::"n"(kBarParts), "n"(kWarps * 32) : "memory"); };
@@ -462,7 +474,7 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1)
         if (ok) ok = __all_sync(0xffffffffu, pipe_wait(&sh.full[slot], parity, &sh.abort));
         if (mine < kKeys / kUnit) {
           const int key0 = b * kKeys + mine * kUnit;
-          if (ok && key0 < f.keys) r.keys(smem + slot * F::kStage, mine * kUnit, key0, f.keys, box_rows, maps.v_first, sh, lane);
+          if (ok && key0 < f.keys) r.keys(smem + slot * F::kStage, mine * kUnit, key0, f.keys, box_shift, maps.v_first, sh, lane);
           mine += kWarps;
         }
         mine -= kKeys / kUnit;

@@ -329,23 +329,29 @@ bool encode_packed(PackedMaps* m, const dflash_packed_cache* c, int rows) {
          encode_packed_map(&m->v_scale, sc, 3, c->v_scale, sdims, sstrides, sbox);
 }
 
-// And of K and V together; false where they do not lie like that.
+// And of K and V together, where their distance is one that a tensor map can hold.
 bool encode_pair(PairMaps* m, const dflash_packed_cache* c, int rows) {
-  const char *k = static_cast<char*>(c->k), *v = static_cast<char*>(c->v);
-  const char *ks = static_cast<char*>(c->k_scale), *vs = static_cast<char*>(c->v_scale);
-  const long apart = v - k, sapart = vs - ks;
-  m->v_first[0] = apart < 0;
-  m->v_first[1] = sapart < 0;
-  if (apart == 0 || sapart == 0 || std::abs(apart) >= (1L << 40) || std::abs(sapart) >= (1L << 40)) return false;
   const uint64_t heads = c->n_kv_heads, page = c->page_size, n_pages = c->n_pages;
+  auto encode = [&](CUtensorMap* maps, int* pair, int* v_first, const void* k, const void* v, int element, uint32_t rank,
+                    const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
+    const long apart = static_cast<const char*>(v) - static_cast<const char*>(k);
+    // (boxes of fewer than 128 bytes lie 128 apart, and so by themselves)
+    *pair = apart != 0 && std::abs(apart) < (1L << 40) && (element == 1 || rows * element >= 128);
+    *v_first = *pair && apart < 0;
+    uint64_t st[4];
+    std::copy(strides, strides + rank - 1, st);
+    st[rank - 1] = (uint64_t)std::abs(apart);
+    if (*pair) return encode_packed_map(maps, element, rank + 1, *v_first ? v : k, dims, st, box);
+    return encode_packed_map(maps, element, rank, k, dims, st, box) &&
+           encode_packed_map(maps + 1, element, rank, v, dims, st, box);
+  };
   const uint64_t dims[5] = {(uint64_t)c->head_dim / 2, heads, page, n_pages, 2}, sdims[4] = {page, heads, n_pages, 2};
-  const uint64_t strides[4] = {(uint64_t)c->head_stride, (uint64_t)c->row_stride, (uint64_t)c->page_stride,
-                               (uint64_t)std::abs(apart)};
-  const uint64_t sstrides[3] = {(uint64_t)c->scale_head_stride, (uint64_t)c->scale_page_stride,
-                                (uint64_t)std::abs(sapart)};
+  const uint64_t strides[3] = {(uint64_t)c->head_stride, (uint64_t)c->row_stride, (uint64_t)c->page_stride};
+  const uint64_t sstrides[2] = {(uint64_t)c->scale_head_stride, (uint64_t)c->scale_page_stride};
   const uint32_t box[5] = {(uint32_t)c->head_dim / 2, 1, (uint32_t)rows, 1, 2}, sbox[4] = {(uint32_t)rows, 1, 1, 2};
-  return encode_packed_map(&m->codes, 1, 5, std::min(k, v), dims, strides, box) &&
-         encode_packed_map(&m->scales, c->head_dim / 16, 4, std::min(ks, vs), sdims, sstrides, sbox);
+  return encode(m->codes, m->pair, m->v_first, c->k, c->v, 1, 4, dims, strides, box) &&
+         encode(m->scales, m->pair + 1, m->v_first + 1, c->k_scale, c->v_scale, c->head_dim / 16, 3, sdims, sstrides,
+                sbox);
 }
 
 bool encode_queries(CUtensorMap* m, const StepAttnArgs& a, const dflash_attention_args* p, int dtype) {
@@ -471,15 +477,16 @@ int dflash_step_attention_packed(const dflash_packed_cache* cache, const dflash_
   // 364 us without it); else the other one for all (with a launch more that finds
   // nothing to do, 8 ragged verifications 16 -> 25 us).
   const long mean = ((long)step->n_rows * a.G + step->n_seq - 1) / step->n_seq;
-  PairMaps pair;
-  const bool some = a.n_cta > a.n_wide && mean <= kFewRows && encode_pair(&pair, cache, a.box_rows);
+  const bool some = a.n_cta > a.n_wide && mean <= kFewRows;
   a.few_rows = mean <= 8 && a.G <= 8 ? 8 : kFewRows;
   const bool alone = some && (step->prefix_len == 0 || (long)step->n_rows * a.G <= a.few_rows) && !a.by_cta &&
                      step_fits<FewCosts>(a, a.s.room());
   if (!some) a.n_cta = a.n_wide;
   CUtensorMap mq;
   PackedMaps m;
-  if (!alone && (!encode_queries(&mq, a, p, cache->dtype) || !encode_packed(&m, cache, a.box_rows)))
+  PairMaps pair;
+  if ((!alone && (!encode_queries(&mq, a, p, cache->dtype) || !encode_packed(&m, cache, a.box_rows))) ||
+      (some && !encode_pair(&pair, cache, a.box_rows)))
     return fail(DFLASH_ERR_CUDA, "tensor map of the queries or the cache was refused");
   cudaError_t e = alone ? cudaSuccess : launch_step_attention4(a, mq, m, s);
   if (e == cudaSuccess && some) e = launch_step_attention_few(a, pair, !alone, s);

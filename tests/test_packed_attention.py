@@ -286,6 +286,29 @@ def test_repeats_bit_for_bit_and_replays(T):
         close(out, lse, P.attend_step(q, *f64(mem), starts, lens, table, pre, 2053, 16, causal=True, scale=0.125))
 
 
+def test_pools_in_any_order_and_in_one(T):
+    """K above V in memory, codes and scales each way, both in one pool side by side, and one buffer for both."""
+    rows, kv = [1, 2, 1], [300, 90, 1000]
+    for d, page in ((128, 64), (64, 16)):
+        starts, kv, table, pre, n_pages = R.make_step(rows, kv, page, seed=1)
+        mem = pools(n_pages, page, 2, d, seed=2)
+        q = torch.randn(4, 8, d, generator=torch.Generator().manual_seed(3)).to(BF).to(DEV)
+        step = T.Step(i32(starts), i32(kv), table.to(DEV))
+        k64, v64 = f64(mem)
+        want = {}
+        for swap in (False, True):
+            a, b = (v64, k64) if swap else (k64, v64)
+            want[swap] = P.attend_step(q, a, b, starts, kv, table, pre, 0, page, causal=True, scale=d ** -0.5)
+        want["k"] = P.attend_step(q, k64, k64, starts, kv, table, pre, 0, page, causal=True, scale=d ** -0.5)
+        both = torch.stack([m.transpose(1, 2).contiguous() for m in mem[:2]], 1).transpose(2, 3)
+        sboth = torch.stack([m.transpose(1, 2).contiguous() for m in mem[2:]], 1).transpose(2, 3)
+        for key, pool in ((False, mem), (True, [mem[1], mem[0], mem[3], mem[2]]), ("k", [mem[0], mem[0], mem[2], mem[2]]),
+                          (False, [both[:, 0], both[:, 1], sboth[:, 0], sboth[:, 1]]),
+                          (True, [both[:, 1], both[:, 0], mem[3], mem[2]])):
+            o, lse = T.attention(T.PagedCache4(*pool), step, q)
+            close(o, lse, want[key])
+
+
 def test_calls_on_two_streams_at_once(T):
     case = ([1, 20, 3], [900, 700, 50], 8, 2, 128, 64, BF, True, 200, True)
     (starts, kv, table, pre, mem, q, step, cache), o, lse = attend_case(T, case, seed=30)
