@@ -11,8 +11,9 @@
 // that pass through (and 16-bit ones times a power of two) are exact: their
 // quotients by s are taken so that a tie stays one.  Normed or rotated keys
 // carry an f32 error of at most `slack` times their pair: a row with a code or a
-// scale that changes within it (one warp pass in fifty of normal rows) is
-// computed again in 64 bits.
+// scale that changes within it (one pass of a warp in fifty over normal rows) is
+// computed again in two floats, and if that is not enough (2^-38 of a pair) in 64
+// bits.  64 bits at once took 18 us for one such row.
 //
 // Bytes bound it as in step_append.cu, whose division of rows among warps and
 // lanes it shares.
@@ -36,14 +37,15 @@ __device__ __forceinline__ float odd_float(double x) {
   const float f = __double2float_rz(x);
   return (double)f == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
-// The same of a / b, b with few significant bits, r = 1 / b rounded.  EXACT16: a
-// has at most 11 bits, and a quotient that is no tie is further from one than f32's
-// step.
+// The same of a / b, b with few significant bits, r = 1 / b rounded; large ones as
+// they come.  EXACT16: a has at most 11 bits, and a quotient that is no tie is further
+// from one than f32's step.
 template <bool EXACT16>
 __device__ __forceinline__ float odd_quotient(float a, float b, float r) {
   const float q0 = a * r;
+  if (!(fabsf(q0) < 0x1p20f) || q0 == 0.f) return q0;
   const float q = fmaf(fmaf(-q0, b, a), r, q0);   // a / b to the nearest; exact where that is
-  if (EXACT16 || a == 0.f) return a == 0.f ? a : q;
+  if (EXACT16) return q;
   const float rest = fmaf(-q, b, a);
   if (rest == 0.f) return q;
   const bool below = (rest < 0.f) != (q < 0.f);   // the quotient is nearer to zero than q
@@ -56,39 +58,95 @@ struct Codes {
   uint32_t scale;     // their blocks' scales, the first chunk's in the low byte
 };
 
-// A lane's two chunks once more, in 64 bits (all lanes of a warp come here).
-struct Again {
-  float x[16];
-  const float* gain;
-  int c0, c1;
-  int lanes;          // of a head row
-  bool rot, inter;
-  int from0, from1;   // lane that holds the other chunk of each chunk's block
-  bool second0, second1;   // as its second chunk
-  float inv_unit;
+// Which elements of a head row a lane has: the two chunks that RoPE pairs, or two of
+// the chunks behind the rotated ones; and who has the other chunk of each one's block.
+template <int D>
+struct Lane {
+  static constexpr int kLanes = D / 16;        // lanes of a head row
+  int c0, c1;                                  // the chunks' first elements
+  int from0, from1;                            // lanes that hold the other chunk
+  bool rot, second0, second1;                  // (as their second one)
+  __device__ __forceinline__ Lane(int rot_dim, int lane) {
+    const int pairs = rot_dim / 16, l = lane % kLanes;
+    rot = l < pairs;
+    c0 = 8 * (rot ? l : 2 * pairs + (l - pairs));
+    c1 = rot ? c0 + 8 * pairs : c0 + 8 * (kLanes - pairs);
+    auto holder = [&](int chunk, bool& second) {
+      const int n = chunk < 2 * pairs ? pairs : kLanes - pairs, at = chunk < 2 * pairs ? chunk : chunk - 2 * pairs;
+      second = at >= n;
+      return (lane & ~(kLanes - 1)) + (chunk < 2 * pairs ? 0 : pairs) + at - (second ? n : 0);
+    };
+    from0 = holder((c0 / 8) ^ 1, second0);
+    from1 = holder((c1 / 8) ^ 1, second1);
+  }
 };
 
-__device__ __forceinline__ double max16(const double* y) {
+// Codes and scales of a lane's chunks of a key or value row into the cache, and the
+// values they stand for to where they are wanted.
+template <typename Out, int D>
+__device__ __forceinline__ void store_codes(const Append4Args& p, int c0, int c1, const Codes& c, long row, int h, long dst,
+                                            long sdst) {
+  const AppendArgs& a = p.a;
+  const bool is_v = h >= a.n_heads + a.c.n_kv_heads;
+  const int kv = h - a.n_heads - (is_v ? a.c.n_kv_heads : 0);
+  uint8_t* o = static_cast<uint8_t*>(is_v ? a.c.v : a.c.k) + dst + kv * a.c.head_stride;
+  *reinterpret_cast<uint32_t*>(o + c0 / 2) = c.code[0];
+  *reinterpret_cast<uint32_t*>(o + c1 / 2) = c.code[1];
+  uint8_t* so = static_cast<uint8_t*>(is_v ? p.sc.v : p.sc.k) + sdst + kv * p.sc.head_stride;
+  if (!(c0 & 8)) so[c0 / 16] = (uint8_t)c.scale;
+  if (!(c1 & 8)) so[c1 / 16] = (uint8_t)(c.scale >> 8);
+  Out* vo = static_cast<Out*>(is_v ? p.v_values : p.k_values);
+  if (!vo) return;
+  vo += row * (is_v ? p.v_values_stride : p.k_values_stride) + (long)kv * D;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float f = e4m3_to1(c.scale >> (8 * i)) * (is_v ? p.v_unit : p.k_unit);
+    uint32_t e[4];
+    e2m1_to8(c.code[i], e);
+    Chunk y;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 t = __half22float2(as_half2(e[j]));
+      y.v[2 * j] = t.x * f;
+      y.v[2 * j + 1] = t.y * f;
+    }
+    store8(vo + (i ? c1 : c0), y);
+  }
+}
+
+__device__ __forceinline__ double largest8(const double* y) {
   double m = 0.0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) m = fabs(y[j]) > m || isnan(y[j]) ? fabs(y[j]) : m;
   return m;
 }
 
-__device__ __noinline__ Codes code_again(const Again& g, const Append4Args& p, uint64_t pos, double2* cs) {
+// A warp's key rows (head h of each lane's group) in 64 bits.
+template <typename In, typename Out, int D, bool INTER>
+__device__ __noinline__ void code_exactly(const Append4Args& p, long row, int h, long dst, long sdst, uint64_t pos,
+                                        double2* cs) {
   const AppendArgs& a = p.a;
   const int lane = threadIdx.x & 31;
+  const Lane<D> at(a.rot, lane);
+  const bool mine = h >= a.n_heads && h < a.n_heads + a.c.n_kv_heads;
   double y[16];
+  {
+    Raw<In> x0, x1;
+    const In* src = static_cast<const In*>(a.k) + row * a.k_stride + (long)(mine ? h - a.n_heads : 0) * D;
+    x0.load(src + at.c0);
+    x1.load(src + at.c1);
+    const Chunk z0 = x0.get(), z1 = x1.get();
 #pragma unroll
-  for (int j = 0; j < 16; ++j) y[j] = g.x[j];
-  double ss = 0.0;
+    for (int j = 0; j < 8; ++j) y[j] = z0.v[j], y[8 + j] = z1.v[j];
+  }
+  if (a.k_gain) {
+    double ss = 0.0;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) ss += y[j] * y[j];
-  for (int o = g.lanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (g.gain) {
-    const double r = 1.0 / sqrt(ss / (16 * g.lanes) + p.eps);
+    for (int j = 0; j < 16; ++j) ss += y[j] * y[j];
+    for (int o = Lane<D>::kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const double r = 1.0 / sqrt(ss / D + p.eps);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) y[j] *= r * (double)g.gain[(j < 8 ? g.c0 : g.c1 - 8) + j];
+    for (int j = 0; j < 16; ++j) y[j] *= r * (double)a.k_gain[(j < 8 ? at.c0 : at.c1 - 8) + j];
   }
   if (a.rot) {
     for (int i = lane; i < a.rot / 2; i += 32) {
@@ -97,27 +155,25 @@ __device__ __noinline__ Codes code_again(const Again& g, const Append4Args& p, u
       cs[i] = make_double2(cn * p.mscale, sn * p.mscale);
     }
     __syncwarp();
-    if (g.rot) {
+    if (at.rot) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const double2 w = g.inter ? *pair_angles<true>(cs, j, g.c0, g.c1) : *pair_angles<false>(cs, j, g.c0, g.c1);
-        const int at = (j < 4 ? 0 : 8) + 2 * (j & 3), ia = g.inter ? at : j, ib = g.inter ? at + 1 : j + 8;
-        double ya = 0, yb = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) ya = i == ia ? y[i] : ya, yb = i == ib ? y[i] : yb;
-        const double na = ya * w.x - yb * w.y, nb = yb * w.x + ya * w.y;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = i == ia ? na : i == ib ? nb : y[i];
+        const double2 w = *pair_angles<INTER>(cs, j, at.c0, at.c1);
+        const int first = (j < 4 ? 0 : 8) + 2 * (j & 3);
+        double &ya = y[INTER ? first : j], &yb = y[INTER ? first + 1 : j + 8];
+        const double u = ya, t = yb;
+        ya = u * w.x - t * w.y;
+        yb = t * w.x + u * w.y;
       }
     }
     __syncwarp();
   }
 #pragma unroll
-  for (int j = 0; j < 16; ++j) y[j] *= g.inv_unit;
-  const double m0 = max16(y), m1 = max16(y + 8);
-  const double a0 = __shfl_sync(0xffffffffu, m0, g.from0), a1 = __shfl_sync(0xffffffffu, m1, g.from0);
-  const double b0 = __shfl_sync(0xffffffffu, m0, g.from1), b1 = __shfl_sync(0xffffffffu, m1, g.from1);
-  const double o[2] = {g.second0 ? a1 : a0, g.second1 ? b1 : b0}, m[2] = {m0, m1};
+  for (int j = 0; j < 16; ++j) y[j] *= p.k_inv_unit;
+  const double m0 = largest8(y), m1 = largest8(y + 8);
+  const double a0 = __shfl_sync(0xffffffffu, m0, at.from0), a1 = __shfl_sync(0xffffffffu, m1, at.from0);
+  const double b0 = __shfl_sync(0xffffffffu, m0, at.from1), b1 = __shfl_sync(0xffffffffu, m1, at.from1);
+  const double o[2] = {at.second0 ? a1 : a0, at.second1 ? b1 : b0}, m[2] = {m0, m1};
   Codes c;
   c.scale = 0;
 #pragma unroll
@@ -128,11 +184,196 @@ __device__ __noinline__ Codes code_again(const Again& g, const Append4Args& p, u
     const float s = fine ? e4m3_to1(sc) : 0.f;
     float q[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = s > 0.f ? odd_float(y[8 * i + j] / s) : fine ? copysignf(0.f, (float)y[8 * i + j]) : 0.f;
+    for (int j = 0; j < 8; ++j)
+      q[j] = s > 0.f ? odd_float(y[8 * i + j] / s) : fine ? copysignf(0.f, (float)y[8 * i + j]) : 0.f;
     c.code[i] = e2m1_of8(q);
     c.scale |= sc << (8 * i);
   }
-  return c;
+  if (mine && dst >= 0) store_codes<Out, D>(p, at.c0, at.c1, c, row, h, dst, sdst);
+}
+
+// Numbers of two floats (the second at most half a step of the first): about 2^-46 of
+// a sum's or product's terms is lost.
+struct Two {
+  float h, l;
+};
+__device__ __forceinline__ Two quick(float a, float b) {   // |a| >= |b|
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Two sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two product(float a, float b) {
+  const float p = __fmul_rn(a, b);
+  return {p, __fmaf_rn(a, b, -p)};
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+  const Two s = sum(a.h, b.h);
+  return quick(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  const Two p = product(a.h, b.h);
+  return quick(p.h, __fadd_rn(p.l, __fmaf_rn(a.h, b.l, __fmul_rn(a.l, b.h))));
+}
+__device__ __forceinline__ Two operator*(Two a, float b) {
+  const Two p = product(a.h, b);
+  return quick(p.h, __fmaf_rn(a.l, b, p.l));
+}
+__device__ __forceinline__ Two operator-(Two a) { return {-a.h, -a.l}; }
+// (sums above lose the sign of a zero, which one float's arithmetic gives)
+__device__ __forceinline__ Two zero_as(Two a, float z) { return a.h == 0.f ? Two{z, 0.f} : a; }
+__device__ __forceinline__ Two two(double x) {
+  const float h = (float)x;
+  return {h, (float)(x - h)};
+}
+
+// Sine and cosine of u / 2^64 turns: quarters off, then the Taylor series, whose terms
+// from the fifth on are small enough for one float (up to 4e-7 of the sum: 2^-45).
+__device__ __forceinline__ void sine_cosine(uint64_t u, Two& sn, Two& cn) {
+  const uint64_t quarter = (u + (1ull << 61)) >> 62;
+  const long long r = (long long)(u - (quarter << 62));
+  const float rh = __ll2float_rn(r), rl = __ll2float_rn(r - (long long)rh);
+  const Two x = quick(rh, rl) * Two{0x1.921fb6p-62f, -0x1.777a5cp-87f};   // 2 pi / 2^64
+  const Two z = x * x;
+  const float zh = z.h;
+  // sin x = x (1 - z/3! + z^2/5! - ...), cos x = 1 - z/2! + z^2/4! - ...
+  const float s4 = fmaf(zh, fmaf(zh, fmaf(zh, -7.6471637e-13f, 1.6059044e-10f), -2.5052108e-8f), 2.7557319e-6f);
+  const float c4 = fmaf(zh, fmaf(zh, fmaf(zh, fmaf(zh, 4.7794773e-14f, -1.1470746e-11f), 2.0876757e-9f), -2.7557319e-7f),
+                        2.4801587e-5f);
+  Two s = z * s4 + Two{-0x1.a01a02p-13f, 0x1.7f97fap-39f};
+  Two c = z * c4 + Two{-0x1.6c16c2p-10f, 0x1.27d27ep-35f};
+  s = z * s, c = z * c;
+  s = s + Two{0x1.111112p-7f, -0x1.dddddep-32f};
+  c = c + Two{0x1.555556p-5f, -0x1.555556p-30f};
+  s = z * s + Two{-0x1.555556p-3f, 0x1.555556p-28f};
+  c = z * c + Two{-0.5f, 0.f};
+  s = x * (z * s + Two{1.f, 0.f});
+  c = z * c + Two{1.f, 0.f};
+  sn = quarter & 1 ? c : s;
+  cn = quarter & 1 ? s : c;
+  if (quarter & 2) sn = -sn;
+  if ((quarter + 1) & 2) cn = -cn;
+}
+
+// a / b as odd_quotient has it; unsure where a is nearer than `off` to a tie.
+__device__ __forceinline__ float odd_quotient(Two a, float b, float r, float off, bool& unsure) {
+  const float q0 = a.h * r;
+  if (!(fabsf(q0) < 0x1p20f) || q0 == 0.f) return q0;
+  const float q = fmaf(fmaf(-q0, b, a.h) + a.l, r, q0);
+  const float rest = fmaf(-q, b, a.h) + a.l;
+  unsure |= fabsf(rest) <= off && !(__float_as_uint(q) & 0xFFFFu);   // (ties have 7 bits at most)
+  const bool below = (rest < 0.f) != (q < 0.f);
+  return rest == 0.f ? q : __uint_as_float((__float_as_uint(q) - below) | 1u);
+}
+
+// A warp's key rows (head h of each lane's group) once more, in two floats.
+template <typename In, typename Out, int D, bool INTER>
+__device__ __noinline__ void code_again(const Append4Args& p, long row, int h, long dst, long sdst, uint64_t pos,
+                                        double2* cs64) {
+  const AppendArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+  const Lane<D> at(a.rot, lane);
+  const bool mine = h >= a.n_heads && h < a.n_heads + a.c.n_kv_heads;
+  float4* cs = reinterpret_cast<float4*>(cs64);
+  float x[16];
+  {
+    Raw<In> x0, x1;
+    const In* src = static_cast<const In*>(a.k) + row * a.k_stride + (long)(mine ? h - a.n_heads : 0) * D;
+    x0.load(src + at.c0);
+    x1.load(src + at.c1);
+    const Chunk z0 = x0.get(), z1 = x1.get();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = z0.v[j], x[8 + j] = z1.v[j];
+  }
+  Two y[16];
+  if (a.k_gain) {
+    Two ss{0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 16; ++j) ss = ss + product(x[j], x[j]);
+    for (int o = Lane<D>::kLanes / 2; o; o >>= 1)
+      ss = ss + Two{__shfl_xor_sync(0xffffffffu, ss.h, o), __shfl_xor_sync(0xffffffffu, ss.l, o)};
+    const Two m = ss * (1.f / D) + two(p.eps);
+    // 1 / sqrt m = r + r (1 - m r^2) / 2 to the square of the first one's error
+    const float r0 = rsqrtf(m.h);
+    const Two one = m * product(r0, r0);
+    const float miss = (1.f - one.h) - one.l;
+    const Two r = quick(r0, 0.5f * r0 * miss);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const Two g = r * a.k_gain[(j < 8 ? at.c0 : at.c1 - 8) + j];
+      y[j] = zero_as(g * x[j], g.h * x[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) y[j] = {x[j], 0.f};
+  }
+  if (a.rot) {
+    const Two ms = two(p.mscale);
+    for (int i = lane; i < a.rot / 2; i += 32) {
+      Two sn, cn;
+      sine_cosine(pos * a.turns[i], sn, cn);
+      sn = sn * ms, cn = cn * ms;
+      cs[i] = make_float4(cn.h, cn.l, sn.h, sn.l);
+    }
+    __syncwarp();
+    if (at.rot) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float4 w = *pair_angles<INTER>(cs, j, at.c0, at.c1);
+        const int first = (j < 4 ? 0 : 8) + 2 * (j & 3);
+        Two &ya = y[INTER ? first : j], &yb = y[INTER ? first + 1 : j + 8];
+        const Two u = ya, t = yb, cn{w.x, w.y}, sn{w.z, w.w};
+        ya = zero_as(u * cn + -(t * sn), u.h * cn.h - t.h * sn.h);
+        yb = zero_as(t * cn + u * sn, t.h * cn.h + u.h * sn.h);
+      }
+    }
+    __syncwarp();
+  }
+  // a chunk's largest, and its largest pair (as its error goes)
+  Two top[2] = {{0.f, 0.f}, {0.f, 0.f}};
+  float wide[2] = {0.f, 0.f};
+  uint32_t bits[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const int i = j / 8;
+    const Two v = y[j].h < 0.f ? -y[j] : y[j];
+    if (v.h > top[i].h || (v.h == top[i].h && v.l > top[i].l)) top[i] = v;
+    bits[i] = max(bits[i], __float_as_uint(fabsf(y[j].h)));
+    wide[i] = fmaxf(wide[i], fabsf(y[j].h) + fabsf(y[INTER ? j ^ 1 : j ^ 8].h));
+  }
+  Codes c;
+  c.scale = 0;
+  bool unsure = false;
+  const Two t0 = top[0], t1 = top[1];
+  const float w0 = wide[0], w1 = wide[1];
+  const uint32_t b0 = bits[0], b1 = bits[1];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int from = i ? at.from1 : at.from0;
+    const bool second = i ? at.second1 : at.second0;
+    auto other = [&](auto v0, auto v1) {
+      const auto x0 = __shfl_sync(0xffffffffu, v0, from), x1 = __shfl_sync(0xffffffffu, v1, from);
+      return second ? x1 : x0;
+    };
+    const Two o{other(t0.h, t1.h), other(t0.l, t1.l)};
+    Two big = i ? t1 : t0;
+    if (o.h > big.h || (o.h == big.h && o.l > big.l)) big = o;
+    const float off = 0x1p-38f * fmaxf(i ? w1 : w0, other(w0, w1));
+    const bool fine = max(i ? b1 : b0, other(b0, b1)) < 0x7F800000u;
+    bool open = false;
+    const uint32_t sc = e4m3_of2(odd_quotient(big * p.k_inv_unit, 6.f, 1.f / 6.f, off * p.k_inv_unit, open), 0.f) & 0xFF;
+    const float sf = e4m3_to1(sc), r = sf > 0.f ? __frcp_rn(sf) * p.k_inv_unit : 0.f;
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = odd_quotient(y[8 * i + j], sf * p.k_unit, r, off, open);
+    c.code[i] = fine ? e2m1_of8(q) : 0;
+    c.scale |= (fine ? sc : kScaleNaN) << (8 * i);
+    unsure |= fine && open;
+  }
+  if (__any_sync(0xffffffffu, mine && unsure)) return code_exactly<In, Out, D, INTER>(p, row, h, dst, sdst, pos, cs64);
+  if (mine && dst >= 0) store_codes<Out, D>(p, at.c0, at.c1, c, row, h, dst, sdst);
 }
 
 // Resident CTAs of an SM (the same as in step_append.cu).
@@ -150,37 +391,26 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
   pdl_launch_dependents();
   const AppendArgs& a = p.a;
   const StepView& s = a.s;
-  const int lane = threadIdx.x & 31, l = lane % kLanes;
+  const int lane = threadIdx.x & 31;
   const int id = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
   const int first = id % WARPS * kGroups + lane / kLanes;   // this lane's first head
   const int Hq = a.n_heads, Hkv = a.c.n_kv_heads, heads = Hq + 2 * Hkv;
   double2* cs64 = cs_all[threadIdx.x >> 5];
   float2* cs = reinterpret_cast<float2*>(cs64);
-  // the two chunks of a head row this lane holds: a RoPE pair, or two of the
-  // chunks behind the rotated ones
-  const int pairs = a.rot / 16;
-  const bool rot = l < pairs;
-  const int c0 = 8 * (rot ? l : 2 * pairs + (l - pairs));
-  const int c1 = rot ? c0 + 8 * pairs : c0 + 8 * (kLanes - pairs);
-  // who holds the other chunk of a chunk's block, and as its second one
-  auto holder = [&](int chunk, bool& second) {
-    const int n = chunk < 2 * pairs ? pairs : kLanes - pairs, at = chunk < 2 * pairs ? chunk : chunk - 2 * pairs;
-    second = at >= n;
-    return (lane & ~(kLanes - 1)) + (chunk < 2 * pairs ? 0 : pairs) + at - (second ? n : 0);
-  };
-  bool second0, second1;
-  const int from0 = holder((c0 / 8) ^ 1, second0), from1 = holder((c1 / 8) ^ 1, second1);
-  const bool across = pairs & 1;               // else both are the neighbour's chunk of the same place
+  const Lane<D> at(a.rot, lane);
+  const int c0 = at.c0, c1 = at.c1, from0 = at.from0, from1 = at.from1;
+  const bool rot = at.rot;
+  const bool across = a.rot / 16 & 1;          // else both are the neighbour's chunk of the same place
   // turns per position of the angles this lane forms
   uint64_t turn[D / 64];
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) turn[i] = a.turns[lane + 32 * i];
   // The f32 error of a key element, as a part of |y| + |other of its pair|, in
-  // units of 2^-24: the norm's 21 (sum of squares 20 halved, its root 2, two
-  // products and the rest), the rotation's 7 (angle 1.6, sine and cosine 1 of
-  // themselves, mscale 1, the sum 2) times sqrt 2 for a pair seen after its
-  // rotation, and the quotient's 2.
-  const float slack = (a.k_gain ? (rot ? 42.f : 23.f) : rot ? 12.f : 0.f) * 0x1p-24f;
+  // units of 2^-24: the norm's 17 (20 of the sum of squares halved, its root 4, two
+  // products), the rotation's 8 (angle 1.6, sine and cosine 2, mscale 1 and its
+  // product 1, the sum 2) times sqrt 2 for a pair seen after its rotation, and the
+  // quotient's 2.
+  const float slack = (a.k_gain ? (rot ? 38.f : 20.f) : rot ? 14.f : 0.f) * 0x1p-24f;
 
   const int stride = gridDim.x * (kAppendThreads / 32) / WARPS;
   for (int row = id / WARPS; row < s.n_rows; row += stride) {
@@ -238,6 +468,7 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
       __syncwarp();
     };
     if (a.rot) angles();
+    uint32_t again = 0;                                    // passes over heads with a border
     for (int h = first; __any_sync(0xffffffffu, h < heads); h += kStep) {
       if (h != first) fetch(h);
       const bool is_q = h < Hq, is_v = h >= Hq + Hkv;
@@ -270,45 +501,32 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
       }
       if (!__any_sync(0xffffffffu, h >= Hq && h < heads)) continue;
       // ---- 4 bits
-      const float inv_unit = is_v ? p.v_inv_unit : p.k_inv_unit;
+      const float inv_unit = is_v ? p.v_inv_unit : p.k_inv_unit, unit = is_v ? p.v_unit : p.k_unit;
       const float eps = is_v ? 0.f : slack;
-      float d0[8], d1[8];                     // what each element can be off by
-      float hi[2], lo[2];                     // of the chunks' largest
-      {
-        uint32_t top[2] = {0, 0};
+      // the chunks' largest element (as bits: NaN is above all) and their largest pair,
+      // then their blocks'
+      uint32_t top[2] = {0, 0};
+      float wide[2] = {0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          // (beyond any code all the same, and still finite)
-          top[0] = max(top[0], __float_as_uint(fabsf(y0.v[j])));
-          top[1] = max(top[1], __float_as_uint(fabsf(y1.v[j])));
-          y0.v[j] = fminf(fmaxf(y0.v[j] * inv_unit, -0x1p100f), 0x1p100f);
-          y1.v[j] = fminf(fmaxf(y1.v[j] * inv_unit, -0x1p100f), 0x1p100f);
-        }
-        float m[2] = {0.f, 0.f}, n[2] = {0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float u0 = INTER ? y0.v[j ^ 1] : y1.v[j], u1 = INTER ? y1.v[j ^ 1] : y0.v[j];
-          d0[j] = eps * (fabsf(y0.v[j]) + fabsf(u0));
-          d1[j] = eps * (fabsf(y1.v[j]) + fabsf(u1));
-          m[0] = fmaxf(m[0], fabsf(y0.v[j]) + d0[j]);
-          m[1] = fmaxf(m[1], fabsf(y1.v[j]) + d1[j]);
-          n[0] = fmaxf(n[0], fabsf(y0.v[j]) - d0[j]);
-          n[1] = fmaxf(n[1], fabsf(y1.v[j]) - d1[j]);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (top[i] >= 0x7F800000u) m[i] = INFINITY;
-          const float mo = __shfl_sync(0xffffffffu, m[i], i ? from1 : from0);
-          const float no = __shfl_sync(0xffffffffu, n[i], i ? from1 : from0);
-          hi[i] = fmaxf(m[i], mo);
-          lo[i] = fmaxf(n[i], no);
-        }
-        if (across) {                          // (the block's other chunk may lie in another place)
-          const float mo0 = __shfl_sync(0xffffffffu, m[1], from0), no0 = __shfl_sync(0xffffffffu, n[1], from0);
-          const float mo1 = __shfl_sync(0xffffffffu, m[0], from1), no1 = __shfl_sync(0xffffffffu, n[0], from1);
-          if (second0) hi[0] = fmaxf(m[0], mo0), lo[0] = fmaxf(n[0], no0);
-          if (!second1) hi[1] = fmaxf(m[1], mo1), lo[1] = fmaxf(n[1], no1);
-        }
+      for (int j = 0; j < 8; ++j) {
+        top[0] = max(top[0], __float_as_uint(fabsf(y0.v[j])));
+        top[1] = max(top[1], __float_as_uint(fabsf(y1.v[j])));
+        if (!INTER) wide[0] = fmaxf(wide[0], fabsf(y0.v[j]) + fabsf(y1.v[j]));
+        else if (j & 1) wide[0] = fmaxf(wide[0], fabsf(y0.v[j]) + fabsf(y0.v[j ^ 1])),
+                        wide[1] = fmaxf(wide[1], fabsf(y1.v[j]) + fabsf(y1.v[j ^ 1]));
+      }
+      if (!INTER) wide[1] = wide[0];
+      const uint32_t t0 = top[0], t1 = top[1];
+      const float w0 = wide[0], w1 = wide[1];
+      top[0] = max(t0, __shfl_sync(0xffffffffu, t0, from0));
+      top[1] = max(t1, __shfl_sync(0xffffffffu, t1, from1));
+      wide[0] = fmaxf(w0, __shfl_sync(0xffffffffu, w0, from0));
+      wide[1] = fmaxf(w1, __shfl_sync(0xffffffffu, w1, from1));
+      if (across) {                            // (the block's other chunk may lie in another place)
+        const uint32_t o0 = __shfl_sync(0xffffffffu, t1, from0), o1 = __shfl_sync(0xffffffffu, t0, from1);
+        const float v0 = __shfl_sync(0xffffffffu, w1, from0), v1 = __shfl_sync(0xffffffffu, w0, from1);
+        if (at.second0) top[0] = max(t0, o0), wide[0] = fmaxf(w0, v0);
+        if (!at.second1) top[1] = max(t1, o1), wide[1] = fmaxf(w1, v1);
       }
       Codes c;
       c.scale = 0;
@@ -316,74 +534,48 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const Chunk& y = i ? y1 : y0;
-        const float* d = i ? d1 : d0;
-        const bool fine = hi[i] < INFINITY;
-        float q[8];
+        const bool fine = top[i] < 0x7F800000u;
+        const float big = __uint_as_float(top[i]);
         uint32_t sc;
         if (eps == 0.f) {
-          sc = e4m3_of2(odd_quotient<kExact16>(fminf(hi[i], 0x1p20f), 6.f, 1.f / 6.f), 0.f) & 0xFF;
+          sc = e4m3_of2(odd_quotient<kExact16>(big * inv_unit, 6.f, 1.f / 6.f), 0.f) & 0xFF;
         } else {
-          const uint32_t two = e4m3_of2(lo[i] * (1.f / 6.f) * (1.f - 0x1p-22f), hi[i] * (1.f / 6.f) * (1.f + 0x1p-22f));
+          const float off = eps * wide[i], six = inv_unit * (1.f / 6.f);
+          const uint32_t two = e4m3_of2((big - off) * six * (1.f - 0x1p-22f), (big + off) * six * (1.f + 0x1p-22f));
           sc = two & 0xFF;
           border |= fine && sc != two >> 8;
         }
-        const float sf = e4m3_to1(sc), r = fine && sf > 0.f ? __frcp_rn(sf) : 0.f;
+        const float sf = e4m3_to1(sc), r = sf > 0.f ? __frcp_rn(sf) * inv_unit : 0.f;
+        float q[8];
         if (eps == 0.f) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) q[j] = r > 0.f ? odd_quotient<kExact16>(y.v[j], sf, r) : fine ? y.v[j] * 0.f : 0.f;
+          for (int j = 0; j < 8; ++j) q[j] = odd_quotient<kExact16>(y.v[j], sf * unit, r);
           c.code[i] = e2m1_of8(q);
         } else {
           float t[8];
+          const float er = eps * r;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float e = d[j] * r;
-            q[j] = fine ? fmaf(y.v[j], r, -e) : 0.f;
-            t[j] = fine ? fmaf(y.v[j], r, e) : 0.f;
+            const float e = er * (fabsf(y.v[j]) + fabsf(INTER ? y.v[j ^ 1] : (i ? y0 : y1).v[j]));
+            q[j] = fmaf(y.v[j], r, -e);
+            t[j] = fmaf(y.v[j], r, e);
           }
           c.code[i] = e2m1_of8(q);
-          border |= c.code[i] != e2m1_of8(t);
+          border |= fine && c.code[i] != e2m1_of8(t);
         }
-        c.scale |= (fine ? sc : kScaleNaN) << (8 * i);
+        if (!fine) c.code[i] = 0, sc = kScaleNaN;
+        c.scale |= sc << (8 * i);
       }
-      border &= h >= Hq && h < heads;
-      if (__any_sync(0xffffffffu, border)) {
-        Again g;
-        const Chunk z0 = x0.get(), z1 = x1.get();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g.x[j] = h < heads ? z0.v[j] : 0.f, g.x[8 + j] = h < heads ? z1.v[j] : 0.f;
-        g.gain = h < heads ? gain : nullptr;
-        g.c0 = c0, g.c1 = c1, g.lanes = kLanes, g.rot = rot, g.inter = INTER;
-        g.from0 = from0, g.from1 = from1, g.second0 = second0, g.second1 = second1;
-        g.inv_unit = inv_unit;
-        const Codes b = code_again(g, p, pos, cs64);
-        if (eps != 0.f) c = b;
-      }
-      if (h < Hq || h >= heads || dst < 0) continue;
-      const int kv = h - Hq - (is_v ? Hkv : 0);
-      uint8_t* o = static_cast<uint8_t*>(is_v ? a.c.v : a.c.k) + dst + kv * a.c.head_stride;
-      *reinterpret_cast<uint32_t*>(o + c0 / 2) = c.code[0];
-      *reinterpret_cast<uint32_t*>(o + c1 / 2) = c.code[1];
-      uint8_t* so = static_cast<uint8_t*>(is_v ? p.sc.v : p.sc.k) + sdst + kv * p.sc.head_stride;
-      if (!(c0 & 8)) so[c0 / 16] = (uint8_t)c.scale;
-      if (!(c1 & 8)) so[c1 / 16] = (uint8_t)(c.scale >> 8);
-      Out* vo = static_cast<Out*>(is_v ? p.v_values : p.k_values);
-      if (vo) {
-        vo += row * (is_v ? p.v_values_stride : p.k_values_stride) + (long)kv * D;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float f = e4m3_to1(c.scale >> (8 * i)) * (is_v ? p.v_unit : p.k_unit);
-          uint32_t e[4];
-          e2m1_to8(c.code[i], e);
-          Chunk y;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 t = __half22float2(as_half2(e[j]));
-            y.v[2 * j] = t.x * f;
-            y.v[2 * j + 1] = t.y * f;
-          }
-          store8(vo + (i ? c1 : c0), y);
-        }
-      }
+      if (__any_sync(0xffffffffu, border && h >= Hq && h < heads)) again |= 1u << min((h - first) / kStep, 31);
+      if (h >= Hq && h < heads && dst >= 0) store_codes<Out, D>(p, c0, c1, c, row, h, dst, sdst);
+    }
+    // those with a border, when nothing else is held (bit 31: all from there on)
+    for (int i = 0; again; ++i) {
+      if (!(again >> min(i, 31) & 1)) continue;
+      if (i < 31) again &= ~(1u << i);
+      const int h = first + i * kStep;
+      if (!__any_sync(0xffffffffu, h < heads)) break;
+      code_again<In, Out, D, INTER>(p, row, h, dst, sdst, pos, cs64);
     }
   }
 }
