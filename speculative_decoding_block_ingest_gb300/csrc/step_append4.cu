@@ -52,6 +52,18 @@ __device__ __forceinline__ float odd_quotient(float a, float b, float r) {
   return __uint_as_float((__float_as_uint(q) - below) | 1u);
 }
 
+// And of 16-bit elements that are not beyond the largest code.
+__device__ __forceinline__ float exact_quotient(float a, float b, float r) {
+  const float q0 = a * r;
+  return copysignf(fmaf(fmaf(-q0, b, a), r, q0), a);   // (of a zero too)
+}
+// The larger, or NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // What the rounded blocks of a lane's two chunks come to.
 struct Codes {
   uint32_t code[2];   // eight codes each
@@ -192,6 +204,10 @@ __device__ __noinline__ void code_exactly(const Append4Args& p, long row, int h,
   if (mine && dst >= 0) store_codes<Out, D>(p, at.c0, at.c1, c, row, h, dst, sdst);
 }
 
+// Resident CTAs of an SM.  Many rows: three (four, and code_again out of line for
+// their registers: 253 us for 34912 rows of 32 and 16 heads, three 246).
+constexpr int append_ctas(int warps) { return warps == kManyWarps ? 3 : 2; }
+
 // Numbers of two floats (the second at most half a step of the first): about 2^-46 of
 // a sum's or product's terms is lost.
 struct Two {
@@ -270,13 +286,14 @@ __device__ __forceinline__ float odd_quotient(Two a, float b, float r, float off
 
 // A warp's key rows (head h of each lane's group) once more, in two floats.
 template <typename In, typename Out, int D, bool INTER>
-__device__ __noinline__ void code_again(const Append4Args& p, long row, int h, long dst, long sdst, uint64_t pos,
+__device__ __forceinline__ void code_again(const Append4Args& p, long row, int h, long dst, long sdst, uint64_t pos,
                                         double2* cs64) {
   const AppendArgs& a = p.a;
   const int lane = threadIdx.x & 31;
   const Lane<D> at(a.rot, lane);
   const bool mine = h >= a.n_heads && h < a.n_heads + a.c.n_kv_heads;
   float4* cs = reinterpret_cast<float4*>(cs64);
+  bool unsure = false;
   float x[16];
   {
     Raw<In> x0, x1;
@@ -295,6 +312,7 @@ __device__ __noinline__ void code_again(const Append4Args& p, long row, int h, l
     for (int o = Lane<D>::kLanes / 2; o; o >>= 1)
       ss = ss + Two{__shfl_xor_sync(0xffffffffu, ss.h, o), __shfl_xor_sync(0xffffffffu, ss.l, o)};
     const Two m = ss * (1.f / D) + two(p.eps);
+    unsure = !(m.h < INFINITY && m.h > 0.f);
     // 1 / sqrt m = r + r (1 - m r^2) / 2 to the square of the first one's error
     const float r0 = rsqrtf(m.h);
     const Two one = m * product(r0, r0);
@@ -345,7 +363,6 @@ __device__ __noinline__ void code_again(const Append4Args& p, long row, int h, l
   }
   Codes c;
   c.scale = 0;
-  bool unsure = false;
   const Two t0 = top[0], t1 = top[1];
   const float w0 = wide[0], w1 = wide[1];
   const uint32_t b0 = bits[0], b1 = bits[1];
@@ -376,10 +393,7 @@ __device__ __noinline__ void code_again(const Append4Args& p, long row, int h, l
   if (mine && dst >= 0) store_codes<Out, D>(p, at.c0, at.c1, c, row, h, dst, sdst);
 }
 
-// Resident CTAs of an SM (the same as in step_append.cu).
-constexpr int append_ctas(int warps) { return warps == kManyWarps ? 4 : 2; }
-
-template <typename In, typename Out, int D, int WARPS, bool INTER>
+template <typename In, typename Out, int D, int WARPS, bool INTER, bool QUERIES>
 __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
     step_append4_kernel(const __grid_constant__ Append4Args p) {
   constexpr int kLanes = D / 16;               // lanes of a head row
@@ -393,8 +407,8 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
   const StepView& s = a.s;
   const int lane = threadIdx.x & 31;
   const int id = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
-  const int first = id % WARPS * kGroups + lane / kLanes;   // this lane's first head
-  const int Hq = a.n_heads, Hkv = a.c.n_kv_heads, heads = Hq + 2 * Hkv;
+    const int Hq = a.n_heads, Hkv = a.c.n_kv_heads, heads = Hq + 2 * Hkv;
+  const int first = id % WARPS * kGroups + lane / kLanes + (QUERIES ? 0 : Hq);   // this lane's first head
   double2* cs64 = cs_all[threadIdx.x >> 5];
   float2* cs = reinterpret_cast<float2*>(cs64);
   const Lane<D> at(a.rot, lane);
@@ -406,18 +420,18 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) turn[i] = a.turns[lane + 32 * i];
   // The f32 error of a key element, as a part of |y| + |other of its pair|, in
-  // units of 2^-24: the norm's 17 (20 of the sum of squares halved, its root 4, two
-  // products), the rotation's 8 (angle 1.6, sine and cosine 2, mscale 1 and its
-  // product 1, the sum 2) times sqrt 2 for a pair seen after its rotation, and the
-  // quotient's 2.
-  const float slack = (a.k_gain ? (rot ? 38.f : 20.f) : rot ? 14.f : 0.f) * 0x1p-24f;
+  // units of 2^-24: the norm's 17 (20 of the sum of squares halved, its root 4, the
+  // products with the gain and with the quotient's factor), the rotation's 8 (angle 1.6,
+  // sine and cosine 2, mscale 1 and its product 1, the sum 2) times sqrt 2 for a pair seen
+  // after its rotation, and the quotient's 3.
+  const float slack = (a.k_gain ? (rot ? 39.f : 21.f) : rot ? 15.f : 0.f) * 0x1p-24f;
 
   const int stride = gridDim.x * (kAppendThreads / 32) / WARPS;
   for (int row = id / WARPS; row < s.n_rows; row += stride) {
     Raw<In> x0, x1;
     auto fetch = [&](int h) {
       if (h < heads) {
-        const In* src = h < Hq ? static_cast<const In*>(a.q) + row * a.q_stride + (long)h * D
+        const In* src = QUERIES && h < Hq ? static_cast<const In*>(a.q) + row * a.q_stride + (long)h * D
                         : h < Hq + Hkv ? static_cast<const In*>(a.k) + row * a.k_stride + (long)(h - Hq) * D
                                        : static_cast<const In*>(a.v) + row * a.v_stride + (long)(h - Hq - Hkv) * D;
         x0.load(src + c0);
@@ -470,104 +484,114 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
     if (a.rot) angles();
     uint32_t again = 0;                                    // passes over heads with a border
     for (int h = first; __any_sync(0xffffffffu, h < heads); h += kStep) {
-      if (h != first) fetch(h);
-      const bool is_q = h < Hq, is_v = h >= Hq + Hkv;
-      const float* gain = is_q ? a.q_gain : (is_v ? nullptr : a.k_gain);
+      const bool is_q = QUERIES && h < Hq, is_v = h >= Hq + Hkv;
+      const float* gain = h >= heads || is_v ? nullptr : is_q ? a.q_gain : a.k_gain;
       Chunk y0 = x0.get(), y1 = x1.get();
+      fetch(h + kStep);      // (on its way under this one's arithmetic)
+      float rn = 1.f;        // the norm's factor, which the rotation lets pass
       if (a.q_gain || a.k_gain) {
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss += y0.v[j] * y0.v[j] + y1.v[j] * y1.v[j];
 #pragma unroll
         for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (h < heads && gain) {
-          const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        if (gain) {
+          rn = rsqrtf(ss * (1.f / D) + a.eps);
           Raw<float> g;
           g.load(gain + c0);
           Chunk x = g.get();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y0.v[j] *= r * x.v[j];
+          for (int j = 0; j < 8; ++j) y0.v[j] *= x.v[j];
           g.load(gain + c1);
           x = g.get();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y1.v[j] *= r * x.v[j];
+          for (int j = 0; j < 8; ++j) y1.v[j] *= x.v[j];
         }
       }
       if (rot && !is_v) rotate<INTER>(y0, y1, w);
-      if (h < heads && is_q) {
+      if (QUERIES && is_q) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y0.v[j] *= rn, y1.v[j] *= rn;
         Out* o = static_cast<Out*>(a.q_out) + row * a.q_out_stride + (long)h * D;
         store8(o + c0, y0);
         store8(o + c1, y1);
       }
-      if (!__any_sync(0xffffffffu, h >= Hq && h < heads)) continue;
+      if (QUERIES && !__any_sync(0xffffffffu, h >= Hq && h < heads)) continue;
       // ---- 4 bits
-      const float inv_unit = is_v ? p.v_inv_unit : p.k_inv_unit, unit = is_v ? p.v_unit : p.k_unit;
-      const float eps = is_v ? 0.f : slack;
-      // the chunks' largest element (as bits: NaN is above all) and their largest pair,
-      // then their blocks'
-      uint32_t top[2] = {0, 0};
-      float wide[2] = {0.f, 0.f};
+      // the chunks' largest element (NaN is above all) and largest pair, then their blocks'
+      float t0 = 0.f, t1 = 0.f, w0 = 0.f, w1 = 0.f, both[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        top[0] = max(top[0], __float_as_uint(fabsf(y0.v[j])));
-        top[1] = max(top[1], __float_as_uint(fabsf(y1.v[j])));
-        if (!INTER) wide[0] = fmaxf(wide[0], fabsf(y0.v[j]) + fabsf(y1.v[j]));
-        else if (j & 1) wide[0] = fmaxf(wide[0], fabsf(y0.v[j]) + fabsf(y0.v[j ^ 1])),
-                        wide[1] = fmaxf(wide[1], fabsf(y1.v[j]) + fabsf(y1.v[j ^ 1]));
+        t0 = max_nan(t0, fabsf(y0.v[j]));
+        t1 = max_nan(t1, fabsf(y1.v[j]));
+        const int at = (j < 4 ? 0 : 1), k = 2 * (j & 3);
+        both[j] = INTER ? fabsf((at ? y1 : y0).v[k]) + fabsf((at ? y1 : y0).v[k + 1]) : fabsf(y0.v[j]) + fabsf(y1.v[j]);
+        if (!INTER || j < 4) w0 = fmaxf(w0, both[j]);
+        else w1 = fmaxf(w1, both[j]);
       }
-      if (!INTER) wide[1] = wide[0];
-      const uint32_t t0 = top[0], t1 = top[1];
-      const float w0 = wide[0], w1 = wide[1];
-      top[0] = max(t0, __shfl_sync(0xffffffffu, t0, from0));
-      top[1] = max(t1, __shfl_sync(0xffffffffu, t1, from1));
+      if (!INTER) w1 = w0;
+      float top[2], wide[2];
+      top[0] = max_nan(t0, __shfl_sync(0xffffffffu, t0, from0));
+      top[1] = max_nan(t1, __shfl_sync(0xffffffffu, t1, from1));
       wide[0] = fmaxf(w0, __shfl_sync(0xffffffffu, w0, from0));
       wide[1] = fmaxf(w1, __shfl_sync(0xffffffffu, w1, from1));
       if (across) {                            // (the block's other chunk may lie in another place)
-        const uint32_t o0 = __shfl_sync(0xffffffffu, t1, from0), o1 = __shfl_sync(0xffffffffu, t0, from1);
+        const float o0 = __shfl_sync(0xffffffffu, t1, from0), o1 = __shfl_sync(0xffffffffu, t0, from1);
         const float v0 = __shfl_sync(0xffffffffu, w1, from0), v1 = __shfl_sync(0xffffffffu, w0, from1);
-        if (at.second0) top[0] = max(t0, o0), wide[0] = fmaxf(w0, v0);
-        if (!at.second1) top[1] = max(t1, o1), wide[1] = fmaxf(w1, v1);
+        if (at.second0) top[0] = max_nan(t0, o0), wide[0] = fmaxf(w0, v0);
+        if (!at.second1) top[1] = max_nan(t1, o1), wide[1] = fmaxf(w1, v1);
       }
       Codes c;
       c.scale = 0;
       bool border = false;
+      if (is_v || slack == 0.f) {
+        const float inv_unit = is_v ? p.v_inv_unit : p.k_inv_unit, unit = is_v ? p.v_unit : p.k_unit;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const Chunk& y = i ? y1 : y0;
-        const bool fine = top[i] < 0x7F800000u;
-        const float big = __uint_as_float(top[i]);
-        uint32_t sc;
-        if (eps == 0.f) {
-          sc = e4m3_of2(odd_quotient<kExact16>(big * inv_unit, 6.f, 1.f / 6.f), 0.f) & 0xFF;
-        } else {
-          const float off = eps * wide[i], six = inv_unit * (1.f / 6.f);
-          const uint32_t two = e4m3_of2((big - off) * six * (1.f - 0x1p-22f), (big + off) * six * (1.f + 0x1p-22f));
-          sc = two & 0xFF;
-          border |= fine && sc != two >> 8;
+        for (int i = 0; i < 2; ++i) {
+          const Chunk& y = i ? y1 : y0;
+          const uint32_t sc = e4m3_of2(odd_quotient<kExact16>(top[i] * inv_unit, 6.f, 1.f / 6.f), 0.f) & 0xFF;
+          const float sf = e4m3_to1(sc), r = sf > 0.f ? __frcp_rn(sf) * inv_unit : 0.f, s = sf * unit;
+          float q[8];
+          if (top[i] * r < 64.f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              q[j] = kExact16 ? exact_quotient(y.v[j], s, r) : odd_quotient<false>(y.v[j], s, r);
+          } else {             // beyond the largest code (or not finite): as they come
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[j] = odd_quotient<kExact16>(y.v[j], s, r);
+          }
+          const bool fine = top[i] < INFINITY;
+          c.code[i] = fine ? e2m1_of8(q) : 0;
+          c.scale |= (fine ? sc : kScaleNaN) << (8 * i);
         }
-        const float sf = e4m3_to1(sc), r = sf > 0.f ? __frcp_rn(sf) * inv_unit : 0.f;
-        float q[8];
-        if (eps == 0.f) {
+      } else {
+        border = !(rn < INFINITY);             // (a sum of squares that is 0 or not finite is looked at again)
+        const float scaled = p.k_inv_unit * rn, six = scaled * (1.f / 6.f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) q[j] = odd_quotient<kExact16>(y.v[j], sf * unit, r);
-          c.code[i] = e2m1_of8(q);
-        } else {
-          float t[8];
-          const float er = eps * r;
+        for (int i = 0; i < 2; ++i) {
+          const Chunk& y = i ? y1 : y0;
+          const float off = slack * wide[i];
+          const uint32_t two = e4m3_of2((top[i] - off) * six * (1.f - 0x1p-22f), (top[i] + off) * six * (1.f + 0x1p-22f));
+          const uint32_t sc = two & 0xFF;
+          const float sf = e4m3_to1(sc), r = sf > 0.f ? __frcp_rn(sf) * scaled : 0.f, er = slack * r;
+          float q[8], t[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float e = er * (fabsf(y.v[j]) + fabsf(INTER ? y.v[j ^ 1] : (i ? y0 : y1).v[j]));
+            const float e = er * both[INTER ? 4 * i + j / 2 : j];
             q[j] = fmaf(y.v[j], r, -e);
             t[j] = fmaf(y.v[j], r, e);
           }
-          c.code[i] = e2m1_of8(q);
-          border |= fine && c.code[i] != e2m1_of8(t);
+          const bool fine = top[i] < INFINITY;
+          const uint32_t code = e2m1_of8(q);
+          border |= fine && (sc != two >> 8 || code != e2m1_of8(t));
+          c.code[i] = fine ? code : 0;
+          c.scale |= (fine ? sc : kScaleNaN) << (8 * i);
         }
-        if (!fine) c.code[i] = 0, sc = kScaleNaN;
-        c.scale |= sc << (8 * i);
+        border |= !(rn > 0.f);
       }
-      if (__any_sync(0xffffffffu, border && h >= Hq && h < heads)) again |= 1u << min((h - first) / kStep, 31);
-      if (h >= Hq && h < heads && dst >= 0) store_codes<Out, D>(p, c0, c1, c, row, h, dst, sdst);
+      const bool mine = h >= Hq && h < heads;
+      if (__any_sync(0xffffffffu, border && mine)) again |= 1u << min((h - first) / kStep, 31);
+      if (mine && dst >= 0) store_codes<Out, D>(p, c0, c1, c, row, h, dst, sdst);
     }
     // those with a border, when nothing else is held (bit 31: all from there on)
     for (int i = 0; again; ++i) {
@@ -589,10 +613,10 @@ cudaError_t launch(const Append4Args& p, int n_sm, cudaStream_t s) {
   const long ctas = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
   const long most = (long)append_ctas(few ? kFewWarps : kManyWarps) * n_sm;
   const dim3 grid((unsigned)(ctas < most ? ctas : most)), block(kAppendThreads);
-  auto* kernel = few ? (a.c.d == 128 ? step_append4_kernel<In, Out, 128, kFewWarps, INTER>
-                                     : step_append4_kernel<In, Out, 64, kFewWarps, INTER>)
-                     : (a.c.d == 128 ? step_append4_kernel<In, Out, 128, kManyWarps, INTER>
-                                     : step_append4_kernel<In, Out, 64, kManyWarps, INTER>);
+  auto* kernel = few ? (a.c.d == 128 ? step_append4_kernel<In, Out, 128, kFewWarps, INTER, true>
+                                     : step_append4_kernel<In, Out, 64, kFewWarps, INTER, true>)
+                     : (a.c.d == 128 ? step_append4_kernel<In, Out, 128, kManyWarps, INTER, false>
+                                     : step_append4_kernel<In, Out, 64, kManyWarps, INTER, false>);
   return launch_pdl(kernel, grid, block, 0, s, p);
 }
 
@@ -607,6 +631,14 @@ cudaError_t launch(const Append4Args& p, int in_dtype, int out_dtype, int n_sm, 
 }  // namespace
 
 cudaError_t launch_step_append4(const Append4Args& p, int in_dtype, int out_dtype, int n_sm, cudaStream_t s) {
+  // Many rows' queries go by themselves, as into a cache without kv heads: together
+  // their registers spill (34912 rows of 32 and 16 heads 293 us).
+  if ((long)p.a.s.n_rows * kFewWarps > 64L * n_sm && p.a.n_heads > 0) {
+    AppendArgs q = p.a;
+    q.c.n_kv_heads = 0;
+    const cudaError_t e = launch_step_append(q, in_dtype, out_dtype, n_sm, s);
+    if (e != cudaSuccess) return e;
+  }
   return p.a.interleaved ? launch<true>(p, in_dtype, out_dtype, n_sm, s)
                          : launch<false>(p, in_dtype, out_dtype, n_sm, s);
 }
