@@ -450,8 +450,12 @@ __global__ void __launch_bounds__(step_threads(PACKED), 1)
       if (!ok) sh.abort = 1;
     } else if (warp == 10) {
       // ------------------------------------------------------------------ fragments
-      plan_pieces<WideCosts>(Walk(a, PACKED && a.n_cta > a.n_wide ? kManyRows : kAnyRows), a.n_wide, sh.frag, sh.ffull,
-                             sh.fempty, kFrags, lane, [](const Frag&) {});
+      // (the kinds of rows at compile time: three prompt pieces 157 us, else 168)
+      auto plan = [&](auto w) {
+        plan_pieces(w, a.n_wide, sh.frag, sh.ffull, sh.fempty, kFrags, lane, [](const Frag&) {});
+      };
+      if (PACKED && a.n_cta > a.n_wide) plan(WalkT<WideCosts, kManyRows>(a));
+      else plan(Walk(a));
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(soft_regs(PACKED)));

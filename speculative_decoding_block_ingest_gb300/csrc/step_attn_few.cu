@@ -445,8 +445,12 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1)
   if (warp == kWarps) {
     // ------------------------------------------------------------------ plan and loads
     BlockLoader<D, NT> loader{a, maps, sh, smem, lane};
-    plan_pieces<FewCosts>(WalkT<FewCosts>(a, wide_ran ? kOnlyFewRows : kAnyRows), a.n_cta - a.n_wide, sh.frag, sh.ffull,
-                          sh.fempty, kFewFrags, lane, [&](const Frag& f) { loader.piece(f); });
+    auto plan = [&](auto w) {
+      plan_pieces(w, a.n_cta - a.n_wide, sh.frag, sh.ffull, sh.fempty, kFewFrags, lane,
+                  [&](const Frag& f) { loader.piece(f); });
+    };
+    if (wide_ran) plan(WalkT<FewCosts, kOnlyFewRows>(a));
+    else plan(WalkT<FewCosts, kAnyRows>(a));
     loader.drain();
   } else {
     int slot = 0, mine = warp;                           // this warp's next unit, from the next block on

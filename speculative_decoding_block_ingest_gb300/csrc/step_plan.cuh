@@ -54,10 +54,9 @@ struct Frag {
 // than a block, so the CTAs of an item are consecutive, and an item of one block
 // is whole (with the ends in front, 48 such items were 96 pieces).  On the device
 // a converged warp walks (it skips sequences without rows 32 at a time).
-template <class Costs>
+template <class Costs, RowKind KIND>
 struct WalkT {
   const StepAttnArgs& a;
-  const RowKind kind;
   int pair_tok;        // tokens of an item: two tiles
   int rows;            // rows of all sequences
   int pre_blocks, pre_tiles;
@@ -67,13 +66,13 @@ struct WalkT {
   int seg, seq, h, tile;
   int row0, T, len;    // the sequence's first row, rows and keys
 
-  __host__ __device__ explicit WalkT(const StepAttnArgs& args, RowKind k = kAnyRows) : a(args), kind(k) {
+  __host__ __device__ explicit WalkT(const StepAttnArgs& args) : a(args) {
     pair_tok = Costs::tokens(a);
     rows = a.s.start(a.s.n_seq);
     pre_blocks = (a.s.prefix_len + kKeys - 1) / kKeys;
     pre_tiles = pre_blocks && mine(rows) ? (rows + pair_tok - 1) / pair_tok : 0;
   }
-  __host__ __device__ bool mine(int T) const { return kind == kAnyRows || (T * (long)a.G <= a.few_rows) == (kind == kOnlyFewRows); }
+  __host__ __device__ bool mine(int T) const { return KIND == kAnyRows || (T <= a.few_rows / a.G) == (KIND == kOnlyFewRows); }
   // rows of sequence i (none where its items are another kernel's)
   __host__ __device__ int tokens(int i) const {
     const int T = max(a.s.start(i + 1) - a.s.start(i), 0);
@@ -216,7 +215,7 @@ struct WalkT {
   }
 };
 
-using Walk = WalkT<WideCosts>;
+using Walk = WalkT<WideCosts, kAnyRows>;
 
 // The units of all sequences' own keys on the host's worst case, and of the
 // prefix: an upper bound that fits 31 bits, or more work than is accepted.  (It
