@@ -574,7 +574,7 @@ typedef struct dflash_packed_append_args {
   dflash_append_args rows;   /* as of dflash_step_append                   */
   void *k_values, *v_values; /* device [n_rows, n_kv_heads, head_dim] in the
                                 cache's dtype, or NULL: what the rows stand
-                                for once rounded                           */
+                                for once rounded; not over k or v          */
   int64_t k_values_stride, v_values_stride;
 } dflash_packed_append_args;
 
@@ -585,7 +585,8 @@ typedef struct dflash_packed_append_args {
  * infinity gets s = NaN.  The codes are those of y in exact arithmetic (eps at
  * least 2^-80, angles to 2^-40 of a turn at positions below 2^24): they do not
  * depend on the order of sums, nor on the rows beside them.  Rows of k_values and
- * v_values whose keys or values are not written stay as they are.  One launch. */
+ * v_values whose keys or values are not written stay as they are.  One launch, or
+ * one more for the queries where rows are many. */
 int dflash_step_append_packed(const dflash_packed_cache *cache, const dflash_step *step,
                               const dflash_packed_append_args *args, void *stream);
 
@@ -598,7 +599,7 @@ int dflash_step_append_packed(const dflash_packed_cache *cache, const dflash_ste
  * last key has no effect.  A NaN scale leaves its block's 16 elements NaN in every row
  * that sees the key (of a key: the row's whole result) and, in the step's own rows,
  * only there; before the step's rows it may spread to the whole sequence (the
- * prefix's to the batch). */
+ * prefix's to the batch).  Up to three launches. */
 int dflash_step_attention_packed_workspace(const dflash_packed_cache *cache, int32_t n_rows, int32_t n_heads,
                                            size_t *bytes);
 int dflash_step_attention_packed(const dflash_packed_cache *cache, const dflash_step *step,

@@ -126,8 +126,8 @@ __device__ __forceinline__ void convert_row(uint8_t* tile, const uint8_t* codes,
 }
 
 // ---------------------------------------------------------------- the kernel
-// PACKED: the cache holds codes and scales, which four more warps turn into the
-// tiles that are loaded as they lie otherwise: K in the queries' type, V in f16.
+// PACKED: the cache holds codes and scales, which eight more warps turn into
+// the tiles that are loaded as they lie otherwise: K in the queries' type, V in f16.
 template <int D, bool BF16, bool PACKED>
 __global__ void __launch_bounds__(step_threads(PACKED), 1)
     step_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,

@@ -395,6 +395,8 @@ int dflash_step_append_packed(const dflash_packed_cache* cache, const dflash_ste
                              {p->v_values, p->v_values_stride}})
     if (ptr && !rows_ok(ptr, stride, (long)cache->n_kv_heads * cache->head_dim, 8))
       return invalid("rows must start on 16-byte boundaries and strides hold a row");
+    else if (ptr && (ptr == p->rows.k || ptr == p->rows.v))   // (keys may be read again behind the first codes)
+      return invalid("rounded rows go elsewhere than to k and v");
   Append4Args a{};
   if (int rc = append_args(a.a, &shape, step, &p->rows)) return rc;
   a.a.c = {cache->k, cache->v, cache->page_stride, cache->row_stride, cache->head_stride, cache->n_kv_heads,
@@ -477,6 +479,8 @@ int dflash_step_attention_packed(const dflash_packed_cache* cache, const dflash_
   // 364 us without it); else the other one for all (with a launch more that finds
   // nothing to do, 8 ragged verifications 16 -> 25 us).
   const long mean = ((long)step->n_rows * a.G + step->n_seq - 1) / step->n_seq;
+  // (Among others few rows are one item a head, which the other kernel's bound on units
+  // holds too; alone they may be more.)
   const bool some = a.n_cta > a.n_wide && mean <= kFewRows;
   a.few_rows = mean <= 8 && a.G <= 8 ? 8 : kFewRows;
   const bool alone = some && (step->prefix_len == 0 || (long)step->n_rows * a.G <= a.few_rows) && !a.by_cta &&

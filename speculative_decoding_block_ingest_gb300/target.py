@@ -185,8 +185,9 @@ class PagedCache4:
     half) and scales ``[n_pages, page_size, n_kv_heads, head_dim / 16]``
     (float8_e4m3fn, or uint8), each any strides whose last is 1; the scales of a
     head's rows of a page lie together (``[n_pages, n_kv_heads, page_size,
-    head_dim / 16]`` pools pass their transposes).  An element is e2m1 code x e4m3 scale of its 16 x ``unit`` (powers of two).  ``dtype``: of
-    queries, results and rounded rows."""
+    head_dim / 16]`` pools pass their transposes).  An element is e2m1 code x e4m3
+    scale of its 16 x ``unit`` (powers of two).  ``dtype``: of queries, results and
+    rounded rows."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, *,
                  dtype: torch.dtype = torch.bfloat16, k_unit: float = 1.0, v_unit: float = 1.0):
@@ -309,7 +310,8 @@ def append(cache: AnyCache, step: Step, q: Optional[torch.Tensor], k: torch.Tens
     ``[head_dim]``; positions int32 ``[n_rows]`` (default: prefix_len plus the
     row's own key index); q may be None.  ``q_out`` may be q itself.  A
     :class:`PagedCache4` takes the rows rounded to 4 bits; ``k_values`` and
-    ``v_values`` ``[n_rows, n_kv_heads, head_dim]`` then get what they stand for."""
+    ``v_values`` ``[n_rows, n_kv_heads, head_dim]`` (not k or v themselves) then get
+    what they stand for."""
     dev = cache.device
     if _elsewhere(dev, stream):
         with _on(dev, stream):

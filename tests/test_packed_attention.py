@@ -149,6 +149,13 @@ def test_long(T, case):
     expect(case, attend_case(T, case, seed=40))
 
 
+def test_many_short_sequences_and_a_long_one(T):
+    # more rows than the merge goes over one by one, the items of both kernels cut by the CTAs' shares
+    rows, kv = [3] * 400 + [40], [3 + 7 * i % 61 for i in range(399)] + [5000, 2500]
+    case = (rows, kv, 32, 8, 64, 16, BF, True, 0, False)
+    expect(case, attend_case(T, case, seed=77))
+
+
 def test_units_scale_and_strided_rows(T):
     """Large scores, a scale of the caller's, units of both sides, queries and results inside wider rows."""
     case = ([20, 1, 3], [900, 77, 400], 6, 2, 128, 64, BF, True, 300, True)

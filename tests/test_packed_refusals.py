@@ -65,7 +65,7 @@ def test_step_refused(lib, kw, code):  # noqa: F811
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=dflash.F16), UNS), (dict(n_heads=-1), INV), (dict(rot_dim=8), INV), (dict(rot_dim=144), INV),
     (dict(inv_freq=None), INV), (dict(mscale=float("nan")), INV), (dict(k_gain=P, eps=0.0), INV), (dict(k=None), INV),
-    (dict(q_out=None), INV), (dict(k_stride=255), INV), (dict(k_values=P + 8), INV), (dict(k_values_stride=128), INV),
+    (dict(q_out=None), INV), (dict(k_stride=255), INV), (dict(k_values=P), INV), (dict(v_values=P), INV), (dict(k_values=P + 8), INV), (dict(k_values_stride=128), INV),
     (dict(v_values_stride=260), INV)])
 def test_append_refused(lib, kw, code):  # noqa: F811
     assert lib.dflash_step_append_packed(ref(packed()), ref(step()), ref(packed_append(**kw)), None) == code
