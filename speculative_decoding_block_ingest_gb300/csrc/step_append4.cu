@@ -52,11 +52,19 @@ __device__ __forceinline__ float odd_quotient(float a, float b, float r) {
   return __uint_as_float((__float_as_uint(q) - below) | 1u);
 }
 
-// And of 16-bit elements that are not beyond the largest code.
-__device__ __forceinline__ float exact_quotient(float a, float b, float r) {
-  const float q0 = a * r;
-  return copysignf(fmaf(fmaf(-q0, b, a), r, q0), a);   // (of a zero too)
-}
+// The reciprocal of a scale, rounded down, and what that leaves: with both, fmaf(a, h, a l)
+// of a 16-bit a is a tie where a / s is one (49 products of a scale's bits with a tie's,
+// each checked: one float alone misses 11), and keeps a zero's sign.
+struct Reciprocal {
+  float h, l;
+  __device__ __forceinline__ Reciprocal(float s, float inv_unit) : h(0.f), l(0.f) {
+    if (s > 0.f) {
+      const float r = __frcp_rd(s);
+      h = r * inv_unit;
+      l = fmaf(-r, s, 1.f) * h;
+    }
+  }
+};
 // The larger, or NaN where one is.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float m;
@@ -135,7 +143,7 @@ __device__ __forceinline__ double largest8(const double* y) {
 
 // A warp's key rows (head h of each lane's group) in 64 bits.
 template <typename In, typename Out, int D, bool INTER>
-__device__ __noinline__ void code_exactly(const Append4Args& p, long row, int h, long dst, long sdst, uint64_t pos,
+__device__ __forceinline__ void code_exactly(const Append4Args& p, long row, int h, long dst, long sdst, uint64_t pos,
                                         double2* cs) {
   const AppendArgs& a = p.a;
   const int lane = threadIdx.x & 31;
@@ -400,6 +408,7 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
   constexpr int kGroups = 32 / kLanes;         // head rows of a warp at once
   constexpr int kStep = WARPS * kGroups;       // heads between a lane's
   constexpr bool kExact16 = sizeof(In) == 2;
+  constexpr int kCtaRows = kAppendThreads / 32 / WARPS;   // rows of a CTA at a time
   __shared__ __align__(16) double2 cs_all[kAppendThreads / 32][D / 2];   // in f32, and in 64 bits where that is wanted
   pdl_wait();
   pdl_launch_dependents();
@@ -426,8 +435,26 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
   // after its rotation, and the quotient's 3.
   const float slack = (a.k_gain ? (rot ? 39.f : 21.f) : rot ? 15.f : 0.f) * 0x1p-24f;
 
+  // A CTA's rows: each warp takes the next one where a row is a warp's, because one that
+  // is computed again takes twice as long.
+  __shared__ int taken;
+  if (WARPS == 1) {
+    if (threadIdx.x == 0) taken = kCtaRows;
+    __syncthreads();
+  }
   const int stride = gridDim.x * (kAppendThreads / 32) / WARPS;
-  for (int row = id / WARPS; row < s.n_rows; row += stride) {
+  int row = id / WARPS;
+  auto another = [&]() {
+    if (WARPS > 1) {
+      row += stride;
+      return;
+    }
+    int k = 0;
+    if (lane == 0) k = atomicAdd(&taken, 1);
+    k = __shfl_sync(0xffffffffu, k, 0);
+    row = k / kCtaRows * stride + blockIdx.x * kCtaRows + k % kCtaRows;
+  };
+  for (; row < s.n_rows; another()) {
     Raw<In> x0, x1;
     auto fetch = [&](int h) {
       if (h < heads) {
@@ -489,7 +516,8 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
       Chunk y0 = x0.get(), y1 = x1.get();
       fetch(h + kStep);      // (on its way under this one's arithmetic)
       float rn = 1.f;        // the norm's factor, which the rotation lets pass
-      if (a.q_gain || a.k_gain) {
+      const bool only_v = __all_sync(0xffffffffu, is_v);
+      if (!only_v && (a.q_gain || a.k_gain)) {
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss += y0.v[j] * y0.v[j] + y1.v[j] * y1.v[j];
@@ -519,27 +547,34 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
       if (QUERIES && !__any_sync(0xffffffffu, h >= Hq && h < heads)) continue;
       // ---- 4 bits
       // the chunks' largest element (NaN is above all) and largest pair, then their blocks'
-      float t0 = 0.f, t1 = 0.f, w0 = 0.f, w1 = 0.f, both[8];
+      float t0 = 0.f, t1 = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         t0 = max_nan(t0, fabsf(y0.v[j]));
         t1 = max_nan(t1, fabsf(y1.v[j]));
-        const int at = (j < 4 ? 0 : 1), k = 2 * (j & 3);
-        both[j] = INTER ? fabsf((at ? y1 : y0).v[k]) + fabsf((at ? y1 : y0).v[k + 1]) : fabsf(y0.v[j]) + fabsf(y1.v[j]);
-        if (!INTER || j < 4) w0 = fmaxf(w0, both[j]);
-        else w1 = fmaxf(w1, both[j]);
       }
-      if (!INTER) w1 = w0;
-      float top[2], wide[2];
-      top[0] = max_nan(t0, __shfl_sync(0xffffffffu, t0, from0));
-      top[1] = max_nan(t1, __shfl_sync(0xffffffffu, t1, from1));
-      wide[0] = fmaxf(w0, __shfl_sync(0xffffffffu, w0, from0));
-      wide[1] = fmaxf(w1, __shfl_sync(0xffffffffu, w1, from1));
-      if (across) {                            // (the block's other chunk may lie in another place)
-        const float o0 = __shfl_sync(0xffffffffu, t1, from0), o1 = __shfl_sync(0xffffffffu, t0, from1);
-        const float v0 = __shfl_sync(0xffffffffu, w1, from0), v1 = __shfl_sync(0xffffffffu, w0, from1);
-        if (at.second0) top[0] = max_nan(t0, o0), wide[0] = fmaxf(w0, v0);
-        if (!at.second1) top[1] = max_nan(t1, o1), wide[1] = fmaxf(w1, v1);
+      // a lane's two values to its blocks' (whose other chunk may lie in another place)
+      auto of_blocks = [&](float x0, float x1, auto larger, float* to) {
+        to[0] = larger(x0, __shfl_sync(0xffffffffu, x0, from0));
+        to[1] = larger(x1, __shfl_sync(0xffffffffu, x1, from1));
+        if (across) {
+          const float o0 = __shfl_sync(0xffffffffu, x1, from0), o1 = __shfl_sync(0xffffffffu, x0, from1);
+          if (at.second0) to[0] = larger(x0, o0);
+          if (!at.second1) to[1] = larger(x1, o1);
+        }
+      };
+      float top[2], wide[2] = {0.f, 0.f}, both[8];
+      of_blocks(t0, t1, [](float x, float y) { return max_nan(x, y); }, top);
+      if (!only_v && (a.k_gain || a.rot)) {
+        float w0 = 0.f, w1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int at = (j < 4 ? 0 : 1), k = 2 * (j & 3);
+          both[j] = INTER ? fabsf((at ? y1 : y0).v[k]) + fabsf((at ? y1 : y0).v[k + 1]) : fabsf(y0.v[j]) + fabsf(y1.v[j]);
+          if (!INTER || j < 4) w0 = fmaxf(w0, both[j]);
+          else w1 = fmaxf(w1, both[j]);
+        }
+        of_blocks(w0, INTER ? w1 : w0, [](float x, float y) { return fmaxf(x, y); }, wide);
       }
       Codes c;
       c.scale = 0;
@@ -550,16 +585,12 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
         for (int i = 0; i < 2; ++i) {
           const Chunk& y = i ? y1 : y0;
           const uint32_t sc = e4m3_of2(odd_quotient<kExact16>(top[i] * inv_unit, 6.f, 1.f / 6.f), 0.f) & 0xFF;
-          const float sf = e4m3_to1(sc), r = sf > 0.f ? __frcp_rn(sf) * inv_unit : 0.f, s = sf * unit;
+          const float sf = e4m3_to1(sc);
+          const Reciprocal r(sf, inv_unit);
           float q[8];
-          if (top[i] * r < 64.f) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              q[j] = kExact16 ? exact_quotient(y.v[j], s, r) : odd_quotient<false>(y.v[j], s, r);
-          } else {             // beyond the largest code (or not finite): as they come
-#pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = odd_quotient<kExact16>(y.v[j], s, r);
-          }
+          for (int j = 0; j < 8; ++j)
+            q[j] = kExact16 ? fmaf(y.v[j], r.h, y.v[j] * r.l) : odd_quotient<false>(y.v[j], sf * unit, r.h);
           const bool fine = top[i] < INFINITY;
           c.code[i] = fine ? e2m1_of8(q) : 0;
           c.scale |= (fine ? sc : kScaleNaN) << (8 * i);
