@@ -585,8 +585,7 @@ typedef struct dflash_packed_append_args {
  * infinity gets s = NaN.  The codes are those of y in exact arithmetic (eps at
  * least 2^-80, angles to 2^-40 of a turn at positions below 2^24): they do not
  * depend on the order of sums, nor on the rows beside them.  Rows of k_values and
- * v_values whose keys or values are not written stay as they are.  One launch, or
- * one more for the queries where rows are many. */
+ * v_values whose keys or values are not written stay as they are.  One launch. */
 int dflash_step_append_packed(const dflash_packed_cache *cache, const dflash_step *step,
                               const dflash_packed_append_args *args, void *stream);
 

@@ -15,8 +15,10 @@
 // computed again in two floats, and if that is not enough (2^-38 of a pair) in 64
 // bits.  64 bits at once took 18 us for one such row.
 //
-// Bytes bound it as in step_append.cu, whose division of rows among warps and
-// lanes it shares.
+// 34912 rows of 32 query and 16 other heads take 195 us (4.1 TB/s; instructions, 58% of
+// the issue slots of 16 warps an SM); step_append.cu, whose division of rows among
+// warps and lanes it shares, is bound by the bytes.  The later computations are inline:
+// a call among them cost every row 40 us of the 250 it took then.
 #include "../../include/dflash.h"
 #include "fp4.cuh"
 #include "kernels.cuh"
@@ -212,9 +214,9 @@ __device__ __forceinline__ void code_exactly(const Append4Args& p, long row, int
   if (mine && dst >= 0) store_codes<Out, D>(p, at.c0, at.c1, c, row, h, dst, sdst);
 }
 
-// Resident CTAs of an SM.  Many rows: three (four, and code_again out of line for
-// their registers: 253 us for 34912 rows of 32 and 16 heads, three 246).
-constexpr int append_ctas(int warps) { return warps == kManyWarps ? 3 : 2; }
+// Resident CTAs of an SM (34912 rows of 32 and 16 heads: 195 us; three, whose registers
+// spill, 293).
+constexpr int kAppendCtas = 2;
 
 // Numbers of two floats (the second at most half a step of the first): about 2^-46 of
 // a sum's or product's terms is lost.
@@ -401,8 +403,8 @@ __device__ __forceinline__ void code_again(const Append4Args& p, long row, int h
   if (mine && dst >= 0) store_codes<Out, D>(p, at.c0, at.c1, c, row, h, dst, sdst);
 }
 
-template <typename In, typename Out, int D, int WARPS, bool INTER, bool QUERIES>
-__global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
+template <typename In, typename Out, int D, int WARPS, bool INTER>
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
     step_append4_kernel(const __grid_constant__ Append4Args p) {
   constexpr int kLanes = D / 16;               // lanes of a head row
   constexpr int kGroups = 32 / kLanes;         // head rows of a warp at once
@@ -416,8 +418,8 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
   const StepView& s = a.s;
   const int lane = threadIdx.x & 31;
   const int id = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
-    const int Hq = a.n_heads, Hkv = a.c.n_kv_heads, heads = Hq + 2 * Hkv;
-  const int first = id % WARPS * kGroups + lane / kLanes + (QUERIES ? 0 : Hq);   // this lane's first head
+  const int Hq = a.n_heads, Hkv = a.c.n_kv_heads, heads = Hq + 2 * Hkv;
+  const int first = id % WARPS * kGroups + lane / kLanes;   // this lane's first head
   double2* cs64 = cs_all[threadIdx.x >> 5];
   float2* cs = reinterpret_cast<float2*>(cs64);
   const Lane<D> at(a.rot, lane);
@@ -435,37 +437,33 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
   // after its rotation, and the quotient's 3.
   const float slack = (a.k_gain ? (rot ? 39.f : 21.f) : rot ? 15.f : 0.f) * 0x1p-24f;
 
-  // A CTA's rows: each warp takes the next one where a row is a warp's, because one that
-  // is computed again takes twice as long.
+  // A CTA's rows: each warp takes the next one where a row is a warp's, because some are
+  // computed again.
   __shared__ int taken;
   if (WARPS == 1) {
     if (threadIdx.x == 0) taken = kCtaRows;
     __syncthreads();
   }
   const int stride = gridDim.x * (kAppendThreads / 32) / WARPS;
-  int row = id / WARPS;
-  auto another = [&]() {
-    if (WARPS > 1) {
-      row += stride;
-      return;
-    }
+  auto behind = [&](int row) -> int {
+    if (WARPS > 1) return row + stride;
     int k = 0;
     if (lane == 0) k = atomicAdd(&taken, 1);
     k = __shfl_sync(0xffffffffu, k, 0);
-    row = k / kCtaRows * stride + blockIdx.x * kCtaRows + k % kCtaRows;
+    return k / kCtaRows * stride + (int)blockIdx.x * kCtaRows + k % kCtaRows;
   };
-  for (; row < s.n_rows; another()) {
-    Raw<In> x0, x1;
-    auto fetch = [&](int h) {
-      if (h < heads) {
-        const In* src = QUERIES && h < Hq ? static_cast<const In*>(a.q) + row * a.q_stride + (long)h * D
-                        : h < Hq + Hkv ? static_cast<const In*>(a.k) + row * a.k_stride + (long)(h - Hq) * D
-                                       : static_cast<const In*>(a.v) + row * a.v_stride + (long)(h - Hq - Hkv) * D;
-        x0.load(src + c0);
-        x1.load(src + c1);
-      }
-    };
-    fetch(first);
+  Raw<In> x0, x1;   // the next head's chunks
+  auto fetch = [&](int row, int h) {
+    if (h < heads) {
+      const In* src = h < Hq ? static_cast<const In*>(a.q) + row * a.q_stride + (long)h * D
+                      : h < Hq + Hkv ? static_cast<const In*>(a.k) + row * a.k_stride + (long)(h - Hq) * D
+                                     : static_cast<const In*>(a.v) + row * a.v_stride + (long)(h - Hq - Hkv) * D;
+      x0.load(src + c0);
+      x1.load(src + c1);
+    }
+  };
+  for (int row = id / WARPS; row < s.n_rows; row = behind(row)) {
+    fetch(row, first);
     // the row's sequence: as many end at or before the row as lie below it
     // (each lane looks at the end of one 32nd of what is left)
     int seq = 0;
@@ -511,10 +509,10 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
     if (a.rot) angles();
     uint32_t again = 0;                                    // passes over heads with a border
     for (int h = first; __any_sync(0xffffffffu, h < heads); h += kStep) {
-      const bool is_q = QUERIES && h < Hq, is_v = h >= Hq + Hkv;
+      const bool is_q = h < Hq, is_v = h >= Hq + Hkv;
       const float* gain = h >= heads || is_v ? nullptr : is_q ? a.q_gain : a.k_gain;
       Chunk y0 = x0.get(), y1 = x1.get();
-      fetch(h + kStep);      // (on its way under this one's arithmetic)
+      fetch(row, h + kStep);   // (on its way under this one's arithmetic)
       float rn = 1.f;        // the norm's factor, which the rotation lets pass
       const bool only_v = __all_sync(0xffffffffu, is_v);
       if (!only_v && (a.q_gain || a.k_gain)) {
@@ -537,14 +535,14 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(WARPS))
         }
       }
       if (rot && !is_v) rotate<INTER>(y0, y1, w);
-      if (QUERIES && is_q) {
+      if (is_q) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) y0.v[j] *= rn, y1.v[j] *= rn;
         Out* o = static_cast<Out*>(a.q_out) + row * a.q_out_stride + (long)h * D;
         store8(o + c0, y0);
         store8(o + c1, y1);
       }
-      if (QUERIES && !__any_sync(0xffffffffu, h >= Hq && h < heads)) continue;
+      if (!__any_sync(0xffffffffu, h >= Hq && h < heads)) continue;
       // ---- 4 bits
       // the chunks' largest element (NaN is above all) and largest pair, then their blocks'
       float t0 = 0.f, t1 = 0.f;
@@ -642,12 +640,12 @@ cudaError_t launch(const Append4Args& p, int n_sm, cudaStream_t s) {
   const bool few = (long)a.s.n_rows * kFewWarps <= 64L * n_sm;
   const long warps = (long)a.s.n_rows * (few ? kFewWarps : kManyWarps);
   const long ctas = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
-  const long most = (long)append_ctas(few ? kFewWarps : kManyWarps) * n_sm;
+  const long most = (long)kAppendCtas * n_sm;
   const dim3 grid((unsigned)(ctas < most ? ctas : most)), block(kAppendThreads);
-  auto* kernel = few ? (a.c.d == 128 ? step_append4_kernel<In, Out, 128, kFewWarps, INTER, true>
-                                     : step_append4_kernel<In, Out, 64, kFewWarps, INTER, true>)
-                     : (a.c.d == 128 ? step_append4_kernel<In, Out, 128, kManyWarps, INTER, false>
-                                     : step_append4_kernel<In, Out, 64, kManyWarps, INTER, false>);
+  auto* kernel = few ? (a.c.d == 128 ? step_append4_kernel<In, Out, 128, kFewWarps, INTER>
+                                     : step_append4_kernel<In, Out, 64, kFewWarps, INTER>)
+                     : (a.c.d == 128 ? step_append4_kernel<In, Out, 128, kManyWarps, INTER>
+                                     : step_append4_kernel<In, Out, 64, kManyWarps, INTER>);
   return launch_pdl(kernel, grid, block, 0, s, p);
 }
 
@@ -662,14 +660,6 @@ cudaError_t launch(const Append4Args& p, int in_dtype, int out_dtype, int n_sm, 
 }  // namespace
 
 cudaError_t launch_step_append4(const Append4Args& p, int in_dtype, int out_dtype, int n_sm, cudaStream_t s) {
-  // Many rows' queries go by themselves, as into a cache without kv heads: together
-  // their registers spill (34912 rows of 32 and 16 heads 293 us).
-  if ((long)p.a.s.n_rows * kFewWarps > 64L * n_sm && p.a.n_heads > 0) {
-    AppendArgs q = p.a;
-    q.c.n_kv_heads = 0;
-    const cudaError_t e = launch_step_append(q, in_dtype, out_dtype, n_sm, s);
-    if (e != cudaSuccess) return e;
-  }
   return p.a.interleaved ? launch<true>(p, in_dtype, out_dtype, n_sm, s)
                          : launch<false>(p, in_dtype, out_dtype, n_sm, s);
 }
