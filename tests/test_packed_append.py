@@ -52,6 +52,10 @@ CASES = [
     ([7, 2], [7, 30], 4, 2, 128, 112, 16, F4, BF, False, False, False, True, 3, (1.0, 1.0)),
     ([1300, 1], [1300, 2000], 8, 2, 128, 128, 64, BF, BF, True, False, False, True, 0, (1.0, 1.0)),   # a warp a row
     ([900, 800], [900, 900], 4, 4, 64, 64, 16, F4, HF, False, True, True, False, 9, (2.0, 0.5)),
+    # many rows, queries, keys and values in one pass of a warp
+    ([1300, 3], [1300, 9], 1, 1, 128, 128, 16, HF, HF, True, True, False, True, 0, (1.0, 1.0)),
+    ([3, 1500], [40, 1500], 3, 3, 64, 32, 32, F4, BF, False, False, True, False, 2, (0.5, 1.0)),
+    ([700] * 3, [700, 900, 701], 2, 5, 64, 16, 64, BF, BF, True, False, False, True, 1, (1.0, 2.0 ** 20)),
 ]
 
 
