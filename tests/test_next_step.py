@@ -77,6 +77,9 @@ CASES = [
     (256, 32, 300, 17, 300, 17, 4352, True, 0.0),
     (257, 16, 90, 3, 5, 40, 9000, True, 0.2),          # pages run out
     (1000, 128, 500, 16, 900, 16, 7000, True, 0.1),    # room for rows runs out
+    (1024, 16, 300, 9, 4000, 40, 9000, True, 0.1),     # sizes at which the CTAs change
+    (1025, 32, 300, 9, 900, 40, 30000, True, 0.1),
+    (2049, 16, 90, 5, 6000, 20, 50000, True, 0.2),
     (4096, 16, 60, 2, 3000, 1, 4096, False, 0.05),
     (4096, 16, 100, 17, 500, 90, 300000, True, 0.4),
     (3, 16, 30000, 0, 3000, 9000, 30000, False, 0.3),
