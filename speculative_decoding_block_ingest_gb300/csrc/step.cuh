@@ -155,7 +155,8 @@ struct StepAttnArgs {
   const void* q;       // (step_attn_few.cu; the other kernel loads boxes)
   long q_stride;
 };
-// A CTA's partial row among all CTAs'.
+// Partial rows of a CTA, and one of them among all CTAs'.
+__host__ __device__ inline int cta_rows(const StepAttnArgs& a, int cta) { return cta < a.n_wide ? 256 : 16; }
 __host__ __device__ inline long cta_row(const StepAttnArgs& a, int cta, int row) {
   return cta < a.n_wide ? cta * 256L + row : a.n_wide * 256L + (cta - a.n_wide) * 16L + row;
 }

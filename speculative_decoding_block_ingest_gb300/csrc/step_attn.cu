@@ -771,7 +771,8 @@ __device__ __forceinline__ void merge_row(const StepAttnArgs& a, bool live, long
     const float* src = nullptr;
     if (i < total) {
       const int cta = (seg ? own.first : pre.first) + k;
-      const long at = cta_row(a, cta, seg ? own.trow : pre.trow);
+      // (where row starts decrease, what says so was never written: any CTA, any row)
+      const long at = cta_row(a, cta, min(seg ? own.trow : pre.trow, cta_rows(a, cta) - 1));
       ml = k == 0 ? (seg ? own.ml : pre.ml) : a.cta_ml[at];
       src = k == 0 ? (seg ? a.seg_o[1] : a.seg_o[0]) + item * D : a.cta_o + at * D;
       bad |= a.status[cta < a.n_wide ? cta : cta - a.n_wide] != 0;
