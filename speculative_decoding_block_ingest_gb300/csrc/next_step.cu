@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kMostThreads) next_step_kernel(const __grid_co
     run = run + Sums{max(-now, 0), max(now, 0), want[k]};
   }
   const int n_give = (int)all.give, n_take = (int)all.take, n_rows = (int)all.rows;
+  const long long top = (long long)n_free + n_give;   // of the stack, once all are given (may pass 31 bits)
   if (tid == 0) {
     row0[n] = n_rows;
     take0[n] = n_take;
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kMostThreads) next_step_kernel(const __grid_co
     const int col = pages(kept[j] + row0[j + 1] - row0[j]) + x - give0[j];
     return a.block_table[j * a.table_stride + col];
   };
-  auto taken = [&](int x) { return x < n_give ? given(x) : a.free[n_free + n_give - 1 - x]; };
+  auto taken = [&](int x) { return x < n_give ? given(x) : a.free[top - 1 - x]; };
   const int at = blockIdx.x * threads + tid, stride = gridDim.x * threads;
   for (int r = at; r < n_rows; r += stride) {
     const int i = holder(row0, n, r), own = kept[i] + r - row0[i], col = own >> shift;
@@ -158,12 +159,12 @@ __global__ void __launch_bounds__(kMostThreads) next_step_kernel(const __grid_co
     if (a.positions) a.positions[r] = a.prefix_len + own;
     if (a.sequences) a.sequences[r] = i;
   }
-  for (int x = at; x < n_take; x += stride) {
+  for (int x = at; x < n_take; x += stride) {           // (a row takes a page at most: far from 31 bits)
     const int i = holder(take0, n, x);
     a.block_table[i * a.table_stride + have[i] + x - take0[i]] = taken(x);
   }
-  for (int x = at; x < n_give; x += stride)
-    if (n_free + n_give - 1 - x < a.n_pages) a.free[n_free + n_give - 1 - x] = given(x);
+  for (long long x = at; x < n_give; x += stride)
+    if (top - 1 - x < a.n_pages) a.free[top - 1 - x] = given((int)x);
 
   // nobody reads the old lengths any more
   if (gridDim.x > 1) {
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kMostThreads) next_step_kernel(const __grid_co
   }
   if (tid == 0) {
     a.row_start_out[n] = n_rows;
-    *a.n_free_out = min(n_free + n_give - n_take, a.n_pages);
+    *a.n_free_out = (int)min(top - n_take, (long long)a.n_pages);
   }
 }
 
