@@ -26,6 +26,8 @@
 // and loads their blocks, ahead into the next ones.  (Smaller loads for a warp each are
 // too many: 64 decoding sequences took 231 us with TMA boxes of 16 keys, 247 with 32,
 // 220 with cp.async; 185 with 11 warps for 8 rows too.)
+#include <float.h>
+
 #include <atomic>
 
 #include "../../include/dflash.h"
@@ -208,7 +210,9 @@ struct Rows {
       for (int j = 0; j < kSteps; ++j) q[nt][j][0] = w[2 * j], q[nt][j][1] = w[2 * j + 1];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        sc[nt][c] = a.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * t + c) * 4);
+        // (a normal float: times 0 a masked score, -inf, would be NaN, and a score of 0 times
+        // infinity.  Scores that the lower bound changes are less than 2^-92.)
+        sc[nt][c] = fminf(fmaxf(a.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * t + c) * 4), FLT_MIN), FLT_MAX);
         const int at = (8 * nt + 2 * t + c) / a.G;
         lim[nt][c] = at < f.ntok && f.seg == 1 && a.causal ? min(max(f.lim0 + at, 0), f.keys) : f.keys;
         nm[nt][c] = kNoMax;

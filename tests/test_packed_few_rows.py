@@ -1,0 +1,72 @@
+"""Attention over a 4-bit cache on the GPU by the kernel for few query rows:
+scales, units and queries that its own conversions see, against 64-bit forms.
+
+Every step here has at most 8 query rows of a kv head and sequence on average
+(one tile of rows) or at most 16 (two)."""
+import numpy as np
+import pytest
+import torch
+
+import _packed_ref as P
+import _target_ref as R
+from test_packed_attention import BF, DEV, HF, T, close, f64, i32, pools  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+# rows, kv, hq, hkv, d, page, causal, prefix: key counts that are no multiple of 32
+ONE = ([1, 3, 2, 1], [300, 77, 400, 33], 4, 2, 128, 64, True, 0)
+ONE_PREFIX = ([1, 3, 2, 1], [300, 77, 400, 33], 3, 1, 64, 16, True, 301)
+TWO = ([3, 4, 1, 2], [301, 70, 45, 1], 10, 2, 128, 16, True, 0)
+TWO_PREFIX = ([1, 1], [170, 90], 16, 1, 64, 32, True, 45)
+STEPS = pytest.mark.parametrize("case", [ONE, ONE_PREFIX, TWO, TWO_PREFIX], ids=["8", "8-prefix", "16", "16-prefix"])
+
+
+def few(case, dt, seed, mem=None):
+    rows, kv, hq, hkv, d, page, causal, prefix = case
+    assert sum(rows) * (hq // hkv) <= 16 * len(rows)
+    starts, kv, table, pre, n_pages = R.make_step(rows, kv, page, prefix=prefix, seed=seed)
+    mem = pools(n_pages, page, hkv, d, hnd=bool(seed % 2), seed=seed + 1) if mem is None else mem(n_pages, page, hkv, d)
+    q = torch.randn(starts[-1], hq, d, generator=torch.Generator().manual_seed(seed + 2))
+    return starts, kv, table, pre, mem, q
+
+
+def run(T, case, parts, q, units=(1.0, 1.0), **kw):  # noqa: F811
+    starts, kv, table, pre, mem, _ = parts
+    cache = T.PagedCache4(*mem, dtype=q.dtype, k_unit=units[0], v_unit=units[1])
+    ws = torch.empty(cache.workspace_bytes(q.shape[0], q.shape[1]), dtype=torch.uint8, device=DEV)
+    got = T.attention(cache, T.Step(i32(starts), i32(kv), table.to(DEV), pre.to(DEV), case[7]), q, causal=case[6],
+                      workspace=ws, **kw)
+    T.attention_status(ws)
+    return got
+
+
+def want(case, parts, q, units=(1.0, 1.0), scale=None):
+    starts, kv, table, pre, mem, _ = parts
+    return P.attend_step(q, *f64(mem, units), starts, kv, table, pre, case[7], case[5], causal=case[6],
+                         scale=scale or case[4] ** -0.5)
+
+
+@STEPS
+@pytest.mark.parametrize("k_unit,scale", [(1.0, None), (2.0 ** -22, None), (2.0 ** -60, None), (1.0, 2.0 ** -28),
+                                          (2.0 ** 20, 2.0 ** -100), (2.0 ** -60, 2.0 ** 50)])
+@pytest.mark.parametrize("dt", [BF, HF], ids=["bf16", "f16"])
+def test_query_rows_of_zeros_and_tiny_ones(T, case, k_unit, scale, dt):  # noqa: F811
+    """A row whose scores are all zero (or lost beside 1) weighs its keys alike, whatever its masked keys hold."""
+    parts = few(case, dt, 31)
+    q = parts[5]
+    small = [0.0, 2.0 ** -133, 2.0 ** -126, 2.0 ** -100, 2.0 ** -60] if dt == BF else [0.0, 2.0 ** -24, 2.0 ** -14]
+    for i in range(q.shape[0]):
+        for h in range(q.shape[1]):
+            q[i, h] *= small[(i + h) % len(small)]
+    q = q.to(dt).to(DEV)
+    close(*run(T, case, parts, q, (k_unit, 0.5), scale=scale), want(case, parts, q, (k_unit, 0.5), scale))
+
+
+@STEPS
+def test_large_query_rows_over_keys_of_zeros(T, case):  # noqa: F811
+    """Scores of 0 however large the row and the scale are."""
+    parts = few(case, BF, 35)
+    q = (torch.sign(parts[5]) * 2.0 ** 127).to(BF).to(DEV)
+    for m in parts[4][::2]:
+        m.zero_()
+    close(*run(T, case, parts, q, scale=2.0 ** 40), want(case, parts, q, scale=2.0 ** -100))   # (any: 0 in 64 bits too)
