@@ -45,7 +45,7 @@ constexpr int kUnit = 2 * kGroup;           // and of a warp at a time
 constexpr int kFewFrags = 4;                // pieces described ahead
 constexpr int kBarParts = 1;                // named barrier of those warps
 constexpr float kFewBias = 7.f;             // weights are 2^7 times as large (see pack2)
-constexpr float kNoMax = 1e30f;             // bias minus a maximum below any
+constexpr float kNoMax = FLT_MAX;           // bias minus a maximum below any
 
 template <int D, int NT>
 struct Few {

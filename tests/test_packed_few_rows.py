@@ -70,3 +70,28 @@ def test_large_query_rows_over_keys_of_zeros(T, case):  # noqa: F811
     for m in parts[4][::2]:
         m.zero_()
     close(*run(T, case, parts, q, scale=2.0 ** 40), want(case, parts, q, scale=2.0 ** -100))   # (any: 0 in 64 bits too)
+
+
+@pytest.mark.parametrize("case", [ONE, ONE_PREFIX, TWO, TWO_PREFIX, ([40], [300], 4, 2, 128, 64, True, 0)],
+                         ids=["8", "8-prefix", "16", "16-prefix", "many"])
+@pytest.mark.parametrize("dt", [BF, HF], ids=["bf16", "f16"])
+def test_scores_far_below_any_other(T, case, dt):  # noqa: F811
+    """Rows all of whose scores lie below -1e30 (and are exact floats) have keys all the same."""
+    rows, kv, hq, hkv, d, page, causal, prefix = case
+    starts, kv, table, pre, n_pages = R.make_step(rows, kv, page, prefix=prefix, seed=41)
+    mem = pools(n_pages, page, hkv, d, seed=42)
+    mem[0].zero_()
+    mem[0][..., 0] = 6                       # 4 times a scale of 0.5, and zeros
+    mem[2].fill_(0x30)
+    q = torch.zeros(starts[-1], hq, d)
+    q[..., 0] = -2.0 ** (110 if dt == BF else 14)
+    scale = 2.0 ** (0 if dt == BF else 96)
+    q = q.to(dt).to(DEV)
+    parts = (starts, kv, table, pre, mem, q)
+    o, lse = (x.double().cpu().numpy() for x in run(T, case, parts, q, scale=scale))
+    # 64-bit results of equal scores; f16 weights of 1 are exact: f32 sums and the rounding to the type
+    wo, _, wl, _ = want(case, (starts, kv, table, pre, [torch.zeros_like(mem[0])] + mem[1:], q), q, scale=1.0)
+    n = prefix + max(kv)
+    assert np.all(np.abs(o - wo) <= R.EPS[dt] * np.abs(wo) + (n + 64) * 2.0 ** -23 * 6 + (2.0 ** -25 if dt == HF else 0))
+    none = np.isinf(wl)                      # rows before any key
+    assert np.all(lse[none] == -np.inf) and np.all(np.abs(lse[~none] + 2.0 ** 111) <= 2.0 ** -22 * 2.0 ** 111)
