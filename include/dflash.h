@@ -461,13 +461,11 @@ typedef struct dflash_append_args {
                                 dtype; may be q itself when the types and
                                 strides are the same                       */
   int64_t q_out_stride;
-  int32_t interleaved;       /* RoPE pairs: 0: elements j, j + rot_dim / 2
-                                (halves), else 2 j, 2 j + 1                */
 } dflash_append_args;
 
 /* Queries and keys of the step's rows: per head x / sqrt(mean x^2 + eps) *
- * gain (the sum of x^2 a finite float), then RoPE (pairs as `interleaved`
- * says; the rest of a head passes through); keys and values go to their rows of the
+ * gain (the sum of x^2 a finite float), then RoPE (of elements j and j +
+ * rot_dim / 2; the rest of a head passes through); keys and values go to their rows of the
  * cache, queries to q_out, each rounded once.  Row pointers start on 16-byte boundaries (bases and
  * strides).  Rows of the caches that no row of the step names stay as they
  * are; a row whose own index would be negative, or past the block table,
@@ -475,6 +473,9 @@ typedef struct dflash_append_args {
  * the same row of the cache.  One launch. */
 int dflash_step_append(const dflash_paged_cache *cache, const dflash_step *step, const dflash_append_args *args,
                        void *stream);
+/* The same with RoPE of elements 2 j and 2 j + 1. */
+int dflash_step_append_interleaved(const dflash_paged_cache *cache, const dflash_step *step,
+                                   const dflash_append_args *args, void *stream);
 
 /* Bytes of workspace for dflash_step_attention of up to n_rows rows (the
  * current device's SM count sizes it).  Start: 256-byte aligned.  Calls that
@@ -572,13 +573,15 @@ typedef struct dflash_packed_cache {
 
 typedef struct dflash_packed_append_args {
   dflash_append_args rows;   /* as of dflash_step_append                   */
+  int32_t interleaved;       /* RoPE pairs: 0: elements j, j + rot_dim / 2,
+                                else 2 j, 2 j + 1                          */
   void *k_values, *v_values; /* device [n_rows, n_kv_heads, head_dim] in the
                                 cache's dtype, or NULL: what the rows stand
                                 for once rounded; not over k or v          */
   int64_t k_values_stride, v_values_stride;
 } dflash_packed_append_args;
 
-/* dflash_step_append into a packed cache.  With y a key after norm and RoPE, or
+/* dflash_step_append (or _interleaved) into a packed cache.  With y a key after norm and RoPE, or
  * a value: s = max |y| / (6 unit) of the block rounded to e4m3 (nearest, ties to
  * even, at most 448), c = y / (s unit) rounded to e2m1 (nearest, ties to the even
  * code, at most 6; the sign kept, also of 0; 0 where s is).  A block with a NaN or an

@@ -188,7 +188,7 @@ int check_append(const dflash_paged_cache* cache, const dflash_step* step, const
 
 // All of an append's arguments but the cache's.
 int append_args(AppendArgs& a, const dflash_paged_cache* cache, const dflash_step* step,
-                const dflash_append_args* p) {
+                const dflash_append_args* p, bool interleaved) {
   a.s = view(cache, step);
   a.q = p->q;
   a.k = p->k;
@@ -201,7 +201,7 @@ int append_args(AppendArgs& a, const dflash_paged_cache* cache, const dflash_ste
   a.k_gain = p->k_gain;
   a.eps = (float)p->eps;
   a.rot = p->rot_dim;
-  a.interleaved = p->interleaved != 0;
+  a.interleaved = interleaved;
   a.mscale = (float)p->mscale;
   a.positions = p->positions;
   a.q_out = p->q_out;
@@ -212,6 +212,23 @@ int append_args(AppendArgs& a, const dflash_paged_cache* cache, const dflash_ste
     a.turns[i] = (uint64_t)std::ldexp(t - std::floor(t), 64);
   }
   return DFLASH_OK;
+}
+
+int step_append(const dflash_paged_cache* cache, const dflash_step* step, const dflash_append_args* p,
+                bool interleaved, void* stream) {
+  report_error(DFLASH_OK, "");
+  if (int rc = check_cache(cache)) return rc;
+  if (int rc = check_step(cache, step)) return rc;
+  if (int rc = check_append(cache, step, p)) return rc;
+  if (step->n_rows == 0) return DFLASH_OK;
+  AppendArgs a{};
+  if (int rc = append_args(a, cache, step, p, interleaved)) return rc;
+  a.c = {cache->k, cache->v, cache->page_stride, cache->row_stride, cache->head_stride, cache->n_kv_heads,
+         cache->head_dim};
+  int n_sm = 0;
+  if (int rc = sm_count(&n_sm)) return rc;
+  return launched(launch_step_append(a, p->dtype, cache->dtype, n_sm, static_cast<cudaStream_t>(stream)),
+                  "step append");
 }
 
 // A packed cache's shape, for the checks that know the other kind.
@@ -367,19 +384,11 @@ extern "C" {
 
 int dflash_step_append(const dflash_paged_cache* cache, const dflash_step* step, const dflash_append_args* p,
                        void* stream) {
-  report_error(DFLASH_OK, "");
-  if (int rc = check_cache(cache)) return rc;
-  if (int rc = check_step(cache, step)) return rc;
-  if (int rc = check_append(cache, step, p)) return rc;
-  if (step->n_rows == 0) return DFLASH_OK;
-  AppendArgs a{};
-  if (int rc = append_args(a, cache, step, p)) return rc;
-  a.c = {cache->k, cache->v, cache->page_stride, cache->row_stride, cache->head_stride, cache->n_kv_heads,
-         cache->head_dim};
-  int n_sm = 0;
-  if (int rc = sm_count(&n_sm)) return rc;
-  return launched(launch_step_append(a, p->dtype, cache->dtype, n_sm, static_cast<cudaStream_t>(stream)),
-                  "step append");
+  return step_append(cache, step, p, false, stream);
+}
+int dflash_step_append_interleaved(const dflash_paged_cache* cache, const dflash_step* step,
+                                   const dflash_append_args* p, void* stream) {
+  return step_append(cache, step, p, true, stream);
 }
 
 int dflash_step_append_packed(const dflash_packed_cache* cache, const dflash_step* step,
@@ -398,7 +407,7 @@ int dflash_step_append_packed(const dflash_packed_cache* cache, const dflash_ste
     else if (ptr && (ptr == p->rows.k || ptr == p->rows.v))   // (keys may be read again behind the first codes)
       return invalid("rounded rows go elsewhere than to k and v");
   Append4Args a{};
-  if (int rc = append_args(a.a, &shape, step, &p->rows)) return rc;
+  if (int rc = append_args(a.a, &shape, step, &p->rows, p->interleaved != 0)) return rc;
   a.a.c = {cache->k, cache->v, cache->page_stride, cache->row_stride, cache->head_stride, cache->n_kv_heads,
            cache->head_dim};
   a.sc = {cache->k_scale, cache->v_scale, cache->scale_page_stride, cache->scale_row_stride,

@@ -30,9 +30,10 @@ EXPORTS = ("dflash_workspace_bytes", "dflash_create", "dflash_ingest_ctx", "dfla
            "dflash_device_status", "dflash_destroy", "dflash_last_error", "dflash_profile_enable",
            "dflash_profile_read", "dflash_launch_count", "dflash_trace_begin", "dflash_trace_launches",
            "dflash_selftest_wait_timeout", "dflash_attention_plan", "dflash_rope_frequencies", "dflash_step_append",
-           "dflash_step_attention_workspace", "dflash_step_attention", "dflash_step_attention_status",
-           "dflash_step_attention_plan", "dflash_verify_tokens", "dflash_step_append_packed",
-           "dflash_step_attention_packed_workspace", "dflash_step_attention_packed", "dflash_next_step")
+           "dflash_step_append_interleaved", "dflash_step_attention_workspace", "dflash_step_attention",
+           "dflash_step_attention_status", "dflash_step_attention_plan", "dflash_verify_tokens",
+           "dflash_step_append_packed", "dflash_step_attention_packed_workspace", "dflash_step_attention_packed",
+           "dflash_next_step")
 TRACE_WORDS = 16   # u64 words per traced CTA (see dflash_trace_begin)
 KERNEL_KINDS = ("gemm", "attention", "combine", "init", "norm", "finish")
 
@@ -87,7 +88,7 @@ class AppendArgs(ctypes.Structure):
                 ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("q_gain", ctypes.c_void_p),
                 ("k_gain", ctypes.c_void_p), ("eps", ctypes.c_double), ("rot_dim", ctypes.c_int32),
                 ("inv_freq", ctypes.c_void_p), ("mscale", ctypes.c_double), ("positions", ctypes.c_void_p),
-                ("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_int64), ("interleaved", ctypes.c_int32)]
+                ("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_int64)]
 
 
 class PackedCacheDesc(ctypes.Structure):
@@ -100,8 +101,8 @@ class PackedCacheDesc(ctypes.Structure):
 
 
 class PackedAppendArgs(ctypes.Structure):
-    # (the rows' fields, padded as the structure they are in the header)
-    _fields_ = AppendArgs._fields_ + [("_pad", ctypes.c_int32), ("k_values", ctypes.c_void_p),
+    # (the rows' fields are a structure of their own in the header)
+    _fields_ = AppendArgs._fields_ + [("interleaved", ctypes.c_int32), ("k_values", ctypes.c_void_p),
                                       ("v_values", ctypes.c_void_p), ("k_values_stride", ctypes.c_int64),
                                       ("v_values_stride", ctypes.c_int64)]
 
@@ -194,6 +195,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dflash_rope_frequencies.argtypes = [i32, dbl, dbl, i32, dbl, dbl, PDOUBLE, PDOUBLE]
     cache_p, step_p = ctypes.POINTER(PagedCacheDesc), ctypes.POINTER(StepDesc)
     lib.dflash_step_append.argtypes = [vp, vp, vp, vp]   # structures by reference, or their bytes (packer)
+    lib.dflash_step_append_interleaved.argtypes = [vp, vp, vp, vp]
     lib.dflash_step_attention_workspace.argtypes = [cache_p, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
     lib.dflash_step_attention.argtypes = [vp, vp, vp, vp, ctypes.c_size_t, vp]
     lib.dflash_step_attention_status.argtypes = [vp, vp]

@@ -352,14 +352,16 @@ def append(cache: AnyCache, step: Step, q: Optional[torch.Tensor], k: torch.Tens
                 out[2 + i] = _rows(cache, what, t, n, cache.n_kv_heads)[2]
                 out[i] = t.data_ptr()
         a = _packed_append_args(_dtype(k, "rows"), hq, qp, k.data_ptr(), v.data_ptr(), qs, ks, vs, qg, kg, eps, rot,
-                                freq, ms if rope is None else rope.mscale64, pos, qop, qos, inter, 0, *out)
+                                freq, ms if rope is None else rope.mscale64, pos, qop, qos, inter, *out)
         rc = dflash.load_library().dflash_step_append_packed(cache.ref, step.rows(cache, n), a, _stream(dev))
     else:
         if k_values is not None or v_values is not None:
             _refuse("k_values and v_values go with a 4-bit cache")
         a = _append_args(_dtype(k, "rows"), hq, qp, k.data_ptr(), v.data_ptr(), qs, ks, vs, qg, kg, eps, rot, freq, ms,
-                         pos, qop, qos, inter)
-        rc = dflash.load_library().dflash_step_append(cache.ref, step.rows(cache, n), a, _stream(dev))
+                         pos, qop, qos)
+        lib = dflash.load_library()
+        call = lib.dflash_step_append_interleaved if inter else lib.dflash_step_append
+        rc = call(cache.ref, step.rows(cache, n), a, _stream(dev))
     if rc:
         _check(rc)
     return q_out
