@@ -186,6 +186,33 @@ int check_append(const dflash_paged_cache* cache, const dflash_step* step, const
   return DFLASH_OK;
 }
 
+// f / (2 pi) modulo 1, times 2^64, to the nearest: f's 53 bits times the first 192 bits of
+// 1 / (2 pi), enough for |f| below 2^120 (others get 0).  A quotient of doubles has 53 bits, which
+// is 2^-32 of a turn at position 2^24 for a frequency of 1.
+uint64_t turns_of(double f) {
+  static const uint64_t inverse[3] = {0x36d8a5664f10e410, 0x7f09d5f47d4d3770, 0x28be60db9391054a};   // low word first
+  int e = 0;
+  const uint64_t m = (uint64_t)std::ldexp(std::frexp(std::fabs(f), &e), 53);   // |f| = m 2^(e - 53)
+  if (e > 120) return 0;
+  uint64_t w[5] = {};               // m / (2 pi) times 2^192
+  unsigned __int128 carry = 0;
+  for (int i = 0; i < 3; ++i) {
+    carry += (unsigned __int128)m * inverse[i];
+    w[i] = (uint64_t)carry;
+    carry >>= 64;
+  }
+  w[3] = (uint64_t)carry;
+  const int down = 181 - e;         // bits of w below the result's
+  if (down > 256) return 0;
+  auto bits = [&](int at) {         // 64 of them from bit `at` on (0: below the first)
+    const int i = at >> 6, s = at & 63;
+    if (i > 3) return (uint64_t)0;
+    return s ? w[i] >> s | w[i + 1] << (64 - s) : w[i];
+  };
+  const uint64_t t = bits(down) + (bits(down - 1) & 1);
+  return f < 0 ? 0 - t : t;
+}
+
 // All of an append's arguments but the cache's.
 int append_args(AppendArgs& a, const dflash_paged_cache* cache, const dflash_step* step,
                 const dflash_append_args* p, bool interleaved) {
@@ -207,9 +234,8 @@ int append_args(AppendArgs& a, const dflash_paged_cache* cache, const dflash_ste
   a.q_out = p->q_out;
   a.q_out_stride = p->q_out_stride;
   for (int i = 0; i < p->rot_dim / 2; ++i) {
-    const double t = p->inv_freq[i] / (2.0 * M_PI);
-    if (!std::isfinite(t)) return invalid("RoPE frequencies");
-    a.turns[i] = (uint64_t)std::ldexp(t - std::floor(t), 64);
+    if (!std::isfinite(p->inv_freq[i])) return invalid("RoPE frequencies");
+    a.turns[i] = turns_of(p->inv_freq[i]);
   }
   return DFLASH_OK;
 }
