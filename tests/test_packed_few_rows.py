@@ -95,3 +95,61 @@ def test_scores_far_below_any_other(T, case, dt):  # noqa: F811
     assert np.all(np.abs(o - wo) <= R.EPS[dt] * np.abs(wo) + (n + 64) * 2.0 ** -23 * 6 + (2.0 ** -25 if dt == HF else 0))
     none = np.isinf(wl)                      # rows before any key
     assert np.all(lse[none] == -np.inf) and np.all(np.abs(lse[~none] + 2.0 ** 111) <= 2.0 ** -22 * 2.0 ** 111)
+
+
+@STEPS
+@pytest.mark.parametrize("dt", [BF, HF], ids=["bf16", "f16"])
+def test_units_a_scale_and_strided_rows(T, case, dt):  # noqa: F811
+    """Large scores, a scale of the caller's, units of both sides, queries and results inside wider rows."""
+    parts = few(case, dt, 51)
+    q0 = parts[5]
+    n, hq, d = q0.shape
+    wide = torch.zeros(n, hq + 2, d, dtype=dt, device=DEV)
+    q = wide[:, :hq]
+    q.copy_(3 * q0)
+    out = torch.full((n, hq + 3, d), 5.0, dtype=dt, device=DEV)
+    units = (4.0, 2.0 ** -9)
+    got = run(T, case, parts, q, units, scale=0.125, out=out[:, :hq])
+    close(*got, want(case, parts, q, units, 0.125))
+    assert bool((out[:, hq:] == 5).all())
+
+
+@STEPS
+def test_bf16_queries_outside_the_range_of_f16(T, case):  # noqa: F811
+    """Rows 2^20 and 2^-20 times as large, heads of both sizes in one row, and codes and scales over their whole range."""
+    hkv, d = case[3], case[4]
+    rng = np.random.default_rng(52)
+
+    def any_bytes(n_pages, page, hkv, d):
+        mem = [torch.from_numpy(rng.integers(0, 256, (n_pages, page, hkv, d // 2), dtype=np.uint8)).to(DEV) for _ in range(2)]
+        return mem + [torch.from_numpy(rng.integers(0, 0x7F, (n_pages, hkv, page, d // 16), dtype=np.uint8)).to(DEV)
+                      .transpose(1, 2) for _ in range(2)]
+
+    parts = few(case, BF, 53, any_bytes)
+    q = parts[5]
+    for i in range(q.shape[0]):
+        for h in range(q.shape[1]):
+            q[i, h] *= (2.0 ** 20, 2.0 ** -20, 1.0)[(2 * i + h) % 3]
+    q = q.to(BF).to(DEV)
+    close(*run(T, case, parts, q, scale=2.0 ** -28), want(case, parts, q, scale=2.0 ** -28))
+    # and rows of one size far from 1, whose scores a scale brings back
+    for size in (2.0 ** 100, 2.0 ** -60):
+        x = (parts[5].sign() * size).to(BF).to(DEV)
+        scale = float(2.0 ** -10 / size / 32)
+        close(*run(T, case, parts, x, scale=scale), want(case, parts, x, scale=scale))
+
+
+@pytest.mark.parametrize("case", [ONE, TWO_PREFIX, ([40, 9], [300, 700], 4, 2, 128, 64, True, 129),
+                                  ([1] * 20, [400 + 77 * i for i in range(20)], 16, 2, 128, 64, True, 1500),
+                                  ([1, 60], [3000, 900], 8, 1, 64, 16, True, 0)],
+                         ids=["few", "few-prefix", "many", "decoding", "both"])
+def test_results_are_the_same_bits_every_time(T, case):  # noqa: F811
+    rows, kv, hq, hkv, d, page, causal, prefix = case
+    starts, kv, table, pre, n_pages = R.make_step(rows, kv, page, prefix=prefix, seed=61)
+    parts = (starts, kv, table, pre, pools(n_pages, page, hkv, d, seed=62), None)
+    q = torch.randn(starts[-1], hq, d, generator=torch.Generator().manual_seed(63)).to(BF).to(DEV)
+    o, lse = run(T, case, parts, q)
+    close(o, lse, want(case, parts, q))
+    for _ in range(20):
+        a, b = run(T, case, parts, q)
+        assert torch.equal(a, o) and torch.equal(b, lse)
