@@ -503,7 +503,8 @@ typedef struct dflash_attention_args {
  * that element not finite (NaN within a tile of rows) in every row that sees
  * it, and only there; keys and values before the step's rows are finite or
  * spread to the whole sequence (the prefix's to the batch).  Scores and sums
- * are f32, of weights up to 2^8: values times that and the number of keys are
+ * are f32 (a row with scores past 2^24, whose f32 steps are whole units, may come
+ * out not finite), of weights up to 2^8: values times that and the number of keys are
  * finite floats (f16 ones always are).  Softmax weights are rounded to the
  * cache's type for the product with V (f16: at 2^7 times their size, so that a
  * key's share below 2^-32 of the largest is what can be lost).  Two launches;
@@ -581,9 +582,9 @@ typedef struct dflash_packed_append_args {
   int64_t k_values_stride, v_values_stride;
 } dflash_packed_append_args;
 
-/* dflash_step_append (or _interleaved) into a packed cache.  With y a key after norm and RoPE, or
- * a value: s = max |y| / (6 unit) of the block rounded to e4m3 (nearest, ties to
- * even, at most 448), c = y / (s unit) rounded to e2m1 (nearest, ties to the even
+/* dflash_step_append (or _interleaved) into a packed cache.  With y a key after
+ * norm and RoPE, or a value: s = max |y| / (6 unit) of the block rounded to e4m3
+ * (nearest, ties to even, at most 448), c = y / (s unit) rounded to e2m1 (nearest, ties to the even
  * code, at most 6; the sign kept, also of 0; 0 where s is).  A block with a NaN or an
  * infinity gets s = NaN.  The codes are those of y in exact arithmetic (eps at
  * least 2^-80, angles to 2^-40 of a turn at positions below 2^24): they do not
@@ -596,8 +597,10 @@ int dflash_step_append_packed(const dflash_packed_cache *cache, const dflash_ste
  * workspace rules and status (dflash_step_attention_status), queries and results
  * in the cache's dtype.  Keys and values are what their codes and scales stand
  * for, exactly; softmax weights are rounded to f16 (at 2^7 times their size) for
- * the product with V.  Results are finite floats while unit * 2688 times the
- * number of keys is.  What the cache holds past a sequence's or the prefix's
+ * the product with V.  Where rows are few, bf16 queries go into the product with K
+ * as f16 times a power of two of the row: an element is off by up to 2^-39 of its
+ * row's largest.  Results are finite floats while unit * 2688 times the number of
+ * keys is (and scores are as there).  What the cache holds past a sequence's or the prefix's
  * last key has no effect.  A NaN scale leaves its block's 16 elements NaN in every row
  * that sees the key (of a key: the row's whole result) and, in the step's own rows,
  * only there; before the step's rows it may spread to the whole sequence (the

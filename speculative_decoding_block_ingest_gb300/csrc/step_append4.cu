@@ -218,8 +218,9 @@ __device__ __forceinline__ void code_exactly(const Append4Args& p, long row, int
 // spill, 293).
 constexpr int kAppendCtas = 2;
 
-// Numbers of two floats (the second at most half a step of the first): about 2^-46 of
-// a sum's or product's terms is lost.
+// Numbers of two floats (the second at most half a step of the first), with Knuth's error-free
+// sum, Dekker's for an ordered pair, and the product's error by fma (Ogita, Rump and Oishi,
+// "Accurate sum and dot product", 2005): about 2^-46 of a sum's or product's terms is lost.
 struct Two {
   float h, l;
 };

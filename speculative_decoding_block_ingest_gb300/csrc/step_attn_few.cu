@@ -5,11 +5,12 @@
 // step_attn.cu; what is different is that the keys' bytes bound it, and that codes
 // have to become f16 on the way: 144 bytes a key, 256 values.
 //
-// On the 5th-generation tensor cores an operand comes from shared memory, so every
-// value would be written there as f16 and read again: 1600 cycles for a block of
-// 128 keys that HBM delivers in 790, for 128 query rows of which 16 exist.  Here codes
-// go from shared memory to registers, become f16 there and are a warp-wide product's
-// operand at once (mma.sync, 16 keys or elements by 8 query rows).
+// step_attn.cu writes every value as f16 to a tile in shared memory, where its products
+// take K and V from: 1600 cycles for a block of 128 keys that HBM delivers in 790, for 128
+// query rows of which 16 exist.  Here codes go from shared memory to registers, become f16
+// there and are a warp-wide product's operand at once (mma.sync, 16 keys or elements by 8
+// query rows).  (Tensor memory can hold one operand of a tcgen05.mma; K or V from there is
+// not tried.)
 //
 // For 16 keys of a warp and N tiles of 8 query rows (keys and elements may come in
 // any order, as long as both operands agree):
@@ -189,8 +190,8 @@ struct Rows {
       }
       float up = 1.f;             // what the row's scores are to be multiplied by
       if constexpr (BF16) {
-        // bf16's range in f16: the row times 2^-e, its largest element in [2^14, 2^15); what is
-        // below 2^-24 then is less than 2^-38 of that
+        // bf16's range in f16: the row times 2^-e, its largest element in [2^14, 2^15); an
+        // element is off by half of f16's smallest step, 2^-24, which is 2^-39 of the largest
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) top = max(top, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
