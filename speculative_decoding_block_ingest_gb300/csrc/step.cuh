@@ -131,7 +131,6 @@ struct StepAttnArgs {
   int tpt;             // tokens of a 128-row tile: floor(128 / G)
   int causal;
   float scale_log2;    // scale * log2(e)
-  float out_scale;     // of the results
   int bf16;            // else f16
   int box_rows, boxes; // rows of one cache box (a page, at most 128) and boxes of a 128-key tile
   void* out;
@@ -148,10 +147,12 @@ struct StepAttnArgs {
   float2* seg_ml[2];   // [n_rows][Hq]: its (max, sum)
   float* cta_o;        // [cta_row][d]: the fragment a CTA continues
   float2* cta_ml;      // [cta_row]
-  int few_rows;        // most query rows of an item of step_attn_few.cu: 8 or kFewRows
-  int n_sm;
   int n_cta;           // CTAs that leave partial results: n_wide of step_attn.cu, whose rows come
   int n_wide;          // first, then those of step_attn_few.cu (16 rows each)
+  int n_sm;
+  // (of a packed cache, behind the others: among them they cost the 16-bit kernel 0.7 us of 111)
+  int few_rows;        // most query rows of an item of step_attn_few.cu: 8 or kFewRows
+  float out_scale;     // of the results
   const void* q;       // (step_attn_few.cu; the other kernel loads boxes)
   long q_stride;
 };

@@ -179,7 +179,7 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
 // This CTA's pieces of n_cta CTAs' work, described in a ring (and then given to
 // `each`); seg -1 ends them.  A warp's work.
 template <class AnyWalk, class Each>
-__device__ __forceinline__ void plan_pieces(AnyWalk w, int n_cta, Frag* frag, uint64_t* ffull, uint64_t* fempty,
+__device__ __forceinline__ void plan_pieces(AnyWalk& w, int n_cta, Frag* frag, uint64_t* ffull, uint64_t* fempty,
                                             uint32_t n_frags, int lane, Each&& each) {
   // The warp counts all units, 32 sequences at a time, then looks for the
   // sequence that holds this CTA's first.
